@@ -18,7 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libpfkv.so")
 SOURCES = ["api.cu", "append.cu", "decode.cu", "decode_pers.cu", "decode_pers_d64.cu", "combine_pers.cu",
-           "decode_noalloc.cu", "graph.cu", "mass.cu", "selftest.cu", "stage.cu"]
+           "decode_noalloc.cu", "graph.cu", "mass.cu", "selftest.cu", "stage.cu", "rope.cu", "latent.cu",
+           "latent_decode.cu", "latent_prefill.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "-Xptxas", "-v",
          "--expt-relaxed-constexpr", "-I" + os.path.join(ROOT, "include")]
@@ -33,7 +34,8 @@ def _nvcc():
 
 def _inputs():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files += [os.path.join(ROOT, "include", "pfkv.h"), __file__]
+    include = os.path.join(ROOT, "include")
+    files += [os.path.join(include, f) for f in os.listdir(include)] + [__file__]
     return files
 
 

@@ -6,6 +6,7 @@
 #include <cstdint>
 #include <cstring>
 
+#include "latent_internal.cuh"
 #include "pfkv_internal.cuh"
 
 namespace pfkv {
@@ -15,6 +16,8 @@ constexpr int kMaxDevices = 64;
 // per-device: 0 = unknown, 1 = supported (sm_103), 2 = unsupported; SM count
 std::atomic<int> g_dev_state[kMaxDevices];
 std::atomic<int> g_dev_sms[kMaxDevices];
+
+}  // namespace
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -46,6 +49,10 @@ pfkv_status device_check(int *num_sms) {
             if (e == cudaSuccess) e = preload_split_generic();
             if (e == cudaSuccess) e = preload_mass();
             if (e == cudaSuccess) e = preload_stage();
+            if (e == cudaSuccess) e = preload_rope();
+            if (e == cudaSuccess) e = preload_latent();
+            if (e == cudaSuccess) e = preload_latent_decode();
+            if (e == cudaSuccess) e = preload_latent_prefill();
             if (e != cudaSuccess) {
                 cudaGetLastError();
                 return PFKV_ERR_CUDA;
@@ -90,6 +97,8 @@ pfkv_status check_pages(const pfkv_cache *c, const pfkv_pages *p) {
     if (p->expected_tags && !aligned(p->expected_tags, 4)) return PFKV_ERR_ALIGNMENT;
     return PFKV_OK;
 }
+
+namespace {
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 

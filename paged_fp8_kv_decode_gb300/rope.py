@@ -1,0 +1,148 @@
+"""ctypes binding of the rotary append of libpfkv.so (argument marshalling only).
+
+Every function has the name of the C entry point that it calls (see
+``include/pfkv_rope.h`` for the full contract); caches, tables, streams and
+errors are those of ``binding``.
+"""
+from __future__ import annotations
+
+import ctypes
+import dataclasses
+from typing import Optional
+
+import torch
+
+from . import binding as B
+
+# every symbol include/pfkv_rope.h declares
+EXPORTED = ("pfkv_rope_append",)
+
+
+class _CRope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class _CRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64),
+                ("stride_t", ctypes.c_int64), ("stride_h", ctypes.c_int64)]
+
+
+class _CNewTokens(ctypes.Structure):
+    _fields_ = [("num_new_tokens", ctypes.c_int32), ("positions", ctypes.c_void_p),
+                ("new_lens", ctypes.c_void_p), ("rope_positions", ctypes.c_void_p),
+                ("row_starts", ctypes.c_void_p), ("total_rows", ctypes.c_int64)]
+
+
+@dataclasses.dataclass
+class Rope:
+    """The rotation: inv_freq float32 CUDA tensor [rot_dim / 2] (radians per
+    position), pairs interleaved or half the rotated part apart, and a factor
+    on the turned elements."""
+    inv_freq: torch.Tensor
+    interleaved: bool = False
+    scale: float = 1.0
+
+    def c_struct(self) -> _CRope:
+        if self.inv_freq.dtype != torch.float32 or not self.inv_freq.is_contiguous():
+            raise ValueError("inv_freq: contiguous float32")
+        return _CRope(B._ptr(self.inv_freq), 2 * self.inv_freq.numel(), int(bool(self.interleaved)),
+                      float(self.scale))
+
+
+def _rows(x: torch.Tensor, packed: bool, heads: bool, name: str, dim: Optional[int] = None) -> _CRows:
+    """bf16 rows as the C ABI takes them: [B][T][H][D] padded or [rows][H][D]
+    packed, without H where the rows are shared by all heads; any strides that
+    leave a row's elements contiguous."""
+    want = 2 + (not packed) + heads
+    if x.dtype != torch.bfloat16 or x.dim() != want or (x.shape[-1] > 1 and x.stride(-1) != 1):
+        raise ValueError(f"{name}: bfloat16 tensor of {want} dimensions with contiguous rows")
+    if dim is not None and x.shape[-1] != dim:
+        raise ValueError(f"{name}: rows of {dim} elements")
+    s = x.stride()
+    sb = 0 if packed else s[0]
+    st = s[0] if packed else s[1]
+    return _CRows(B._ptr(x), sb, st, s[-2] if heads else 0)
+
+
+def _i32(t: Optional[torch.Tensor], name: str):
+    if t is not None and t.dtype != torch.int32:
+        raise ValueError(f"{name}: int32")
+    return B._ptr(t)
+
+
+def _new_tokens(first: torch.Tensor, batch: int, positions, new_lens, rope_positions, row_starts,
+                max_new_tokens) -> _CNewTokens:
+    """`first`: the tensor of new rows that gives T or the number of rows."""
+    if row_starts is None:
+        if first.shape[0] != batch:
+            raise ValueError("padded rows: one entry per request")
+        T, total = int(first.shape[1]), 0
+        if max_new_tokens is not None and int(max_new_tokens) != T:
+            raise ValueError("padded rows: max_new_tokens is their second dimension")
+    else:
+        if max_new_tokens is None:
+            raise ValueError("packed rows need max_new_tokens")
+        if row_starts.numel() != batch + 1:
+            raise ValueError("row_starts: batch + 1 entries")
+        T, total = int(max_new_tokens), int(first.shape[0])
+    return _CNewTokens(T, _i32(positions, "positions"), _i32(new_lens, "new_lens"),
+                       _i32(rope_positions, "rope_positions"), _i32(row_starts, "row_starts"), total)
+
+
+def _queries(q, q_out, first, packed, dim):
+    """(q rows, q_out rows, heads), or three empty ones without queries."""
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out: both or neither")
+    if q is None:
+        return None, None, 0
+    lead = 1 if packed else 2
+    if q.shape != q_out.shape or q.shape[:lead] != first.shape[:lead]:
+        raise ValueError("q and q_out: rows for the same tokens as the new keys")
+    return _rows(q, packed, True, "q", dim), _rows(q_out, packed, True, "q_out", dim), int(q.shape[-2])
+
+
+def _ref(s):
+    return None if s is None else ctypes.byref(s)
+
+
+def lib() -> ctypes.CDLL:
+    """libpfkv.so with these calls' signatures set."""
+    L = B.lib()
+    if not getattr(L, "_rope_calls", False):
+        P, I32 = ctypes.c_void_p, ctypes.c_int32
+        rows = ctypes.POINTER(_CRows)
+        L.pfkv_rope_append.argtypes = [ctypes.POINTER(B._CCache), ctypes.POINTER(B._CPages),
+                                       ctypes.POINTER(_CRope), ctypes.POINTER(_CNewTokens), rows,
+                                       rows, rows, rows, I32, P, P]
+        L.pfkv_rope_append.restype = ctypes.c_int
+        L._rope_calls = True
+    return L
+
+
+def pfkv_rope_append(cache: B.Cache, pages: B.Pages, rope: Rope, positions: torch.Tensor,
+                     k_new: torch.Tensor, v_new: torch.Tensor, q: Optional[torch.Tensor] = None,
+                     q_out: Optional[torch.Tensor] = None,
+                     new_lens: Optional[torch.Tensor] = None,
+                     rope_positions: Optional[torch.Tensor] = None,
+                     row_starts: Optional[torch.Tensor] = None,
+                     max_new_tokens: Optional[int] = None, flags: Optional[torch.Tensor] = None,
+                     stream=None) -> None:
+    """k_new, v_new: bf16 [B][T][Hkv][D] (padded), or [rows][Hkv][D] with
+    row_starts (int32 [B + 1]) and max_new_tokens; q, q_out the same with the
+    query heads (q_out may be q); positions, new_lens int32 with the length
+    strides of ``pages``, rope_positions int32 [B]; flags uint8
+    [>= round_up(B, 4)] (OR-ed)."""
+    packed = row_starts is not None
+    D, heads = int(cache.k_pages.shape[3]), int(cache.k_pages.shape[1])
+    tok = _new_tokens(k_new, pages.batch, positions, new_lens, rope_positions, row_starts,
+                      max_new_tokens)
+    if k_new.shape != v_new.shape or k_new.shape[-2] != heads:
+        raise ValueError("k_new and v_new: one row per kv head")
+    k, v = _rows(k_new, packed, True, "k_new", D), _rows(v_new, packed, True, "v_new", D)
+    qr, qo, hq = _queries(q, q_out, k_new, packed, D)
+    c, p, r = cache.c_struct(), pages.c_struct(), rope.c_struct()
+    B._check(lib().pfkv_rope_append(ctypes.byref(c), ctypes.byref(p), ctypes.byref(r),
+                                    ctypes.byref(tok), ctypes.byref(k), ctypes.byref(v), _ref(qr),
+                                    _ref(qo), hq, B._ptr(flags), B._stream(stream)),
+             "pfkv_rope_append")
