@@ -131,8 +131,8 @@ pfkv_status pfkv_latent_gather(const pfkv_latent_cache *cache, const pfkv_pages 
  * BF16 pools: q, c, r are exact; a softmax weight is rounded once to bf16.  FP8
  * pools: e4m3 values are exact in f16; q_c enters as f16 after a power-of-two
  * scaling a row (exact for elements within 2^14 of the row's largest); a weight
- * times its page's scale, over a running power-of-two-free reference, is rounded
- * once to f16.  The weights' sum is of the rounded weights.  Scores, the running
+ * times its page's scale is rounded once to f16 (within 2^-11, or 2^-32 of the
+ * row's largest where that is more).  The weights' sum is of the rounded weights.  Scores, the running
  * maximum, sums and the merge of partial results are fp32.
  */
 pfkv_status pfkv_latent_decode_workspace_size(const pfkv_latent_cache *cache, const pfkv_pages *pages,

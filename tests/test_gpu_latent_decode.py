@@ -48,7 +48,16 @@ def check(cache, bt, lens, qc, qr, out, scale=SCALE, skip=()):
             k = torch.cat((c[:m], r[:m]), 1)
             q = torch.cat((qc[b, t], qr[b, t]), 1).double()
             err = score_error(q, k, scale)
-            o, tol = softmax_attend(q @ k.T * scale, c[:m], F16 if fp8 else BF16, err)
+            s = q @ k.T * scale
+            o, tol = softmax_attend(s, c[:m], F16 if fp8 else BF16, err)
+            if fp8:
+                # f16 weights p_j z_j (z_j: the page's scale) over a reference that leaves
+                # the largest at 2^7 or more: below 2^-14 they have an absolute step of
+                # 2^-24, half of it is 2^-25 = 2^-32 of the largest.  In p_j that is 2^-32
+                # max(p z) / z_j, which meets c_j in the product and o in the sum.
+                z = cache.c_scale[bt[b, :(m + PAGE - 1) // PAGE].long()].double().repeat_interleave(PAGE)[:m]
+                pz = (torch.softmax(s, -1) * z).amax(-1, keepdim=True)
+                tol = tol + 2.0 ** -32 * pz * ((c[:m].abs() / z[:, None]).sum(0) + o.abs() * (1 / z).sum())
             close(out[b, t], o, tol, (b, t, n))
 
 
