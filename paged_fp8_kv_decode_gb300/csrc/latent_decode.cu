@@ -23,9 +23,10 @@
 // CTAs.  Each latent is thus read from HBM once, and from L2 twice.  Shared
 // memory (Q 72 KB, K 72 KB, V 64 KB, P 16 KB) leaves no room for second buffers;
 // instead every chunk's slot is refilled as soon as its last product has
-// completed, and an L2 prefetch runs two tiles ahead.
+// completed, from registers that the next tile's latents were loaded into, and an
+// L2 prefetch runs ahead of that.
 //
-// Softmax: one pass.  Two threads hold a row (64 tokens each), in log2 units, with
+// Softmax: one pass.  Four threads hold a row (32 tokens each), in log2 units, with
 // a running reference that moves only when the maximum has grown by 2^8 (then O
 // is rescaled in tensor memory).  FP8: a weight enters the second product times
 // its page's scale z_j; the reference is of s_j + log2 z_j, so that the f16
@@ -37,10 +38,12 @@
 // directly; parts of a pair go to the workspace (normalised rows and their
 // log2-sum-exp) and a second kernel merges them.
 //
-// Roles of a CTA's sixteen warps: 0-3 softmax and output; 4 issues the products
-// (even CTA) or passes on to it that the odd CTA's operands are in place; 5 and 6
-// load K and V (BF16: TMA, one box of 16 tokens x 64 values a page and chunk); FP8:
-// 8-11 and 12-15 convert K and V to f16 between L2 and shared memory; 8-11 load Q.
+// Roles of a CTA's twenty warps: 0-7 softmax and output (four threads a row); 8, in
+// the even CTA, issues the pair's products; 9 loads the rotated keys and 10 V of BF16
+// pools by TMA; 11 looks up pages, checks and scales six tiles ahead of their use and
+// prefetches them into L2; 12-19 carry latents through registers, the next tile's
+// loaded while this one is stored: K of BF16 pools (two warps a stage), or K (a warp
+// a stage) and V (a warp a chunk) of FP8 pools, converted to f16 on the way.
 #include <type_traits>
 
 #include "latent_internal.cuh"
@@ -54,9 +57,17 @@ constexpr int kTile = 128;                    // tokens a tile
 constexpr int kTilePages = kTile / kPage;
 constexpr int kRowsCta = 64, kRowBlock = 128;
 constexpr int kKChunks = 9;                   // 8 of latents, 1 of rotated keys
+constexpr int kKStages = 5;                   // two chunks each, the rotated keys alone
+constexpr int kRing = 6;                      // tiles looked up ahead
 constexpr uint32_t kChunkB = kRowsCta * 128;  // Q, K and P chunks: 64 rows of 128 bytes
 constexpr uint32_t kVChunkB = kTile * 128;
-constexpr int kThreads = 512;
+// V of one block of 256 values: two chunks of 64.  FP8: chunk by chunk, 128 tokens
+// each.  BF16: page by page, both chunks of 16 tokens each, as one TMA box brings them.
+template <bool FP8>
+constexpr uint32_t kVLbo = FP8 ? kVChunkB : 2048u;  // to the next chunk
+template <bool FP8>
+constexpr uint32_t kVStep = FP8 ? 2048u : 4096u;    // to the next page
+constexpr int kThreads = 640;
 constexpr uint32_t kOffQ = 0, kOffK = kKChunks * kChunkB, kOffV = 2 * kKChunks * kChunkB,
                    kOffP = kOffV + 4 * kVChunkB, kOffMisc = kOffP + 2 * kChunkB;
 constexpr float kLazyGrowth = 8.f;
@@ -68,18 +79,30 @@ constexpr float kWeightBias = FP8 ? 7.f : 0.f;
 constexpr uint32_t kColS = 256;               // tensor memory: O in columns 0-255, S above
 constexpr float kNegInf = -INFINITY;
 
+// What the roles need to know of a tile.
+struct Tile {
+    int id[kTilePages];      // physical pages, -1 for one that is not to be read
+    float z[kTilePages];     // FP8: their scales
+    int b, block, left;      // request, row block, the request's tokens from this tile's first on
+    uint32_t flags;
+};
+constexpr uint32_t kFirst = 1, kLast = 2, kWhole = 4, kBegins = 8;  // of the part of a (request, row block)
+
 struct Misc {
-    uint64_t kfull[kKChunks], kempty[kKChunks], pk[kKChunks];
-    uint64_t vfull[2], vempty[2], pv[2];
-    uint64_t sfull[2], sq[2], pready, pvdone, qfull, pq, qfree, drain;
-    long long warp_sum[kThreads / 32];
+    // operands of both CTAs in place (in the even CTA), slots free again (in both)
+    uint64_t kfull[kKStages], kempty[kKStages], vfull[2], vempty[2];
+    uint64_t mfull[kRing], mempty[kRing];
+    uint64_t sfull[2], pready, pvdone, qfull, drain;
+    Tile tile[kRing];
+    union {
+        long long warp_sum[kThreads / 32];
+        float xm[4][kRowsCta];
+    };
     long long x0, x1, off;
     int b0;
     uint32_t tmem, gave_up;
-    float xm[kRowBlock];
-    float qscale[2][kRowsCta];
 };
-constexpr size_t kSmemBytes = kOffMisc + sizeof(Misc) + 1024;
+constexpr size_t kSmemBytes = kOffMisc + sizeof(Misc);
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
 // Workspace: normalised partial rows and their log2-sum-exp, two blocks a
@@ -89,6 +112,7 @@ struct Parts {
     float *o;        // [clusters][2][rows][512]
     float *lse;      // [clusters][2][rows]
     uint32_t *gave_up;  // [clusters][2]
+    uint32_t *status;   // [request x row block + cluster]: flags of the pages that the cluster looked up
     int rows;        // min(R, 128)
 };
 
@@ -137,41 +161,6 @@ struct Walk {
     }
 };
 
-// The same, a tile at a time.
-struct TileWalk {
-    Walk w;
-    Segment s;
-    int t;
-    bool first, last, live;
-    __device__ __forceinline__ void start(const LatentDecodeArgs &a, int blocks, const Walk &walk) {
-        w = walk;
-        live = w.next(a, blocks, s);
-        t = live ? s.t0 : 0;
-        first = true;
-        last = live && t + 1 == s.t1;
-    }
-    __device__ __forceinline__ void step(const LatentDecodeArgs &a, int blocks) {
-        if (++t < s.t1) {
-            first = false;
-        } else {
-            live = w.next(a, blocks, s);
-            t = live ? s.t0 : 0;
-            first = true;
-        }
-        last = live && t + 1 == s.t1;
-    }
-};
-
-// The physical page of logical page p of request b, or -1 for one that is not to
-// be read (past the length, a bad id, a stale tag: the merge kernel flags those
-// and zeroes the request).
-__device__ __forceinline__ int page_of(const LatentDecodeArgs &a, int b, int p, int n) {
-    if (p >= (n + kPage - 1) / kPage) return -1;
-    const long long bi = (long long)b * a.pool.bt_sb + p;
-    const int id = a.pool.block_tables[bi];
-    return latent_entry_bits(a.pool, id, bi) ? -1 : id;
-}
-
 __device__ __forceinline__ uint4 cvt_e4m3x8(uint32_t lo, uint32_t hi) {
     uint4 r;
     asm("{\n\t.reg .b16 a, b, c, d;\n\tmov.b32 {a, b}, %4;\n\tmov.b32 {c, d}, %5;\n\t"
@@ -187,116 +176,122 @@ __device__ __forceinline__ uint4 *piece(uint8_t *chunk, int r, int c) {
     return reinterpret_cast<uint4 *>(chunk + r * 128 + ((c ^ (r & 7)) << 4));
 }
 
-// Query rows of one segment into shared memory, by 128 threads: two a row.  FP8:
-// the latent part as f16 over a power of two that puts its largest element in
-// [1, 2); the rotated part stays bf16.  Rows past the last are zero.
-template <bool FP8>
-__device__ __forceinline__ void load_queries(const LatentDecodeArgs &a, const Segment &s, int R, uint32_t rank,
-                                             uint8_t *q, float *qscale, int i) {
-    const int r = i >> 1, sub = i & 1;
-    const int row = s.block * kRowBlock + (int)rank * kRowsCta + r;
-    const bool live = row < R;
-    const int t = live ? row / a.H : 0, h = live ? row - t * a.H : 0;
-    const uint4 *c = reinterpret_cast<const uint4 *>(a.qc.p + (long long)s.b * a.qc.sb + (long long)t * a.qc.st +
-                                                     (long long)h * a.qc.sh);
-    const uint4 *e = reinterpret_cast<const uint4 *>(a.qr.p + (long long)s.b * a.qr.sb + (long long)t * a.qr.st +
-                                                     (long long)h * a.qr.sh);
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    float inv = 1.f;
-    if constexpr (FP8) {
-        uint32_t top = 0;  // largest magnitude as bf16 bits (integers order as magnitudes do)
+// Eight query rows, r0 .. r0 + 7 of the CTA's 64, into shared memory by one warp, all
+// copies in flight at once; rows past the last are zero.
+__device__ __forceinline__ void copy_queries(const LatentDecodeArgs &a, int b, int block, int R, uint32_t rank,
+                                             uint8_t *q, int r0, int lane) {
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            uint4 w[16];
+    for (int g = 0; g < 2; ++g) {
+        const int r = r0 + g * 4 + (lane >> 3), pc = lane & 7;
+        const int row = block * kRowBlock + (int)rank * kRowsCta + r;
+        const bool live = row < R;
+        const int t = live ? row / a.H : 0, h = live ? row - t * a.H : 0;
+        const __nv_bfloat16 *c = a.qc.p + (long long)b * a.qc.sb + (long long)t * a.qc.st + (long long)h * a.qc.sh;
+        const __nv_bfloat16 *e = a.qr.p + (long long)b * a.qr.sb + (long long)t * a.qr.st + (long long)h * a.qr.sh;
+        const uint32_t bytes = live ? 16u : 0u;  // the rest of a copy's 16 bytes is filled with zeros
 #pragma unroll
-            for (int j = 0; j < 16; ++j) w[j] = live ? c[(g * 16 + j) * 2 + sub] : zero;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) top = max(top, max(u[k] & 0x7FFFu, (u[k] >> 16) & 0x7FFFu));
-            }
-        }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        // biased exponent, kept where both 2^e and 2^-e are normal fp32 numbers
-        const int eb = min(253, max(1, (int)(top >> 7)));
-        inv = __uint_as_float((uint32_t)(254 - eb) << 23);
-        if (sub == 0) qscale[r] = __uint_as_float((uint32_t)eb << 23);
-    }
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        uint4 w[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = live ? c[(g * 8 + j) * 2 + sub] : zero;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int p = (g * 8 + j) * 2 + sub;
-            if constexpr (FP8) {
-                const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-                uint32_t o[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 f = bf16x2_to_float2(u[k]);
-                    const __half2 v = __floats2half2_rn(f.x * inv, f.y * inv);
-                    o[k] = *reinterpret_cast<const uint32_t *>(&v);
-                }
-                w[j] = make_uint4(o[0], o[1], o[2], o[3]);
-            }
-            *piece(q + (p >> 3) * kChunkB, r, p & 7) = w[j];
+        for (int j = 0; j < kKChunks; ++j) {
+            const __nv_bfloat16 *src = (j < 8 ? c + j * 64 : e) + pc * 8;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(piece(q + j * kChunkB, r, pc))),
+                         "l"(src), "r"(bytes)
+                         : "memory");
         }
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) *piece(q + 8 * kChunkB, r, j * 2 + sub) = live ? e[j * 2 + sub] : zero;
 }
 
-// Rows valid .. 127 of the two V chunks at `v`, by one warp: slots past the last
-// token may hold anything, NaN among it, and meet weights of zero.
-__device__ __forceinline__ void zero_rows(uint8_t *v, int valid, int lane) {
-    for (int i = valid * 8 + lane; i < kTile * 8; i += 32) {
-        reinterpret_cast<uint4 *>(v)[i] = make_uint4(0u, 0u, 0u, 0u);
-        reinterpret_cast<uint4 *>(v + kVChunkB)[i] = make_uint4(0u, 0u, 0u, 0u);
+// FP8: the latent part of a row's quarter, in place, to f16 over the power of two
+// that puts the row's largest element in [1, 2) (the rotated part stays bf16).
+// First its largest magnitude, as bf16 bits (integers order as magnitudes do).
+__device__ __forceinline__ uint32_t largest_query(uint8_t *q, int r, int part) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const uint4 w = *piece(q + (part * 2 + (j >> 3)) * kChunkB, r, j & 7);
+        top = max(max(top, max(w.x & 0x7FFFu, (w.x >> 16) & 0x7FFFu)), max(w.y & 0x7FFFu, (w.y >> 16) & 0x7FFFu));
+        top = max(max(top, max(w.z & 0x7FFFu, (w.z >> 16) & 0x7FFFu)), max(w.w & 0x7FFFu, (w.w >> 16) & 0x7FFFu));
     }
+    return top;
+}
+__device__ __forceinline__ uint32_t scaled_half2(uint32_t w, float f) {
+    const float2 x = bf16x2_to_float2(w);
+    const __half2 v = __floats2half2_rn(x.x * f, x.y * f);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ void convert_query(uint8_t *q, int r, int part, float inv) {
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+        uint4 w[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) w[u] = *piece(q + (part * 2 + (j >> 3)) * kChunkB, r, (j + u) & 7);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            *piece(q + (part * 2 + (j >> 3)) * kChunkB, r, (j + u) & 7) =
+                make_uint4(scaled_half2(w[u].x, inv), scaled_half2(w[u].y, inv), scaled_half2(w[u].z, inv),
+                           scaled_half2(w[u].w, inv));
+    }
+}
+
+// A barrier of 128 threads that tells whether any of them says so.
+__device__ __forceinline__ bool bar_any(int id, bool says) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\tbar.red.or.pred q, %1, 128, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"(id), "r"((uint32_t)says)
+                 : "memory");
+    return r != 0;
 }
 
 template <bool FP8>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_split_kernel(const __grid_constant__ CUtensorMap mapc, const __grid_constant__ CUtensorMap mapr,
                         LatentDecodeArgs a, int R, int blocks, int clusters, Parts parts) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t sm[];  // no static shared memory: the window's aligned base
     Misc &m = *reinterpret_cast<Misc *>(sm + kOffMisc);
     uint8_t *const q = sm + kOffQ, *const k = sm + kOffK, *const v = sm + kOffV, *const p = sm + kOffP;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank();
     const int w = blockIdx.x >> 1;
     if (tid == 0) {
-        for (int c = 0; c < kKChunks; ++c) {
-            mbar_init(&m.kfull[c], FP8 && c < 8 ? 4 : 1);
+        for (int c = 0; c < kKStages; ++c) {
+            mbar_init(&m.kfull[c], c == 4 ? 1 : FP8 ? 2 : 4);
             mbar_init(&m.kempty[c], 1);
-            mbar_init(&m.pk[c], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&m.vfull[i], FP8 ? 4 : 1);
+            mbar_init(&m.vfull[i], FP8 ? 4 : 2);
             mbar_init(&m.vempty[i], 1);
-            mbar_init(&m.pv[i], 1);
             mbar_init(&m.sfull[i], 1);
-            mbar_init(&m.sq[i], 4);
         }
-        mbar_init(&m.pready, 8);
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&m.mfull[i], 1);
+            mbar_init(&m.mempty[i], 1);
+        }
+        mbar_init(&m.pready, 16);
         mbar_init(&m.pvdone, 1);
-        mbar_init(&m.qfull, 4);
-        mbar_init(&m.pq, 1);
-        mbar_init(&m.qfree, 1);
+        mbar_init(&m.qfull, 16);
         mbar_init(&m.drain, 1);
-        m.gave_up = 0u;
+        m.gave_up = (smem_addr(sm) & 1023u) != 0u;  // nothing runs on a base that the swizzle cannot take
         m.x0 = m.x1 = 0;
         m.off = 0;
         m.b0 = 0;
         fence_mbar_init();
     }
-    if (warp == 4) tmem_alloc512<2>(&m.tmem);
+    if (warp == 8) tmem_alloc512<2>(&m.tmem);
+    tmem_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers are initialised
+    tmem_fence_after();
     pdl_enter();
 
+    {
+        // the block tables into L2, while the list of tiles is counted
+        const int lines = (a.pool.max_pages * 4 + 127) / 128 + 1;
+        for (long long i = (long long)blockIdx.x * kThreads + tid; i < (long long)a.B * lines; i += (long long)gridDim.x * kThreads) {
+            const int b = (int)(i / lines);
+            const long long e = min((i - (long long)b * lines) * 32, (long long)a.pool.max_pages - 1);
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(a.pool.block_tables + (long long)b * a.pool.bt_sb + e));
+        }
+    }
     // this cluster's range of the list of tiles
     {
         const int per = (a.B + kThreads - 1) / kThreads;
@@ -310,9 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane >= d) incl += y;
         }
         if (lane == 31) m.warp_sum[warp] = incl;
-        tmem_fence_before();
         __syncthreads();
-        tmem_fence_after();
         long long before = 0, U = 0;
         for (int i = 0; i < kThreads / 32; ++i) {
             if (i < warp) before += m.warp_sum[i];
@@ -321,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int W = (int)min((long long)clusters, U);
         const long long x0 = w < W ? range_start(w, U, W) : 0, x1 = w < W ? range_start(w + 1, U, W) : 0;
         before += incl - mine;
-        if (x0 < x1 && before <= x0 && x0 < before + mine) {
+        if (x0 < x1 && before <= x0 && x0 < before + mine && !m.gave_up) {
             long long at = before;
             int b = lo;
             for (;; ++b) {
@@ -336,502 +329,538 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncthreads();
-    cluster_sync();  // both CTAs' barriers are initialised
-    const Walk walk{m.x0, m.x1, m.off, m.b0};
+    const int N = (int)(m.x1 - m.x0);  // tiles of this cluster: every role counts them
     const uint32_t tmem = m.tmem;
     volatile uint32_t *const gave_up = &m.gave_up;
+    // Waits until tile t is looked up; false when a wait of this CTA has given up
+    // (the entry may then be anything, and is not used).
+    auto looked_up = [&](int t) { return bar_wait(&m.mfull[t % kRing], (t / kRing) & 1, gave_up); };
 
-    if (warp < 4) {
+    // Registers of the five warpgroups, of 5 x 96 at launch: 2 x 120 + 64 + 2 x 88.  No role
+    // may spill: with 230 KB of shared memory there is next to no L1 to catch it
+    // After waits have given up: copies in flight (into either CTA) are left time to land.
+    auto drain_copies = [&]() {
+        const unsigned long long t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < kWaitLimitNs) {}
+    };
+
+    if (warp < 8) {
         // ------------------------- softmax and output -------------------------
-        const int half = warp >> 1, r = tid & 63;    // lanes 64-127 hold tokens 64-127 of rows 0-63
-        const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+        // lanes 64-127 of tensor memory hold tokens 64-127 of rows 0-63; warps 4-7
+        // take the upper 32 of each 64 tokens, and columns 128-255 of O
+        reg_share_more<120>();
+        const int quad = warp & 3, half = quad >> 1, cw = warp >> 2, r = (quad & 1) * 32 + lane;
+        const int part = half * 2 + cw;  // of a row's four threads
+        const int bar = 1 + (quad & 1);
+        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
         const float a2 = a.sm_scale * kLog2e;
-        TileWalk tw, nx;
-        tw.start(a, blocks, walk);
-        nx = tw;
-        float z[4] = {1.f, 1.f, 1.f, 1.f};
-        int zid[4] = {-1, -1, -1, -1};
-        auto load_ids = [&](const TileWalk &t) {  // pages of this half of the tile (FP8: their scales)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                zid[i] = t.live ? page_of(a, t.s.b, t.t * kTilePages + half * 4 + i, t.s.n) : -1;
-        };
-        if constexpr (FP8) {
-            load_ids(tw);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) z[i] = zid[i] >= 0 ? a.pool.c_scale[zid[i]] : 1.f;
-            if (nx.live) nx.step(a, blocks);
-            load_ids(nx);
-        }
         float ref = kNegInf, sum = 0.f, qs = 0.f;
-        int lim = 0, row = 0, seg = 0;
+        int hidden = 0, row = 0;  // hidden: candidates after this row's own
         bool live = false, any_live = false;
-        for (int t = 0; tw.live; ++t) {
-            if (tw.first) {
-                row = tw.s.block * kRowBlock + (int)rank * kRowsCta + r;
+        // Q of the part that begins with tile t; its slots are free once the scores of
+        // the tile before are there.  The copies run while the last part is written out.
+        auto fetch_queries = [&](int b, int block) {
+            copy_queries(a, b, block, R, rank, q, (quad & 1) * 32 + part * 8, lane);
+        };
+        auto finish_queries = [&]() {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            if constexpr (FP8) {
+                asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");  // the row block's copies are in
+                const uint32_t mine = largest_query(q, r, part);
+                m.xm[part][r] = __uint_as_float(mine);
+                asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");
+                const uint32_t top = max(max(__float_as_uint(m.xm[0][r]), __float_as_uint(m.xm[1][r])),
+                                         max(__float_as_uint(m.xm[2][r]), __float_as_uint(m.xm[3][r])));
+                // biased exponent, kept where both 2^e and 2^-e are normal fp32 numbers
+                const int eb = min(253, max(1, (int)(top >> 7)));
+                convert_query(q, r, part, __uint_as_float((uint32_t)(254 - eb) << 23));
+                qs = a2 * __uint_as_float((uint32_t)eb << 23);
+                asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");  // xm is free
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) bar_arrive_at(&m.qfull, 0);
+        };
+        if (N > 0) {
+            fetch_queries(m.b0, (int)(m.off / tiles_of(live_len(a, m.b0))));
+            finish_queries();
+        }
+        for (int t = 0; t < N; ++t) {
+            const bool ok = looked_up(t);
+            const Tile &ti = m.tile[t % kRing];
+            uint32_t flags = ok ? ti.flags : 0u;
+            const int b = ti.b;
+            if (flags & kFirst) {
+                row = ti.block * kRowBlock + (int)rank * kRowsCta + r;
                 live = row < R;
-                any_live = __any_sync(0xffffffffu, live);
-                lim = tw.s.n - a.kq + 1 + (live ? row / a.H : a.kq - 1);
+                hidden = a.kq - 1 - (live ? row / a.H : a.kq - 1);
                 ref = kNegInf;
                 sum = 0.f;
             }
-            float zn[4];
+            live = live && ok;
+            any_live = __any_sync(0xffffffffu, live);
+            const int seen = ti.left - hidden - part * 32;  // of this thread's 32 tokens
+            float z[2], lz[2], iz[2];
             if constexpr (FP8) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) zn[i] = zid[i] >= 0 ? a.pool.c_scale[zid[i]] : 1.f;
+                for (int i = 0; i < 2; ++i) {
+                    z[i] = ti.z[part * 2 + i];
+                    const float zc = fmaxf(z[i], 7.888609052210118e-31f);  // 2^-100
+                    lz[i] = __log2f(zc);
+                    iz[i] = __frcp_rn(zc);
+                }
             }
             bar_wait(&m.sfull[t & 1], (t >> 1) & 1, gave_up);
             tmem_fence_after();
-            if (FP8 && tw.first) {
-                bar_wait(&m.sq[seg & 1], (seg >> 1) & 1, gave_up);
-                qs = a2 * m.qscale[seg & 1][r];
-            }
-            seg += tw.last;
-            bool waited = false;
+            float x[32];
+            float top = kNegInf;
             if (any_live) {
-                float x[2][32];
-                const uint32_t cs = lanes + kColS + (t & 1) * 128;
-                tmem_ld32(cs, x[0]);
-                tmem_ld32(cs + 32, x[1]);
-                tmem_wait_ld();
-                float lz[4], iz[4];
+                const uint32_t cs = lanes + kColS + (t & 1) * 128 + cw * 32;
+                tmem_ld32(cs, x);
                 if constexpr (FP8) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float zc = fmaxf(z[i], 7.888609052210118e-31f);  // 2^-100
-                        lz[i] = __log2f(zc);
-                        iz[i] = __frcp_rn(zc);
-                    }
-#pragma unroll
                     for (int g = 0; g < 2; ++g) {
-                        float y[32];
-                        tmem_ld32(cs + 64 + g * 32, y);
+                        float y[16];
+                        tmem_ld16(cs + 64 + g * 16, y);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const int i = g * 2 + (j >> 4);
-                            x[g][j] = fmaf(x[g][j], qs * z[i], fmaf(y[j], a2, lz[i]));
-                        }
+                        for (int j = 0; j < 16; ++j) x[g * 16 + j] = fmaf(x[g * 16 + j], qs * z[g], fmaf(y[j], a2, lz[g]));
                     }
                 } else {
+                    tmem_wait_ld();
 #pragma unroll
-                    for (int g = 0; g < 2; ++g)
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) x[g][j] *= a2;
+                    for (int j = 0; j < 32; ++j) x[j] *= a2;
                 }
-                const int seen = lim - (tw.t * kTile + half * 64);  // of this thread's 64 tokens
-                if (seen < 64) {
+                if (seen < 32) {
 #pragma unroll
-                    for (int g = 0; g < 2; ++g)
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (g * 32 + j >= seen) x[g][j] = kNegInf;
+                    for (int j = 0; j < 32; ++j)
+                        if (j >= seen) x[j] = kNegInf;
                 }
-                float top = kNegInf;
 #pragma unroll
-                for (int g = 0; g < 2; ++g)
+                for (int j = 0; j < 32; ++j) top = fmaxf(top, x[j]);
+            }
+            m.xm[part][r] = top;
+            // all of the row block's threads know the tile, or none goes by it: they meet at
+            // the barriers below by its flags
+            if (bar_any(bar, !ok)) flags = 0u;
+            top = fmaxf(fmaxf(m.xm[0][r], m.xm[1][r]), fmaxf(m.xm[2][r], m.xm[3][r]));
+            float shrink = 1.f;
+            if (top > ref + kLazyGrowth || (ref == kNegInf && top > kNegInf)) {
+                shrink = fast_exp2(ref - top);  // 0 when nothing was seen yet
+                sum *= shrink;
+                ref = top;
+            }
+            // the weights, in registers until P's slot is free
+            uint32_t pw[16];
+            if (any_live) {
+                const float base = ref == kNegInf ? 0.f : ref - kWeightBias<FP8>;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) top = fmaxf(top, x[g][j]);
-                m.xm[tid] = top;
-                // rows' two halves: warps w and w + 2
-                asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 1)) : "memory");
-                top = fmaxf(top, m.xm[tid ^ 64]);
-                asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 1)) : "memory");
-                float shrink = 1.f;
-                if (top > ref + kLazyGrowth || (ref == kNegInf && top > kNegInf)) {
-                    shrink = fast_exp2(ref - top);  // 0 when nothing was seen yet
-                    sum *= shrink;
-                    ref = top;
+                for (int j = 0; j < 32; j += 2) {
+                    const float w0 = fast_exp2(x[j] - base), w1 = fast_exp2(x[j + 1] - base);
+                    if constexpr (FP8) {
+                        const __half2 hw = __floats2half2_rn(w0, w1);
+                        const float2 f = __half22float2(hw);
+                        sum = fmaf(f.x + f.y, iz[j >> 4], sum);
+                        pw[j >> 1] = *reinterpret_cast<const uint32_t *>(&hw);
+                    } else {
+                        const __nv_bfloat162 hw = __floats2bfloat162_rn(w0, w1);
+                        const float2 f = __bfloat1622float2(hw);
+                        sum += f.x + f.y;
+                        pw[j >> 1] = *reinterpret_cast<const uint32_t *>(&hw);
+                    }
                 }
-                if (t > 0) {
-                    bar_wait(&m.pvdone, (t - 1) & 1, gave_up);  // P is free, O is at rest
-                    tmem_fence_after();
-                    waited = true;
-                }
-                if (!tw.first && __any_sync(0xffffffffu, shrink != 1.f)) {
+            }
+            if (t > 0) {
+                bar_wait(&m.pvdone, (t - 1) & 1, gave_up);  // P is free, O is at rest
+                tmem_fence_after();
+            }
+            if (any_live) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    *piece(p + half * kChunkB, r, cw * 4 + c) = make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
+                if (!(flags & kFirst) && __any_sync(0xffffffffu, shrink != 1.f)) {
 #pragma unroll 1
                     for (int g = 0; g < 8; ++g) {
-                        float o[32];
-                        tmem_ld32(lanes + g * 32, o);
+                        float o[16];
+                        tmem_ld16(lanes + cw * 128 + g * 16, o);
                         tmem_wait_ld();
-                        uint32_t u[32];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(o[j] * shrink);
-                        tmem_st32(lanes + g * 32, u);
+                        for (int j = 0; j < 16; ++j) o[j] *= shrink;
+                        tmem_st16(lanes + cw * 128 + g * 16, o);
                     }
                     tmem_wait_st();
                 }
-                const float base = ref == kNegInf ? 0.f : ref - kWeightBias<FP8>;
-                uint8_t *pc = p + half * kChunkB;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    uint32_t o[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int j = c * 8 + e * 2;
-                        const float w0 = fast_exp2(x[j >> 5][j & 31] - base);
-                        const float w1 = fast_exp2(x[(j + 1) >> 5][(j + 1) & 31] - base);
-                        if constexpr (FP8) {
-                            const __half2 hw = __floats2half2_rn(w0, w1);
-                            const float2 f = __half22float2(hw);
-                            sum = fmaf(f.x + f.y, iz[c >> 1], sum);
-                            o[e] = *reinterpret_cast<const uint32_t *>(&hw);
-                        } else {
-                            const __nv_bfloat162 hw = __floats2bfloat162_rn(w0, w1);
-                            const float2 f = __bfloat1622float2(hw);
-                            sum += f.x + f.y;
-                            o[e] = *reinterpret_cast<const uint32_t *>(&hw);
-                        }
-                    }
-                    *piece(pc, r, c) = make_uint4(o[0], o[1], o[2], o[3]);
-                }
                 fence_proxy_async_smem();
             }
-            if (!waited && t > 0) bar_wait(&m.pvdone, (t - 1) & 1, gave_up);
             tmem_fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive_at(&m.pready, 0);
-            if (tw.last) {
-                bar_wait(&m.pvdone, t & 1, gave_up);
+            if (flags & kLast) {
+                if (t + 1 < N && looked_up(t + 1)) fetch_queries(m.tile[(t + 1) % kRing].b, m.tile[(t + 1) % kRing].block);
+                const bool whole = (flags & kWhole) != 0;
+                const int slot = w * 2 + ((flags & kBegins) ? 1 : 0);
+                const bool done = bar_wait(&m.pvdone, t & 1, gave_up);
                 tmem_fence_after();
+                asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");  // xm has been read
+                m.xm[part][r] = sum;
+                asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");
+                const float total = (m.xm[0][r] + m.xm[1][r]) + (m.xm[2][r] + m.xm[3][r]);
+                if (t + 1 < N) {  // the next part's scores are taken while this one is written
+                    asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");  // xm has been read
+                    finish_queries();
+                }
                 if (any_live) {
-                    m.xm[tid] = sum;
-                    asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 1)) : "memory");
-                    const float total = sum + m.xm[tid ^ 64];
-                    asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 1)) : "memory");
-                    const float inv = total > 0.f ? __fdiv_rn(1.f, total) : total == 0.f ? 0.f : total;  // NaN stays
-                    const bool whole = tw.s.t1 - tw.s.t0 == tw.s.tiles;
-                    const int brow = (int)rank * kRowsCta + r;
-                    const int slot = w * 2 + (tw.s.t0 == 0 ? 1 : 0);
-                    float *po = parts.o + ((long long)slot * parts.rows + brow) * kDC;
-                    if (!whole && live && half == 0)
-                        parts.lse[(long long)slot * parts.rows + brow] = total == 0.f ? kNegInf : ref - kWeightBias<FP8> + __log2f(total);
-                    __nv_bfloat16 *out = a.out.p;
-                    if (live) {
-                        const int tok = row / a.H;
-                        out += (long long)tw.s.b * a.out.sb + (long long)tok * a.out.st +
-                               (long long)(row - tok * a.H) * a.out.sh;
+                    const float inv = total > 0.f ? __fdiv_rn(1.f, total) : total;  // zero and NaN stay
+                    const bool store = live && done;
+                    if (!whole && store && part == 0)
+                        parts.lse[(long long)slot * parts.rows + rank * kRowsCta + r] =
+                            total == 0.f ? kNegInf : ref - kWeightBias<FP8> + __log2f(total);
+                    // Columns 128 cw ..: values 256 cw .., each half a row's threads' share.
+                    // Sixteen columns at a time pass through 2 KB of P's slots a warp, so that a store
+                    // covers 64 bytes of eight rows (a thread's own row would make it 32 rows); the
+                    // slots are those of the row block's own weights, which its next barrier guards.
+                    const int d = cw * 256 + half * 128;
+                    float4 *const stage = reinterpret_cast<float4 *>(p + half * kChunkB + (quad & 1) * 4096 + cw * 2048);
+                    const int r4 = lane >> 2, c4 = lane & 3;
+                    const uint32_t rows = __ballot_sync(0xffffffffu, store);
+                    // this lane's eight-row steps: rows r4, r4 + 8, ..
+                    long long at[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int rr = (quad & 1) * 32 + i * 8 + r4, br = (int)rank * kRowsCta + rr;
+                        const int gr = row - r + rr;  // row of the request
+                        if (whole) {
+                            const int tok = gr / a.H;
+                            at[i] = (long long)b * a.out.sb + (long long)tok * a.out.st + (long long)(gr - tok * a.H) * a.out.sh;
+                        } else {
+                            at[i] = ((long long)slot * parts.rows + br) * kDC;
+                        }
                     }
+                    float o[16];
+                    tmem_ld16(lanes + cw * 128, o);
 #pragma unroll 1
                     for (int g = 0; g < 8; ++g) {
-                        float o[32];
-                        tmem_ld32(lanes + g * 32, o);
                         tmem_wait_ld();
-                        // columns 0-127: values 0-255, 128-255: values 256-511; each half a row's threads' share
-                        const int d = (g >> 2) * 256 + half * 128 + (g & 3) * 32;
-                        if (!live) continue;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = total == 0.f ? 0.f : o[j] * inv;
-                        if (whole) {
-#pragma unroll
-                            for (int j = 0; j < 32; j += 8) {
-                                uint32_t u[4];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const __nv_bfloat162 h = __floats2bfloat162_rn(o[j + 2 * e], o[j + 2 * e + 1]);
-                                    u[e] = *reinterpret_cast<const uint32_t *>(&h);
-                                }
-                                *reinterpret_cast<uint4 *>(out + d + j) = make_uint4(u[0], u[1], u[2], u[3]);
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; j += 4)
-                                *reinterpret_cast<float4 *>(po + d + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                        for (int j = 0; j < 4; ++j) {
+                            float4 x = make_float4(o[4 * j] * inv, o[4 * j + 1] * inv, o[4 * j + 2] * inv, o[4 * j + 3] * inv);
+                            if (total == 0.f) x = make_float4(0.f, 0.f, 0.f, 0.f);
+                            stage[lane * 4 + (j ^ ((lane >> 1) & 3))] = x;
                         }
+                        if (g < 7) tmem_ld16(lanes + cw * 128 + (g + 1) * 16, o);
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int rr = i * 8 + r4;
+                            const float4 x = stage[rr * 4 + (c4 ^ ((rr >> 1) & 3))];
+                            if (!((rows >> rr) & 1u)) continue;
+                            if (whole) {
+                                const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x, x.y), hi = __floats2bfloat162_rn(x.z, x.w);
+                                *reinterpret_cast<uint2 *>(a.out.p + at[i] + d + g * 16 + c4 * 4) =
+                                    make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+                            } else {
+                                *reinterpret_cast<float4 *>(parts.o + at[i] + d + g * 16 + c4 * 4) = x;
+                            }
+                        }
+                        __syncwarp();
                     }
                 }
                 tmem_fence_before();
             }
-            tw.step(a, blocks);
-            if constexpr (FP8) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) z[i] = zn[i];
-                if (nx.live) nx.step(a, blocks);
-                load_ids(nx);
-            }
+            asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");  // xm is free
         }
-    } else if (warp == 4) {
-        // ---------------- products (even CTA), relay (odd CTA) ----------------
-        const uint32_t qa = smem_addr(q), ka = smem_addr(k), va = smem_addr(v), pa = smem_addr(p);
-        constexpr uint32_t idS = umma_idesc(kRowBlock, kTile, !FP8, false, false);
-        constexpr uint32_t idR = umma_idesc(kRowBlock, kTile, true, false, false);
-        constexpr uint32_t idO = umma_idesc(kRowBlock, 256, !FP8, false, true);
-        auto scores = [&](int t, bool first, bool last, int seg) {
-            if (first) {
-                bar_wait(&m.qfull, seg & 1, gave_up);
-                if (rank == 0) bar_wait(&m.pq, seg & 1, gave_up);
-                else if (lane == 0) bar_arrive_at(&m.pq, 0);
-            }
-            const uint32_t cs = tmem + kColS + (t & 1) * 128;
+    } else if (warp == 8) {
+        // ----------------------- products (even CTA) -----------------------
+        reg_share_less<64>();
+        // One thread runs the whole role: the compiler then knows that descriptors are
+        // those of a single thread.
+        if (rank == 0 && elect_one()) {
+            const uint32_t qa = smem_addr(q), ka = smem_addr(k), va = smem_addr(v), pa = smem_addr(p);
+            constexpr uint32_t idS = umma_idesc(kRowBlock, kTile, !FP8, false, false);
+            constexpr uint32_t idR = umma_idesc(kRowBlock, kTile, true, false, false);
+            constexpr uint32_t idO = umma_idesc(kRowBlock, 256, !FP8, false, true);
+            auto values = [&](int t, bool first) {
+                const bool ok = bar_wait(&m.pready, t & 1, gave_up);
+                const uint64_t da = umma_desc(pa, 16, 1024);
 #pragma unroll 1
-            for (int c = 0; c < kKChunks; ++c) {
-                bar_wait(&m.kfull[c], t & 1, gave_up);
-                if (rank != 0) {
-                    __syncwarp();
-                    if (lane == 0) bar_arrive_at(&m.pk[c], 0);
-                    continue;
+                for (int nb = 0; nb < 2; ++nb) {
+                    if (!bar_wait(&m.vfull[nb], t & 1, gave_up) || !ok) continue;
+                    tmem_fence_after();
+                    const uint64_t db = umma_desc(va + nb * 2 * kVChunkB, kVLbo<FP8>, 1024);
+#pragma unroll
+                    for (int s = 0; s < 8; ++s)  // a page a step
+                        umma_ss<2>(tmem + nb * 128, da + (s >> 2) * (kChunkB >> 4) + 2 * (s & 3),
+                                   db + s * (kVStep<FP8> >> 4), idO, s > 0 || !first);
+                    umma_commit_pair(&m.vempty[nb]);
                 }
-                bar_wait(&m.pk[c], t & 1, gave_up);
-                tmem_fence_after();
-                __syncwarp();
-                if (!*gave_up && elect_one()) {
-                    const bool rope = FP8 && c == 8;
-                    const uint64_t da = umma_desc(qa + c * kChunkB, 16, 1024), db = umma_desc(ka + c * kChunkB, 16, 1024);
+                if (ok) {
+                    umma_commit_pair(&m.pvdone);
+                    umma_commit_pair(&m.mempty[t % kRing]);
+                }
+            };
+            int seg = 0;
+            bool pfirst = false;
+            for (int t = 0; t < N; ++t) {
+                const uint32_t flags = looked_up(t) ? m.tile[t % kRing].flags : 0u;
+                const bool first = (flags & kFirst) != 0;
+                // the products of the tile before this one's scores when Q changes between them
+                if (t > 0 && first) values(t - 1, pfirst);
+                if (first) bar_wait(&m.qfull, seg & 1, gave_up);
+                const uint32_t cs = tmem + kColS + (t & 1) * 128;
+                // The rotated keys come first: their one slot is refilled by TMA, which then has
+                // the rest of the tile's time.  (Loops over stages stay loops: unrolled, their
+                // descriptors cost the registers that the other roles need.)
+                bool ok = bar_wait(&m.kfull[4], t & 1, gave_up);
+                uint64_t da = umma_desc(qa, 16, 1024), db = umma_desc(ka, 16, 1024);
+                if (ok) {
+                    tmem_fence_after();
+                    constexpr uint64_t last = 8 * kChunkB >> 4;
 #pragma unroll
                     for (int s = 0; s < 4; ++s)
-                        umma_ss<2>(rope ? cs + 64 : cs, da + 2 * s, db + 2 * s, rope ? idR : idS,
-                                   s > 0 || (c > 0 && !rope));
-                    umma_commit_pair(&m.kempty[c]);
-                    if (c == kKChunks - 1) {
-                        umma_commit_pair(&m.sfull[t & 1]);
-                        if (last) umma_commit_pair(&m.qfree);
-                    }
+                        umma_ss<2>(FP8 ? cs + 64 : cs, da + last + 2 * s, db + last + 2 * s, idR, s > 0);
+                    umma_commit_pair(&m.kempty[4]);
                 }
-                __syncwarp();
-            }
-        };
-        auto values = [&](int t, bool first, int valid) {
-            if (rank == 0) bar_wait(&m.pready, t & 1, gave_up);
 #pragma unroll 1
-            for (int nb = 0; nb < 2; ++nb) {
-                bar_wait(&m.vfull[nb], t & 1, gave_up);
-                if (!FP8 && valid < kTile) {
-                    zero_rows(v + nb * 2 * kVChunkB, valid, lane);
-                    fence_proxy_async_smem();
-                }
-                if (rank != 0) {
-                    __syncwarp();
-                    if (lane == 0) bar_arrive_at(&m.pv[nb], 0);
-                    continue;
-                }
-                bar_wait(&m.pv[nb], t & 1, gave_up);
-                tmem_fence_after();
-                __syncwarp();
-                if (!*gave_up && elect_one()) {
-                    const uint64_t da = umma_desc(pa, 16, 1024);
-                    const uint64_t db = umma_desc(va + nb * 2 * kVChunkB, kVChunkB, 1024);
+                for (int c = 0; c < 4; ++c, da += 2 * kChunkB >> 4, db += 2 * kChunkB >> 4) {
+                    ok = bar_wait(&m.kfull[c], t & 1, gave_up) && ok;
+                    if (!ok) continue;
+                    tmem_fence_after();
 #pragma unroll
-                    for (int s = 0; s < 8; ++s)
-                        umma_ss<2>(tmem + nb * 128, da + (s >> 2) * (kChunkB >> 4) + 2 * (s & 3), db + s * 128, idO,
-                                   s > 0 || !first);
-                    umma_commit_pair(&m.vempty[nb]);
-                    if (nb == 1) umma_commit_pair(&m.pvdone);
+                    for (int s = 0; s < 8; ++s) {
+                        const uint64_t step = (s >> 2) * (kChunkB >> 4) + 2 * (s & 3);
+                        umma_ss<2>(cs, da + step, db + step, idS, !FP8 || s > 0 || c > 0);
+                    }
+                    umma_commit_pair(&m.kempty[c]);
                 }
-                __syncwarp();
+                if (ok) umma_commit_pair(&m.sfull[t & 1]);
+                if (t > 0 && !first) values(t - 1, pfirst);
+                pfirst = first;
+                if (flags & kLast) ++seg;
             }
-        };
-        TileWalk tw;
-        tw.start(a, blocks, walk);
-        int t = 0, seg = 0, pvalid = 0;
-        bool pending = false, pfirst = false;
-        for (; tw.live; ++t) {
-            if (tw.first && pending) {
-                values(t - 1, pfirst, pvalid);
-                pending = false;
-            }
-            scores(t, tw.first, tw.last, seg);
-            if (pending) values(t - 1, pfirst, pvalid);
-            pending = true;
-            pfirst = tw.first;
-            pvalid = tw.s.n - tw.t * kTile;
-            seg += tw.last;
-            tw.step(a, blocks);
-        }
-        if (pending) values(t - 1, pfirst, pvalid);
-        if (rank == 0) {  // nothing in flight when the CTAs leave
-            __syncwarp();
-            if (elect_one()) umma_commit_pair(&m.drain);
-            __syncwarp();
+            if (N > 0) values(N - 1, pfirst);
+            // nothing in flight when the CTAs leave
+            umma_commit_pair(&m.drain);
             bar_drain(&m.drain, 0);
         }
-    } else if (warp == 5) {
-        // ---------------- K: TMA (FP8: the rotated keys alone) ----------------
-        const uint64_t pol = l2_policy_evict_normal();
-        TileWalk tw, ah;
-        tw.start(a, blocks, walk);
-        ah = tw;
-        // own pages of a tile into L2: this CTA's half, its peer takes the other
-        auto ahead = [&]() {
-            if (ah.live) ah.step(a, blocks);
-            if (ah.live && lane < 4) {
-                const int id = page_of(a, ah.s.b, ah.t * kTilePages + (int)rank * 4 + lane, ah.s.n);
-                if (id >= 0) {
-                    const uint32_t cb = kPage * kDC * (FP8 ? 1 : 2);
-                    l2_prefetch(static_cast<const uint8_t *>(a.pool.c_pages) + (long long)id * cb, cb);
-                    l2_prefetch(a.pool.r_pages + (long long)id * kPage * PFKV_LATENT_ROPE, kPage * PFKV_LATENT_ROPE * 2);
-                }
+        __syncwarp();
+    } else if (warp == 9) {
+        // -------------------------- rotated keys: TMA --------------------------
+        reg_share_less<64>();
+        if (elect_one()) {
+            const uint64_t pol = l2_policy_evict_normal();
+            for (int t = 0; t < N && looked_up(t); ++t) {
+                const Tile &ti = m.tile[t % kRing];
+                int id[4];
+                uint32_t pages = 0;
+#pragma unroll
+                for (int i = 0; i < kTilePages; ++i) pages += ti.id[i] >= 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) id[i] = ti.id[rank * 4 + i];
+                if (!bar_wait(&m.kempty[4], (t & 1) ^ 1, gave_up)) break;
+                if (rank == 0) mbar_arrive_expect_tx(&m.kfull[4], pages * 2048u);  // both CTAs' bytes
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (id[i] >= 0) tma_box3_pair(k + 8 * kChunkB + i * 2048, &mapr, 0, 0, id[i], &m.kfull[4], pol);
             }
-        };
-        ahead();
-        int t = 0;
-        for (; tw.live; ++t) {
-            ahead();
-            const int id = lane < 4 ? page_of(a, tw.s.b, tw.t * kTilePages + (int)rank * 4 + lane, tw.s.n) : -1;
-            const uint32_t bytes = 2048u * __popc(__ballot_sync(0xffffffffu, id >= 0));
-#pragma unroll 1
-            for (int c = FP8 ? 8 : 0; c < kKChunks; ++c) {
-                bar_wait(&m.kempty[c], (t & 1) ^ 1, gave_up);
-                if (*gave_up) break;
-                if (lane == 0) mbar_arrive_expect_tx(&m.kfull[c], bytes);
-                __syncwarp();
-                if (id >= 0) {
-                    uint8_t *dst = k + c * kChunkB + lane * 2048;
-                    if (c < 8) tma_box3(dst, &mapc, c * 64, 0, id, &m.kfull[c], pol);
-                    else tma_box3(dst, &mapr, 0, 0, id, &m.kfull[c], pol);
-                }
-            }
-            __syncwarp();
-            if (*gave_up) break;
-            tw.step(a, blocks);
+            if (*gave_up) drain_copies();
         }
         __syncwarp();
-        if (*gave_up)  // copies in flight: of this tile and the last
-            for (int c = FP8 ? 8 : 0; c < kKChunks; ++c) {
-                bar_drain(&m.kfull[c], 0);
-                bar_drain(&m.kfull[c], 1);
-            }
-    } else if (warp == 6 && !FP8) {
+    } else if (warp == 10) {
         // ------------------------------ V: TMA ------------------------------
+        reg_share_less<64>();
         const uint64_t pol = l2_policy_evict_normal();
-        TileWalk tw;
-        tw.start(a, blocks, walk);
-        for (int t = 0; tw.live; ++t) {
-            const int id = lane < 16 ? page_of(a, tw.s.b, tw.t * kTilePages + (lane & 7), tw.s.n) : -1;
-            const uint32_t bytes = 2048u * __popc(__ballot_sync(0xffffffffu, id >= 0));
+        for (int t = 0; !FP8 && t < N; ++t) {
+            if (!__all_sync(0xffffffffu, looked_up(t))) break;
+            const Tile &ti = m.tile[t % kRing];
+            const int left = ti.left;
+            const int full = min(kTilePages, left / kPage);  // pages without a slot past the last token
 #pragma unroll 1
             for (int nb = 0; nb < 2; ++nb) {
-                bar_wait(&m.vempty[nb], (t & 1) ^ 1, gave_up);
-                if (*gave_up) break;
-                if (lane == 0) mbar_arrive_expect_tx(&m.vfull[nb], bytes);
-                __syncwarp();
-                if (id >= 0)
-                    tma_box3(v + (nb * 2 + (lane >> 3)) * kVChunkB + (lane & 7) * 2048, &mapc,
-                             (nb * 4 + (int)rank * 2 + (lane >> 3)) * 64, 0, id, &m.vfull[nb], pol);
-            }
-            __syncwarp();
-            if (*gave_up) break;
-            tw.step(a, blocks);
-        }
-        __syncwarp();
-        if (*gave_up)
-            for (int nb = 0; nb < 2; ++nb) {
-                bar_drain(&m.vfull[nb], 0);
-                bar_drain(&m.vfull[nb], 1);
-            }
-    } else if (warp >= 8 && warp < 12) {
-        // ------------------- Q; FP8: K converted on the way -------------------
-        const int i = tid - 256;
-        const int kr = i >> 2, part = i & 3;  // row (+ 32) and 16-byte piece of a chunk's 64 bytes
-        TileWalk tw, nx;
-        tw.start(a, blocks, walk);
-        nx = tw;
-        uint4 raw[8][2];
-        int ids[2];
-        bool in[2];
-        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-        auto load_ids = [&](const TileWalk &t) {
+                if (!__all_sync(0xffffffffu, bar_wait(&m.vempty[nb], (t & 1) ^ 1, gave_up))) break;
+                uint8_t *dst = v + nb * 2 * kVChunkB;
+                const int x = (nb * 4 + (int)rank * 2) * 64;
+                if (elect_one()) {
+                    uint32_t pages = 0;
+                    for (int i = 0; i < full; ++i) pages += ti.id[i] >= 0;
+                    // the even CTA counts both CTAs' bytes
+                    if (rank == 0 && full == kTilePages) mbar_arrive_expect_tx(&m.vfull[nb], pages * 8192u);
+                    else if (rank == 0) bar_expect_tx(&m.vfull[nb], pages * 8192u);
+                    else if (full == kTilePages) bar_arrive_at(&m.vfull[nb], 0);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int key = (int)rank * 64 + u * 32 + kr;
-                ids[u] = t.live ? page_of(a, t.s.b, t.t * kTilePages + key / kPage, t.s.n) : -1;
-                in[u] = ids[u] >= 0 && t.t * kTile + key < t.s.n;
-            }
-        };
-        auto load = [&](int c) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-                raw[c][u] = in[u] ? reinterpret_cast<const uint4 *>(a.pool.c_pages)[((long long)ids[u] * kPage + (kr & 15)) * (kDC / 16) + c * 4 + part]
-                                  : zero;
-        };
-        if constexpr (FP8) {
-            load_ids(tw);
-            for (int c = 0; c < 8; ++c) load(c);
-            if (nx.live) nx.step(a, blocks);
-            load_ids(nx);
-        }
-        int seg = 0;
-        for (int t = 0; tw.live; ++t) {
-            if (tw.first) {
-                bar_wait(&m.qfree, (seg & 1) ^ 1, gave_up);
-                load_queries<FP8>(a, tw.s, R, rank, q, m.qscale[seg & 1], i);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    bar_arrive(&m.qfull);
-                    bar_arrive(&m.sq[seg & 1]);
+                    for (int i = 0; i < kTilePages; ++i) {
+                        const int id = ti.id[i];
+                        if (i >= full || id < 0) continue;
+                        tma_box4_pair(dst + i * 4096, &mapc, 0, 0, x / 64, id, &m.vfull[nb], pol);
+                    }
                 }
-                ++seg;
-            }
-            if constexpr (FP8) {
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    bar_wait(&m.kempty[c], (t & 1) ^ 1, gave_up);
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int r = u * 32 + kr;
-                        *piece(k + c * kChunkB, r, 2 * part) = cvt_e4m3x8(raw[c][u].x, raw[c][u].y);
-                        *piece(k + c * kChunkB, r, 2 * part + 1) = cvt_e4m3x8(raw[c][u].z, raw[c][u].w);
+                __syncwarp();
+                if (full < kTilePages) {
+                    // the page that the last token is in, and zeros for every slot past it:
+                    // those may hold anything, NaN among it, and meet weights of zero
+                    const int id = left % kPage ? ti.id[full] : -1;
+                    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+                    for (int e = lane; e < (kTile - full * kPage) * 16; e += 32) {
+                        const int r = full * kPage + (e >> 4), c = e & 15;  // row, 16-byte piece of its 256
+                        uint4 w = zero;
+                        if (r < left && id >= 0)
+                            w = reinterpret_cast<const uint4 *>(a.pool.c_pages)[((long long)id * kPage + (r & 15)) * (kDC / 8) + x / 8 + c];
+                        *piece(dst + (r >> 4) * 4096 + (c >> 3) * 2048, r & 15, c & 7) = w;
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) bar_arrive(&m.kfull[c]);
-                    load(c);  // the next tile's
+                    if (lane == 0) bar_arrive_at(&m.vfull[nb], 0);
                 }
-                if (nx.live) nx.step(a, blocks);
-                load_ids(nx);
             }
-            tw.step(a, blocks);
         }
-    } else if (warp >= 12 && FP8) {
-        // ---------------------- V converted on the way ----------------------
-        const int i = tid - 384;
-        const int kr = i >> 2, part = i & 3;
-        TileWalk tw, nx;
-        tw.start(a, blocks, walk);
-        nx = tw;
-        uint4 raw[4][4];
-        int ids[4];
-        bool in[4];
-        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-        auto load_ids = [&](const TileWalk &t) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int key = u * 32 + kr;
-                ids[u] = t.live ? page_of(a, t.s.b, t.t * kTilePages + key / kPage, t.s.n) : -1;
-                in[u] = ids[u] >= 0 && t.t * kTile + key < t.s.n;
-            }
-        };
-        auto load = [&](int s) {  // chunk s holds values (s / 2) * 256 + rank * 128 + (s & 1) * 64 ...
-            const int g = (s >> 1) * 4 + (int)rank * 2 + (s & 1);
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                raw[s][u] = in[u] ? reinterpret_cast<const uint4 *>(a.pool.c_pages)[((long long)ids[u] * kPage + (kr & 15)) * (kDC / 16) + g * 4 + part]
-                                  : zero;
-        };
-        load_ids(tw);
-        for (int s = 0; s < 4; ++s) load(s);
-        if (nx.live) nx.step(a, blocks);
-        load_ids(nx);
-        for (int t = 0; tw.live; ++t) {
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                if ((s & 1) == 0) bar_wait(&m.vempty[s >> 1], (t & 1) ^ 1, gave_up);
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int r = u * 32 + kr;
-                    *piece(v + s * kVChunkB, r, 2 * part) = cvt_e4m3x8(raw[s][u].x, raw[s][u].y);
-                    *piece(v + s * kVChunkB, r, 2 * part + 1) = cvt_e4m3x8(raw[s][u].z, raw[s][u].w);
+        if (!FP8 && *gave_up) drain_copies();
+        __syncwarp();
+    } else if (warp == 11) {
+        // ------------- pages, checks, scales; two tiles at a time -------------
+        reg_share_less<64>();
+        Walk walk{m.x0, m.x1, m.off, m.b0};
+        Segment s;
+        const int i = (lane >> 3) & 1, pg = lane & 7;  // tile of the two, page of the tile
+        int t = 0;
+        while (walk.next(a, blocks, s)) {
+            uint32_t bits = 0;
+            for (int at = s.t0; at < s.t1; at += 2) {
+                const int tile = at + i, lp = tile * kTilePages + pg;
+                int id = -1;
+                uint32_t bad = 0;
+                float z = 1.f;
+                if (lane < 16 && tile < s.t1 && lp < (s.n + kPage - 1) / kPage) {
+                    const long long bi = (long long)s.b * a.pool.bt_sb + lp;
+                    id = a.pool.block_tables[bi];
+                    bad = latent_entry_bits(a.pool, id, bi);
+                    if (bad) id = -1;  // not read; the merge kernel flags and zeroes the request
                 }
-                load(s);
-                if (s & 1) {
-                    fence_proxy_async_smem();
+                bits |= bad;
+                if (id >= 0 && FP8) z = a.pool.c_scale[id];
+                for (int j = 0; j < min(2, s.t1 - at); ++j, ++t) {
+                    Tile &ti = m.tile[t % kRing];
+                    if (!__all_sync(0xffffffffu, bar_wait(&m.mempty[t % kRing], ((t / kRing) & 1) ^ 1, gave_up))) continue;
+                    if (lane < 16 && i == j) {
+                        ti.id[pg] = id;
+                        ti.z[pg] = z;
+                        if (pg == 0) {
+                            ti.b = s.b;
+                            ti.block = s.block;
+                            ti.left = s.n - tile * kTile;
+                            ti.flags = (tile == s.t0 ? kFirst : 0u) | (tile + 1 == s.t1 ? kLast : 0u) |
+                                       (s.t1 - s.t0 == s.tiles ? kWhole : 0u) | (s.t0 == 0 ? kBegins : 0u);
+                        }
+                        // this CTA's half into L2; its peer takes the other
+                        if (id >= 0 && (uint32_t)(pg >> 2) == rank) {
+                            const uint32_t cb = kPage * kDC * (FP8 ? 1 : 2);
+                            l2_prefetch(static_cast<const uint8_t *>(a.pool.c_pages) + (long long)id * cb, cb);
+                            l2_prefetch(a.pool.r_pages + (long long)id * kPage * PFKV_LATENT_ROPE,
+                                        kPage * PFKV_LATENT_ROPE * 2);
+                        }
+                    }
                     __syncwarp();
-                    if (lane == 0) bar_arrive(&m.vfull[s >> 1]);
+                    if (lane == 0) bar_arrive(&m.mfull[t % kRing]);
                 }
             }
-            if (nx.live) nx.step(a, blocks);
-            load_ids(nx);
-            tw.step(a, blocks);
+            bits = __reduce_or_sync(0xffffffffu, bits);
+            if (lane == 0 && rank == 0) parts.status[(long long)s.b * blocks + s.block + w] = bits;
+        }
+    } else if (!FP8 || warp < 16) {
+        // ------------------------- K through registers -------------------------
+        // stage j holds chunks 2j and 2j + 1; a thread's words of the next tile are
+        // loaded as soon as this tile's are stored
+        const int j = FP8 ? warp - 12 : (warp - 12) >> 1;
+        const int row0 = FP8 ? 0 : ((warp - 12) & 1) * 32;
+        // FP8: 8 lanes a row of 128 bytes, 64 rows; BF16: 16 lanes a row of 256, 32 rows
+        const int r_in = FP8 ? lane >> 3 : lane >> 4, pc = FP8 ? lane & 7 : lane & 15;
+        constexpr int RPS = FP8 ? 4 : 2;  // rows a step of 32 lanes
+        uint8_t *const dst = k + 2 * j * kChunkB;
+        // A page that is not to be read is read as page 0, which exists: its rows are past
+        // the last token and stored as zeros, or its request is flagged and zeroed.
+        constexpr long long PAGEB = (long long)kPage * kDC * (FP8 ? 1 : 2);
+        const uint8_t *const src = static_cast<const uint8_t *>(a.pool.c_pages) + r_in * (FP8 ? 512 : 1024) +
+                                   j * (FP8 ? 128 : 256) + pc * 16;
+        reg_share_less<88>();
+        uint4 raw[16];
+        int left = 0;
+        auto load = [&](int t) {
+            const bool ok = t < N && looked_up(t);
+            const Tile &ti = m.tile[t % kRing];
+            left = ok ? ti.left - (int)rank * 64 : 0;
+            constexpr int PAGES = 16 * RPS / kPage;
+            const uint8_t *page[PAGES];
+#pragma unroll
+            for (int i = 0; i < PAGES; ++i)
+                page[i] = src + PAGEB * (ok ? max(0, ti.id[rank * 4 + row0 / kPage + i]) : 0);
+#pragma unroll
+            for (int u = 0; u < 16; ++u)
+                raw[u] = *reinterpret_cast<const uint4 *>(page[u * RPS / kPage] + (u * RPS % kPage) * (FP8 ? 512 : 1024));
+        };
+        load(0);
+        for (int t = 0; t < N; ++t) {
+            if (left < row0 + 16 * RPS) {
+#pragma unroll
+                for (int u = 0; u < 16; ++u)
+                    if (row0 + u * RPS + r_in >= left) raw[u] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            bar_wait(&m.kempty[j], (t & 1) ^ 1, gave_up);
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+                const int r = row0 + u * RPS + r_in;
+                if constexpr (FP8) {
+                    // lanes 4-7 of a row hold the second chunk: they store their odd piece first,
+                    // so that the eight lanes' pieces lie in different banks
+                    const int c = pc >> 2, q2 = 2 * (pc & 3);
+                    const uint4 lo = cvt_e4m3x8(raw[u].x, raw[u].y), hi = cvt_e4m3x8(raw[u].z, raw[u].w);
+                    *piece(dst + c * kChunkB, r, q2 + c) = c ? hi : lo;
+                    *piece(dst + c * kChunkB, r, q2 + 1 - c) = c ? lo : hi;
+                } else {
+                    *piece(dst + (pc >> 3) * kChunkB, r, pc & 7) = raw[u];
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) bar_arrive_at(&m.kfull[j], 0);
+            load(t + 1);
+        }
+    } else {
+        // ------------------ FP8: V converted on the way, a warp a chunk ------------------
+        const int s = warp - 16;
+        const int g = (s >> 1) * 4 + (int)rank * 2 + (s & 1);  // chunk of the latent's eight
+        const int r_in = lane >> 2, pc = lane & 3;
+        uint8_t *const dst = v + s * kVChunkB;
+        const uint8_t *const src = static_cast<const uint8_t *>(a.pool.c_pages) + r_in * kDC + g * 64 + pc * 16;
+        reg_share_less<88>();
+        uint4 raw[16];
+        int left = 0;
+        auto load = [&](int t) {
+            const bool ok = t < N && looked_up(t);
+            const Tile &ti = m.tile[t % kRing];
+            left = ok ? ti.left : 0;
+#pragma unroll
+            for (int i = 0; i < kTilePages; ++i) {
+                const uint8_t *page = src + (long long)(kPage * kDC) * (ok ? max(0, ti.id[i]) : 0);
+                raw[2 * i] = *reinterpret_cast<const uint4 *>(page);
+                raw[2 * i + 1] = *reinterpret_cast<const uint4 *>(page + 8 * kDC);
+            }
+        };
+        load(0);
+        for (int t = 0; t < N; ++t) {
+            if (left < kTile) {
+#pragma unroll
+                for (int u = 0; u < 16; ++u)
+                    if (u * 8 + r_in >= left) raw[u] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            bar_wait(&m.vempty[s >> 1], (t & 1) ^ 1, gave_up);
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+                const int r = u * 8 + r_in;
+                *piece(dst, r, 2 * pc) = cvt_e4m3x8(raw[u].x, raw[u].y);
+                *piece(dst, r, 2 * pc + 1) = cvt_e4m3x8(raw[u].z, raw[u].w);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) bar_arrive_at(&m.vfull[s >> 1], 0);
+            load(t + 1);
         }
     }
     __syncthreads();
@@ -839,14 +868,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_fence_before();
     cluster_sync();  // the even CTA's products read the odd one's shared memory
     tmem_fence_after();
-    if (warp == 4) tmem_free512<2>(tmem);
+    if (warp == 8) tmem_free512<2>(tmem);
 }
 
 // --------------------------------------------------------------------------
-// Merge: a warp a row.  Before its wait for the split kernel it checks what the
-// flags depend on: the length, and the id and tag of every live page.
+// Merge: a warp half a row.  What depends on the call's inputs alone (the list of
+// tiles) comes before its wait for the split kernel.
 // --------------------------------------------------------------------------
-constexpr int kMergeWarps = 8;
+constexpr int kMergeWarps = 8, kMergeRows = kMergeWarps / 2;
 
 __global__ void __launch_bounds__(kMergeWarps * 32)
     latent_merge_kernel(LatentDecodeArgs a, int R, int blocks, int clusters, Parts parts, int groups) {
@@ -856,11 +885,6 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int raw = a.pool.seq_lens[(long long)b * a.pool.len_sb];
     const int n = live_len(a, b);
-    uint32_t bits = raw != n ? PFKV_FLAG_BAD_LENGTH : 0u;
-    for (int i = tid; i < (n + kPage - 1) / kPage; i += blockDim.x) {
-        const long long bi = (long long)b * a.pool.bt_sb + i;
-        bits |= latent_entry_bits(a.pool, a.pool.block_tables[bi], bi);
-    }
     long long before = 0, all = 0;
     for (int i = tid; i < a.B; i += blockDim.x) {
         const long long u = (long long)tiles_of(live_len(a, i)) * blocks;
@@ -871,70 +895,100 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     for (int d = 16; d > 0; d >>= 1) {
         before += __shfl_xor_sync(0xffffffffu, before, d);
         all += __shfl_xor_sync(0xffffffffu, all, d);
-        bits |= __shfl_xor_sync(0xffffffffu, bits, d);
     }
     if (lane == 0) {
         sums[0][warp] = before;
         sums[1][warp] = all;
     }
-    uint32_t flag = 0;
-#pragma unroll
-    for (uint32_t f = 1; f < 8; f <<= 1)
-        if (__syncthreads_or(bits & f)) flag |= f;
+    __syncthreads();
     before = all = 0;
     for (int i = 0; i < kMergeWarps; ++i) {
         before += sums[0][i];
         all += sums[1][i];
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tiles = tiles_of(n);
     const int W = (int)min((long long)clusters, all);
     auto cluster_of = [&](long long x) { return (int)(x * W / all); };
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    uint32_t flag = raw != n ? PFKV_FLAG_BAD_LENGTH : 0u;
     if (tiles > 0) {
         const int w0 = cluster_of(before), w1 = cluster_of(before + (long long)tiles * blocks - 1);
-        int up = 0;
-        for (int i = w0 * 2 + tid; i < (w1 + 1) * 2; i += blockDim.x) up |= parts.gave_up[i] != 0u;
-        if (__syncthreads_or(up)) flag |= PFKV_FLAG_DEVICE_TIMEOUT;
+        uint32_t bits = 0;
+        for (int i = w0 * 2 + tid; i < (w1 + 1) * 2; i += blockDim.x)
+            if (parts.gave_up[i]) bits |= PFKV_FLAG_DEVICE_TIMEOUT;
+        for (int k = 0; k < blocks; ++k) {  // every cluster that holds a part of row block k
+            const long long first = before + (long long)k * tiles;
+            const int last = cluster_of(first + tiles - 1);
+            for (int i = cluster_of(first) + tid; i <= last; i += blockDim.x)
+                bits |= parts.status[(long long)b * blocks + k + i];
+        }
+#pragma unroll
+        for (uint32_t f = 1; f < 16; f <<= 1)
+            if (__syncthreads_or(bits & f)) flag |= f;
     }
     if (g == 0 && tid == 0 && a.flags) a.flags[b] = (uint8_t)flag;
-    const int row = g * kMergeWarps + warp;
+    const int row = g * kMergeRows + (warp >> 1);
     if (row >= R) return;
     const int t = row / a.H, h = row - t * a.H;
-    __nv_bfloat16 *out = a.out.p + (long long)b * a.out.sb + (long long)t * a.out.st + (long long)h * a.out.sh;
-    // lane l: values 4 l + 128 i .. + 3
-    float o[4][4] = {};
+    __nv_bfloat16 *out = a.out.p + (long long)b * a.out.sb + (long long)t * a.out.st + (long long)h * a.out.sh +
+                         (warp & 1) * 256;
+    // lane l: values 4 l + 128 i .. + 3 of the half
+    float o[2][4] = {};
     if (!flag && tiles > 0) {
         const int block = row / kRowBlock, brow = row - block * kRowBlock;
         const long long first = before + (long long)block * tiles;
         const int w0 = cluster_of(first), w1 = cluster_of(first + tiles - 1);
         if (w0 == w1) return;  // one part: written by the split kernel
+        auto place = [&](int w) { return (long long)(w * 2 + (w == w0 ? 1 : 0)) * parts.rows + brow; };
         float ref = kNegInf, sum = 0.f;
-        for (int w = w0; w <= w1; ++w) {
-            const long long at = (long long)(w * 2 + (w == w0 ? 1 : 0)) * parts.rows + brow;
-            const float l = parts.lse[at];
-            if (l == kNegInf) continue;
-            const float4 *src = reinterpret_cast<const float4 *>(parts.o + at * kDC) + lane;
-            const float top = fmaxf(ref, l);
-            const float old = ref == kNegInf ? 0.f : exp2f(ref - top), now = exp2f(l - top);
-            ref = top;
-            sum = sum * old + now;
+        for (int at = w0; at <= w1; at += 32) {  // 32 parts at once: a lane has one's weight
+            const float l = at + lane <= w1 ? parts.lse[place(at + lane)] : kNegInf;
+            float top = l;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float4 y = src[i * 32];
-                o[i][0] = o[i][0] * old + y.x * now;
-                o[i][1] = o[i][1] * old + y.y * now;
-                o[i][2] = o[i][2] * old + y.z * now;
-                o[i][3] = o[i][3] * old + y.w * now;
+            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            top = fmaxf(ref, top);
+            if (top == kNegInf) continue;
+            const float old = exp2f(ref - top), mine = exp2f(l - top);
+            ref = top;
+            float s = mine;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+            sum = sum * old + s;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][e] *= old;
+            const int count = min(32, w1 - at + 1);
+            for (int j = 0; j < count; j += 8) {  // eight parts' loads in flight
+                float4 y[8][2];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const float4 *src = reinterpret_cast<const float4 *>(parts.o + place(min(at + j + u, w1)) * kDC + (warp & 1) * 256) + lane;
+                    y[u][0] = src[0];
+                    y[u][1] = src[32];
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const float f = __shfl_sync(0xffffffffu, mine, min(31, j + u));
+                    if (j + u >= count || f == 0.f) continue;  // parts that saw nothing hold zeros
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        o[i][0] += y[u][i].x * f;
+                        o[i][1] += y[u][i].y * f;
+                        o[i][2] += y[u][i].z * f;
+                        o[i][3] += y[u][i].w * f;
+                    }
+                }
             }
         }
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][e] *= inv;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
         const __nv_bfloat162 x = __floats2bfloat162_rn(o[i][0], o[i][1]), y = __floats2bfloat162_rn(o[i][2], o[i][3]);
         *reinterpret_cast<uint2 *>(out + 4 * lane + 128 * i) =
             make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
@@ -942,18 +996,20 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
 }
 
 struct Layout {
-    size_t lse, gave_up, total;
+    size_t lse, gave_up, status, total;
     int rows;
 };
 
-Layout workspace_layout(int R, int clusters) {
+Layout workspace_layout(int B, int R, int clusters) {
     Layout l;
     l.rows = R < kRowBlock ? R : kRowBlock;
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
     const size_t rows = (size_t)clusters * 2 * l.rows;
     l.lse = up(rows * kDC * sizeof(float));
     l.gave_up = l.lse + up(rows * sizeof(float));
-    l.total = l.gave_up + up((size_t)clusters * 2 * sizeof(uint32_t));
+    l.status = l.gave_up + up((size_t)clusters * 2 * sizeof(uint32_t));
+    const size_t pairs = (size_t)B * ((R + kRowBlock - 1) / kRowBlock);
+    l.total = l.status + up((pairs + clusters) * sizeof(uint32_t));
     return l;
 }
 
@@ -979,16 +1035,17 @@ cudaError_t launch_split(const CUtensorMap &mapc, const CUtensorMap &mapr, const
 
 }  // namespace
 
-size_t latent_decode_workspace(int, int H, int kq, int, int num_sms) {
-    return workspace_layout(H * kq, max(1, num_sms / 2)).total;
+size_t latent_decode_workspace(int B, int H, int kq, int, int num_sms) {
+    return workspace_layout(B, H * kq, max(1, num_sms / 2)).total;
 }
 
 cudaError_t launch_latent_decode(const LatentDecodeArgs &a, int num_sms, cudaStream_t s) {
     const int R = a.H * a.kq, blocks = (R + kRowBlock - 1) / kRowBlock, clusters = max(1, num_sms / 2);
-    const Layout l = workspace_layout(R, clusters);
+    const Layout l = workspace_layout(a.B, R, clusters);
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
     const Parts parts{reinterpret_cast<float *>(ws), reinterpret_cast<float *>(ws + l.lse),
-                      reinterpret_cast<uint32_t *>(ws + l.gave_up), l.rows};
+                      reinterpret_cast<uint32_t *>(ws + l.gave_up), reinterpret_cast<uint32_t *>(ws + l.status),
+                      l.rows};
     alignas(64) CUtensorMap mapc, mapr;
     const uint64_t np = (uint64_t)a.pool.num_pages;
     cudaError_t e = bf16_map3(&mapr, a.pool.r_pages, PFKV_LATENT_ROPE, kPage, np, PFKV_LATENT_ROPE,
@@ -996,13 +1053,13 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs &a, int num_sms, cudaStr
     if (e != cudaSuccess) return e;
     mapc = mapr;  // FP8 pools: not read
     if (!a.pool.fp8) {
-        e = bf16_map3(&mapc, a.pool.c_pages, kDC, kPage, np, kDC, kPage * kDC, kPage, 1);
+        e = bf16_map4(&mapc, a.pool.c_pages, kPage, kDC / 64, np, kDC, 64, kPage * kDC, kPage, 2);
         if (e != cudaSuccess) return e;
     }
     e = a.pool.fp8 ? launch_split<true>(mapc, mapr, a, R, blocks, clusters, parts, s)
                    : launch_split<false>(mapc, mapr, a, R, blocks, clusters, parts, s);
     if (e != cudaSuccess) return e;
-    const int groups = (R + kMergeWarps - 1) / kMergeWarps;
+    const int groups = (R + kMergeRows - 1) / kMergeRows;
     if ((long long)groups * a.B > 0x7fffffffLL) return cudaErrorInvalidValue;
     return launch_pdl(latent_merge_kernel, dim3((unsigned)(groups * a.B)), dim3(kMergeWarps * 32), 0, s, a, R, blocks,
                       clusters, parts, groups);

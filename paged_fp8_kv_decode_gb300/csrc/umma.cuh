@@ -113,6 +113,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&r)[32]) {
           "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
         : "r"(addr));
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&r)[16]) {
+    uint32_t *u = reinterpret_cast<uint32_t *>(r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(addr));
+}
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&u)[32]) {
     asm volatile(
@@ -124,7 +132,25 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&u)[32]
         "r"(u[29]), "r"(u[30]), "r"(u[31]), "r"(addr)
         : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const float (&r)[16]) {
+    const uint32_t *u = reinterpret_cast<const uint32_t *>(r);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(u[0]),
+        "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]),
+        "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(addr)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// A warpgroup's registers a thread, of those that the block was launched with.
+template <int N>
+__device__ __forceinline__ void reg_share_less() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_share_more() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 // --------------------------------------------------------------------------
 // barriers
@@ -133,22 +159,34 @@ __device__ __forceinline__ void bar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// Arrive on the barrier at this offset in CTA `rank` of the cluster.
+// More bytes for the current phase, without an arrival.
+__device__ __forceinline__ void bar_expect_tx(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
+}
+
+// Arrive on the barrier at this offset in CTA `rank` of the cluster.  Arrivals and
+// waits keep the default scope also between CTAs: what they order is read by
+// matrix products, whose writers have fenced the async proxy, never by ordinary
+// loads.  (A wait that acquires at cluster scope cost 0.4 us each: 176 us instead
+// of the FIGURE us of a 140K-token FP8 batch of 128 heads.)
 __device__ __forceinline__ void bar_arrive_at(uint64_t *bar, uint32_t rank) {
     asm volatile(
         "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
-        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_addr(bar)),
+        "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_addr(bar)),
         "r"(rank)
         : "memory");
 }
 
-__device__ __forceinline__ bool bar_try_cluster(uint64_t *bar, uint32_t parity) {
+// A wait that sleeps: the warp is woken when the phase completes, or after about
+// `ns`.  (Waiting warps that poll take issue slots from the ones that work.)
+constexpr uint32_t kSleepNs = 20000;
+__device__ __forceinline__ bool mbar_try_wait_for(uint64_t *bar, uint32_t parity, uint32_t ns) {
     uint32_t ok;
     asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(ns)
         : "memory");
     return ok != 0;
 }
@@ -157,10 +195,10 @@ __device__ __forceinline__ bool bar_try_cluster(uint64_t *bar, uint32_t parity) 
 // wait of the CTA returns at once, and the roles run to their end without issuing
 // copies or products.  Returns false then.
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *gave_up) {
-    if (bar_try_cluster(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     const unsigned long long t0 = globaltimer_ns();
     while (!*gave_up) {
-        if (bar_try_cluster(bar, parity)) return true;
+        if (mbar_try_wait_for(bar, parity, kSleepNs)) return true;
         if (globaltimer_ns() - t0 > kWaitLimitNs) *gave_up = 1u;
     }
     return false;
@@ -169,7 +207,7 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatil
 // The same, however the CTA's other waits went: for work that is in flight.
 __device__ __forceinline__ void bar_drain(uint64_t *bar, uint32_t parity) {
     const unsigned long long t0 = globaltimer_ns();
-    while (!bar_try_cluster(bar, parity) && globaltimer_ns() - t0 <= kWaitLimitNs) {}
+    while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 <= kWaitLimitNs) {}
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -188,6 +226,27 @@ __device__ __forceinline__ void tma_box3(void *dst, const CUtensorMap *map, int 
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
         " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar)), "l"(policy)
+        : "memory");
+}
+
+// The same by either CTA of a pair, counted on the even CTA's barrier at this offset.
+__device__ __forceinline__ void tma_box3_pair(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar,
+                                              uint64_t policy) {
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %5, 0;\n\t"
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4}], [a], %6;\n\t}" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar)), "l"(policy)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_box4_pair(void *dst, const CUtensorMap *map, int x, int y, int z, int w,
+                                              uint64_t *bar, uint64_t policy) {
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %6, 0;\n\t"
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5}], [a], %7;\n\t}" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar)), "l"(policy)
         : "memory");
 }
 
@@ -234,6 +293,22 @@ inline cudaError_t bf16_map3(CUtensorMap *map, const void *p, uint64_t d0, uint6
     const cuuint32_t box[3] = {64, box1, box2};
     const cuuint32_t one[3] = {1, 1, 1};
     const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box, one,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// A bf16 tensor [d3][d2][d1][64] with element strides s3, s2, s1, read in boxes of
+// 64 x box1 x box2 x 1 with the 128-byte swizzle.
+inline cudaError_t bf16_map4(CUtensorMap *map, const void *p, uint64_t d1, uint64_t d2, uint64_t d3, uint64_t s1,
+                             uint64_t s2, uint64_t s3, uint32_t box1, uint32_t box2) {
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = umma_map_encoder();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t dims[4] = {64, d1, d2, d3};
+    const cuuint64_t strides[3] = {s1 * 2, s2 * 2, s3 * 2};
+    const cuuint32_t box[4] = {64, box1, box2, 1};
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, strides, box, one,
                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
