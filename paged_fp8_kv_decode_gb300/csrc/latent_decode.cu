@@ -22,9 +22,8 @@
 // values (V: four chunks, 16 KB each), as V's columns are split between the
 // CTAs.  Each latent is thus read from HBM once, and from L2 twice.  Shared
 // memory (Q 72 KB, K 72 KB, V 64 KB, P 16 KB) leaves no room for second buffers;
-// instead every chunk's slot is refilled as soon as its last product has
-// completed, from registers that the next tile's latents were loaded into, and an
-// L2 prefetch runs ahead of that.
+// instead every stage's slot is refilled as soon as its last product has completed,
+// and an L2 prefetch runs ahead of that.
 //
 // Softmax: one pass.  Four threads hold a row (32 tokens each), in log2 units, with
 // a running reference that moves only when the maximum has grown by 2^8 (then O
@@ -39,11 +38,11 @@
 // log2-sum-exp) and a second kernel merges them.
 //
 // Roles of a CTA's twenty warps: 0-7 softmax and output (four threads a row); 8, in
-// the even CTA, issues the pair's products; 9 loads the rotated keys and 10 V of BF16
-// pools by TMA; 11 looks up pages, checks and scales six tiles ahead of their use and
-// prefetches them into L2; 12-19 carry latents through registers, the next tile's
-// loaded while this one is stored: K of BF16 pools (two warps a stage), or K (a warp
-// a stage) and V (a warp a chunk) of FP8 pools, converted to f16 on the way.
+// the even CTA, issues the pair's products; 9 and 10 load rotated keys, K and V by TMA
+// (K and V of BF16 pools: through registers, K of BF16 cost 2.7 us a tile, by TMA
+// 2.15); 11 looks up pages, checks and scales six tiles ahead of their use and
+// prefetches them into L2; FP8: 12-15 and 16-19 carry K and V through registers and
+// convert them to f16, the next tile's loaded while this one is stored.
 #include <type_traits>
 
 #include "latent_internal.cuh"
@@ -90,9 +89,9 @@ constexpr uint32_t kFirst = 1, kLast = 2, kWhole = 4, kBegins = 8;  // of the pa
 
 struct Misc {
     // operands of both CTAs in place (in the even CTA), slots free again (in both)
-    uint64_t kfull[kKStages], kempty[kKStages], vfull[2], vempty[2];
+    uint64_t kfull[kKStages], vfull[2], pready, kempty[kKStages], vempty[2];
     uint64_t mfull[kRing], mempty[kRing];
-    uint64_t sfull[2], pready, pvdone, qfull, drain;
+    uint64_t sfull[2], pvdone, qfull, drain;
     Tile tile[kRing];
     union {
         long long warp_sum[kThreads / 32];
@@ -171,6 +170,10 @@ __device__ __forceinline__ uint4 cvt_e4m3x8(uint32_t lo, uint32_t hi) {
     return r;
 }
 
+__device__ __forceinline__ void store_shared(uint32_t at, const uint4 &w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+}
+
 // Piece c (16 bytes) of row r of a swizzled chunk.
 __device__ __forceinline__ uint4 *piece(uint8_t *chunk, int r, int c) {
     return reinterpret_cast<uint4 *>(chunk + r * 128 + ((c ^ (r & 7)) << 4));
@@ -245,6 +248,7 @@ __device__ __forceinline__ bool bar_any(int id, bool says) {
 template <bool FP8>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_split_kernel(const __grid_constant__ CUtensorMap mapc, const __grid_constant__ CUtensorMap mapr,
+                        const __grid_constant__ CUtensorMap mapk,
                         LatentDecodeArgs a, int R, int blocks, int clusters, Parts parts) {
     extern __shared__ __align__(1024) uint8_t sm[];  // no static shared memory: the window's aligned base
     Misc &m = *reinterpret_cast<Misc *>(sm + kOffMisc);
@@ -254,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int w = blockIdx.x >> 1;
     if (tid == 0) {
         for (int c = 0; c < kKStages; ++c) {
-            mbar_init(&m.kfull[c], c == 4 ? 1 : FP8 ? 2 : 4);
+            mbar_init(&m.kfull[c], c < 4 && FP8 ? 2 : 1);
             mbar_init(&m.kempty[c], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -600,8 +604,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             int seg = 0;
             bool pfirst = false;
-            for (int t = 0; t < N; ++t) {
-                const uint32_t flags = looked_up(t) ? m.tile[t % kRing].flags : 0u;
+            uint32_t flags = N > 0 && looked_up(0) ? m.tile[0].flags : 0u, next = 0;
+            for (int t = 0; t < N; ++t, flags = next) {
                 const bool first = (flags & kFirst) != 0;
                 // the products of the tile before this one's scores when Q changes between them
                 if (t > 0 && first) values(t - 1, pfirst);
@@ -633,6 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     umma_commit_pair(&m.kempty[c]);
                 }
                 if (ok) umma_commit_pair(&m.sfull[t & 1]);
+                next = t + 1 < N && looked_up(t + 1) ? m.tile[(t + 1) % kRing].flags : 0u;
                 if (t > 0 && !first) values(t - 1, pfirst);
                 pfirst = first;
                 if (flags & kLast) ++seg;
@@ -644,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp == 9) {
-        // -------------------------- rotated keys: TMA --------------------------
+        // ------------- rotated keys, and K of BF16 pools: TMA -------------
         reg_share_less<64>();
         if (elect_one()) {
             const uint64_t pol = l2_policy_evict_normal();
@@ -661,6 +666,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (id[i] >= 0) tma_box3_pair(k + 8 * kChunkB + i * 2048, &mapr, 0, 0, id[i], &m.kfull[4], pol);
+                if constexpr (!FP8) {
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        if (!bar_wait(&m.kempty[c], (t & 1) ^ 1, gave_up)) break;
+                        if (rank == 0) mbar_arrive_expect_tx(&m.kfull[c], pages * 4096u);
+                        uint8_t *dst = k + 2 * c * kChunkB;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (id[i] < 0) continue;
+                            tma_box3_pair(dst + i * 2048, &mapk, c * 128, 0, id[i], &m.kfull[c], pol);
+                            tma_box3_pair(dst + kChunkB + i * 2048, &mapk, c * 128 + 64, 0, id[i], &m.kfull[c], pol);
+                        }
+                    }
+                }
             }
             if (*gave_up) drain_copies();
         }
@@ -764,58 +783,49 @@ __global__ void __launch_bounds__(kThreads, 1)
             bits = __reduce_or_sync(0xffffffffu, bits);
             if (lane == 0 && rank == 0) parts.status[(long long)s.b * blocks + s.block + w] = bits;
         }
-    } else if (!FP8 || warp < 16) {
-        // ------------------------- K through registers -------------------------
-        // stage j holds chunks 2j and 2j + 1; a thread's words of the next tile are
-        // loaded as soon as this tile's are stored
-        const int j = FP8 ? warp - 12 : (warp - 12) >> 1;
-        const int row0 = FP8 ? 0 : ((warp - 12) & 1) * 32;
-        // FP8: 8 lanes a row of 128 bytes, 64 rows; BF16: 16 lanes a row of 256, 32 rows
-        const int r_in = FP8 ? lane >> 3 : lane >> 4, pc = FP8 ? lane & 7 : lane & 15;
-        constexpr int RPS = FP8 ? 4 : 2;  // rows a step of 32 lanes
-        uint8_t *const dst = k + 2 * j * kChunkB;
+    } else if (!FP8) {
+        reg_share_less<24>();  // BF16: nothing to convert
+    } else if (warp < 16) {
+        // ------------------ FP8: K converted on the way, a warp a stage ------------------
+        // stage j holds chunks 2j and 2j + 1 of 64 tokens, 8 lanes a row of 128 bytes; a
+        // thread's words of the next tile are loaded as soon as this tile's are stored
+        reg_share_less<88>();
+        const int j = warp - 12, r_in = lane >> 3, pc = lane & 7;
         // A page that is not to be read is read as page 0, which exists: its rows are past
         // the last token and stored as zeros, or its request is flagged and zeroed.
-        constexpr long long PAGEB = (long long)kPage * kDC * (FP8 ? 1 : 2);
-        const uint8_t *const src = static_cast<const uint8_t *>(a.pool.c_pages) + r_in * (FP8 ? 512 : 1024) +
-                                   j * (FP8 ? 128 : 256) + pc * 16;
-        reg_share_less<88>();
+        const uint8_t *const src = static_cast<const uint8_t *>(a.pool.c_pages) + r_in * kDC + j * 128 + pc * 16;
+        // where the thread's first piece of rows 4 i + r_in goes
+        uint32_t at[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            at[i] = smem_addr(k + 2 * j * kChunkB) + (pc >> 2) * kChunkB + r_in * 128 +
+                    (((2 * (pc & 3)) ^ (4 * i + r_in)) << 4);
         uint4 raw[16];
         int left = 0;
         auto load = [&](int t) {
             const bool ok = t < N && looked_up(t);
             const Tile &ti = m.tile[t % kRing];
             left = ok ? ti.left - (int)rank * 64 : 0;
-            constexpr int PAGES = 16 * RPS / kPage;
-            const uint8_t *page[PAGES];
 #pragma unroll
-            for (int i = 0; i < PAGES; ++i)
-                page[i] = src + PAGEB * (ok ? max(0, ti.id[rank * 4 + row0 / kPage + i]) : 0);
+            for (int i = 0; i < 4; ++i) {
+                const uint8_t *page = src + (long long)(kPage * kDC) * (ok ? max(0, ti.id[rank * 4 + i]) : 0);
 #pragma unroll
-            for (int u = 0; u < 16; ++u)
-                raw[u] = *reinterpret_cast<const uint4 *>(page[u * RPS / kPage] + (u * RPS % kPage) * (FP8 ? 512 : 1024));
+                for (int u = 0; u < 4; ++u) raw[4 * i + u] = *reinterpret_cast<const uint4 *>(page + u * 4 * kDC);
+            }
         };
         load(0);
         for (int t = 0; t < N; ++t) {
-            if (left < row0 + 16 * RPS) {
+            if (left < 64) {
 #pragma unroll
                 for (int u = 0; u < 16; ++u)
-                    if (row0 + u * RPS + r_in >= left) raw[u] = make_uint4(0u, 0u, 0u, 0u);
+                    if (u * 4 + r_in >= left) raw[u] = make_uint4(0u, 0u, 0u, 0u);
             }
             bar_wait(&m.kempty[j], (t & 1) ^ 1, gave_up);
 #pragma unroll
             for (int u = 0; u < 16; ++u) {
-                const int r = row0 + u * RPS + r_in;
-                if constexpr (FP8) {
-                    // lanes 4-7 of a row hold the second chunk: they store their odd piece first,
-                    // so that the eight lanes' pieces lie in different banks
-                    const int c = pc >> 2, q2 = 2 * (pc & 3);
-                    const uint4 lo = cvt_e4m3x8(raw[u].x, raw[u].y), hi = cvt_e4m3x8(raw[u].z, raw[u].w);
-                    *piece(dst + c * kChunkB, r, q2 + c) = c ? hi : lo;
-                    *piece(dst + c * kChunkB, r, q2 + 1 - c) = c ? lo : hi;
-                } else {
-                    *piece(dst + (pc >> 3) * kChunkB, r, pc & 7) = raw[u];
-                }
+                const uint32_t to = at[u & 1] + u * 512;
+                store_shared(to, cvt_e4m3x8(raw[u].x, raw[u].y));
+                store_shared(to ^ 16u, cvt_e4m3x8(raw[u].z, raw[u].w));
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -829,6 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r_in = lane >> 2, pc = lane & 3;
         uint8_t *const dst = v + s * kVChunkB;
         const uint8_t *const src = static_cast<const uint8_t *>(a.pool.c_pages) + r_in * kDC + g * 64 + pc * 16;
+        const uint32_t at = smem_addr(dst) + r_in * 128 + (((2 * pc) ^ r_in) << 4);
         reg_share_less<88>();
         uint4 raw[16];
         int left = 0;
@@ -852,10 +863,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             bar_wait(&m.vempty[s >> 1], (t & 1) ^ 1, gave_up);
 #pragma unroll
-            for (int u = 0; u < 16; ++u) {
-                const int r = u * 8 + r_in;
-                *piece(dst, r, 2 * pc) = cvt_e4m3x8(raw[u].x, raw[u].y);
-                *piece(dst, r, 2 * pc + 1) = cvt_e4m3x8(raw[u].z, raw[u].w);
+            for (int u = 0; u < 16; ++u) {  // row u * 8 + r_in
+                store_shared(at + u * 1024, cvt_e4m3x8(raw[u].x, raw[u].y));
+                store_shared((at ^ 16u) + u * 1024, cvt_e4m3x8(raw[u].z, raw[u].w));
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -1014,7 +1024,7 @@ Layout workspace_layout(int B, int R, int clusters) {
 }
 
 template <bool FP8>
-cudaError_t launch_split(const CUtensorMap &mapc, const CUtensorMap &mapr, const LatentDecodeArgs &a, int R, int blocks,
+cudaError_t launch_split(const CUtensorMap &mapc, const CUtensorMap &mapr, const CUtensorMap &mapk, const LatentDecodeArgs &a, int R, int blocks,
                          int clusters, const Parts &parts, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)clusters * 2);
@@ -1030,7 +1040,7 @@ cudaError_t launch_split(const CUtensorMap &mapc, const CUtensorMap &mapr, const
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, latent_split_kernel<FP8>, mapc, mapr, a, R, blocks, clusters, parts);
+    return cudaLaunchKernelEx(&cfg, latent_split_kernel<FP8>, mapc, mapr, mapk, a, R, blocks, clusters, parts);
 }
 
 }  // namespace
@@ -1046,18 +1056,20 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs &a, int num_sms, cudaStr
     const Parts parts{reinterpret_cast<float *>(ws), reinterpret_cast<float *>(ws + l.lse),
                       reinterpret_cast<uint32_t *>(ws + l.gave_up), reinterpret_cast<uint32_t *>(ws + l.status),
                       l.rows};
-    alignas(64) CUtensorMap mapc, mapr;
+    alignas(64) CUtensorMap mapc, mapr, mapk;
     const uint64_t np = (uint64_t)a.pool.num_pages;
     cudaError_t e = bf16_map3(&mapr, a.pool.r_pages, PFKV_LATENT_ROPE, kPage, np, PFKV_LATENT_ROPE,
                               kPage * PFKV_LATENT_ROPE, kPage, 1);
     if (e != cudaSuccess) return e;
-    mapc = mapr;  // FP8 pools: not read
+    mapc = mapk = mapr;  // FP8 pools: not read
     if (!a.pool.fp8) {
+        e = bf16_map3(&mapk, a.pool.c_pages, kDC, kPage, np, kDC, kPage * kDC, kPage, 1);
+        if (e != cudaSuccess) return e;
         e = bf16_map4(&mapc, a.pool.c_pages, kPage, kDC / 64, np, kDC, 64, kPage * kDC, kPage, 2);
         if (e != cudaSuccess) return e;
     }
-    e = a.pool.fp8 ? launch_split<true>(mapc, mapr, a, R, blocks, clusters, parts, s)
-                   : launch_split<false>(mapc, mapr, a, R, blocks, clusters, parts, s);
+    e = a.pool.fp8 ? launch_split<true>(mapc, mapr, mapk, a, R, blocks, clusters, parts, s)
+                   : launch_split<false>(mapc, mapr, mapk, a, R, blocks, clusters, parts, s);
     if (e != cudaSuccess) return e;
     const int groups = (R + kMergeRows - 1) / kMergeRows;
     if ((long long)groups * a.B > 0x7fffffffLL) return cudaErrorInvalidValue;

@@ -177,30 +177,28 @@ __device__ __forceinline__ void bar_arrive_at(uint64_t *bar, uint32_t rank) {
         : "memory");
 }
 
-// A wait that sleeps: the warp is woken when the phase completes, or after about
-// `ns`.  (Waiting warps that poll take issue slots from the ones that work.)
+// Waits that give up.  A try sleeps until the phase completes, or for about kSleepNs
+// at most; after kTries of them (0.1 to 2 s, whatever a sleep comes to) `gave_up` is
+// set, every later wait of the CTA returns soon, and the roles run to their end
+// without issuing copies or products.  Returns false then.  (Short on purpose: with
+// five roles at work the instruction cache is what is scarce, and a wait is inlined
+// in thirty places.)
 constexpr uint32_t kSleepNs = 20000;
-__device__ __forceinline__ bool mbar_try_wait_for(uint64_t *bar, uint32_t parity, uint32_t ns) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity), "r"(ns)
-        : "memory");
-    return ok != 0;
-}
-
-// Waits that give up: after one has (kWaitLimitNs), `gave_up` is set, every later
-// wait of the CTA returns at once, and the roles run to their end without issuing
-// copies or products.  Returns false then.
+constexpr int kTries = 100000;
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *gave_up) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = globaltimer_ns();
-    while (!*gave_up) {
-        if (mbar_try_wait_for(bar, parity, kSleepNs)) return true;
-        if (globaltimer_ns() - t0 > kWaitLimitNs) *gave_up = 1u;
+#pragma unroll 1
+    for (int i = 0; i < kTries; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_addr(bar)), "r"(parity), "r"(kSleepNs)
+            : "memory");
+        if (ok) return true;
+        if (*gave_up) return false;
     }
+    *gave_up = 1u;
     return false;
 }
 
