@@ -244,12 +244,19 @@ pfkv_status pfkv_latent_prefill_attn(int32_t batch, int32_t num_heads, const int
     if (!q_starts || !k_starts) return PFKV_ERR_INVALID_ARG;
     if (!aligned(q_starts, 4) || !aligned(k_starts, 4)) return PFKV_ERR_ALIGNMENT;
     if (flags && !aligned(flags, 4)) return PFKV_ERR_ALIGNMENT;
-    const pfkv_rows *per_head[] = {q_nope, q_rope, k_nope, v, out};
-    for (const pfkv_rows *r : per_head) {
-        const pfkv_status st = check_rows(r, false, true);
-        if (st != PFKV_OK) return st;
-    }
-    pfkv_status st = check_rows(k_rope, false, false);
+    // arrays without rows are not read; rows that share an address cannot be copied as a box
+    auto check = [](const pfkv_rows *r, bool use_h, int64_t rows) {
+        if (!r) return PFKV_ERR_INVALID_ARG;
+        if (rows == 0) return PFKV_OK;
+        const pfkv_status st = check_rows(r, false, use_h);
+        return st == PFKV_OK && rows > 1 && r->stride_t == 0 ? PFKV_ERR_UNSUPPORTED : st;
+    };
+    pfkv_status st = check(q_nope, true, total_q);
+    if (st == PFKV_OK) st = check(q_rope, true, total_q);
+    if (st == PFKV_OK) st = check(out, true, total_q);
+    if (st == PFKV_OK) st = check(k_nope, true, total_k);
+    if (st == PFKV_OK) st = check(k_rope, false, total_k);
+    if (st == PFKV_OK) st = check(v, true, total_k);
     if (st != PFKV_OK) return st;
     int sms = 0;
     st = device_check(&sms);

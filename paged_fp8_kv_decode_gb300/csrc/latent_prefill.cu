@@ -1,70 +1,465 @@
 // latent_prefill.cu -- pfkv_latent_prefill_attn: ragged causal attention of
 // prompts in the expanded form (declared in pfkv_latent.h).
 //
-// First form: one warp a query row and head, a running maximum and sum over the
-// keys one at a time.
+// Mathematics.  For each request and head S = scale (Qn Kn^T + Qr Kr^T), O =
+// softmax(S) V with 128 + 64 and 128 columns: 640 operations a (query, key) pair,
+// against 512 bytes of K and V a key and head that a tile of 256 queries shares.
+// It is bound by the tensor cores.
+//
+// A CTA takes 256 queries of one head, as two tiles of 128 that alternate: while
+// one tile's softmax runs, the other tile's products do.  A step of 128 keys costs
+// the tensor cores 12 products of 128 x 128 x 16 for S (64 cycles each) and 16 of
+// 128 x 64 x 16 for O (32 cycles) a tile: 2,560 cycles for both.  Tensor memory
+// holds S of both tiles (a tile's weights overwrite its scores, bf16, and are read
+// from there as the A operand) and O of both: all 512 columns.  Shared memory holds
+// Q of both (96 KB) and a ring of eight 16 KB slots (128 keys x 64 columns) through
+// which K (three slots a step) and V (two) pass in the order of their use.
+//
+// Softmax: one thread a row, one pass, with a running reference that moves only
+// when the maximum has grown by 2^8 (O is then rescaled in tensor memory).
+//
+// The kernel is persistent.  Work items are ordered so that the CTAs at work share
+// the K and V of few heads (two rounds of items a group of heads), longest first
+// within a group, and dealt out in turns that change direction, so that each CTA
+// gets long and short ones.
+//
+// Roles of a CTA's twelve warps: 0-3 and 4-7 softmax and output of the two tiles; 8
+// issues the products; 9 loads K and V, 10 loads Q (TMA); 11 looks up items.
 #include "latent_internal.cuh"
+#include "umma.cuh"
 
 namespace pfkv {
 namespace {
 
-constexpr int kSimpleRows = 8;
+constexpr int kQTile = 128, kItemRows = 2 * kQTile, kKeys = 128;
+constexpr uint32_t kSlotB = 128 * 128;  // 128 rows of 128 bytes
+constexpr int kSlots = 8, kQChunks = 3;
+constexpr int kStepSlots = 5;           // K: chunks 0 and 1, rotated; V: chunks 0 and 1
+constexpr int kPreThreads = 384;
+constexpr int kItems = 3;               // items looked up ahead
+constexpr uint32_t kOffRing = 2 * kQChunks * kSlotB, kOffPre = kOffRing + kSlots * kSlotB;
+constexpr uint32_t kColO = 256;
+constexpr float kGrowth = 8.f;
+constexpr float kMinusInf = -INFINITY;
 
-__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float *x) {
-    const uint2 w = *reinterpret_cast<const uint2 *>(p);
-    const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
-    x[0] = a.x;
-    x[1] = a.y;
-    x[2] = b.x;
-    x[3] = b.y;
-}
+struct Item {
+    int b, h;        // b < 0: no more
+    int q0, nq;      // the request's first query row, and its queries from this item's first on
+    int k0, nk;      // the request's first key row and key rows
+    int sees0;       // keys that the item's first query sees (each further one sees one more if causal)
+    int n0, n1;      // steps of the two tiles
+};
 
-__global__ void __launch_bounds__(kSimpleRows * 32) latent_prefill_kernel(LatentPrefillArgs a) {
-    pdl_enter();
-    const int b = blockIdx.z, h = blockIdx.y, lane = threadIdx.x & 31;
-    const int q0 = a.q_starts[b], q1 = a.q_starts[b + 1], k0 = a.k_starts[b], k1 = a.k_starts[b + 1];
-    const bool bad = q0 < 0 || q1 < q0 || q1 > a.total_q || k0 < 0 || k1 < k0 || k1 > a.total_k || q1 - q0 > a.max_q_len;
-    if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0 && a.flags) a.flags[b] = bad ? PFKV_FLAG_BAD_LENGTH : 0;
-    if (bad) return;
-    const int i = blockIdx.x * kSimpleRows + (threadIdx.x >> 5);
-    if (i >= q1 - q0) return;
-    const int nk = k1 - k0;
-    const int sees = a.causal ? min(nk, i + 1 + nk - (q1 - q0)) : nk;
-    float q[4], o[4] = {};
-    load4(a.qn.p + (long long)(q0 + i) * a.qn.st + (long long)h * a.qn.sh + lane * 4, q);
-    const __nv_bfloat16 *qr = a.qr.p + (long long)(q0 + i) * a.qr.st + (long long)h * a.qr.sh + 2 * lane;
-    const float r0 = __bfloat162float(qr[0]), r1 = __bfloat162float(qr[1]);
-    float m = -INFINITY, l = 0.f;
-    for (int j = 0; j < sees; ++j) {
-        float k[4], v[4];
-        load4(a.kn.p + (long long)(k0 + j) * a.kn.st + (long long)h * a.kn.sh + lane * 4, k);
-        load4(a.v.p + (long long)(k0 + j) * a.v.st + (long long)h * a.v.sh + lane * 4, v);
-        const __nv_bfloat16 *kr = a.kr.p + (long long)(k0 + j) * a.kr.st + 2 * lane;
-        float s = r0 * __bfloat162float(kr[0]) + r1 * __bfloat162float(kr[1]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s += q[e] * k[e];
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        s *= a.sm_scale;
-        const float mn = fmaxf(m, s), f = __expf(m - mn), w = __expf(s - mn);
-        m = mn;
-        l = l * f + w;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = o[e] * f + w * v[e];
+struct PreMisc {
+    uint64_t full[kSlots], empty[kSlots];
+    uint64_t qfull[2], qempty[2], sfull[2], pready[2], odone[2];
+    uint64_t ifull[kItems], iempty[kItems], drain;
+    Item item[kItems];
+    uint32_t tmem, gave_up;
+};
+constexpr size_t kPreSmem = kOffPre + sizeof(PreMisc);
+static_assert(kPreSmem <= 232448, "shared memory of one CTA");
+
+// How the items are numbered: groups of `pairs` (request, head) pairs; within a
+// group the last tiles of all pairs first.
+struct Deal {
+    int tiles;     // items of the longest request allowed
+    int pairs;     // pairs a group
+    long long items;
+};
+
+__global__ void __launch_bounds__(kPreThreads, 1)
+    latent_prefill_kernel(const __grid_constant__ CUtensorMap mapqn, const __grid_constant__ CUtensorMap mapqr,
+                          const __grid_constant__ CUtensorMap mapkn, const __grid_constant__ CUtensorMap mapkr,
+                          const __grid_constant__ CUtensorMap mapv, LatentPrefillArgs a, Deal deal, uint32_t idS,
+                          int qn_h, int qr_h, int kn_h, int v_h) {
+    extern __shared__ __align__(1024) uint8_t psm[];  // no static shared memory: the window's aligned base
+    PreMisc &m = *reinterpret_cast<PreMisc *>(psm + kOffPre);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(&m.full[i], 1);
+            mbar_init(&m.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&m.qfull[i], 1);
+            mbar_init(&m.qempty[i], 1);
+            mbar_init(&m.sfull[i], 1);
+            mbar_init(&m.pready[i], 4);
+            mbar_init(&m.odone[i], 1);
+        }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&m.ifull[i], 1);
+            mbar_init(&m.iempty[i], 11);  // eight softmax warps and three threads
+        }
+        mbar_init(&m.drain, 1);
+        m.gave_up = (smem_addr(psm) & 1023u) != 0u;  // nothing runs on a base that the swizzle cannot take
+        fence_mbar_init();
     }
-    __nv_bfloat16 *out = a.out.p + (long long)(q0 + i) * a.out.st + (long long)h * a.out.sh + lane * 4;
+    if (warp == 8) tmem_alloc512<1>(&m.tmem);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    pdl_enter();
+    const uint32_t tmem = m.tmem;
+    volatile uint32_t *const gave_up = &m.gave_up;
+    // Waits for item number i of this CTA; false when there is none, or a wait has given up.
+    auto item_ready = [&](int i) {
+        return bar_wait(&m.ifull[i % kItems], (i / kItems) & 1, gave_up) && m.item[i % kItems].b >= 0;
+    };
+
+    if (warp < 8) {
+        // ------------------------- softmax and output -------------------------
+        reg_share_more<208>();
+        const int tile = warp >> 2, r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t cs = lanes + tile * 128, co = lanes + kColO + tile * 128;
+        const float a2 = fmaxf(fabsf(a.sm_scale) * 1.4426950408889634f, 1.1754944e-38f);
+        uint32_t done = 0;   // steps of this tile so far, of all items
+        uint32_t outs = 0;   // items that it had steps in
+        uint32_t base_pos = 0;
+        for (int i = 0; __all_sync(0xffffffffu, item_ready(i)); ++i) {
+            const Item &it = m.item[i % kItems];
+            const int steps = tile ? it.n1 : it.n0, all = max(it.n0, it.n1);
+            const int row = tile * kQTile + r, nk = it.nk, b = it.b;
+            const bool live = row < it.nq;
+            const int sees = a.causal ? min(nk, it.sees0 + row) : nk;
+            float ref = kMinusInf, sum = 0.f;
+            bool ok = true;
+            for (int j = 0; j < steps; ++j, ++done) {
+                ok = bar_wait(&m.sfull[tile], done & 1, gave_up);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tmem_fence_after();
+                float x[4][32];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) out[e] = __float2bfloat16(sees > 0 ? o[e] / l : 0.f);
+                for (int g = 0; g < 4; ++g) tmem_ld32(cs + g * 32, x[g]);
+                tmem_wait_ld();
+                const int seen = sees - j * kKeys;
+                if (__any_sync(0xffffffffu, seen < kKeys)) {
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (g * 32 + e >= seen) x[g][e] = kMinusInf;
+                }
+                float top = kMinusInf;
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) top = fmaxf(top, x[g][e]);
+                top *= a2;
+                float shrink = 1.f;
+                if (top > ref + kGrowth || (ref == kMinusInf && top > kMinusInf)) {
+                    shrink = fast_exp2(ref - top);  // 0 when nothing was seen yet
+                    sum *= shrink;
+                    ref = top;
+                }
+                // the scores are here, so the products before them (O among them) are done
+                if (j > 0 && __any_sync(0xffffffffu, shrink != 1.f)) {
+#pragma unroll 1
+                    for (int g = 0; g < 8; ++g) {
+                        float o[16];
+                        tmem_ld16(co + g * 16, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] *= shrink;
+                        tmem_st16(co + g * 16, o);
+                    }
+                }
+                const float base = ref == kMinusInf ? 0.f : -ref;
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    float w[16];  // packed pairs
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(fast_exp2(fmaf(x[g][e], a2, base)),
+                                                                       fast_exp2(fmaf(x[g][e + 1], a2, base)));
+                        const float2 f = __bfloat1622float2(h);
+                        sum += f.x + f.y;
+                        w[e >> 1] = __uint_as_float(*reinterpret_cast<const uint32_t *>(&h));
+                    }
+                    tmem_st16(cs + g * 16, w);
+                }
+                if (nk - j * kKeys < kKeys) {
+                    // key rows past the request's last may hold anything, NaN among it, and
+                    // meet weights of zero: V's are zeroed where they lie
+                    const int valid = nk - j * kKeys;
+#pragma unroll 1
+                    for (int c = 0; c < 2; ++c) {
+                        const uint32_t pos = base_pos + j * kStepSlots + 3 + c;
+                        ok = bar_wait(&m.full[pos % kSlots], (pos / kSlots) & 1, gave_up) && ok;
+                        uint4 *v = reinterpret_cast<uint4 *>(psm + kOffRing + (pos % kSlots) * kSlotB);
+                        for (int e = valid * 8 + r; e < kKeys * 8; e += kQTile) v[e] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                }
+                tmem_wait_st();
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&m.pready[tile]);
+            }
+            if (steps > 0) {
+                ok = bar_wait(&m.odone[tile], outs++ & 1, gave_up) && ok;
+                tmem_fence_after();
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            const float inv = sum > 0.f ? __fdiv_rn(1.f, sum) : sum;  // zero and NaN stay
+            __nv_bfloat16 *out = a.out.p + (long long)(it.q0 + row) * a.out.st + (long long)it.h * a.out.sh;
+#pragma unroll 1
+            for (int g = 0; g < 4; ++g) {
+                float o[32];
+                if (steps > 0) {
+                    tmem_ld32(co + g * 32, o);
+                    tmem_wait_ld();
+                }
+                if (!live || !ok) continue;
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    uint32_t u[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        // a row that sees no key is zero
+                        const float lo = sum == 0.f ? 0.f : o[e + 2 * k] * inv, hi = sum == 0.f ? 0.f : o[e + 2 * k + 1] * inv;
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+                        u[k] = *reinterpret_cast<const uint32_t *>(&h);
+                    }
+                    *reinterpret_cast<uint4 *>(out + g * 32 + e) = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+            }
+            if (!ok && lane == 0 && a.flags) atomic_or_byte(a.flags, b, PFKV_FLAG_DEVICE_TIMEOUT);
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&m.iempty[i % kItems]);
+            if (!ok) break;
+            base_pos += all * kStepSlots;
+        }
+    } else if (warp == 8) {
+        // ------------------------------ products ------------------------------
+        reg_share_less<80>();
+        if (elect_one()) {
+            constexpr uint32_t idO = umma_idesc(kQTile, 64, true, false, true);
+            const uint32_t qa = smem_addr(psm), ra = qa + kOffRing;
+            // parities: bit `tile` of each word (no arrays: they would live in memory)
+            uint32_t weighed = 0, queried = 0, base_pos = 0;
+            bool ok = true;
+            for (int i = 0; ok && item_ready(i); ++i) {
+                const int n0 = m.item[i % kItems].n0, n1 = m.item[i % kItems].n1, n = max(n0, n1);
+                bar_arrive(&m.iempty[i % kItems]);
+                // step j of a tile: O of step j - 1, then S of step j
+#pragma unroll 1
+                for (int x = 0; x < 2 * (n + 1) && ok; ++x) {
+                    const int j = x >> 1, tile = x & 1, mine = tile ? n1 : n0;
+                    if (j > 0 && j <= mine) {
+                        const bool last_use = tile == 1 || j - 1 >= n1;
+                        ok = bar_wait(&m.pready[tile], (weighed >> tile) & 1, gave_up);
+                        weighed ^= 1u << tile;
+#pragma unroll 1
+                        for (int c = 0; c < 2; ++c) {
+                            const uint32_t pos = base_pos + (j - 1) * kStepSlots + 3 + c, slot = pos % kSlots;
+                            ok = bar_wait(&m.full[slot], (pos / kSlots) & 1, gave_up) && ok;
+                            if (!ok) break;
+                            tmem_fence_after();
+                            const uint64_t db = umma_desc(ra + slot * kSlotB, 16, 1024);
+#pragma unroll
+                            for (int s = 0; s < 8; ++s)
+                                umma_ts(tmem + kColO + tile * 128 + c * 64, tmem + tile * 128 + s * 8, db + s * 128, idO, j > 1 || s > 0);
+                            if (last_use) umma_commit(&m.empty[slot]);
+                        }
+                        if (ok && j == mine) umma_commit(&m.odone[tile]);
+                    }
+                    if (ok && j < mine) {
+                        const bool last_use = tile == 1 || j >= n1;
+                        if (j == 0) {
+                            ok = bar_wait(&m.qfull[tile], (queried >> tile) & 1, gave_up);
+                            queried ^= 1u << tile;
+                        }
+#pragma unroll 1
+                        for (int c = 0; c < kQChunks; ++c) {
+                            const uint32_t pos = base_pos + j * kStepSlots + c, slot = pos % kSlots;
+                            ok = bar_wait(&m.full[slot], (pos / kSlots) & 1, gave_up) && ok;
+                            if (!ok) break;
+                            tmem_fence_after();
+                            const uint64_t da = umma_desc(qa + (tile * kQChunks + c) * kSlotB, 16, 1024);
+                            const uint64_t db = umma_desc(ra + slot * kSlotB, 16, 1024);
+#pragma unroll
+                            for (int s = 0; s < 4; ++s) umma_ss<1>(tmem + tile * 128, da + 2 * s, db + 2 * s, idS, c > 0 || s > 0);
+                            if (last_use) umma_commit(&m.empty[slot]);
+                        }
+                        if (ok) {
+                            umma_commit(&m.sfull[tile]);
+                            if (j + 1 == mine) umma_commit(&m.qempty[tile]);
+                        }
+                    }
+                }
+                base_pos += n * kStepSlots;
+            }
+            // nothing in flight when the CTA leaves
+            umma_commit(&m.drain);
+            bar_drain(&m.drain, 0);
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // ------------------------------ K and V ------------------------------
+        reg_share_less<80>();
+        if (elect_one()) {
+            const uint64_t pol = l2_policy_evict_normal();
+            uint32_t pos = 0;
+            bool ok = true;
+            for (int i = 0; ok && item_ready(i); ++i) {
+                const int n = max(m.item[i % kItems].n0, m.item[i % kItems].n1);
+                const int h = m.item[i % kItems].h, k0 = m.item[i % kItems].k0;
+                bar_arrive(&m.iempty[i % kItems]);
+                for (int j = 0; ok && j < n; ++j)
+#pragma unroll 1
+                    for (int c = 0; c < kStepSlots; ++c, ++pos) {
+                        ok = bar_wait(&m.empty[pos % kSlots], ((pos / kSlots) & 1) ^ 1, gave_up);
+                        if (!ok) break;
+                        uint64_t *full = &m.full[pos % kSlots];
+                        uint8_t *dst = psm + kOffRing + (pos % kSlots) * kSlotB;
+                        const int y = k0 + j * kKeys;
+                        mbar_arrive_expect_tx(full, kSlotB);
+                        if (c < 2) tma_box3(dst, &mapkn, c * 64, kn_h ? h : 0, y, full, pol);
+                        else if (c == 2) tma_box3(dst, &mapkr, 0, 0, y, full, pol);
+                        else tma_box3(dst, &mapv, (c - 3) * 64, v_h ? h : 0, y, full, pol);
+                    }
+            }
+            if (*gave_up) {  // copies in flight are left time to land
+                const unsigned long long t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < kWaitLimitNs) {}
+            }
+        }
+        __syncwarp();
+    } else if (warp == 10) {
+        // --------------------------------- Q ---------------------------------
+        reg_share_less<80>();
+        if (elect_one()) {
+            const uint64_t pol = l2_policy_evict_first();
+            uint32_t used = 0;  // parities: bit `tile`
+            bool ok = true;
+            for (int i = 0; ok && item_ready(i); ++i) {
+                const int n0 = m.item[i % kItems].n0, n1 = m.item[i % kItems].n1;
+                const int h = m.item[i % kItems].h, q0 = m.item[i % kItems].q0;
+                bar_arrive(&m.iempty[i % kItems]);
+#pragma unroll 1
+                for (int tile = 0; tile < 2; ++tile) {
+                    if ((tile ? n1 : n0) == 0 || !ok) continue;
+                    ok = bar_wait(&m.qempty[tile], ((used >> tile) & 1) ^ 1, gave_up);
+                    used ^= 1u << tile;
+                    if (!ok) continue;
+                    uint64_t *full = &m.qfull[tile];
+                    uint8_t *dst = psm + tile * kQChunks * kSlotB;
+                    const int y = q0 + tile * kQTile;
+                    mbar_arrive_expect_tx(full, kQChunks * kSlotB);
+                    tma_box3(dst, &mapqn, 0, qn_h ? h : 0, y, full, pol);
+                    tma_box3(dst + kSlotB, &mapqn, 64, qn_h ? h : 0, y, full, pol);
+                    tma_box3(dst + 2 * kSlotB, &mapqr, 0, qr_h ? h : 0, y, full, pol);
+                }
+            }
+            if (*gave_up) {
+                const unsigned long long t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < kWaitLimitNs) {}
+            }
+        }
+        __syncwarp();
+    } else {
+        // -------------------------- items, and the flags --------------------------
+        reg_share_less<80>();
+        auto range = [&](int b, int &q0, int &nq, int &k0, int &nk) {
+            q0 = a.q_starts[b];
+            const int q1 = a.q_starts[b + 1], k1 = a.k_starts[b + 1];
+            k0 = a.k_starts[b];
+            nq = q1 - q0;
+            nk = k1 - k0;
+            return q0 >= 0 && q1 >= q0 && q1 <= a.total_q && k0 >= 0 && k1 >= k0 && k1 <= a.total_k && nq <= a.max_q_len;
+        };
+        int q0, nq, k0, nk;
+        if (a.flags)
+            for (int b = blockIdx.x * 32 + lane; b < a.B; b += gridDim.x * 32)
+                a.flags[b] = range(b, q0, nq, k0, nk) ? 0 : PFKV_FLAG_BAD_LENGTH;
+        if (lane == 0) {
+            int i = 0;
+            bool ok = true;
+            auto publish = [&](const Item &it) {
+                ok = bar_wait(&m.iempty[i % kItems], ((i / kItems) & 1) ^ 1, gave_up);
+                if (!ok) return;
+                m.item[i % kItems] = it;
+                bar_arrive(&m.ifull[i % kItems]);
+                ++i;
+            };
+            for (long long turn = 0; ok; ++turn) {
+                const long long x = turn * gridDim.x + ((turn & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+                if (turn * gridDim.x >= deal.items) break;
+                if (x >= deal.items) continue;
+                const long long group = x / ((long long)deal.pairs * deal.tiles);
+                const int in_group = (int)(x - group * deal.pairs * deal.tiles);
+                const int t = deal.tiles - 1 - in_group / deal.pairs;
+                const long long pair = group * deal.pairs + in_group % deal.pairs;
+                if (pair >= (long long)a.B * a.H) continue;
+                Item it;
+                it.b = (int)(pair / a.H);
+                it.h = (int)(pair - (long long)it.b * a.H);
+                if (!range(it.b, q0, nq, k0, nk) || t * kItemRows >= nq) continue;
+                it.q0 = q0 + t * kItemRows;
+                it.nq = nq - t * kItemRows;
+                it.k0 = k0;
+                it.nk = nk;
+                it.sees0 = nk - nq + 1 + t * kItemRows;
+                auto steps = [&](int tile) {
+                    const int rows = min(kQTile, it.nq - tile * kQTile);
+                    const int most = a.causal ? min(nk, it.sees0 + tile * kQTile + rows - 1) : nk;
+                    return rows > 0 && most > 0 ? (most + kKeys - 1) / kKeys : 0;
+                };
+                it.n0 = steps(0);
+                it.n1 = steps(1);
+                publish(it);
+            }
+            Item end{};
+            end.b = -1;
+            if (ok) publish(end);
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == 8) tmem_free512<1>(tmem);
 }
 
 }  // namespace
 
-cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, int, cudaStream_t s) {
-    if (a.B > 65535) return cudaErrorInvalidValue;
-    const unsigned tiles = (unsigned)max(1, (a.max_q_len + kSimpleRows - 1) / kSimpleRows);
-    return launch_pdl(latent_prefill_kernel, dim3(tiles, a.H, a.B), dim3(kSimpleRows * 32), 0, s, a);
+cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, int num_sms, cudaStream_t s) {
+    CUtensorMap qn{}, qr{}, kn{}, kr{}, v{};
+    // [rows][heads][width]; heads that share a row (stride 0), and a single head, are one
+    auto map = [](CUtensorMap *m, const RowsArg &r, int width, int heads, long long rows, int *per_head) {
+        *per_head = heads > 1 && r.sh > 0;
+        const uint64_t h = *per_head ? heads : 1;
+        return bf16_map3(m, r.p, width, h, rows, *per_head ? r.sh : 8, r.st > 0 ? r.st : 8, 1, 128);
+    };
+    int qn_h = 0, qr_h = 0, kn_h = 0, v_h = 0, one = 0;
+    cudaError_t e = cudaSuccess;
+    if (a.total_q > 0 && a.total_k > 0) {
+        e = map(&qn, a.qn, PFKV_LATENT_NOPE, a.H, a.total_q, &qn_h);
+        if (e == cudaSuccess) e = map(&qr, a.qr, PFKV_LATENT_ROPE, a.H, a.total_q, &qr_h);
+        if (e == cudaSuccess) e = map(&kn, a.kn, PFKV_LATENT_NOPE, a.H, a.total_k, &kn_h);
+        if (e == cudaSuccess) e = map(&kr, a.kr, PFKV_LATENT_ROPE, 1, a.total_k, &one);
+        if (e == cudaSuccess) e = map(&v, a.v, PFKV_LATENT_VDIM, a.H, a.total_k, &v_h);
+        if (e != cudaSuccess) return e;
+    }
+    Deal d;
+    d.tiles = a.total_q > 0 ? (int)(((long long)a.max_q_len + kItemRows - 1) / kItemRows) : 0;
+    const long long pairs = (long long)a.B * a.H;
+    d.pairs = (int)min(pairs, d.tiles > 0 ? (2LL * num_sms + d.tiles - 1) / d.tiles : 1LL);
+    d.items = (pairs + d.pairs - 1) / d.pairs * d.pairs * d.tiles;
+    const unsigned grid = (unsigned)max(1LL, min(d.items, (long long)num_sms));
+    // a negative scale is the operands' sign: the softmax works with its magnitude
+    const uint32_t idS = umma_idesc(kQTile, kKeys, true, false, false) | (a.sm_scale < 0.f ? 1u << 13 : 0u);
+    return launch_pdl(latent_prefill_kernel, dim3(grid), dim3(kPreThreads), kPreSmem, s, qn, qr, kn, kr, v, a, d, idS,
+                      qn_h, qr_h, kn_h, v_h);
 }
 
-cudaError_t preload_latent_prefill() { return preload_kernel(latent_prefill_kernel); }
+cudaError_t preload_latent_prefill() {
+    const cudaError_t e =
+        cudaFuncSetAttribute(latent_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPreSmem);
+    return e == cudaSuccess ? preload_kernel(latent_prefill_kernel) : e;
+}
 
 }  // namespace pfkv
