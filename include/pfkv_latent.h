@@ -168,8 +168,8 @@ pfkv_status pfkv_latent_decode_attn(const pfkv_latent_cache *cache, const pfkv_p
  * A query that sees no key gives a zero row.  A request whose rows are not
  * within the arrays is flagged and nothing of it is written.  Rows outside every
  * request's range are left as they were.  Arithmetic: tensor cores with fp32
- * accumulation, softmax statistics in fp32, a weight rounded once to bf16, the
- * weights' sum of the rounded weights.
+ * accumulation, softmax statistics in fp32, a weight rounded once to bf16 where it
+ * enters the second product.
  */
 pfkv_status pfkv_latent_prefill_attn(int32_t batch, int32_t num_heads, const int32_t *q_starts,
                                      const int32_t *k_starts, int64_t total_q, int64_t total_k,

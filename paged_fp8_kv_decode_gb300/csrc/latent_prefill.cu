@@ -142,12 +142,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                         for (int e = 0; e < 32; ++e)
                             if (g * 32 + e >= seen) x[g][e] = kMinusInf;
                 }
-                float top = kMinusInf;
+                float tops[4] = {kMinusInf, kMinusInf, kMinusInf, kMinusInf};  // four chains, not one
 #pragma unroll
-                for (int g = 0; g < 4; ++g)
+                for (int e = 0; e < 32; e += 2)
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) top = fmaxf(top, x[g][e]);
-                top *= a2;
+                    for (int g = 0; g < 4; ++g) tops[g] = fmaxf(tops[g], fmaxf(x[g][e], x[g][e + 1]));
+                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * a2;
                 float shrink = 1.f;
                 if (top > ref + kGrowth || (ref == kMinusInf && top > kMinusInf)) {
                     shrink = fast_exp2(ref - top);  // 0 when nothing was seen yet
@@ -167,19 +167,23 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                     }
                 }
                 const float base = ref == kMinusInf ? 0.f : -ref;
+                const float2 scale2 = make_float2(a2, a2), base2 = make_float2(base, base);
+                float2 sums[4] = {};
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     float w[16];  // packed pairs
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(fast_exp2(fmaf(x[g][e], a2, base)),
-                                                                       fast_exp2(fmaf(x[g][e + 1], a2, base)));
-                        const float2 f = __bfloat1622float2(h);
-                        sum += f.x + f.y;
+                        float2 y = fma2(make_float2(x[g][e], x[g][e + 1]), scale2, base2);
+                        y = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                        sums[(e >> 1) & 3] = add2(sums[(e >> 1) & 3], y);
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(y.x, y.y);
                         w[e >> 1] = __uint_as_float(*reinterpret_cast<const uint32_t *>(&h));
                     }
                     tmem_st16(cs + g * 16, w);
                 }
+                const float2 s2 = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
+                sum += s2.x + s2.y;
                 if (nk - j * kKeys < kKeys) {
                     // key rows past the request's last may hold anything, NaN among it, and
                     // meet weights of zero: V's are zeroed where they lie
