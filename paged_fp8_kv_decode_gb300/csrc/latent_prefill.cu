@@ -33,11 +33,12 @@ namespace {
 
 constexpr int kQTile = 128, kItemRows = 2 * kQTile, kKeys = 128;
 constexpr uint32_t kSlotB = 128 * 128;  // 128 rows of 128 bytes
-constexpr int kSlots = 8, kQChunks = 3;
-constexpr int kStepSlots = 5;           // K: chunks 0 and 1, rotated; V: chunks 0 and 1
+constexpr int kKSlots = 4, kKChunks = 3;  // K: chunks 0 and 1, rotated
+constexpr int kVSlots = 2;                // V: both chunks
 constexpr int kPreThreads = 384;
 constexpr int kItems = 3;               // items looked up ahead
-constexpr uint32_t kOffRing = 2 * kQChunks * kSlotB, kOffPre = kOffRing + kSlots * kSlotB;
+constexpr uint32_t kOffK = 2 * kKChunks * kSlotB, kOffV = kOffK + kKSlots * kSlotB;
+constexpr uint32_t kOffPre = kOffV + kVSlots * 2 * kSlotB;
 constexpr uint32_t kColO = 256;
 constexpr float kGrowth = 8.f;
 constexpr float kMinusInf = -INFINITY;
@@ -51,8 +52,8 @@ struct Item {
 };
 
 struct PreMisc {
-    uint64_t full[kSlots], empty[kSlots];
-    uint64_t qfull[2], qempty[2], sfull[2], pready[2], odone[2];
+    uint64_t kfull[kKSlots], kempty[kKSlots], vfull[kVSlots], vempty[kVSlots];
+    uint64_t qfull[2], qempty[2], sfull[2], pready[2][2], odone[2];
     uint64_t ifull[kItems], iempty[kItems], drain;
     Item item[kItems];
     uint32_t tmem, gave_up;
@@ -77,15 +78,20 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     PreMisc &m = *reinterpret_cast<PreMisc *>(psm + kOffPre);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
-        for (int i = 0; i < kSlots; ++i) {
-            mbar_init(&m.full[i], 1);
-            mbar_init(&m.empty[i], 1);
+        for (int i = 0; i < kKSlots; ++i) {
+            mbar_init(&m.kfull[i], 1);
+            mbar_init(&m.kempty[i], 1);
+        }
+        for (int i = 0; i < kVSlots; ++i) {
+            mbar_init(&m.vfull[i], 1);
+            mbar_init(&m.vempty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&m.qfull[i], 1);
             mbar_init(&m.qempty[i], 1);
             mbar_init(&m.sfull[i], 1);
-            mbar_init(&m.pready[i], 4);
+            mbar_init(&m.pready[i][0], 4);
+            mbar_init(&m.pready[i][1], 4);
             mbar_init(&m.odone[i], 1);
         }
         for (int i = 0; i < kItems; ++i) {
@@ -166,41 +172,46 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                         tmem_st16(co + g * 16, o);
                     }
                 }
-                const float base = ref == kMinusInf ? 0.f : -ref;
-                const float2 scale2 = make_float2(a2, a2), base2 = make_float2(base, base);
-                float2 sums[4] = {};
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    float w[16];  // packed pairs
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        float2 y = fma2(make_float2(x[g][e], x[g][e + 1]), scale2, base2);
-                        y = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-                        sums[(e >> 1) & 3] = add2(sums[(e >> 1) & 3], y);
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(y.x, y.y);
-                        w[e >> 1] = __uint_as_float(*reinterpret_cast<const uint32_t *>(&h));
-                    }
-                    tmem_st16(cs + g * 16, w);
-                }
-                const float2 s2 = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
-                sum += s2.x + s2.y;
                 if (nk - j * kKeys < kKeys) {
                     // key rows past the request's last may hold anything, NaN among it, and
                     // meet weights of zero: V's are zeroed where they lie
-                    const int valid = nk - j * kKeys;
+                    const uint32_t pos = base_pos + j;
+                    ok = bar_wait(&m.vfull[pos % kVSlots], (pos / kVSlots) & 1, gave_up);
+                    uint4 *v = reinterpret_cast<uint4 *>(psm + kOffV + (pos % kVSlots) * 2 * kSlotB);
 #pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        const uint32_t pos = base_pos + j * kStepSlots + 3 + c;
-                        ok = bar_wait(&m.full[pos % kSlots], (pos / kSlots) & 1, gave_up) && ok;
-                        uint4 *v = reinterpret_cast<uint4 *>(psm + kOffRing + (pos % kSlots) * kSlotB);
-                        for (int e = valid * 8 + r; e < kKeys * 8; e += kQTile) v[e] = make_uint4(0u, 0u, 0u, 0u);
+                    for (int e = (nk - j * kKeys) * 8 + r; e < kKeys * 8; e += kQTile) {
+                        v[e] = make_uint4(0u, 0u, 0u, 0u);
+                        v[e + kSlotB / 16] = make_uint4(0u, 0u, 0u, 0u);
                     }
                     fence_proxy_async_smem();
                 }
-                tmem_wait_st();
-                tmem_fence_before();
-                __syncwarp();
-                if (lane == 0) bar_arrive(&m.pready[tile]);
+                const float base = ref == kMinusInf ? 0.f : -ref;
+                const float2 scale2 = make_float2(a2, a2), base2 = make_float2(base, base);
+                float2 sums[4] = {};
+                // the weights of 64 keys at a time: the products with the first half's V start
+                // while the second half is computed
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                    for (int g = 2 * half; g < 2 * half + 2; ++g) {
+                        float w[16];  // packed pairs
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float2 y = fma2(make_float2(x[g][e], x[g][e + 1]), scale2, base2);
+                            y = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                            sums[(e >> 1) & 3] = add2(sums[(e >> 1) & 3], y);
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(y.x, y.y);
+                            w[e >> 1] = __uint_as_float(*reinterpret_cast<const uint32_t *>(&h));
+                        }
+                        tmem_st16(cs + g * 16, w);
+                    }
+                    tmem_wait_st();
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&m.pready[tile][half]);
+                }
+                const float2 s2 = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
+                sum += s2.x + s2.y;
             }
             if (steps > 0) {
                 ok = bar_wait(&m.odone[tile], outs++ & 1, gave_up) && ok;
@@ -235,67 +246,86 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             __syncwarp();
             if (lane == 0) bar_arrive(&m.iempty[i % kItems]);
             if (!ok) break;
-            base_pos += all * kStepSlots;
+            base_pos += all;
         }
     } else if (warp == 8) {
         // ------------------------------ products ------------------------------
-        reg_share_less<80>();
+        reg_share_less<88>();
         if (elect_one()) {
-            constexpr uint32_t idO = umma_idesc(kQTile, 64, true, false, true);
-            const uint32_t qa = smem_addr(psm), ra = qa + kOffRing;
+            constexpr uint32_t idO = umma_idesc(kQTile, 128, true, false, true);
+            const uint32_t qa = smem_addr(psm), ka = qa + kOffK, va = qa + kOffV;
             // parities: bit `tile` of each word (no arrays: they would live in memory)
-            uint32_t weighed = 0, queried = 0, base_pos = 0;
+            uint32_t weighed = 0, queried = 0, base_pos = 0, kpos = 0;
             bool ok = true;
+            bool weights = false, values = false;  // the next tile's barriers, asked ahead
             for (int i = 0; ok && item_ready(i); ++i) {
                 const int n0 = m.item[i % kItems].n0, n1 = m.item[i % kItems].n1, n = max(n0, n1);
                 bar_arrive(&m.iempty[i % kItems]);
-                // step j of a tile: O of step j - 1, then S of step j
+                // step j of a tile: O of step j - 1, then S of step j.  K and V are waited for
+                // where the first tile of the two uses them, and released by the last.
 #pragma unroll 1
                 for (int x = 0; x < 2 * (n + 1) && ok; ++x) {
-                    const int j = x >> 1, tile = x & 1, mine = tile ? n1 : n0;
+                    const int j = x >> 1, tile = x & 1, mine = tile ? n1 : n0, other = tile ? n0 : n1;
+                    const bool scores = j < mine, first = tile == 0 || j >= n0, last = tile == 1 || j >= n1;
+                    bool keys = scores && first && bar_passed(&m.kfull[kpos % kKSlots], (kpos / kKSlots) & 1);
                     if (j > 0 && j <= mine) {
-                        const bool last_use = tile == 1 || j - 1 >= n1;
-                        ok = bar_wait(&m.pready[tile], (weighed >> tile) & 1, gave_up);
-                        weighed ^= 1u << tile;
-#pragma unroll 1
-                        for (int c = 0; c < 2; ++c) {
-                            const uint32_t pos = base_pos + (j - 1) * kStepSlots + 3 + c, slot = pos % kSlots;
-                            ok = bar_wait(&m.full[slot], (pos / kSlots) & 1, gave_up) && ok;
-                            if (!ok) break;
-                            tmem_fence_after();
-                            const uint64_t db = umma_desc(ra + slot * kSlotB, 16, 1024);
+                        const uint32_t pos = base_pos + j - 1, slot = pos % kVSlots, parity = (weighed >> tile) & 1;
+                        ok = weights || bar_wait(&m.pready[tile][0], parity, gave_up);
+                        if (tile == 0 || j > n0) ok = (values || bar_wait(&m.vfull[slot], (pos / kVSlots) & 1, gave_up)) && ok;
+                        if (!ok) break;
+                        const bool rest = bar_passed(&m.pready[tile][1], parity);
+                        tmem_fence_after();
+                        const uint64_t db = umma_desc(va + slot * 2 * kSlotB, kSlotB, 1024);
 #pragma unroll
-                            for (int s = 0; s < 8; ++s)
-                                umma_ts(tmem + kColO + tile * 128 + c * 64, tmem + tile * 128 + s * 8, db + s * 128, idO, j > 1 || s > 0);
-                            if (last_use) umma_commit(&m.empty[slot]);
-                        }
-                        if (ok && j == mine) umma_commit(&m.odone[tile]);
+                        for (int s = 0; s < 4; ++s)
+                            umma_ts(tmem + kColO + tile * 128, tmem + tile * 128 + s * 8, db + s * 128, idO, j > 1 || s > 0);
+                        ok = rest || bar_wait(&m.pready[tile][1], parity, gave_up);
+                        weighed ^= 1u << tile;
+                        if (!ok) break;
+                        tmem_fence_after();
+#pragma unroll
+                        for (int s = 4; s < 8; ++s)
+                            umma_ts(tmem + kColO + tile * 128, tmem + tile * 128 + s * 8, db + s * 128, idO, true);
+                        if (tile == 1 || j > n1) umma_commit(&m.vempty[slot]);
+                        if (j == mine) umma_commit(&m.odone[tile]);
                     }
-                    if (ok && j < mine) {
-                        const bool last_use = tile == 1 || j >= n1;
+                    weights = values = false;
+                    if (scores) {
                         if (j == 0) {
                             ok = bar_wait(&m.qfull[tile], (queried >> tile) & 1, gave_up);
                             queried ^= 1u << tile;
                         }
+                        uint32_t at = first ? kpos : kpos - kKChunks;
 #pragma unroll 1
-                        for (int c = 0; c < kQChunks; ++c) {
-                            const uint32_t pos = base_pos + j * kStepSlots + c, slot = pos % kSlots;
-                            ok = bar_wait(&m.full[slot], (pos / kSlots) & 1, gave_up) && ok;
+                        for (int c = 0; c < kKChunks; ++c, ++at) {
+                            const uint32_t slot = at % kKSlots;
+                            ok = (!first || keys || bar_wait(&m.kfull[slot], (at / kKSlots) & 1, gave_up)) && ok;
                             if (!ok) break;
-                            tmem_fence_after();
-                            const uint64_t da = umma_desc(qa + (tile * kQChunks + c) * kSlotB, 16, 1024);
-                            const uint64_t db = umma_desc(ra + slot * kSlotB, 16, 1024);
+                            if (c + 1 < kKChunks) {
+                                keys = first && bar_passed(&m.kfull[(at + 1) % kKSlots], ((at + 1) / kKSlots) & 1);
+                            } else {
+                                const int jn = (x + 1) >> 1;  // step of the next tile
+                                if (jn > 0 && jn <= other) {
+                                    weights = bar_passed(&m.pready[tile ^ 1][0], (weighed >> (tile ^ 1)) & 1);
+                                    const uint32_t pos = base_pos + jn - 1;
+                                    values = bar_passed(&m.vfull[pos % kVSlots], (pos / kVSlots) & 1);
+                                }
+                            }
+                            const uint64_t da = umma_desc(qa + (tile * kKChunks + c) * kSlotB, 16, 1024);
+                            const uint64_t db = umma_desc(ka + slot * kSlotB, 16, 1024);
 #pragma unroll
                             for (int s = 0; s < 4; ++s) umma_ss<1>(tmem + tile * 128, da + 2 * s, db + 2 * s, idS, c > 0 || s > 0);
-                            if (last_use) umma_commit(&m.empty[slot]);
+                            if (last) umma_commit(&m.kempty[slot]);
                         }
+                        if (first) kpos += kKChunks;
                         if (ok) {
                             umma_commit(&m.sfull[tile]);
                             if (j + 1 == mine) umma_commit(&m.qempty[tile]);
                         }
                     }
                 }
-                base_pos += n * kStepSlots;
+                base_pos += n;
+                weights = values = false;
             }
             // nothing in flight when the CTA leaves
             umma_commit(&m.drain);
@@ -304,28 +334,35 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         __syncwarp();
     } else if (warp == 9) {
         // ------------------------------ K and V ------------------------------
-        reg_share_less<80>();
+        reg_share_less<88>();
         if (elect_one()) {
             const uint64_t pol = l2_policy_evict_normal();
-            uint32_t pos = 0;
+            uint32_t kpos = 0, vpos = 0;
             bool ok = true;
             for (int i = 0; ok && item_ready(i); ++i) {
                 const int n = max(m.item[i % kItems].n0, m.item[i % kItems].n1);
                 const int h = m.item[i % kItems].h, k0 = m.item[i % kItems].k0;
                 bar_arrive(&m.iempty[i % kItems]);
-                for (int j = 0; ok && j < n; ++j)
+                for (int j = 0; ok && j < n; ++j, ++vpos) {
+                    const int y = k0 + j * kKeys;
 #pragma unroll 1
-                    for (int c = 0; c < kStepSlots; ++c, ++pos) {
-                        ok = bar_wait(&m.empty[pos % kSlots], ((pos / kSlots) & 1) ^ 1, gave_up);
+                    for (int c = 0; ok && c < kKChunks; ++c, ++kpos) {
+                        const uint32_t slot = kpos % kKSlots;
+                        ok = bar_wait(&m.kempty[slot], ((kpos / kKSlots) & 1) ^ 1, gave_up);
                         if (!ok) break;
-                        uint64_t *full = &m.full[pos % kSlots];
-                        uint8_t *dst = psm + kOffRing + (pos % kSlots) * kSlotB;
-                        const int y = k0 + j * kKeys;
-                        mbar_arrive_expect_tx(full, kSlotB);
-                        if (c < 2) tma_box3(dst, &mapkn, c * 64, kn_h ? h : 0, y, full, pol);
-                        else if (c == 2) tma_box3(dst, &mapkr, 0, 0, y, full, pol);
-                        else tma_box3(dst, &mapv, (c - 3) * 64, v_h ? h : 0, y, full, pol);
+                        uint8_t *dst = psm + kOffK + slot * kSlotB;
+                        mbar_arrive_expect_tx(&m.kfull[slot], kSlotB);
+                        if (c < 2) tma_box3(dst, &mapkn, c * 64, kn_h ? h : 0, y, &m.kfull[slot], pol);
+                        else tma_box3(dst, &mapkr, 0, 0, y, &m.kfull[slot], pol);
                     }
+                    const uint32_t slot = vpos % kVSlots;
+                    ok = ok && bar_wait(&m.vempty[slot], ((vpos / kVSlots) & 1) ^ 1, gave_up);
+                    if (!ok) break;
+                    uint8_t *dst = psm + kOffV + slot * 2 * kSlotB;
+                    mbar_arrive_expect_tx(&m.vfull[slot], 2 * kSlotB);
+                    tma_box3(dst, &mapv, 0, v_h ? h : 0, y, &m.vfull[slot], pol);
+                    tma_box3(dst + kSlotB, &mapv, 64, v_h ? h : 0, y, &m.vfull[slot], pol);
+                }
             }
             if (*gave_up) {  // copies in flight are left time to land
                 const unsigned long long t0 = globaltimer_ns();
@@ -335,7 +372,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         __syncwarp();
     } else if (warp == 10) {
         // --------------------------------- Q ---------------------------------
-        reg_share_less<80>();
+        reg_share_less<88>();
         if (elect_one()) {
             const uint64_t pol = l2_policy_evict_first();
             uint32_t used = 0;  // parities: bit `tile`
@@ -351,9 +388,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                     used ^= 1u << tile;
                     if (!ok) continue;
                     uint64_t *full = &m.qfull[tile];
-                    uint8_t *dst = psm + tile * kQChunks * kSlotB;
+                    uint8_t *dst = psm + tile * kKChunks * kSlotB;
                     const int y = q0 + tile * kQTile;
-                    mbar_arrive_expect_tx(full, kQChunks * kSlotB);
+                    mbar_arrive_expect_tx(full, kKChunks * kSlotB);
                     tma_box3(dst, &mapqn, 0, qn_h ? h : 0, y, full, pol);
                     tma_box3(dst + kSlotB, &mapqn, 64, qn_h ? h : 0, y, full, pol);
                     tma_box3(dst + 2 * kSlotB, &mapqr, 0, qr_h ? h : 0, y, full, pol);
@@ -367,7 +404,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         __syncwarp();
     } else {
         // -------------------------- items, and the flags --------------------------
-        reg_share_less<80>();
+        reg_share_less<88>();
         auto range = [&](int b, int &q0, int &nq, int &k0, int &nk) {
             q0 = a.q_starts[b];
             const int q1 = a.q_starts[b + 1], k1 = a.k_starts[b + 1];

@@ -202,6 +202,20 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatil
     return false;
 }
 
+// Whether the wait would end at once.  A thread that issues matrix products asks this
+// before it issues a group, for the barrier of the next one: an answer is asked for in
+// order behind the products queued so far, and a wait between two groups, satisfied or
+// not, lets the tensor cores run dry for about 140 cycles.
+__device__ __forceinline__ bool bar_passed(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0u;
+}
+
 // The same, however the CTA's other waits went: for work that is in flight.
 __device__ __forceinline__ void bar_drain(uint64_t *bar, uint32_t parity) {
     const unsigned long long t0 = globaltimer_ns();
