@@ -585,12 +585,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t idO = umma_idesc(kRowBlock, 256, !FP8, false, true);
             auto values = [&](int t, bool first) {
                 const bool ok = bar_wait(&m.pready, t & 1, gave_up);
-                const uint64_t da = umma_desc(pa, 16, 1024);
+                const uint32_t da = umma_desc(pa, 16);
 #pragma unroll 1
                 for (int nb = 0; nb < 2; ++nb) {
                     if (!bar_wait(&m.vfull[nb], t & 1, gave_up) || !ok) continue;
                     tmem_fence_after();
-                    const uint64_t db = umma_desc(va + nb * 2 * kVChunkB, kVLbo<FP8>, 1024);
+                    const uint32_t db = umma_desc(va + nb * 2 * kVChunkB, kVLbo<FP8>);
 #pragma unroll
                     for (int s = 0; s < 8; ++s)  // a page a step
                         umma_ss<2>(tmem + nb * 128, da + (s >> 2) * (kChunkB >> 4) + 2 * (s & 3),
@@ -615,10 +615,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the rest of the tile's time.  (Loops over stages stay loops: unrolled, their
                 // descriptors cost the registers that the other roles need.)
                 bool ok = bar_wait(&m.kfull[4], t & 1, gave_up);
-                uint64_t da = umma_desc(qa, 16, 1024), db = umma_desc(ka, 16, 1024);
+                uint32_t da = umma_desc(qa, 16), db = umma_desc(ka, 16);
                 if (ok) {
                     tmem_fence_after();
-                    constexpr uint64_t last = 8 * kChunkB >> 4;
+                    constexpr uint32_t last = 8 * kChunkB >> 4;
 #pragma unroll
                     for (int s = 0; s < 4; ++s)
                         umma_ss<2>(FP8 ? cs + 64 : cs, da + last + 2 * s, db + last + 2 * s, idR, s > 0);
@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_fence_after();
 #pragma unroll
                     for (int s = 0; s < 8; ++s) {
-                        const uint64_t step = (s >> 2) * (kChunkB >> 4) + 2 * (s & 3);
+                        const uint32_t step = (s >> 2) * (kChunkB >> 4) + 2 * (s & 3);
                         umma_ss<2>(cs, da + step, db + step, idS, !FP8 || s > 0 || c > 0);
                     }
                     umma_commit_pair(&m.kempty[c]);

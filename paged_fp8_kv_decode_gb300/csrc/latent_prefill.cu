@@ -43,6 +43,11 @@ constexpr uint32_t kColO = 256;
 constexpr float kGrowth = 8.f;
 constexpr float kMinusInf = -INFINITY;
 
+template <int T>
+struct Tile {
+    static constexpr int value = T;
+};
+
 struct Item {
     int b, h;        // b < 0: no more
     int q0, nq;      // the request's first query row, and its queries from this item's first on
@@ -126,10 +131,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         uint32_t base_pos = 0;
         for (int i = 0; __all_sync(0xffffffffu, item_ready(i)); ++i) {
             const Item &it = m.item[i % kItems];
-            const int steps = tile ? it.n1 : it.n0, all = max(it.n0, it.n1);
-            const int row = tile * kQTile + r, nk = it.nk, b = it.b;
-            const bool live = row < it.nq;
-            const int sees = a.causal ? min(nk, it.sees0 + row) : nk;
+            const int steps = tile ? it.n1 : it.n0;
+            const int nk = it.nk;
+            const int sees = a.causal ? min(nk, it.sees0 + tile * kQTile + r) : nk;
             float ref = kMinusInf, sum = 0.f;
             bool ok = true;
             for (int j = 0; j < steps; ++j, ++done) {
@@ -219,6 +223,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             }
             ok = __all_sync(0xffffffffu, ok);
             const float inv = sum > 0.f ? __fdiv_rn(1.f, sum) : sum;  // zero and NaN stay
+            const int row = tile * kQTile + r;
+            const bool live = row < it.nq;
             __nv_bfloat16 *out = a.out.p + (long long)(it.q0 + row) * a.out.st + (long long)it.h * a.out.sh;
 #pragma unroll 1
             for (int g = 0; g < 4; ++g) {
@@ -241,12 +247,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                     *reinterpret_cast<uint4 *>(out + g * 32 + e) = make_uint4(u[0], u[1], u[2], u[3]);
                 }
             }
-            if (!ok && lane == 0 && a.flags) atomic_or_byte(a.flags, b, PFKV_FLAG_DEVICE_TIMEOUT);
+            if (!ok && lane == 0 && a.flags) atomic_or_byte(a.flags, it.b, PFKV_FLAG_DEVICE_TIMEOUT);
+            base_pos += max(it.n0, it.n1);
             tmem_fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive(&m.iempty[i % kItems]);
             if (!ok) break;
-            base_pos += all;
         }
     } else if (warp == 8) {
         // ------------------------------ products ------------------------------
@@ -254,78 +260,75 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         if (elect_one()) {
             constexpr uint32_t idO = umma_idesc(kQTile, 128, true, false, true);
             const uint32_t qa = smem_addr(psm), ka = qa + kOffK, va = qa + kOffV;
-            // parities: bit `tile` of each word (no arrays: they would live in memory)
-            uint32_t weighed = 0, queried = 0, base_pos = 0, kpos = 0;
-            bool ok = true;
-            bool weights = false, values = false;  // the next tile's barriers, asked ahead
-            for (int i = 0; ok && item_ready(i); ++i) {
-                const int n0 = m.item[i % kItems].n0, n1 = m.item[i % kItems].n1, n = max(n0, n1);
-                bar_arrive(&m.iempty[i % kItems]);
-                // step j of a tile: O of step j - 1, then S of step j.  K and V are waited for
-                // where the first tile of the two uses them, and released by the last.
-#pragma unroll 1
-                for (int x = 0; x < 2 * (n + 1) && ok; ++x) {
-                    const int j = x >> 1, tile = x & 1, mine = tile ? n1 : n0, other = tile ? n0 : n1;
-                    const bool scores = j < mine, first = tile == 0 || j >= n0, last = tile == 1 || j >= n1;
-                    bool keys = scores && first && bar_passed(&m.kfull[kpos % kKSlots], (kpos / kKSlots) & 1);
-                    if (j > 0 && j <= mine) {
-                        const uint32_t pos = base_pos + j - 1, slot = pos % kVSlots, parity = (weighed >> tile) & 1;
-                        ok = weights || bar_wait(&m.pready[tile][0], parity, gave_up);
-                        if (tile == 0 || j > n0) ok = (values || bar_wait(&m.vfull[slot], (pos / kVSlots) & 1, gave_up)) && ok;
-                        if (!ok) break;
-                        const bool rest = bar_passed(&m.pready[tile][1], parity);
-                        tmem_fence_after();
-                        const uint64_t db = umma_desc(va + slot * 2 * kSlotB, kSlotB, 1024);
+            // Straight code, a copy a tile: one thread issues all products of the CTA, and what
+            // it does between them is time that the tensor cores wait.
+            uint32_t weighed0 = 0, weighed1 = 0;  // steps of the tiles whose weights were used
+            uint32_t items0 = 0, items1 = 0, vpos = 0, kpos = 0;
+            bool ready = false;                   // the next tile's weights, and V: asked ahead
+            int n0 = 0, n1 = 0;
+            // Step j of a tile: O of step j - 1, then S of step j.  K and V are waited for
+            // where the first tile of the two uses them, and released by the last.
+            auto step = [&](auto which, int j) {
+                constexpr int T = decltype(which)::value;
+                constexpr uint32_t cs = T * 128, co = kColO + T * 128;
+                const int mine = T ? n1 : n0, other = T ? n0 : n1;
+                uint32_t &weighed = T ? weighed1 : weighed0, &items = T ? items1 : items0;
+                const bool first = T == 0 || j >= n0, last = T == 1 || j >= n1;
+                const uint32_t kstart = first ? kpos : kpos - kKChunks;
+                bool keys = T == 0 && bar_passed(&m.kfull[kstart % kKSlots], (kstart / kKSlots) & 1);
+                if (j > 0 && j <= mine) {
+                    const uint32_t pos = vpos + j - 1, slot = pos % kVSlots, parity = weighed++ & 1;
+                    if (!ready && !bar_wait(&m.pready[T][0], parity, gave_up)) return false;
+                    if ((T == 0 ? !ready : j > n0) && !bar_wait(&m.vfull[slot], (pos / kVSlots) & 1, gave_up)) return false;
+                    const bool rest = bar_passed(&m.pready[T][1], parity);
+                    tmem_fence_after();
+                    const uint32_t db = umma_desc(va + slot * 2 * kSlotB, kSlotB);
 #pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            umma_ts(tmem + kColO + tile * 128, tmem + tile * 128 + s * 8, db + s * 128, idO, j > 1 || s > 0);
-                        ok = rest || bar_wait(&m.pready[tile][1], parity, gave_up);
-                        weighed ^= 1u << tile;
-                        if (!ok) break;
-                        tmem_fence_after();
+                    for (int s = 0; s < 4; ++s) umma_ts(tmem + co, tmem + cs + s * 8, db + s * 128, idO, j > 1 || s > 0);
+                    if (!rest && !bar_wait(&m.pready[T][1], parity, gave_up)) return false;
+                    tmem_fence_after();
 #pragma unroll
-                        for (int s = 4; s < 8; ++s)
-                            umma_ts(tmem + kColO + tile * 128, tmem + tile * 128 + s * 8, db + s * 128, idO, true);
-                        if (tile == 1 || j > n1) umma_commit(&m.vempty[slot]);
-                        if (j == mine) umma_commit(&m.odone[tile]);
-                    }
-                    weights = values = false;
-                    if (scores) {
-                        if (j == 0) {
-                            ok = bar_wait(&m.qfull[tile], (queried >> tile) & 1, gave_up);
-                            queried ^= 1u << tile;
-                        }
-                        uint32_t at = first ? kpos : kpos - kKChunks;
-#pragma unroll 1
-                        for (int c = 0; c < kKChunks; ++c, ++at) {
-                            const uint32_t slot = at % kKSlots;
-                            ok = (!first || keys || bar_wait(&m.kfull[slot], (at / kKSlots) & 1, gave_up)) && ok;
-                            if (!ok) break;
-                            if (c + 1 < kKChunks) {
-                                keys = first && bar_passed(&m.kfull[(at + 1) % kKSlots], ((at + 1) / kKSlots) & 1);
-                            } else {
-                                const int jn = (x + 1) >> 1;  // step of the next tile
-                                if (jn > 0 && jn <= other) {
-                                    weights = bar_passed(&m.pready[tile ^ 1][0], (weighed >> (tile ^ 1)) & 1);
-                                    const uint32_t pos = base_pos + jn - 1;
-                                    values = bar_passed(&m.vfull[pos % kVSlots], (pos / kVSlots) & 1);
-                                }
-                            }
-                            const uint64_t da = umma_desc(qa + (tile * kKChunks + c) * kSlotB, 16, 1024);
-                            const uint64_t db = umma_desc(ka + slot * kSlotB, 16, 1024);
-#pragma unroll
-                            for (int s = 0; s < 4; ++s) umma_ss<1>(tmem + tile * 128, da + 2 * s, db + 2 * s, idS, c > 0 || s > 0);
-                            if (last) umma_commit(&m.kempty[slot]);
-                        }
-                        if (first) kpos += kKChunks;
-                        if (ok) {
-                            umma_commit(&m.sfull[tile]);
-                            if (j + 1 == mine) umma_commit(&m.qempty[tile]);
-                        }
-                    }
+                    for (int s = 4; s < 8; ++s) umma_ts(tmem + co, tmem + cs + s * 8, db + s * 128, idO, true);
+                    if (T == 1 || j > n1) umma_commit(&m.vempty[slot]);
+                    if (j == mine) umma_commit(&m.odone[T]);
                 }
-                base_pos += n;
-                weights = values = false;
+                ready = false;
+                if (j >= mine) return true;
+                if (j == 0 && !bar_wait(&m.qfull[T], items++ & 1, gave_up)) return false;
+                const uint32_t da = umma_desc(qa + T * kKChunks * kSlotB, 16);
+#pragma unroll
+                for (int c = 0; c < kKChunks; ++c) {
+                    const uint32_t at = kstart + c, slot = at % kKSlots;
+                    if (first && !keys && !bar_wait(&m.kfull[slot], (at / kKSlots) & 1, gave_up)) return false;
+                    if (c + 1 < kKChunks) {
+                        keys = T == 0 && bar_passed(&m.kfull[(at + 1) % kKSlots], ((at + 1) / kKSlots) & 1);
+                    } else {
+                        const int jn = j + T;  // step of the next tile
+                        const uint32_t pos = vpos + jn - 1, weights = T ? weighed0 : weighed1;
+                        ready = jn > 0 && jn <= other && bar_passed(&m.pready[T ^ 1][0], weights & 1) &&
+                                (T == 0 || bar_passed(&m.vfull[pos % kVSlots], (pos / kVSlots) & 1));
+                    }
+                    const uint32_t db = umma_desc(ka + slot * kSlotB, 16);
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        umma_ss<1>(tmem + cs, da + c * (kSlotB >> 4) + 2 * s, db + 2 * s, idS, c > 0 || s > 0);
+                    if (last) umma_commit(&m.kempty[slot]);
+                }
+                if (first) kpos += kKChunks;
+                umma_commit(&m.sfull[T]);
+                if (j + 1 == mine) umma_commit(&m.qempty[T]);
+                return true;
+            };
+            bool ok = true;
+            for (int i = 0; ok && item_ready(i); ++i) {
+                n0 = m.item[i % kItems].n0;
+                n1 = m.item[i % kItems].n1;
+                bar_arrive(&m.iempty[i % kItems]);
+                const int n = max(n0, n1);
+#pragma unroll 1
+                for (int j = 0; j <= n && ok; ++j) ok = step(Tile<0>{}, j) && step(Tile<1>{}, j);
+                vpos += n;
+                ready = false;
             }
             // nothing in flight when the CTA leaves
             umma_commit(&m.drain);

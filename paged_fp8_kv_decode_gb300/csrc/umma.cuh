@@ -14,15 +14,18 @@ namespace {
 // A matrix operand in shared memory with the 128-byte swizzle: rows of 128 bytes
 // (64 16-bit elements), 16-byte chunk c of row r stored at chunk c ^ (r & 7),
 // eight rows a 1,024-byte atom (so bases are 1,024-byte aligned).
-//   K-major operand: a row holds 64 consecutive k of one m (or n); `sbo` is the
-//     distance between groups of eight rows; a step of 16 k adds 32 bytes.
-//   MN-major operand: a row holds 64 consecutive m (or n) of one k; `lbo` is the
-//     distance to the next 64 of them, `sbo` between groups of eight k; a step of
-//     16 k adds 2 * sbo.
-__device__ __forceinline__ uint64_t umma_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)((lbo >> 4) & 0x3FFF) << 16) |
-           ((uint64_t)((sbo >> 4) & 0x3FFF) << 32) | (1ull << 46) | (2ull << 61);
+//   K-major operand: a row holds 64 consecutive k of one m (or n), groups of eight
+//     rows follow each other; a step of 16 k adds 32 bytes.
+//   MN-major operand: a row holds 64 consecutive m (or n) of one k, groups of eight
+//     k follow each other; `lbo` is the distance to the next 64 m; a step of 16 k adds
+//     2,048 bytes.
+// This is the descriptor's lower word, in units of 16 bytes where steps are added;
+// the upper one (the distance between groups, 1,024 bytes, and the kind of swizzle)
+// is the same for all.
+__device__ __forceinline__ uint32_t umma_desc(uint32_t addr, uint32_t lbo) {
+    return ((addr >> 4) & 0x3FFFu) | (((lbo >> 4) & 0x3FFFu) << 16);
 }
+constexpr uint32_t kDescUpper = (1024u >> 4) | (1u << 14) | (2u << 29);
 
 // Instruction descriptor of kind::f16 with fp32 accumulators: A and B both bf16
 // or both f16; a set `mn` bit marks an operand as MN-major.
@@ -40,24 +43,24 @@ __device__ __forceinline__ bool elect_one() {
 
 // D (+)= A B; CG CTAs of a cluster work on one tile (issued by the even one).
 template <int CG>
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
     if constexpr (CG == 1)
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b),
-                     "r"(idesc), "r"((uint32_t)accumulate)
+        asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\t"
+                     "mov.b64 b, {%2, %5};\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+                     "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "n"(kDescUpper)
                      : "memory");
     else
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b),
-                     "r"(idesc), "r"((uint32_t)accumulate)
+        asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\t"
+                     "mov.b64 b, {%2, %5};\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+                     "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "n"(kDescUpper)
                      : "memory");
 }
 
 // The same with A in tensor memory.
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b),
-                 "r"(idesc), "r"((uint32_t)accumulate)
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc),
+                 "r"((uint32_t)accumulate), "n"(kDescUpper)
                  : "memory");
 }
 
