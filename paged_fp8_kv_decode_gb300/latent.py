@@ -50,12 +50,14 @@ class LatentCache:
         return B.PFKV_KV_BF16 if self.c_pages.dtype == torch.bfloat16 else B.PFKV_KV_FP8_E4M3
 
     def c_struct(self) -> _CLatentCache:
-        NP, PS, D = self.c_pages.shape
-        if (self.r_pages.shape[:2] != (NP, PS) or self.r_pages.dtype != torch.bfloat16
-                or not self.r_pages.is_contiguous() or not self.c_pages.is_contiguous()):
+        c, r = self.c_pages, self.r_pages
+        NP, PS, D = c.shape
+        rNP, rPS, rD = r.shape
+        if (rNP != NP or rPS != PS or r.dtype != torch.bfloat16 or not r.is_contiguous()
+                or not c.is_contiguous()):
             raise ValueError("c_pages [pages][16][512] and bfloat16 r_pages [pages][16][64], contiguous")
-        return _CLatentCache(NP, PS, D, self.r_pages.shape[2], self.dtype, B._ptr(self.c_pages),
-                             B._ptr(self.r_pages), B._ptr(self.c_scale), B._ptr(self.page_tags))
+        return _CLatentCache(NP, PS, D, rD, self.dtype, B._ptr(c), B._ptr(r), B._ptr(self.c_scale),
+                             B._ptr(self.page_tags))
 
 
 def lib() -> ctypes.CDLL:
@@ -97,9 +99,9 @@ def pfkv_latent_append(cache: LatentCache, pages: B.Pages, rope: R.Rope, positio
                         max_new_tokens)
     if c_new.shape[:-1] != r_new.shape[:-1]:
         raise ValueError("c_new and r_new: rows for the same tokens")
-    c = R._rows(c_new, packed, False, "c_new", int(cache.c_pages.shape[2]))
-    r = R._rows(r_new, packed, False, "r_new", int(cache.r_pages.shape[2]))
-    qr, qo, hq = R._queries(q, q_out, c_new, packed, int(cache.r_pages.shape[2]))
+    c = R._rows(c_new, packed, False, "c_new", cache.c_pages.shape[2])
+    r = R._rows(r_new, packed, False, "r_new", cache.r_pages.shape[2])
+    qr, qo, hq = R._queries(q, q_out, c_new, packed, cache.r_pages.shape[2])
     k, p, t = cache.c_struct(), pages.c_struct(), rope.c_struct()
     B._check(lib().pfkv_latent_append(ctypes.byref(k), ctypes.byref(p), ctypes.byref(t),
                                       ctypes.byref(tok), ctypes.byref(c), ctypes.byref(r),
@@ -112,13 +114,13 @@ def pfkv_latent_gather(cache: LatentCache, pages: B.Pages, row_starts: torch.Ten
                        flags: Optional[torch.Tensor] = None, stream=None) -> None:
     """row_starts: int32 [B + 1]; c_out: bf16 [rows][512], r_out: bf16
     [rows][64], rows of any stride."""
-    c = R._rows(c_out, True, False, "c_out", int(cache.c_pages.shape[2]))
-    r = R._rows(r_out, True, False, "r_out", int(cache.r_pages.shape[2]))
+    c = R._rows(c_out, True, False, "c_out", cache.c_pages.shape[2])
+    r = R._rows(r_out, True, False, "r_out", cache.r_pages.shape[2])
     if c_out.shape[0] != r_out.shape[0] or row_starts.numel() != pages.batch + 1:
         raise ValueError("as many rows of c_out as of r_out, and batch + 1 row_starts")
     k, p = cache.c_struct(), pages.c_struct()
     B._check(lib().pfkv_latent_gather(ctypes.byref(k), ctypes.byref(p),
-                                      R._i32(row_starts, "row_starts"), int(c_out.shape[0]),
+                                      R._i32(row_starts, "row_starts"), c_out.shape[0],
                                       int(max_seq_len), c.data, c.stride_t, r.data, r.stride_t,
                                       B._ptr(flags), B._stream(stream)), "pfkv_latent_gather")
 
@@ -144,14 +146,14 @@ def pfkv_latent_decode_attn(cache: LatentCache, pages: B.Pages, q_c: torch.Tenso
     if (q_c.shape != out.shape or q_c.shape[:-1] != q_r.shape[:-1]
             or q_c.shape[0] != pages.batch):
         raise ValueError("q_c and out [B][kq][H][512], q_r [B][kq][H][64]")
-    qc = R._rows(q_c, False, True, "q_c", int(cache.c_pages.shape[2]))
-    qr = R._rows(q_r, False, True, "q_r", int(cache.r_pages.shape[2]))
-    o = R._rows(out, False, True, "out", int(cache.c_pages.shape[2]))
+    qc = R._rows(q_c, False, True, "q_c", cache.c_pages.shape[2])
+    qr = R._rows(q_r, False, True, "q_r", cache.r_pages.shape[2])
+    o = R._rows(out, False, True, "out", cache.c_pages.shape[2])
     k, p = cache.c_struct(), pages.c_struct()
     B._check(lib().pfkv_latent_decode_attn(
-        ctypes.byref(k), ctypes.byref(p), ctypes.byref(qc), ctypes.byref(qr), int(q_c.shape[2]),
-        int(q_c.shape[1]), float(sm_scale), int(max_seq_len), B._ptr(workspace),
-        workspace.numel() * workspace.element_size(), ctypes.byref(o), B._ptr(flags),
+        ctypes.byref(k), ctypes.byref(p), ctypes.byref(qc), ctypes.byref(qr), q_c.shape[2],
+        q_c.shape[1], float(sm_scale), int(max_seq_len), B._ptr(workspace),
+        workspace.nbytes, ctypes.byref(o), B._ptr(flags),
         B._stream(stream)), "pfkv_latent_decode_attn")
 
 
@@ -163,7 +165,7 @@ def pfkv_latent_prefill_attn(q_nope: torch.Tensor, q_rope: torch.Tensor, k_nope:
     """Packed rows: q_nope, out: bf16 [rows][H][128], q_rope: [rows][H][64],
     k_nope, v: [key rows][H][128], k_rope: [key rows][64]; q_starts, k_starts:
     int32 [B + 1]; any strides that leave rows contiguous."""
-    Tq, H, Tk = int(q_nope.shape[0]), int(q_nope.shape[1]), int(k_nope.shape[0])
+    (Tq, H), Tk = q_nope.shape[:2], k_nope.shape[0]
     if (q_nope.shape[:2] != q_rope.shape[:2] or q_nope.shape[:2] != out.shape[:2]
             or k_nope.shape[:2] != v.shape[:2] or k_nope.shape[1] != H or k_rope.shape[0] != Tk
             or q_starts.numel() != k_starts.numel() or q_starts.numel() < 1):

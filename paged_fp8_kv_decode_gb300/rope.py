@@ -50,23 +50,26 @@ class Rope:
                       float(self.scale))
 
 
-def _rows(x: torch.Tensor, packed: bool, heads: bool, name: str, dim: Optional[int] = None) -> _CRows:
+_BF16, _I32, _byref = torch.bfloat16, torch.int32, ctypes.byref
+
+
+def _rows(x: torch.Tensor, packed: bool, heads: bool, name: str, dim: int) -> _CRows:
     """bf16 rows as the C ABI takes them: [B][T][H][D] padded or [rows][H][D]
     packed, without H where the rows are shared by all heads; any strides that
     leave a row's elements contiguous."""
-    want = 2 + (not packed) + heads
-    if x.dtype != torch.bfloat16 or x.dim() != want or (x.shape[-1] > 1 and x.stride(-1) != 1):
-        raise ValueError(f"{name}: bfloat16 tensor of {want} dimensions with contiguous rows")
-    if dim is not None and x.shape[-1] != dim:
-        raise ValueError(f"{name}: rows of {dim} elements")
     s = x.stride()
-    sb = 0 if packed else s[0]
-    st = s[0] if packed else s[1]
-    return _CRows(B._ptr(x), sb, st, s[-2] if heads else 0)
+    want = 2 + (not packed) + heads
+    if x.dtype != _BF16 or len(s) != want or s[-1] != 1:
+        raise ValueError(f"{name}: bfloat16 tensor of {want} dimensions with contiguous rows")
+    if x.shape[-1] != dim:
+        raise ValueError(f"{name}: rows of {dim} elements")
+    if packed:
+        return _CRows(B._ptr(x), 0, s[0], s[1] if heads else 0)
+    return _CRows(B._ptr(x), s[0], s[1], s[2] if heads else 0)
 
 
 def _i32(t: Optional[torch.Tensor], name: str):
-    if t is not None and t.dtype != torch.int32:
+    if t is not None and t.dtype != _I32:
         raise ValueError(f"{name}: int32")
     return B._ptr(t)
 
@@ -77,7 +80,7 @@ def _new_tokens(first: torch.Tensor, batch: int, positions, new_lens, rope_posit
     if row_starts is None:
         if first.shape[0] != batch:
             raise ValueError("padded rows: one entry per request")
-        T, total = int(first.shape[1]), 0
+        T, total = first.shape[1], 0
         if max_new_tokens is not None and int(max_new_tokens) != T:
             raise ValueError("padded rows: max_new_tokens is their second dimension")
     else:
@@ -85,7 +88,7 @@ def _new_tokens(first: torch.Tensor, batch: int, positions, new_lens, rope_posit
             raise ValueError("packed rows need max_new_tokens")
         if row_starts.numel() != batch + 1:
             raise ValueError("row_starts: batch + 1 entries")
-        T, total = int(max_new_tokens), int(first.shape[0])
+        T, total = int(max_new_tokens), first.shape[0]
     return _CNewTokens(T, _i32(positions, "positions"), _i32(new_lens, "new_lens"),
                        _i32(rope_positions, "rope_positions"), _i32(row_starts, "row_starts"), total)
 
@@ -99,11 +102,11 @@ def _queries(q, q_out, first, packed, dim):
     lead = 1 if packed else 2
     if q.shape != q_out.shape or q.shape[:lead] != first.shape[:lead]:
         raise ValueError("q and q_out: rows for the same tokens as the new keys")
-    return _rows(q, packed, True, "q", dim), _rows(q_out, packed, True, "q_out", dim), int(q.shape[-2])
+    return _rows(q, packed, True, "q", dim), _rows(q_out, packed, True, "q_out", dim), q.shape[-2]
 
 
 def _ref(s):
-    return None if s is None else ctypes.byref(s)
+    return None if s is None else _byref(s)
 
 
 def lib() -> ctypes.CDLL:
@@ -134,7 +137,7 @@ def pfkv_rope_append(cache: B.Cache, pages: B.Pages, rope: Rope, positions: torc
     strides of ``pages``, rope_positions int32 [B]; flags uint8
     [>= round_up(B, 4)] (OR-ed)."""
     packed = row_starts is not None
-    D, heads = int(cache.k_pages.shape[3]), int(cache.k_pages.shape[1])
+    _, heads, _, D = cache.k_pages.shape
     tok = _new_tokens(k_new, pages.batch, positions, new_lens, rope_positions, row_starts,
                       max_new_tokens)
     if k_new.shape != v_new.shape or k_new.shape[-2] != heads:
@@ -142,7 +145,7 @@ def pfkv_rope_append(cache: B.Cache, pages: B.Pages, rope: Rope, positions: torc
     k, v = _rows(k_new, packed, True, "k_new", D), _rows(v_new, packed, True, "v_new", D)
     qr, qo, hq = _queries(q, q_out, k_new, packed, D)
     c, p, r = cache.c_struct(), pages.c_struct(), rope.c_struct()
-    B._check(lib().pfkv_rope_append(ctypes.byref(c), ctypes.byref(p), ctypes.byref(r),
-                                    ctypes.byref(tok), ctypes.byref(k), ctypes.byref(v), _ref(qr),
+    B._check(lib().pfkv_rope_append(_byref(c), _byref(p), _byref(r),
+                                    _byref(tok), _byref(k), _byref(v), _ref(qr),
                                     _ref(qo), hq, B._ptr(flags), B._stream(stream)),
              "pfkv_rope_append")
