@@ -17,6 +17,7 @@ namespace {
 
 constexpr int kRopeWarps = 8;
 constexpr int kRopeThreads = kRopeWarps * 32;
+constexpr int kRowsAhead = 2;               // groups of query rows of a warp in flight
 constexpr int kMaxPairs = 64;               // rot_dim / 2 at most
 constexpr int kTrigRows = 2 * kPage - 1;    // tokens whose angles a CTA may need
 
@@ -170,10 +171,39 @@ __device__ __forceinline__ void turn16(float *x, const float4 (&cs)[4][8], int p
     }
 }
 
-__device__ __forceinline__ uint2 encode8(const float *x, float scale) {
+// A unit's scale, its reciprocal, and whether quotients may be taken by it.
+struct Quant {
+    float scale, inv;
+    bool quick;
+};
+
+__device__ __forceinline__ Quant quant_of(float scale) {
+    return Quant{scale, __frcp_rn(scale), scale > 1e-30f && scale < 1e30f};
+}
+
+// The codes of x / scale.  x times the reciprocal is within 2^-23 of the quotient,
+// relative: less than three steps of fp32 from its rounded value.  So they have the same
+// code unless they lie next to the middle between two codes, which for normal codes
+// is the bit pattern 1000... below the third bit of the fraction.  Where one of eight
+// does, or is not zero and below the normal codes, all are divided.
+__device__ __forceinline__ uint2 encode8(const float *x, const Quant &q) {
+    float y[8];
+    uint32_t middle = 0xffffffffu, small = 0xffffffffu;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        y[e] = x[e] * q.inv;
+        const uint32_t u = __float_as_uint(y[e]);
+        middle = min(middle, (u + 4u - 0x80000u) << 12);
+        small = min(small, (u << 1) - 1u);
+    }
+    if (!q.quick || middle <= (8u << 12) || small < (0x3c800000u << 1) - 1u) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = __fdiv_rn(x[e], q.scale);
+    }
     uint32_t w[2] = {0u, 0u};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e >> 2] |= (uint32_t)float_to_e4m3(__fdiv_rn(x[e], scale)) << (8 * (e & 3));
+    for (int e = 0; e < 8; e += 2)
+        w[e >> 2] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(y[e], y[e + 1]), __NV_SATFINITE, __NV_E4M3) << (8 * (e & 3));
     return make_uint2(w[0], w[1]);
 }
 
@@ -200,22 +230,44 @@ __device__ __forceinline__ void turn_queries(const RowsArg &q, const RowsArg &ou
     const int lane = threadIdx.x & 31, p = lane % LANES;
     const Share sh = lane_share(turn, p);
     const int rows = (t1 - t0) * Hq;
-    for (int i = first * RPW + lane / LANES; i < rows; i += step * RPW) {
-        const int t = t0 + i / Hq, h = i % Hq;
-        const uint4 *src = reinterpret_cast<const uint4 *>(row_of(q, tok, sp, b, t, h));
-        uint4 *dst = reinterpret_cast<uint4 *>(row_of(out, tok, sp, b, t, h));
-        const uint4 w0 = src[sh.c0], w1 = src[sh.c1];
-        if (!sh.turned) {
-            dst[sh.c0] = w0;
-            dst[sh.c1] = w1;
-            continue;
+    // the next group's row is on its way while one is turned
+    struct Row {
+        uint4 w0, w1;
+        uint4 *dst;
+        int t;
+    };
+    auto load = [&](int i, Row &r) {
+        if (i >= rows) return;
+        const int t = i / Hq, h = i - t * Hq;
+        const uint4 *src = reinterpret_cast<const uint4 *>(row_of(q, tok, sp, b, t0 + t, h));
+        r.dst = reinterpret_cast<uint4 *>(row_of(out, tok, sp, b, t0 + t, h));
+        r.w0 = src[sh.c0];
+        r.w1 = src[sh.c1];
+        r.t = t0 + t - tlo;
+    };
+    int i = first * RPW + lane / LANES;
+    Row r[kRowsAhead] = {};
+#pragma unroll
+    for (int u = 0; u < kRowsAhead; ++u) load(i + u * step * RPW, r[u]);
+    for (; i < rows; i += kRowsAhead * step * RPW) {
+#pragma unroll
+        for (int u = 0; u < kRowsAhead; ++u) {
+            const int at = i + u * step * RPW;
+            if (at >= rows) continue;
+            const Row now = r[u];
+            load(at + kRowsAhead * step * RPW, r[u]);
+            if (!sh.turned) {
+                now.dst[sh.c0] = now.w0;
+                now.dst[sh.c1] = now.w1;
+                continue;
+            }
+            float x[16];
+            unpack8(now.w0, x);
+            unpack8(now.w1, x + 8);
+            turn16(x, tr.cs[now.t], p, turn.inter);
+            now.dst[sh.c0] = pack8(x);
+            now.dst[sh.c1] = pack8(x + 8);
         }
-        float x[16];
-        unpack8(w0, x);
-        unpack8(w1, x + 8);
-        turn16(x, tr.cs[t - tlo], p, turn.inter);
-        dst[sh.c0] = pack8(x);
-        dst[sh.c1] = pack8(x + 8);
     }
 }
 
@@ -290,34 +342,42 @@ __device__ __forceinline__ void append_turned_unit(const RopeAppendArgs &a, cons
     }
     const long long unit = (long long)phys * a.ap.Hkv + h;
     const long long dst0 = (unit * kPage + u.slot0) * D;
-    float x[PASSES][16];
-    float top = 0.f;
-#pragma unroll
-    for (int j = 0; j < PASSES; ++j) {
-        unpack8(w[j][0], x[j]);
-        unpack8(w[j][1], x[j] + 8);
+    // A row is turned once for the absolute maximum and once for its codes: kept in
+    // fp32 between, the rows take 120 registers a thread, which halves the warps.
+    auto turned = [&](int j, float *x) {
+        unpack8(w[j][0], x);
+        unpack8(w[j][1], x + 8);
         const int t = u.tb + j * RPW + sub;
-        if (sh.turned && t < u.te) turn16(x[j], tr.cs[t - tlo], p, a.turn.inter);
-        if (FP8) top = fmaxf(top, absmax16(x[j]));
-    }
+        if (sh.turned && t < u.te) turn16(x, tr.cs[t - tlo], p, a.turn.inter);
+    };
     if constexpr (FP8) {
         float *scales = is_v ? a.ap.v_scale : a.ap.k_scale;
         float scale;
         if (u.slot0 == 0) {  // this call opens the unit
+            float top = 0.f;
+#pragma unroll
+            for (int j = 0; j < PASSES; ++j) {
+                float x[16];
+                turned(j, x);
+                top = fmaxf(top, absmax16(x));
+            }
             top = warp_max(top);
             scale = top == 0.f ? 1.f : __fdiv_rn(top, 448.f);
             if (lane == 0) scales[unit] = scale;
         } else {
             scale = scales[unit];
         }
+        const Quant qn = quant_of(scale);
         uint8_t *dst = static_cast<uint8_t *>(is_v ? a.ap.v_pages : a.ap.k_pages) + dst0;
 #pragma unroll
         for (int j = 0; j < PASSES; ++j) {
             const int r = j * RPW + sub;
             if (u.tb + r >= u.te) continue;
+            float x[16];
+            turned(j, x);
             uint2 *row = reinterpret_cast<uint2 *>(dst + (long long)r * D);
-            row[sh.c0] = encode8(x[j], scale);
-            row[sh.c1] = encode8(x[j] + 8, scale);
+            row[sh.c0] = encode8(x, qn);
+            row[sh.c1] = encode8(x + 8, qn);
         }
     } else {
         __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(is_v ? a.ap.v_pages : a.ap.k_pages) + dst0;
@@ -326,8 +386,15 @@ __device__ __forceinline__ void append_turned_unit(const RopeAppendArgs &a, cons
             const int r = j * RPW + sub;
             if (u.tb + r >= u.te) continue;
             uint4 *row = reinterpret_cast<uint4 *>(dst + (long long)r * D);
-            row[sh.c0] = sh.turned ? pack8(x[j]) : w[j][0];
-            row[sh.c1] = sh.turned ? pack8(x[j] + 8) : w[j][1];
+            if (!sh.turned) {
+                row[sh.c0] = w[j][0];
+                row[sh.c1] = w[j][1];
+                continue;
+            }
+            float x[16];
+            turned(j, x);
+            row[sh.c0] = pack8(x);
+            row[sh.c1] = pack8(x + 8);
         }
     }
 }
@@ -352,7 +419,7 @@ __device__ __forceinline__ TileTokens tile_tokens(int p0, int n_all, int n_q, in
 }
 
 template <int D, bool FP8>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeAppendArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_append_kernel(RopeAppendArgs a) {
     __shared__ Trig tr;
     pdl_enter();
     const int b = blockIdx.x / a.tiles, k = blockIdx.x - b * a.tiles;
@@ -368,16 +435,15 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeAppendArg
     const bool per_head = a.tok.len_sh != 0;
     const TileTokens tt = tile_tokens(p0, per_head ? sp.n : nq, nq, k, per_head);
     if (tt.t0 >= tt.t1) return;  // uniform: no token of the request in this tile
-    fill_trig(tr, a.turn, a.tok.rope_pos ? a.tok.rope_pos[b] : p0, tt.tlo, tt.t0, tt.t1);
     const int warp = blockIdx.y * kRopeWarps + (threadIdx.x >> 5), warps = gridDim.y * kRopeWarps;
-    int item = warp;
-    for (; item < 2 * a.ap.Hkv; item += warps) {
+    const int units = 2 * a.ap.Hkv, turns = units > warp ? (units - warp + warps - 1) / warps : 0;  // units of this warp
+    const int first = warp + turns * warps - units;  // its first group of query rows
+    fill_trig(tr, a.turn, a.tok.rope_pos ? a.tok.rope_pos[b] : p0, tt.tlo, tt.t0, tt.t1);
+    for (int item = warp; item < units; item += warps) {
         const bool is_v = item >= a.ap.Hkv;
         append_turned_unit<D, FP8>(a, sp, tr, tt.tlo, b, is_v ? item - a.ap.Hkv : item, is_v, k);
     }
-    if (a.Hq > 0)
-        turn_queries<D>(a.q, a.q_out, a.Hq, a.tok, a.turn, sp, tr, tt.tlo, b, tt.q0, tt.q1, item - 2 * a.ap.Hkv,
-                        warps);
+    if (a.Hq > 0) turn_queries<D>(a.q, a.q_out, a.Hq, a.tok, a.turn, sp, tr, tt.tlo, b, tt.q0, tt.q1, first, warps);
 }
 
 // --------------------------------------------------------------------------
@@ -425,6 +491,7 @@ __device__ __forceinline__ void append_latents(const LatentAppendArgs &a, const 
         } else {
             scale = a.pool.c_scale[phys];
         }
+        const Quant qn = quant_of(scale);
         uint8_t *dst = static_cast<uint8_t *>(a.pool.c_pages) + dst0;
 #pragma unroll
         for (int j = 0; j < PASSES; ++j) {
@@ -433,7 +500,7 @@ __device__ __forceinline__ void append_latents(const LatentAppendArgs &a, const 
             float x[16];
             unpack8(w[j][0], x);
             unpack8(w[j][1], x + 8);
-            const uint2 lo = encode8(x, scale), hi = encode8(x + 8, scale);
+            const uint2 lo = encode8(x, qn), hi = encode8(x + 8, qn);
             reinterpret_cast<uint4 *>(dst + (long long)r * PFKV_LATENT_DIM)[chunk / 2] =
                 make_uint4(lo.x, lo.y, hi.x, hi.y);
         }
@@ -470,7 +537,7 @@ __device__ __forceinline__ void append_turned_keys(const LatentAppendArgs &a, co
 }
 
 template <bool FP8>
-__global__ void __launch_bounds__(kRopeThreads) latent_append_kernel(LatentAppendArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 3) latent_append_kernel(LatentAppendArgs a) {
     __shared__ Trig tr;
     __shared__ float red[kLatentWarps];
     pdl_enter();
@@ -485,8 +552,8 @@ __global__ void __launch_bounds__(kRopeThreads) latent_append_kernel(LatentAppen
     const int n = head_tokens(a.tok, sp, l0);
     const TileTokens tt = tile_tokens(p0, n, n, k, false);
     if (tt.t0 >= tt.t1) return;
-    fill_trig(tr, a.turn, a.tok.rope_pos ? a.tok.rope_pos[b] : p0, tt.tlo, tt.t0, tt.t1);
     const int warp = threadIdx.x >> 5;
+    fill_trig(tr, a.turn, a.tok.rope_pos ? a.tok.rope_pos[b] : p0, tt.tlo, tt.t0, tt.t1);
     if (blockIdx.y == 0 && warp <= kLatentWarps) {
         // uniform over these warps, so that the barrier inside is met by all
         const UnitSpan u = unit_span(p0, n, k, a.pool.max_pages);
