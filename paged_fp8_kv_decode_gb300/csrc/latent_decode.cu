@@ -57,7 +57,7 @@ constexpr int kTilePages = kTile / kPage;
 constexpr int kRowsCta = 64, kRowBlock = 128;
 constexpr int kKChunks = 9;                   // 8 of latents, 1 of rotated keys
 constexpr int kKStages = 5;                   // two chunks each, the rotated keys alone
-constexpr int kRing = 6;                      // tiles looked up ahead
+constexpr int kRing = 4;                      // tiles looked up ahead
 constexpr uint32_t kChunkB = kRowsCta * 128;  // Q, K and P chunks: 64 rows of 128 bytes
 constexpr uint32_t kVChunkB = kTile * 128;
 // V of one block of 256 values: two chunks of 64.  FP8: chunk by chunk, 128 tokens
@@ -94,7 +94,7 @@ struct Misc {
     uint64_t sfull[2], pvdone, qfull, drain;
     Tile tile[kRing];
     union {
-        long long warp_sum[kThreads / 32];
+        long long warp_sum[2][kThreads / 32];
         float xm[4][kRowsCta];
     };
     long long x0, x1, off;
@@ -125,6 +125,12 @@ __device__ __forceinline__ int live_len(const LatentDecodeArgs &a, int b) {
     return n < 0 || (long long)n > (long long)a.pool.max_pages * kPage || n > a.max_seq_len ? 0 : n;
 }
 __device__ __forceinline__ int tiles_of(int n) { return (n + kTile - 1) / kTile; }
+
+// The list of (request, row block) parts is dealt to the clusters by cost: a tile is
+// one unit, and the start of a part (new queries, the part before written out while
+// the products wait: 5 to 6 us) as many as kPartUnits tiles.
+constexpr int kPartUnits = 2;
+__device__ __forceinline__ long long units_of(int tiles) { return tiles > 0 ? tiles + kPartUnits : 0; }
 
 // First unit of cluster w's range, U units over W clusters.
 __device__ __forceinline__ long long range_start(long long w, long long U, int W) { return (w * U + W - 1) / W; }
@@ -300,36 +306,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     {
         const int per = (a.B + kThreads - 1) / kThreads;
         const int lo = min(a.B, tid * per), hi = min(a.B, lo + per);
-        long long mine = 0;
-        for (int b = lo; b < hi; ++b) mine += (long long)tiles_of(live_len(a, b)) * blocks;
-        long long incl = mine;
+        long long mine[2] = {0, 0};  // units, and tiles
+        for (int b = lo; b < hi; ++b) {
+            const int tiles = tiles_of(live_len(a, b));
+            mine[0] += units_of(tiles) * blocks;
+            mine[1] += (long long)tiles * blocks;
+        }
+        long long before[2] = {mine[0], mine[1]}, all[2] = {0, 0};
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += y;
-        }
-        if (lane == 31) m.warp_sum[warp] = incl;
-        __syncthreads();
-        long long before = 0, U = 0;
-        for (int i = 0; i < kThreads / 32; ++i) {
-            if (i < warp) before += m.warp_sum[i];
-            U += m.warp_sum[i];
-        }
-        const int W = (int)min((long long)clusters, U);
-        const long long x0 = w < W ? range_start(w, U, W) : 0, x1 = w < W ? range_start(w + 1, U, W) : 0;
-        before += incl - mine;
-        if (x0 < x1 && before <= x0 && x0 < before + mine && !m.gave_up) {
-            long long at = before;
-            int b = lo;
-            for (;; ++b) {
-                const long long u = (long long)tiles_of(live_len(a, b)) * blocks;
-                if (x0 < at + u) break;
-                at += u;
+        for (int d = 1; d < 32; d <<= 1)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const long long y = __shfl_up_sync(0xffffffffu, before[k], d);
+                if (lane >= d) before[k] += y;
             }
-            m.b0 = b;
-            m.off = x0 - at;
-            m.x0 = x0;
-            m.x1 = x1;
+        if (lane == 31) {
+            m.warp_sum[0][warp] = before[0];
+            m.warp_sum[1][warp] = before[1];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            before[k] -= mine[k];
+            for (int i = 0; i < kThreads / 32; ++i) {
+                if (i < warp) before[k] += m.warp_sum[k][i];
+                all[k] += m.warp_sum[k][i];
+            }
+        }
+        const int W = (int)min((long long)clusters, all[1]);
+        if (w < W && !m.gave_up) {
+#pragma unroll 1
+            for (int end = 0; end < 2; ++end) {  // the tiles at which the range begins and ends
+                const long long x = range_start(w + end, all[0], W);
+                if (x == all[0] && tid == 0) m.x1 = all[1];
+                if (x < before[0] || x >= before[0] + mine[0]) continue;
+                long long at = before[0], tile = before[1];
+                for (int b = lo;; ++b) {
+                    const int tiles = tiles_of(live_len(a, b));
+                    const long long u = units_of(tiles);
+                    if (x >= at + u * blocks) {
+                        at += u * blocks;
+                        tile += (long long)tiles * blocks;
+                        continue;
+                    }
+                    const long long block = (x - at) / u;
+                    const long long off = block * tiles + max(0LL, x - at - block * u - kPartUnits);
+                    if (end) {
+                        m.x1 = tile + off;
+                    } else {
+                        m.x0 = tile + off;
+                        m.b0 = b;
+                        m.off = off;
+                    }
+                    break;
+                }
+            }
         }
     }
     __syncthreads();
@@ -882,22 +913,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // --------------------------------------------------------------------------
-// Merge: a warp half a row.  What depends on the call's inputs alone (the list of
-// tiles) comes before its wait for the split kernel.
+// Merge: a warp half a row, or a quarter of its parts.  What depends on the call's
+// inputs alone (the list of tiles) comes before its wait for the split kernel.
 // --------------------------------------------------------------------------
-constexpr int kMergeWarps = 8, kMergeRows = kMergeWarps / 2;
+constexpr int kMergeWarps = 8;
 
+// Ways: warps that share a half row's parts.
+template <int Ways>
 __global__ void __launch_bounds__(kMergeWarps * 32)
     latent_merge_kernel(LatentDecodeArgs a, int R, int blocks, int clusters, Parts parts, int groups) {
-    __shared__ long long sums[2][kMergeWarps];
+    constexpr int kRows = kMergeWarps / 2 / Ways;
+    __shared__ long long sums[3][kMergeWarps];
+    __shared__ float4 shared_o[Ways > 1 ? kMergeWarps : 1][2][32];
+    __shared__ float shared_ref[kMergeWarps], shared_sum[kMergeWarps];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int b = blockIdx.x / groups, g = blockIdx.x - b * groups;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int raw = a.pool.seq_lens[(long long)b * a.pool.len_sb];
     const int n = live_len(a, b);
-    long long before = 0, all = 0;
+    long long before = 0, all = 0, tiles_all = 0;
     for (int i = tid; i < a.B; i += blockDim.x) {
-        const long long u = (long long)tiles_of(live_len(a, i)) * blocks;
+        const int tiles = tiles_of(live_len(a, i));
+        const long long u = units_of(tiles) * blocks;
+        tiles_all += (long long)tiles * blocks;
         all += u;
         if (i < b) before += u;
     }
@@ -905,31 +943,36 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     for (int d = 16; d > 0; d >>= 1) {
         before += __shfl_xor_sync(0xffffffffu, before, d);
         all += __shfl_xor_sync(0xffffffffu, all, d);
+        tiles_all += __shfl_xor_sync(0xffffffffu, tiles_all, d);
     }
     if (lane == 0) {
         sums[0][warp] = before;
         sums[1][warp] = all;
+        sums[2][warp] = tiles_all;
     }
     __syncthreads();
-    before = all = 0;
+    before = all = tiles_all = 0;
     for (int i = 0; i < kMergeWarps; ++i) {
         before += sums[0][i];
         all += sums[1][i];
+        tiles_all += sums[2][i];
     }
     const int tiles = tiles_of(n);
-    const int W = (int)min((long long)clusters, all);
-    auto cluster_of = [&](long long x) { return (int)(x * W / all); };
+    const int W = (int)min((long long)clusters, tiles_all);
+    // the cluster of tile j of row block k
+    auto cluster_of = [&](int k, int j) {
+        return (int)((before + k * units_of(tiles) + kPartUnits + j) * W / all);
+    };
     asm volatile("griddepcontrol.wait;" ::: "memory");
     uint32_t flag = raw != n ? PFKV_FLAG_BAD_LENGTH : 0u;
     if (tiles > 0) {
-        const int w0 = cluster_of(before), w1 = cluster_of(before + (long long)tiles * blocks - 1);
+        const int w0 = cluster_of(0, 0), w1 = cluster_of(blocks - 1, tiles - 1);
         uint32_t bits = 0;
         for (int i = w0 * 2 + tid; i < (w1 + 1) * 2; i += blockDim.x)
             if (parts.gave_up[i]) bits |= PFKV_FLAG_DEVICE_TIMEOUT;
         for (int k = 0; k < blocks; ++k) {  // every cluster that holds a part of row block k
-            const long long first = before + (long long)k * tiles;
-            const int last = cluster_of(first + tiles - 1);
-            for (int i = cluster_of(first) + tid; i <= last; i += blockDim.x)
+            const int last = cluster_of(k, tiles - 1);
+            for (int i = cluster_of(k, 0) + tid; i <= last; i += blockDim.x)
                 bits |= parts.status[(long long)b * blocks + k + i];
         }
 #pragma unroll
@@ -937,27 +980,30 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
             if (__syncthreads_or(bits & f)) flag |= f;
     }
     if (g == 0 && tid == 0 && a.flags) a.flags[b] = (uint8_t)flag;
-    const int row = g * kMergeRows + (warp >> 1);
-    if (row >= R) return;
+    const int half = warp & 1, way = (warp >> 1) % Ways, row = g * kRows + (warp >> 1) / Ways;
+    if (Ways == 1 && row >= R) return;  // otherwise a row a CTA, and all are there
     const int t = row / a.H, h = row - t * a.H;
-    __nv_bfloat16 *out = a.out.p + (long long)b * a.out.sb + (long long)t * a.out.st + (long long)h * a.out.sh +
-                         (warp & 1) * 256;
+    __nv_bfloat16 *out = a.out.p + (long long)b * a.out.sb + (long long)t * a.out.st + (long long)h * a.out.sh + half * 256;
     // lane l: values 4 l + 128 i .. + 3 of the half
     float o[2][4] = {};
     if (!flag && tiles > 0) {
         const int block = row / kRowBlock, brow = row - block * kRowBlock;
-        const long long first = before + (long long)block * tiles;
-        const int w0 = cluster_of(first), w1 = cluster_of(first + tiles - 1);
+        const int w0 = cluster_of(block, 0), w1 = cluster_of(block, tiles - 1);
         if (w0 == w1) return;  // one part: written by the split kernel
-        auto place = [&](int w) { return (long long)(w * 2 + (w == w0 ? 1 : 0)) * parts.rows + brow; };
+        // this warp's parts: those of clusters w0 + way, w0 + way + Ways, ..
+        const int mine_all = (w1 - w0 - way + Ways) / Ways;
+        auto place = [&](int i) {
+            const int w = w0 + way + i * Ways;
+            return (long long)(w * 2 + (w == w0 ? 1 : 0)) * parts.rows + brow;
+        };
         float ref = kNegInf, sum = 0.f;
-        for (int at = w0; at <= w1; at += 32) {  // 32 parts at once: a lane has one's weight
-            const float l = at + lane <= w1 ? parts.lse[place(at + lane)] : kNegInf;
+        for (int at = 0; at < mine_all; at += 32) {  // 32 parts at once: a lane has one's weight
+            const float l = at + lane < mine_all ? parts.lse[place(at + lane)] : kNegInf;
+            if (__all_sync(0xffffffffu, l == kNegInf)) continue;  // (a NaN goes on, and into the sum)
             float top = l;
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             top = fmaxf(ref, top);
-            if (top == kNegInf) continue;
             const float old = exp2f(ref - top), mine = exp2f(l - top);
             ref = top;
             float s = mine;
@@ -968,12 +1014,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[i][e] *= old;
-            const int count = min(32, w1 - at + 1);
+            const int count = min(32, mine_all - at);
             for (int j = 0; j < count; j += 8) {  // eight parts' loads in flight
                 float4 y[8][2];
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
-                    const float4 *src = reinterpret_cast<const float4 *>(parts.o + place(min(at + j + u, w1)) * kDC + (warp & 1) * 256) + lane;
+                    const float4 *src = reinterpret_cast<const float4 *>(parts.o + place(min(at + j + u, mine_all - 1)) * kDC + half * 256) + lane;
                     y[u][0] = src[0];
                     y[u][1] = src[32];
                 }
@@ -991,11 +1037,46 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
                 }
             }
         }
+        if constexpr (Ways > 1) {
+            if (lane == 0) {
+                shared_ref[warp] = ref;
+                shared_sum[warp] = sum;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) shared_o[warp][i][lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+            __syncthreads();  // the flags and the parts are the CTA's: all its warps are here
+            if (way > 0) return;
+            float top = ref;
+#pragma unroll
+            for (int k = 1; k < Ways; ++k) top = fmaxf(top, shared_ref[warp + 2 * k]);
+            const float own = top == kNegInf ? 0.f : exp2f(ref - top);
+            sum *= own;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][e] *= own;
+#pragma unroll
+            for (int k = 1; k < Ways; ++k) {
+                const float f = top == kNegInf ? 0.f : exp2f(shared_ref[warp + 2 * k] - top);
+                sum += shared_sum[warp + 2 * k] * f;
+                if (f == 0.f) continue;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float4 y = shared_o[warp + 2 * k][i][lane];
+                    o[i][0] += y.x * f;
+                    o[i][1] += y.y * f;
+                    o[i][2] += y.z * f;
+                    o[i][3] += y.w * f;
+                }
+            }
+        }
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][e] *= inv;
+    } else if (Ways > 1 && way > 0) {
+        return;
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -1071,17 +1152,21 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs &a, int num_sms, cudaStr
     e = a.pool.fp8 ? launch_split<true>(mapc, mapr, mapk, a, R, blocks, clusters, parts, s)
                    : launch_split<false>(mapc, mapr, mapk, a, R, blocks, clusters, parts, s);
     if (e != cudaSuccess) return e;
-    const int groups = (R + kMergeRows - 1) / kMergeRows;
-    if ((long long)groups * a.B > 0x7fffffffLL) return cudaErrorInvalidValue;
-    return launch_pdl(latent_merge_kernel, dim3((unsigned)(groups * a.B)), dim3(kMergeWarps * 32), 0, s, a, R, blocks,
-                      clusters, parts, groups);
+    if ((long long)R * a.B > 0x7fffffffLL) return cudaErrorInvalidValue;
+    // Few rows have many parts: then a CTA a row, its parts dealt to four warps a half.
+    const bool few = (long long)(R + 3) / 4 * a.B < num_sms;
+    const int groups = few ? R : (R + 3) / 4;
+    auto *const merge = few ? latent_merge_kernel<4> : latent_merge_kernel<1>;
+    return launch_pdl(merge, dim3((unsigned)(groups * a.B)), dim3(kMergeWarps * 32), 0, s, a, R, blocks, clusters, parts,
+                      groups);
 }
 
 cudaError_t preload_latent_decode() {
     cudaError_t e = cudaFuncSetAttribute(latent_split_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(latent_split_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-    if (e == cudaSuccess) e = preload_kernel(latent_merge_kernel);
+    if (e == cudaSuccess) e = preload_kernel(latent_merge_kernel<1>);
+    if (e == cudaSuccess) e = preload_kernel(latent_merge_kernel<4>);
     return e;
 }
 

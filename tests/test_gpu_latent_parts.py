@@ -1,0 +1,94 @@
+"""How the latent kernels share out their work, at the edges: lists of requests of
+very different lengths whose parts begin and end anywhere in a cluster's range,
+NaN among many parts, and prompts with more tiles than the GPU has
+multiprocessors."""
+import pytest
+import torch
+
+import test_gpu_latent_decode as D
+import test_gpu_latent_prefill as P
+from latent_cases import PAGE, SCALE, gen, latent_pool, rows, tables
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("H,kq,lens", [
+    (16, 1, [128] * 300),                            # more parts than clusters, a tile each
+    (128, 1, [1, 0, 129, 2000, 1, 1, 640, 0, 127, 5000, 16]),
+    (64, 3, [3, 300, 0, 1, 1500] * 9),               # two row blocks a request
+    (8, 1, [9000] + [1] * 100),                      # one long among short ones
+    (8, 1, [1] * 100 + [9000]),
+    (128, 2, [257, 256, 255]),                       # fewer tiles than clusters
+    (16, 1, [1]),
+])
+def test_parts_anywhere_in_a_range(H, kq, lens, fp8):
+    g = gen(len(lens) + H)
+    bt, num = tables([(n + PAGE - 1) // PAGE for n in lens], seed=3)
+    cache = latent_pool(g, num, fp8)
+    qc, qr = rows(g, len(lens), kq, H, 512, outliers=0), rows(g, len(lens), kq, H, 64, outliers=0)
+    out, fl = D.run(cache, bt, lens, qc, qr)
+    assert not any(fl)
+    D.check(cache, bt, lens, qc, qr, out)
+    again, _ = D.run(cache, bt, lens, qc, qr)
+    assert torch.equal(out, again)                   # the split and the order of sums are the call's alone
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("many", [1, 40])
+def test_a_nan_in_a_visible_token_reaches_its_request_alone(many, fp8):
+    lens = [12000] + [300] * (many - 1)
+    g = gen(7)
+    bt, num = tables([(n + PAGE - 1) // PAGE for n in lens], seed=5)
+    cache = latent_pool(g, num, fp8)
+    qc, qr = rows(g, many, 1, 16, 512, outliers=0), rows(g, many, 1, 16, 64, outliers=0)
+    page = int(bt[0, 700])                           # of one of the first request's many parts
+    if fp8:
+        cache.c_pages[page, 3, 5] = 0x7F
+    else:
+        cache.c_pages[page, 3, 5] = float("nan")
+    out, fl = D.run(cache, bt, lens, qc, qr)
+    assert not any(fl)
+    assert out[0].isnan().all()
+    assert not out[1:].isnan().any()
+
+
+@pytest.mark.parametrize("H,nq,pre", [
+    (64, [1, 130, 257, 0, 512, 300, 129], [0, 700, 3, 40, 0, 129, 1000]),
+    (16, [64] * 40, [0, 5] * 20),                    # one tile of rows an item, many items a CTA
+    (3, [2000], [0]),
+])
+def test_many_items_of_every_length(H, nq, pre):
+    g = gen(H + len(nq))
+    nk = [q + p for q, p in zip(nq, pre)]
+    qs, ks = P.starts_of(nq), P.starts_of(nk)
+    x = P.inputs(g, sum(nq), sum(nk), H)
+    out, fl = P.run(x, qs, ks, max(nq))
+    assert not any(fl)
+    for b in range(len(nq)):
+        P.check(x, (qs[b], qs[b + 1]), (ks[b], ks[b + 1]), out, heads=[0, H // 2, H - 1])
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_a_negative_scale(causal):
+    g = gen(11)
+    nq, nk = [200, 77], [200, 300]
+    qs, ks = P.starts_of(nq), P.starts_of(nk)
+    x = P.inputs(g, sum(nq), sum(nk), 4)
+    out, _ = P.run(x, qs, ks, max(nq), causal=causal, scale=-SCALE)
+    for b in range(2):
+        P.check(x, (qs[b], qs[b + 1]), (ks[b], ks[b + 1]), out, causal, -SCALE)
+
+
+def test_a_nan_key_reaches_the_rows_that_see_it():
+    g = gen(12)
+    nq = [300, 140]
+    qs = P.starts_of(nq)
+    x = P.inputs(g, sum(nq), sum(nq), 2)
+    x["kn"][150, 1, 7] = float("nan")                # of the first request
+    out, fl = P.run(x, qs, qs, max(nq))
+    assert not any(fl)
+    assert out[150:300, 1].isnan().all()
+    bad = out.isnan().any(-1)
+    bad[150:300, 1] = False
+    assert not bad.any()
