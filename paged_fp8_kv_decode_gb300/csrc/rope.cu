@@ -149,26 +149,26 @@ __device__ __forceinline__ uint4 pack8(const float *x) {
     return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
-// Turns a lane's sixteen elements (its two chunks in order).
-__device__ __forceinline__ void turn16(float *x, const float4 (&cs)[4][8], int p, int inter) {
+// Turns a lane's sixteen elements (its two chunks in order).  One branch for all of
+// them: inside the loops the compiler would issue both forms.
+template <bool Inter>
+__device__ __forceinline__ void turn16(float *x, const float4 (&cs)[4][8], int p) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const float4 w = cs[k][p];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int i = 2 * k + u;
-            const float c = u ? w.z : w.x, s = u ? w.w : w.y;
-            if (inter) {
-                const float a = x[2 * i], b = x[2 * i + 1];
-                x[2 * i] = a * c - b * s;
-                x[2 * i + 1] = b * c + a * s;
-            } else {
-                const float a = x[i], b = x[8 + i];
-                x[i] = a * c - b * s;
-                x[8 + i] = b * c + a * s;
-            }
+            const int i = 2 * k + u, at = Inter ? 2 * i : i, to = Inter ? 2 * i + 1 : 8 + i;
+            const float c = u ? w.z : w.x, s = u ? w.w : w.y, a = x[at], b = x[to];
+            x[at] = a * c - b * s;
+            x[to] = b * c + a * s;
         }
     }
+}
+
+__device__ __forceinline__ void turn16(float *x, const float4 (&cs)[4][8], int p, int inter) {
+    if (inter) turn16<true>(x, cs, p);
+    else turn16<false>(x, cs, p);
 }
 
 // A unit's scale, its reciprocal, and whether quotients may be taken by it.
@@ -184,19 +184,24 @@ __device__ __forceinline__ Quant quant_of(float scale) {
 // The codes of x / scale.  x times the reciprocal is within 2^-23 of the quotient,
 // relative: less than three steps of fp32 from its rounded value.  So they have the same
 // code unless they lie next to the middle between two codes, which for normal codes
-// is the bit pattern 1000... below the third bit of the fraction.  Where one of eight
-// does, or is not zero and below the normal codes, all are divided.
+// is the bit pattern 1000... below the third bit of the fraction.  Below 2^-6 the codes
+// are as far apart as in [2^-6, 2^-5), where adding 2^-6 takes them (and rounds by half a
+// step).  Where one of eight lies there, all are divided.
 __device__ __forceinline__ uint2 encode8(const float *x, const Quant &q) {
+    constexpr uint32_t kBelow = (4u - 0x80000u) * 4096u;  // (u + 4 - middle) << 12: the fraction's other bits go
     float y[8];
-    uint32_t middle = 0xffffffffu, small = 0xffffffffu;
+    uint32_t middle = 0xffffffffu;
+    auto grid = [](float v) {
+        const float m = fabsf(v);
+        return __float_as_uint(m < 0.015625f ? m + 0.015625f : m);
+    };
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < 8; e += 2) {
         y[e] = x[e] * q.inv;
-        const uint32_t u = __float_as_uint(y[e]);
-        middle = min(middle, (u + 4u - 0x80000u) << 12);
-        small = min(small, (u << 1) - 1u);
+        y[e + 1] = x[e + 1] * q.inv;
+        middle = __vimin3_u32(middle, grid(y[e]) * 4096u + kBelow, grid(y[e + 1]) * 4096u + kBelow);
     }
-    if (!q.quick || middle <= (8u << 12) || small < (0x3c800000u << 1) - 1u) {
+    if (!q.quick || middle <= (8u << 12)) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = __fdiv_rn(x[e], q.scale);
     }
