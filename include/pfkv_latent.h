@@ -89,7 +89,7 @@ pfkv_status pfkv_latent_append(const pfkv_latent_cache *cache, const pfkv_pages 
  *   row_starts : int32 [batch + 1]: token j < seq_lens[b] of request b goes to
  *                row row_starts[b] + j, which must lie below row_starts[b + 1]
  *                and total_rows
- *   max_seq_len: host-known upper bound of every length
+ *   max_seq_len: host-known upper bound of every length (0: nothing is done)
  *   c_out      : bf16, row i at c_out + i * c_stride (latent_dim elements);
  *                FP8 pools: e4m3 value x page scale, rounded to bf16
  *   r_out      : bf16, row i at r_out + i * r_stride (rope_dim elements)
@@ -119,7 +119,8 @@ pfkv_status pfkv_latent_gather(const pfkv_latent_cache *cache, const pfkv_pages 
  *   max_seq_len: host-known upper bound of every seq_lens entry
  *   workspace  : >= pfkv_latent_decode_workspace_size(...) bytes, 256-byte
  *          aligned; contents on entry are ignored; not used by two calls at once
- *   flags: uint8 [batch], written (not OR-ed); may be NULL
+ *   flags: uint8 [batch], written (not OR-ed), with PFKV_FLAG_DEVICE_TIMEOUT where a
+ *          wait inside the kernel gave up; may be NULL
  *
  * Query token t attends to the first n - num_query_tokens + 1 + t tokens, n =
  * seq_lens[b]; a row that attends to none is zero.  Every live page id, and its
@@ -132,8 +133,8 @@ pfkv_status pfkv_latent_gather(const pfkv_latent_cache *cache, const pfkv_pages 
  * pools: e4m3 values are exact in f16; q_c enters as f16 after a power-of-two
  * scaling a row (exact for elements within 2^14 of the row's largest); a weight
  * times its page's scale is rounded once to f16 (within 2^-11, or 2^-32 of the
- * row's largest where that is more).  The weights' sum is of the rounded weights.  Scores, the running
- * maximum, sums and the merge of partial results are fp32.
+ * row's largest where that is more), where it enters the second product.  Scores, the
+ * running maximum, the weights' sums and the merge of partial results are fp32.
  */
 pfkv_status pfkv_latent_decode_workspace_size(const pfkv_latent_cache *cache, const pfkv_pages *pages,
                                               int32_t num_q_heads, int32_t num_query_tokens,
@@ -158,12 +159,14 @@ pfkv_status pfkv_latent_decode_attn(const pfkv_latent_cache *cache, const pfkv_p
  *             all heads (stride_h is not read)
  *   v, out  : rows of 128 elements (t, h)
  *             stride_b of every array is not read; strides of h may interleave
- *             arrays (k_nope and v are often two halves of one row)
+ *             arrays (k_nope and v are often two halves of one row).  An array with
+ *             more than one row has stride_t > 0 (else PFKV_ERR_UNSUPPORTED); one
+ *             without rows is not read and may be NULL
  *   max_q_len: host-known upper bound of a request's query rows (a longer one is
- *             flagged PFKV_FLAG_BAD_LENGTH)
+ *             flagged PFKV_FLAG_BAD_LENGTH); a bound far above the lengths costs time
  *   causal  : nonzero: query i of nq sees keys j <= i + nk - nq (the queries are
  *             the last of the keys' tokens); zero: every key
- *   flags   : uint8 [batch], written; may be NULL
+ *   flags   : uint8 [batch], written, with PFKV_FLAG_DEVICE_TIMEOUT as above; may be NULL
  *
  * A query that sees no key gives a zero row.  A request whose rows are not
  * within the arrays is flagged and nothing of it is written.  Rows outside every

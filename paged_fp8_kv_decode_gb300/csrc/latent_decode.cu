@@ -81,7 +81,7 @@ constexpr float kNegInf = -INFINITY;
 // What the roles need to know of a tile.
 struct Tile {
     int id[kTilePages];      // physical pages, -1 for one that is not to be read
-    float z[kTilePages];     // FP8: their scales
+    float z[kTilePages], lz[kTilePages], iz[kTilePages];  // scales, their logarithms and reciprocals     // FP8: their scales
     int b, block, left;      // request, row block, the request's tokens from this tile's first on
     uint32_t flags;
 };
@@ -440,9 +440,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     z[i] = ti.z[part * 2 + i];
-                    const float zc = fmaxf(z[i], 7.888609052210118e-31f);  // 2^-100
-                    lz[i] = __log2f(zc);
-                    iz[i] = __frcp_rn(zc);
+                    lz[i] = ti.lz[part * 2 + i];
+                    iz[i] = ti.iz[part * 2 + i];
                 }
             }
             bar_wait(&m.sfull[t & 1], (t >> 1) & 1, gave_up);
@@ -459,7 +458,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_ld16(cs + 64 + g * 16, y);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) x[g * 16 + j] = fmaf(x[g * 16 + j], qs * z[g], fmaf(y[j], a2, lz[g]));
+                        for (int j = 0; j < 16; j += 2) {
+                            const float2 turned = fma2(make_float2(y[j], y[j + 1]), make_float2(a2, a2), make_float2(lz[g], lz[g]));
+                            const float2 v = fma2(make_float2(x[g * 16 + j], x[g * 16 + j + 1]), make_float2(qs * z[g], qs * z[g]), turned);
+                            x[g * 16 + j] = v.x;
+                            x[g * 16 + j + 1] = v.y;
+                        }
                     }
                 } else {
                     tmem_wait_ld();
@@ -471,8 +475,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 32; ++j)
                         if (j >= seen) x[j] = kNegInf;
                 }
+                float tops[4] = {x[0], x[1], x[2], x[3]};  // four chains, not one
 #pragma unroll
-                for (int j = 0; j < 32; ++j) top = fmaxf(top, x[j]);
+                for (int j = 4; j < 32; ++j) tops[j & 3] = fmaxf(tops[j & 3], x[j]);
+                top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
             }
             m.xm[part][r] = top;
             // all of the row block's threads know the tile, or none goes by it: they meet at
@@ -489,20 +495,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t pw[16];
             if (any_live) {
                 const float base = ref == kNegInf ? 0.f : ref - kWeightBias<FP8>;
+                float2 sums[2][2] = {};  // of 16 tokens (a page) each
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) {
-                    const float w0 = fast_exp2(x[j] - base), w1 = fast_exp2(x[j + 1] - base);
+                    const float2 y = add2(make_float2(x[j], x[j + 1]), make_float2(-base, -base));
+                    const float2 f = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                    sums[j >> 4][(j >> 1) & 1] = add2(sums[j >> 4][(j >> 1) & 1], f);
                     if constexpr (FP8) {
-                        const __half2 hw = __floats2half2_rn(w0, w1);
-                        const float2 f = __half22float2(hw);
-                        sum = fmaf(f.x + f.y, iz[j >> 4], sum);
+                        const __half2 hw = __floats2half2_rn(f.x, f.y);
                         pw[j >> 1] = *reinterpret_cast<const uint32_t *>(&hw);
                     } else {
-                        const __nv_bfloat162 hw = __floats2bfloat162_rn(w0, w1);
-                        const float2 f = __bfloat1622float2(hw);
-                        sum += f.x + f.y;
+                        const __nv_bfloat162 hw = __floats2bfloat162_rn(f.x, f.y);
                         pw[j >> 1] = *reinterpret_cast<const uint32_t *>(&hw);
                     }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float2 f = add2(sums[i][0], sums[i][1]);
+                    if constexpr (FP8) sum = fmaf(f.x + f.y, iz[i], sum);
+                    else sum += f.x + f.y;
                 }
             }
             if (t > 0) {
@@ -792,6 +803,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane < 16 && i == j) {
                         ti.id[pg] = id;
                         ti.z[pg] = z;
+                        if constexpr (FP8) {
+                            const float zc = fmaxf(z, 7.888609052210118e-31f);  // 2^-100
+                            ti.lz[pg] = __log2f(zc);
+                            ti.iz[pg] = __frcp_rn(zc);
+                        }
                         if (pg == 0) {
                             ti.b = s.b;
                             ti.block = s.block;

@@ -420,29 +420,31 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         if (a.flags)
             for (int b = blockIdx.x * 32 + lane; b < a.B; b += gridDim.x * 32)
                 a.flags[b] = range(b, q0, nq, k0, nk) ? 0 : PFKV_FLAG_BAD_LENGTH;
-        if (lane == 0) {
-            int i = 0;
-            bool ok = true;
-            auto publish = [&](const Item &it) {
-                ok = bar_wait(&m.iempty[i % kItems], ((i / kItems) & 1) ^ 1, gave_up);
-                if (!ok) return;
-                m.item[i % kItems] = it;
-                bar_arrive(&m.ifull[i % kItems]);
-                ++i;
-            };
-            for (long long turn = 0; ok; ++turn) {
-                const long long x = turn * gridDim.x + ((turn & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-                if (turn * gridDim.x >= deal.items) break;
-                if (x >= deal.items) continue;
-                const long long group = x / ((long long)deal.pairs * deal.tiles);
-                const int in_group = (int)(x - group * deal.pairs * deal.tiles);
-                const int t = deal.tiles - 1 - in_group / deal.pairs;
-                const long long pair = group * deal.pairs + in_group % deal.pairs;
-                if (pair >= (long long)a.B * a.H) continue;
-                Item it;
+        // A lane a number of the CTA's turns: with a max_q_len far above the lengths most
+        // numbers stand for no item.
+        int i = 0;
+        auto publish = [&](const Item &it) {
+            if (!bar_wait(&m.iempty[i % kItems], ((i / kItems) & 1) ^ 1, gave_up)) return false;
+            m.item[i % kItems] = it;
+            bar_arrive(&m.ifull[i % kItems]);
+            return true;
+        };
+        bool ok = true;
+        Item it{};
+        for (long long turn0 = 0; ok && turn0 * gridDim.x < deal.items; turn0 += 32) {
+            const long long turn = turn0 + lane;
+            const long long x = turn * gridDim.x + ((turn & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            const long long group = x / ((long long)deal.pairs * deal.tiles);
+            const int in_group = (int)(x - group * deal.pairs * deal.tiles);
+            const int t = deal.tiles - 1 - in_group / deal.pairs;
+            const long long pair = group * deal.pairs + in_group % deal.pairs;
+            bool there = x < deal.items && pair < (long long)a.B * a.H;
+            if (there) {
                 it.b = (int)(pair / a.H);
                 it.h = (int)(pair - (long long)it.b * a.H);
-                if (!range(it.b, q0, nq, k0, nk) || t * kItemRows >= nq) continue;
+                there = range(it.b, q0, nq, k0, nk) && t * kItemRows < nq;
+            }
+            if (there) {
                 it.q0 = q0 + t * kItemRows;
                 it.nq = nq - t * kItemRows;
                 it.k0 = k0;
@@ -455,11 +457,15 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 };
                 it.n0 = steps(0);
                 it.n1 = steps(1);
-                publish(it);
             }
-            Item end{};
-            end.b = -1;
-            if (ok) publish(end);
+            for (uint32_t left = __ballot_sync(0xffffffffu, there); ok && left; left &= left - 1, ++i) {
+                const int from = __ffs(left) - 1;
+                ok = __all_sync(0xffffffffu, lane != from || publish(it));
+            }
+        }
+        if (lane == 0 && ok) {
+            it.b = -1;
+            publish(it);
         }
         __syncwarp();
     }
@@ -489,7 +495,7 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, int num_sms, cudaS
         if (e != cudaSuccess) return e;
     }
     Deal d;
-    d.tiles = a.total_q > 0 ? (int)(((long long)a.max_q_len + kItemRows - 1) / kItemRows) : 0;
+    d.tiles = (int)((min((long long)a.max_q_len, a.total_q) + kItemRows - 1) / kItemRows);
     const long long pairs = (long long)a.B * a.H;
     d.pairs = (int)min(pairs, d.tiles > 0 ? (2LL * num_sms + d.tiles - 1) / d.tiles : 1LL);
     d.items = (pairs + d.pairs - 1) / d.pairs * d.pairs * d.tiles;
