@@ -95,7 +95,7 @@ struct Misc {
     Tile tile[kRing];
     union {
         long long warp_sum[2][kThreads / 32];
-        float xm[4][kRowsCta];
+        float xm[2][4][kRowsCta];  // what a row's four threads exchange: maxima by the tile's parity
     };
     long long x0, x1, off;
     int b0;
@@ -113,10 +113,6 @@ struct Parts {
     uint32_t *gave_up;  // [clusters][2]
     uint32_t *status;   // [request x row block + cluster]: flags of the pages that the cluster looked up
     int rows;        // min(R, 128)
-};
-
-struct DecodePlan2 {
-    int R, blocks, W;
 };
 
 // Tokens of request b, 0 for a length that is refused.
@@ -397,15 +393,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto fetch_queries = [&](int b, int block) {
             copy_queries(a, b, block, R, rank, q, (quad & 1) * 32 + part * 8, lane);
         };
-        auto finish_queries = [&]() {
+        auto finish_queries = [&](float (&xm)[4][kRowsCta]) {
             asm volatile("cp.async.wait_all;" ::: "memory");
             if constexpr (FP8) {
                 asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");  // the row block's copies are in
                 const uint32_t mine = largest_query(q, r, part);
-                m.xm[part][r] = __uint_as_float(mine);
+                xm[part][r] = __uint_as_float(mine);
                 asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");
-                const uint32_t top = max(max(__float_as_uint(m.xm[0][r]), __float_as_uint(m.xm[1][r])),
-                                         max(__float_as_uint(m.xm[2][r]), __float_as_uint(m.xm[3][r])));
+                const uint32_t top = max(max(__float_as_uint(xm[0][r]), __float_as_uint(xm[1][r])),
+                                         max(__float_as_uint(xm[2][r]), __float_as_uint(xm[3][r])));
                 // biased exponent, kept where both 2^e and 2^-e are normal fp32 numbers
                 const int eb = min(253, max(1, (int)(top >> 7)));
                 convert_query(q, r, part, __uint_as_float((uint32_t)(254 - eb) << 23));
@@ -418,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         if (N > 0) {
             fetch_queries(m.b0, (int)(m.off / tiles_of(live_len(a, m.b0))));
-            finish_queries();
+            finish_queries(m.xm[1]);
         }
         for (int t = 0; t < N; ++t) {
             const bool ok = looked_up(t);
@@ -480,11 +476,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 4; j < 32; ++j) tops[j & 3] = fmaxf(tops[j & 3], x[j]);
                 top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
             }
-            m.xm[part][r] = top;
+            float (&xm)[4][kRowsCta] = m.xm[t & 1];
+            xm[part][r] = top;
             // all of the row block's threads know the tile, or none goes by it: they meet at
             // the barriers below by its flags
             if (bar_any(bar, !ok)) flags = 0u;
-            top = fmaxf(fmaxf(m.xm[0][r], m.xm[1][r]), fmaxf(m.xm[2][r], m.xm[3][r]));
+            top = fmaxf(fmaxf(xm[0][r], xm[1][r]), fmaxf(xm[2][r], xm[3][r]));
             float shrink = 1.f;
             if (top > ref + kLazyGrowth || (ref == kNegInf && top > kNegInf)) {
                 shrink = fast_exp2(ref - top);  // 0 when nothing was seen yet
@@ -547,13 +544,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int slot = w * 2 + ((flags & kBegins) ? 1 : 0);
                 const bool done = bar_wait(&m.pvdone, t & 1, gave_up);
                 tmem_fence_after();
-                asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");  // xm has been read
-                m.xm[part][r] = sum;
+                float (&sums)[4][kRowsCta] = m.xm[(t & 1) ^ 1];  // read before this tile's first barrier
+                sums[part][r] = sum;
                 asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");
-                const float total = (m.xm[0][r] + m.xm[1][r]) + (m.xm[2][r] + m.xm[3][r]);
+                const float total = (sums[0][r] + sums[1][r]) + (sums[2][r] + sums[3][r]);
                 if (t + 1 < N) {  // the next part's scores are taken while this one is written
-                    asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");  // xm has been read
-                    finish_queries();
+                    asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");  // the sums have been read
+                    finish_queries(sums);
                 }
                 if (any_live) {
                     const float inv = total > 0.f ? __fdiv_rn(1.f, total) : total;  // zero and NaN stay
@@ -613,7 +610,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tmem_fence_before();
             }
-            asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory");  // xm is free
         }
     } else if (warp == 8) {
         // ----------------------- products (even CTA) -----------------------
