@@ -125,16 +125,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&r)[16]) {
         : "r"(addr));
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&u)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(u[0]),
-        "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]),
-        "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]), "r"(u[19]),
-        "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]),
-        "r"(u[29]), "r"(u[30]), "r"(u[31]), "r"(addr)
-        : "memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const float (&r)[16]) {
     const uint32_t *u = reinterpret_cast<const uint32_t *>(r);
     asm volatile(
@@ -170,8 +160,7 @@ __device__ __forceinline__ void bar_expect_tx(uint64_t *bar, uint32_t bytes) {
 // Arrive on the barrier at this offset in CTA `rank` of the cluster.  Arrivals and
 // waits keep the default scope also between CTAs: what they order is read by
 // matrix products, whose writers have fenced the async proxy, never by ordinary
-// loads.  (A wait that acquires at cluster scope cost 0.4 us each: 176 us instead
-// of the FIGURE us of a 140K-token FP8 batch of 128 heads.)
+// loads.  (A wait that acquires at cluster scope cost 0.4 us each.)
 __device__ __forceinline__ void bar_arrive_at(uint64_t *bar, uint32_t rank) {
     asm volatile(
         "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"

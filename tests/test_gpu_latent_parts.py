@@ -7,7 +7,9 @@ import torch
 
 import test_gpu_latent_decode as D
 import test_gpu_latent_prefill as P
-from latent_cases import PAGE, SCALE, gen, latent_pool, rows, tables
+from latent_cases import PAGE, SCALE, gen, i32, latent_pool, pages, rows, tables
+from paged_fp8_kv_decode_gb300 import binding as B
+from paged_fp8_kv_decode_gb300 import latent as L
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +94,69 @@ def test_a_nan_key_reaches_the_rows_that_see_it():
     bad = out.isnan().any(-1)
     bad[150:300, 1] = False
     assert not bad.any()
+
+
+@pytest.mark.parametrize("bound", [60, 4096, 1 << 30])
+def test_a_loose_bound_of_the_queries(bound):
+    g = gen(13)
+    nq = [60, 1, 33, 0] * 16
+    qs = P.starts_of(nq)
+    x = P.inputs(g, sum(nq), sum(nq), 32)
+    out, fl = P.run(x, qs, qs, bound)
+    assert not any(fl)
+    for b in range(len(nq)):
+        P.check(x, (qs[b], qs[b + 1]), (qs[b], qs[b + 1]), out, heads=[0, 31])
+
+
+def test_no_queries_at_all_and_a_bound_of_none():
+    g = gen(14)
+    x = P.inputs(g, 0, 20, 2)
+    _, fl = P.run(x, [0, 0, 0], [0, 5, 20], 7)
+    assert fl == [0, 0]
+    x = P.inputs(g, 9, 9, 2)
+    out, fl = P.run(x, [0, 0, 9], [0, 0, 9], 0)
+    assert fl == [0, B.PFKV_FLAG_BAD_LENGTH] and (out == 7.0).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("scale", [0.0, -SCALE])
+def test_scales_of_zero_and_below(scale, fp8):
+    lens = [300, 5]
+    g = gen(15)
+    bt, num = tables([(n + PAGE - 1) // PAGE for n in lens], seed=9)
+    cache = latent_pool(g, num, fp8)
+    qc, qr = rows(g, 2, 1, 16, 512, outliers=0), rows(g, 2, 1, 16, 64, outliers=0)
+    out, _ = D.run(cache, bt, lens, qc, qr, scale=scale)
+    D.check(cache, bt, lens, qc, qr, out, scale=scale)
+    x = P.inputs(g, 140, 140, 3)
+    out, _ = P.run(x, [0, 140], [0, 140], 140, scale=scale)
+    P.check(x, (0, 140), (0, 140), out, scale=scale)
+
+
+def test_calls_on_two_streams_at_once():
+    """Calls of both attentions in flight together, each with its own workspace and
+    arrays, give what they give alone."""
+    g = gen(16)
+    lens = [3000, 40, 700]
+    bt, num = tables([(n + PAGE - 1) // PAGE for n in lens], seed=11)
+    cache = latent_pool(g, num, True)
+    qc, qr = rows(g, 3, 1, 32, 512, outliers=0), rows(g, 3, 1, 32, 64, outliers=0)
+    want, _ = D.run(cache, bt, lens, qc, qr)
+    x = P.inputs(g, 900, 900, 8)
+    alone, _ = P.run(x, [0, 900], [0, 900], 900)
+    pg = pages(bt, i32(lens))
+    size = L.pfkv_latent_decode_workspace_size(cache, pg, 32, 1, 3000)
+    starts = i32([0, 900])
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    spaces = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    outs, prompt = [torch.zeros_like(qc) for _ in range(2)], torch.zeros_like(alone)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, ws, o in zip(streams, spaces, outs):
+            L.pfkv_latent_decode_attn(cache, pg, qc, qr, SCALE, 3000, ws, o, stream=s)
+        L.pfkv_latent_prefill_attn(x["qn"], x["qr"], x["kn"], x["kr"], x["v"], starts, starts, 900, SCALE, True, prompt,
+                                   stream=streams[2])
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o, want)
+    assert torch.equal(prompt, alone)
