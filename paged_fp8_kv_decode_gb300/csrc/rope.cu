@@ -221,6 +221,16 @@ __device__ __forceinline__ float absmax16(const float *x) {
     return m;
 }
 
+// Of sixteen bf16 elements as they were loaded.
+__device__ __forceinline__ float absmax16(const uint4 &a, const uint4 &b) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[0]));
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i])));
+    const float2 f = __bfloat1622float2(m);
+    return fmaxf(f.x, f.y);
+}
+
 __device__ __forceinline__ float warp_max(float m) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
@@ -368,6 +378,10 @@ __device__ __forceinline__ void append_turned_unit(const RopeAppendArgs &a, cons
             float top = 0.f;
 #pragma unroll
             for (int j = 0; j < PASSES; ++j) {
+                if (!sh.turned) {
+                    top = fmaxf(top, absmax16(w[j][0], w[j][1]));
+                    continue;
+                }
                 float x[16];
                 turned(j, x);
                 top = fmaxf(top, absmax16(x));
@@ -487,13 +501,9 @@ __device__ __forceinline__ void append_latents(const LatentAppendArgs &a, const 
     if constexpr (FP8) {
         float scale;
         if (u.slot0 == 0) {
-            float top = 0.f, x[16];
+            float top = 0.f;
 #pragma unroll
-            for (int j = 0; j < PASSES; ++j) {
-                unpack8(w[j][0], x);
-                unpack8(w[j][1], x + 8);
-                top = fmaxf(top, absmax16(x));
-            }
+            for (int j = 0; j < PASSES; ++j) top = fmaxf(top, absmax16(w[j][0], w[j][1]));
             top = warp_max(top);
             if (lane == 0) red[part] = top;
             asm volatile("bar.sync 1, %0;" ::"n"(kLatentWarps * 32) : "memory");
