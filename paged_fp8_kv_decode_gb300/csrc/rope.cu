@@ -324,9 +324,9 @@ __device__ __forceinline__ UnitSpan unit_span(int p0, int n, int k, int max_page
 // head, K or V, its bf16 words held in registers between the absolute maximum and
 // the encoding, so that each element is read once) or a group of query rows.
 //
-// 16,752 tokens, 32 query and 8 kv heads of 128, FP8: 377 MB in 92 us (4.1 TB/s).  The
-// queries alone run at a copy's rate (43 us); keys and values are bound by
-// instructions (44 us, 28 an element: turning, maximum, codes), not by their bytes.
+// 16,752 tokens, 32 query and 8 kv heads of 128, FP8: 377 MB in 85 us (4.4 TB/s).  The
+// queries' part takes what a copy of them takes (43 us); keys and values (37 us) are
+// bound by instructions (turning, maximum, codes), not by their 103 MB.
 // --------------------------------------------------------------------------
 template <int D, bool FP8>
 __device__ __forceinline__ void append_turned_unit(const RopeAppendArgs &a, const Span &sp, const Trig &tr, int tlo,
