@@ -159,7 +159,8 @@ pfkv_status pfkv_latent_decode_attn(const pfkv_latent_cache *cache, const pfkv_p
  *             all heads (stride_h is not read)
  *   v, out  : rows of 128 elements (t, h)
  *             stride_b of every array is not read; strides of h may interleave
- *             arrays (k_nope and v are often two halves of one row).  An array with
+ *             arrays (k_nope and v are often two halves of one row).  The arrays that
+ *             are read are device memory (tensor copies fetch them).  An array with
  *             more than one row has stride_t > 0 (else PFKV_ERR_UNSUPPORTED); one
  *             without rows is not read and may be NULL
  *   max_q_len: host-known upper bound of a request's query rows (a longer one is

@@ -51,6 +51,7 @@ class LatentCache:
 
     def c_struct(self) -> _CLatentCache:
         c, r = self.c_pages, self.r_pages
+        R._here(c)
         NP, PS, D = c.shape
         rNP, rPS, rD = r.shape
         if (rNP != NP or rPS != PS or r.dtype != torch.bfloat16 or not r.is_contiguous()
@@ -164,12 +165,15 @@ def pfkv_latent_prefill_attn(q_nope: torch.Tensor, q_rope: torch.Tensor, k_nope:
                              stream=None) -> None:
     """Packed rows: q_nope, out: bf16 [rows][H][128], q_rope: [rows][H][64],
     k_nope, v: [key rows][H][128], k_rope: [key rows][64]; q_starts, k_starts:
-    int32 [B + 1]; any strides that leave rows contiguous."""
+    int32 [B + 1]; any strides that leave rows contiguous; the rows in device memory."""
     (Tq, H), Tk = q_nope.shape[:2], k_nope.shape[0]
     if (q_nope.shape[:2] != q_rope.shape[:2] or q_nope.shape[:2] != out.shape[:2]
             or k_nope.shape[:2] != v.shape[:2] or k_nope.shape[1] != H or k_rope.shape[0] != Tk
             or q_starts.numel() != k_starts.numel() or q_starts.numel() < 1):
         raise ValueError("query rows [Tq][H], key rows [Tk][H], and batch + 1 starts of both")
+    R._here(q_nope)
+    if not (q_nope.is_cuda and q_rope.is_cuda and k_nope.is_cuda and k_rope.is_cuda and v.is_cuda):
+        raise ValueError("rows in device memory")
     rows = [R._rows(t, True, h, n, d) for t, h, n, d in (
         (q_nope, True, "q_nope", PFKV_LATENT_NOPE), (q_rope, True, "q_rope", PFKV_LATENT_ROPE),
         (k_nope, True, "k_nope", PFKV_LATENT_NOPE), (k_rope, False, "k_rope", PFKV_LATENT_ROPE),

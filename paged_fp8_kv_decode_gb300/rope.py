@@ -68,6 +68,12 @@ def _rows(x: torch.Tensor, packed: bool, heads: bool, name: str, dim: int) -> _C
     return _CRows(B._ptr(x), s[0], s[1], s[2] if heads else 0)
 
 
+def _here(x: torch.Tensor) -> None:
+    """The kernels run on the current device, whose stream `None` stands for."""
+    if x.is_cuda and x.get_device() != torch.cuda.current_device():
+        raise ValueError("tensors of another device than the current one")
+
+
 def _i32(t: Optional[torch.Tensor], name: str):
     if t is not None and t.dtype != _I32:
         raise ValueError(f"{name}: int32")
@@ -136,6 +142,7 @@ def pfkv_rope_append(cache: B.Cache, pages: B.Pages, rope: Rope, positions: torc
     query heads (q_out may be q); positions, new_lens int32 with the length
     strides of ``pages``, rope_positions int32 [B]; flags uint8
     [>= round_up(B, 4)] (OR-ed)."""
+    _here(cache.k_pages)
     packed = row_starts is not None
     _, heads, _, D = cache.k_pages.shape
     tok = _new_tokens(k_new, pages.batch, positions, new_lens, rope_positions, row_starts,

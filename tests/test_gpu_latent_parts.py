@@ -160,3 +160,20 @@ def test_calls_on_two_streams_at_once():
     for o in outs:
         assert torch.equal(o, want)
     assert torch.equal(prompt, alone)
+
+
+def test_tensors_elsewhere_are_refused(monkeypatch):
+    g = gen(17)
+    x = P.inputs(g, 5, 5, 2)
+    with pytest.raises(ValueError):
+        P.run(dict(x, qn=x["qn"].cpu().pin_memory()), [0, 5], [0, 5], 5, out=torch.zeros_like(x["qn"]))
+    bt, num = tables([1])
+    cache = latent_pool(g, num, False)
+    lens = i32([3])
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)   # as if another device were current
+    with pytest.raises(ValueError):
+        L.pfkv_latent_prefill_attn(x["qn"], x["qr"], x["kn"], x["kr"], x["v"], lens, lens, 5, 1.0, True, x["qn"], stream=0)
+    lens2 = torch.cat((lens, lens))
+    with pytest.raises(ValueError):
+        L.pfkv_latent_gather(cache, pages(bt, lens), lens2, 3, torch.zeros(3, 512, dtype=torch.bfloat16, device="cuda:0"),
+                             torch.zeros(3, 64, dtype=torch.bfloat16, device="cuda:0"), stream=0)
