@@ -27,9 +27,9 @@
 // whole kernel 1.75).  That is 1,450 TFLOP/s.
 //
 // The kernel is persistent.  Work items are ordered so that the CTAs at work share
-// the K and V of few heads (two rounds of items a group of heads), longest first
-// within a group, and dealt out in turns that change direction, so that each CTA
-// gets long and short ones.
+// the K and V of few heads (about two rounds of items a group of heads, or all heads
+// where L2 holds most of their K and V), longest first within a group, and dealt out in turns
+// that change direction, so that each CTA gets long and short ones.
 //
 // Roles of a CTA's twelve warps: 0-3 and 4-7 softmax and output of the two tiles; 8
 // issues the products; 9 loads K and V, 10 loads Q (TMA); 11 looks up items.
@@ -79,6 +79,7 @@ static_assert(kPreSmem <= 232448, "shared memory of one CTA");
 struct Deal {
     int tiles;     // items of the longest request allowed
     int pairs;     // pairs a group
+    bool dense;    // numbers that stand for an item are dealt out, rather than all numbers
     long long items;
 };
 
@@ -428,8 +429,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         if (a.flags)
             for (int b = blockIdx.x * 32 + lane; b < a.B; b += gridDim.x * 32)
                 a.flags[b] = range(b, q0, nq, k0, nk) ? 0 : PFKV_FLAG_BAD_LENGTH;
-        // A lane a number of the CTA's turns: with a max_q_len far above the lengths most
-        // numbers stand for no item.
+        // A lane a number (dense), or a number of the CTA's own turns: with a max_q_len far above
+        // the lengths most numbers stand for no item.
         int i = 0;
         auto publish = [&](const Item &it) {
             if (!bar_wait(&m.iempty[i % kItems], ((i / kItems) & 1) ^ 1, gave_up)) return false;
@@ -439,9 +440,11 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         };
         bool ok = true;
         Item it{};
-        for (long long turn0 = 0; ok && turn0 * gridDim.x < deal.items; turn0 += 32) {
-            const long long turn = turn0 + lane;
-            const long long x = turn * gridDim.x + ((turn & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        const long long turns = (deal.items + gridDim.x - 1) / gridDim.x;
+        uint32_t dealt = 0;  // items so far (dense)
+        for (long long at = 0; ok && at < (deal.dense ? deal.items : turns); at += 32) {
+            const long long turn = at + lane;
+            const long long x = deal.dense ? turn : turn * gridDim.x + ((turn & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
             const long long group = x / ((long long)deal.pairs * deal.tiles);
             const int in_group = (int)(x - group * deal.pairs * deal.tiles);
             const int t = deal.tiles - 1 - in_group / deal.pairs;
@@ -465,6 +468,13 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 };
                 it.n0 = steps(0);
                 it.n1 = steps(1);
+            }
+            if (deal.dense) {
+                const uint32_t all = __ballot_sync(0xffffffffu, there);
+                const uint32_t rank = dealt + __popc(all & ((1u << lane) - 1u)), round = rank / gridDim.x;
+                const uint32_t place = rank - round * gridDim.x;
+                there = there && ((round & 1) ? gridDim.x - 1 - place : place) == blockIdx.x;
+                dealt += __popc(all);
             }
             for (uint32_t left = __ballot_sync(0xffffffffu, there); ok && left; left &= left - 1, ++i) {
                 const int from = __ffs(left) - 1;
@@ -505,8 +515,18 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, int num_sms, cudaS
     Deal d;
     d.tiles = (int)((min((long long)a.max_q_len, a.total_q) + kItemRows - 1) / kItemRows);
     const long long pairs = (long long)a.B * a.H;
-    d.pairs = (int)min(pairs, d.tiles > 0 ? (2LL * num_sms + d.tiles - 1) / d.tiles : 1LL);
+    // One group, all items in order of their length, while K and V of all heads are at most 1.5
+    // times L2 (causal items of one length read them at different times).  Prompts of 3,000,
+    // 2,000 and 1,000 tokens, 64 heads (188 MiB): 242 us, 278 in groups; one of 4,096, 128
+    // heads (256 MiB): 502 us, 438 in groups.
+    // Where there are few numbers, every CTA can look through all of them (32 a step of the
+    // looking warp) and items alone are dealt out, which evens out ragged lengths: 5 prompts
+    // of up to 777 tokens, 16 heads, 26.5 us, 33.9 with all numbers dealt.
+    const bool fits = a.total_k * a.H * (PFKV_LATENT_NOPE + PFKV_LATENT_VDIM) * 2 <= (192LL << 20) &&
+                      pairs <= (1LL << 30) / max(1, d.tiles);  // numbers within a group are 32-bit
+    d.pairs = (int)min(pairs, fits ? pairs : (2LL * num_sms + d.tiles - 1) / max(1, d.tiles));
     d.items = (pairs + d.pairs - 1) / d.pairs * d.pairs * d.tiles;
+    d.dense = d.items <= 16LL * num_sms;
     const unsigned grid = (unsigned)max(1LL, min(d.items, (long long)num_sms));
     // a negative scale is the operands' sign: the softmax works with its magnitude
     const uint32_t idS = umma_idesc(kQTile, kKeys, true, false, false) | (a.sm_scale < 0.f ? 1u << 13 : 0u);
