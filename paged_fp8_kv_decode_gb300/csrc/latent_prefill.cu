@@ -21,10 +21,10 @@
 // What bounds it: one thread issues all products of the CTA, and they need it to be
 // quick.  A wait between two groups of them, satisfied or not, costs the tensor cores
 // about 140 cycles, and loops and descriptors in 64 bits as much again: 4,096 tokens of
-// 128 heads took 704 us with those, 473 us with barriers asked a group ahead and straight
+// 128 heads took 704 us with those, 477 us with barriers asked a group ahead and straight
 // code.  Then shared memory: S reads 128 bytes a cycle, all there is, and the copies of
 // K and V write beside it (1.39 us a pair of steps without them, 1.64 with them; the
-// whole kernel 1.75).  That is 1,450 TFLOP/s.
+// whole kernel 1.75).  That is 1,440 TFLOP/s.
 //
 // The kernel is persistent.  Work items are ordered so that the CTAs at work share
 // the K and V of few heads (about two rounds of items a group of heads, or all heads
