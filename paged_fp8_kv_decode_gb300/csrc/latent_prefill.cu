@@ -45,6 +45,7 @@ constexpr int kKSlots = 4, kKChunks = 3;  // K: chunks 0 and 1, rotated
 constexpr int kVSlots = 2;                // V: both chunks
 constexpr int kPreThreads = 384;
 constexpr int kItems = 3;               // items looked up ahead
+constexpr int kItemTries = 100 * kTries;  // waits that last as long as an item: 2^31 keys take 30 s
 constexpr uint32_t kOffK = 2 * kKChunks * kSlotB, kOffV = kOffK + kKSlots * kSlotB;
 constexpr uint32_t kOffPre = kOffV + kVSlots * 2 * kSlotB;
 constexpr uint32_t kColO = 256;
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 #pragma unroll 1
                 for (int tile = 0; tile < 2; ++tile) {
                     if ((tile ? n1 : n0) == 0 || !ok) continue;
-                    ok = bar_wait(&m.qempty[tile], ((used >> tile) & 1) ^ 1, gave_up);
+                    ok = bar_wait<kItemTries>(&m.qempty[tile], ((used >> tile) & 1) ^ 1, gave_up);
                     used ^= 1u << tile;
                     if (!ok) continue;
                     uint64_t *full = &m.qfull[tile];
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         // the lengths most numbers stand for no item.
         int i = 0;
         auto publish = [&](const Item &it) {
-            if (!bar_wait(&m.iempty[i % kItems], ((i / kItems) & 1) ^ 1, gave_up)) return false;
+            if (!bar_wait<kItemTries>(&m.iempty[i % kItems], ((i / kItems) & 1) ^ 1, gave_up)) return false;
             m.item[i % kItems] = it;
             bar_arrive(&m.ifull[i % kItems]);
             return true;
