@@ -61,11 +61,12 @@ def _rows(x: torch.Tensor, packed: bool, heads: bool, name: str, dim: int) -> _C
     want = 2 + (not packed) + heads
     if x.dtype != _BF16 or len(s) != want or s[-1] != 1:
         raise ValueError(f"{name}: bfloat16 tensor of {want} dimensions with contiguous rows")
-    if x.shape[-1] != dim:
+    if x.size(-1) != dim:
         raise ValueError(f"{name}: rows of {dim} elements")
+    p = x.data_ptr() if x.is_cuda else B._ptr(x)
     if packed:
-        return _CRows(B._ptr(x), 0, s[0], s[1] if heads else 0)
-    return _CRows(B._ptr(x), s[0], s[1], s[2] if heads else 0)
+        return _CRows(p, 0, s[0], s[1] if heads else 0)
+    return _CRows(p, s[0], s[1], s[2] if heads else 0)
 
 
 def _here(x: torch.Tensor) -> None:
