@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int w = blockIdx.x >> 1;
     if (tid == 0) {
         for (int c = 0; c < kKStages; ++c) {
-            mbar_init(&m.kfull[c], c < 4 && FP8 ? 2 : 1);
+            mbar_init(&m.kfull[c], 2);  // both CTAs, whether or not they bring keys
             mbar_init(&m.kempty[c], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -709,7 +709,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) id[i] = ti.id[rank * 4 + i];
                 if (!bar_wait(&m.kempty[4], (t & 1) ^ 1, gave_up)) break;
+                // The odd CTA arrives too, with its ids in registers: where its four pages are
+                // past the last token its bytes hold nothing up, and the ring's entry and the
+                // barriers' phases would go on without it.
                 if (rank == 0) mbar_arrive_expect_tx(&m.kfull[4], pages * 2048u);  // both CTAs' bytes
+                else bar_arrive_at(&m.kfull[4], 0);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (id[i] >= 0) tma_box3_pair(k + 8 * kChunkB + i * 2048, &mapr, 0, 0, id[i], &m.kfull[4], pol);
@@ -718,6 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < 4; ++c) {
                         if (!bar_wait(&m.kempty[c], (t & 1) ^ 1, gave_up)) break;
                         if (rank == 0) mbar_arrive_expect_tx(&m.kfull[c], pages * 4096u);
+                        else bar_arrive_at(&m.kfull[c], 0);
                         uint8_t *dst = k + 2 * c * kChunkB;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
