@@ -751,17 +751,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint8_t *dst = v + nb * 2 * kVChunkB;
                 const int x = (nb * 4 + (int)rank * 2) * 64;
                 if (elect_one()) {
+                    // The ids are read before the arrival: where no page is to be read nothing
+                    // else holds up the products, and with them the entry's refill.
+                    int id[kTilePages];
                     uint32_t pages = 0;
-                    for (int i = 0; i < full; ++i) pages += ti.id[i] >= 0;
+#pragma unroll
+                    for (int i = 0; i < kTilePages; ++i) {
+                        id[i] = i < full ? ti.id[i] : -1;
+                        pages += id[i] >= 0;
+                    }
                     // the even CTA counts both CTAs' bytes
                     if (rank == 0 && full == kTilePages) mbar_arrive_expect_tx(&m.vfull[nb], pages * 8192u);
                     else if (rank == 0) bar_expect_tx(&m.vfull[nb], pages * 8192u);
                     else if (full == kTilePages) bar_arrive_at(&m.vfull[nb], 0);
 #pragma unroll
                     for (int i = 0; i < kTilePages; ++i) {
-                        const int id = ti.id[i];
-                        if (i >= full || id < 0) continue;
-                        tma_box4_pair(dst + i * 4096, &mapc, 0, 0, x / 64, id, &m.vfull[nb], pol);
+                        if (id[i] < 0) continue;
+                        tma_box4_pair(dst + i * 4096, &mapc, 0, 0, x / 64, id[i], &m.vfull[nb], pol);
                     }
                 }
                 __syncwarp();
