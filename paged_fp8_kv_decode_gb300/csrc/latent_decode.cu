@@ -690,9 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (flags & kLast) ++seg;
             }
             if (N > 0) values(N - 1, pfirst);
-            // nothing in flight when the CTAs leave
             umma_commit_pair(&m.drain);
-            bar_drain(&m.drain, 0);
         }
         __syncwarp();
     } else if (warp == 9) {
@@ -938,6 +936,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     if (tid == 0) parts.gave_up[w * 2 + rank] = m.gave_up;
+    // Nothing in flight when the CTAs leave: the products' last arrivals come to the barriers
+    // of both, and each waits for its own (that the even CTA's have come says nothing of the
+    // odd one's).
+    if (warp == 8 && elect_one()) bar_drain(&m.drain, 0);
+    __syncwarp();
     tmem_fence_before();
     cluster_sync();  // the even CTA's products read the odd one's shared memory
     tmem_fence_after();
