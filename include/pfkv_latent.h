@@ -167,7 +167,8 @@ pfkv_status pfkv_latent_decode_attn(const pfkv_latent_cache *cache, const pfkv_p
  *             flagged PFKV_FLAG_BAD_LENGTH); a bound far above the lengths costs time
  *   causal  : nonzero: query i of nq sees keys j <= i + nk - nq (the queries are
  *             the last of the keys' tokens); zero: every key
- *   flags   : uint8 [batch], written, with PFKV_FLAG_DEVICE_TIMEOUT as above; may be NULL
+ *   flags   : uint8 [batch], written; PFKV_FLAG_DEVICE_TIMEOUT in all of them where a
+ *             wait inside the kernel gave up (any row may then be unwritten); may be NULL
  *
  * A query that sees no key gives a zero row.  A request whose rows are not
  * within the arrays is flagged and nothing of it is written.  Rows outside every
@@ -182,6 +183,20 @@ pfkv_status pfkv_latent_prefill_attn(int32_t batch, int32_t num_heads, const int
                                      const pfkv_rows *k_rope, const pfkv_rows *v, float sm_scale,
                                      int32_t causal, const pfkv_rows *out, uint8_t *flags,
                                      void *stream);
+
+/*
+ * pfkv_selftest_latent_prefill -- pfkv_latent_prefill_attn with waits that give up
+ * after `tries` tries (0 .. 100000, which is what the call itself takes; about 4 us
+ * each), so that a test can let them run out: the call ends, its requests are flagged
+ * PFKV_FLAG_DEVICE_TIMEOUT, and the context stays usable.
+ */
+pfkv_status pfkv_selftest_latent_prefill(int32_t tries, int32_t batch, int32_t num_heads,
+                                         const int32_t *q_starts, const int32_t *k_starts,
+                                         int64_t total_q, int64_t total_k, int32_t max_q_len,
+                                         const pfkv_rows *q_nope, const pfkv_rows *q_rope,
+                                         const pfkv_rows *k_nope, const pfkv_rows *k_rope,
+                                         const pfkv_rows *v, float sm_scale, int32_t causal,
+                                         const pfkv_rows *out, uint8_t *flags, void *stream);
 
 #ifdef __cplusplus
 }

@@ -238,6 +238,16 @@ pfkv_status pfkv_latent_prefill_attn(int32_t batch, int32_t num_heads, const int
                                      const pfkv_rows *q_nope, const pfkv_rows *q_rope, const pfkv_rows *k_nope,
                                      const pfkv_rows *k_rope, const pfkv_rows *v, float sm_scale, int32_t causal,
                                      const pfkv_rows *out, uint8_t *flags, void *stream) {
+    return pfkv_selftest_latent_prefill(kTries, batch, num_heads, q_starts, k_starts, total_q, total_k, max_q_len,
+                                        q_nope, q_rope, k_nope, k_rope, v, sm_scale, causal, out, flags, stream);
+}
+
+pfkv_status pfkv_selftest_latent_prefill(int32_t tries, int32_t batch, int32_t num_heads, const int32_t *q_starts,
+                                         const int32_t *k_starts, int64_t total_q, int64_t total_k, int32_t max_q_len,
+                                         const pfkv_rows *q_nope, const pfkv_rows *q_rope, const pfkv_rows *k_nope,
+                                         const pfkv_rows *k_rope, const pfkv_rows *v, float sm_scale, int32_t causal,
+                                         const pfkv_rows *out, uint8_t *flags, void *stream) {
+    if (tries < 0 || tries > kTries) return PFKV_ERR_INVALID_ARG;
     if (batch < 0 || num_heads <= 0 || total_q < 0 || total_k < 0 || max_q_len < 0) return PFKV_ERR_INVALID_ARG;
     if (!std::isfinite(sm_scale)) return PFKV_ERR_INVALID_ARG;
     if (batch == 0) return PFKV_OK;
@@ -279,6 +289,8 @@ pfkv_status pfkv_latent_prefill_attn(int32_t batch, int32_t num_heads, const int
     a.max_q_len = max_q_len;
     a.causal = causal != 0;
     a.sm_scale = sm_scale;
+    a.tries = tries;
+    a.item_tries = 100 * tries;
     return launch_latent_prefill(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PFKV_OK : PFKV_ERR_CUDA;
 }
 

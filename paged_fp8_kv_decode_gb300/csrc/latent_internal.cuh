@@ -19,6 +19,9 @@ pfkv_status check_rows(const pfkv_rows *r, bool use_b, bool use_h);
 // host checks (latent.cu)
 pfkv_status check_latent(const pfkv_latent_cache *c, const pfkv_pages *p);
 
+// Tries of a wait inside the attention kernels (umma.cuh), unless a self-test asks for fewer.
+constexpr int kTries = 100000;
+
 struct RowsArg {
     __nv_bfloat16 *p;
     long long sb, st, sh;
@@ -96,6 +99,7 @@ struct LatentPrefillArgs {
     uint8_t *flags;
     int B, H, max_q_len, causal;
     float sm_scale;
+    int tries, item_tries;  // of a wait, and of one that lasts as long as an item
 };
 
 size_t latent_decode_workspace(int B, int H, int kq, int max_seq_len, int num_sms);

@@ -32,7 +32,7 @@
 // that change direction, so that each CTA gets long and short ones.
 //
 // Roles of a CTA's twelve warps: 0-3 and 4-7 softmax and output of the two tiles; 8
-// issues the products; 9 loads K and V, 10 loads Q (TMA); 11 looks up items.
+// issues the products; 9 loads K and V, 10 loads Q (TMA); 11 looks up items.  The flags are written by a launch before it.
 #include "latent_internal.cuh"
 #include "umma.cuh"
 
@@ -45,7 +45,6 @@ constexpr int kKSlots = 4, kKChunks = 3;  // K: chunks 0 and 1, rotated
 constexpr int kVSlots = 2;                // V: both chunks
 constexpr int kPreThreads = 384;
 constexpr int kItems = 3;               // items looked up ahead
-constexpr int kItemTries = 100 * kTries;  // waits that last as long as an item: 2^31 keys take 30 s
 constexpr uint32_t kOffK = 2 * kKChunks * kSlotB, kOffV = kOffK + kKSlots * kSlotB;
 constexpr uint32_t kOffPre = kOffV + kVSlots * 2 * kSlotB;
 constexpr uint32_t kColO = 256;
@@ -83,6 +82,26 @@ struct Deal {
     bool dense;    // numbers that stand for an item are dealt out, rather than all numbers
     long long items;
 };
+
+// The rows of request b; false where they are not within the arrays or the bound.
+__device__ __forceinline__ bool request_rows(const LatentPrefillArgs &a, int b, int &q0, int &nq, int &k0, int &nk) {
+    q0 = a.q_starts[b];
+    const int q1 = a.q_starts[b + 1], k1 = a.k_starts[b + 1];
+    k0 = a.k_starts[b];
+    nq = q1 - q0;
+    nk = k1 - k0;
+    return q0 >= 0 && q1 >= q0 && q1 <= a.total_q && k0 >= 0 && k1 >= k0 && k1 <= a.total_k && nq <= a.max_q_len;
+}
+
+// The flags that depend on the starts alone: in a launch of its own, so that no CTA that starts
+// late writes over the flag of one whose waits gave up.
+constexpr int kFlagThreads = 256;
+__global__ void __launch_bounds__(kFlagThreads) latent_prefill_flags_kernel(LatentPrefillArgs a) {
+    pdl_enter();
+    int q0, nq, k0, nk;
+    for (long long b = (long long)blockIdx.x * kFlagThreads + threadIdx.x; b < a.B; b += gridDim.x * kFlagThreads)
+        a.flags[b] = request_rows(a, (int)b, q0, nq, k0, nk) ? 0 : PFKV_FLAG_BAD_LENGTH;
+}
 
 __global__ void __launch_bounds__(kPreThreads, 1)
     latent_prefill_kernel(const __grid_constant__ CUtensorMap mapqn, const __grid_constant__ CUtensorMap mapqr,
@@ -126,7 +145,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     volatile uint32_t *const gave_up = &m.gave_up;
     // Waits for item number i of this CTA; false when there is none, or a wait has given up.
     auto item_ready = [&](int i) {
-        return bar_wait(&m.ifull[i % kItems], (i / kItems) & 1, gave_up) && m.item[i % kItems].b >= 0;
+        return bar_wait(&m.ifull[i % kItems], (i / kItems) & 1, gave_up, a.tries) && m.item[i % kItems].b >= 0;
     };
 
     if (warp < 8) {
@@ -147,7 +166,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             float ref = kMinusInf, sum = 0.f;
             bool ok = true;
             for (int j = 0; j < steps; ++j, ++done) {
-                ok = bar_wait(&m.sfull[tile], done & 1, gave_up);
+                ok = bar_wait(&m.sfull[tile], done & 1, gave_up, a.tries);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 tmem_fence_after();
                 float x[4][32];
@@ -190,7 +209,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                     // key rows past the request's last may hold anything, NaN among it, and
                     // meet weights of zero: V's are zeroed where they lie
                     const uint32_t pos = base_pos + j;
-                    ok = bar_wait(&m.vfull[pos % kVSlots], (pos / kVSlots) & 1, gave_up);
+                    ok = bar_wait(&m.vfull[pos % kVSlots], (pos / kVSlots) & 1, gave_up, a.tries);
                     uint4 *v = reinterpret_cast<uint4 *>(psm + kOffV + (pos % kVSlots) * 2 * kSlotB);
 #pragma unroll 1
                     for (int e = (nk - j * kKeys) * 8 + r; e < kKeys * 8; e += kQTile) {
@@ -228,7 +247,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 sum += s2.x + s2.y;
             }
             if (steps > 0) {
-                ok = bar_wait(&m.odone[tile], outs++ & 1, gave_up) && ok;
+                ok = bar_wait(&m.odone[tile], outs++ & 1, gave_up, a.tries) && ok;
                 tmem_fence_after();
             }
             ok = __all_sync(0xffffffffu, ok);
@@ -257,7 +276,6 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                     *reinterpret_cast<uint4 *>(out + g * 32 + e) = make_uint4(u[0], u[1], u[2], u[3]);
                 }
             }
-            if (!ok && lane == 0 && a.flags) atomic_or_byte(a.flags, it.b, PFKV_FLAG_DEVICE_TIMEOUT);
             base_pos += max(it.n0, it.n1);
             tmem_fence_before();
             __syncwarp();
@@ -288,14 +306,14 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 bool keys = T == 0 && bar_passed(&m.kfull[kstart % kKSlots], (kstart / kKSlots) & 1);
                 if (j > 0 && j <= mine) {
                     const uint32_t pos = vpos + j - 1, slot = pos % kVSlots, parity = weighed++ & 1;
-                    if (!ready && !bar_wait(&m.pready[T][0], parity, gave_up)) return false;
-                    if ((T == 0 ? !ready : j > n0) && !bar_wait(&m.vfull[slot], (pos / kVSlots) & 1, gave_up)) return false;
+                    if (!ready && !bar_wait(&m.pready[T][0], parity, gave_up, a.tries)) return false;
+                    if ((T == 0 ? !ready : j > n0) && !bar_wait(&m.vfull[slot], (pos / kVSlots) & 1, gave_up, a.tries)) return false;
                     const bool rest = bar_passed(&m.pready[T][1], parity);
                     tmem_fence_after();
                     const uint32_t db = umma_desc(va + slot * 2 * kSlotB, kSlotB);
 #pragma unroll
                     for (int s = 0; s < 4; ++s) umma_ts(tmem + co, tmem + cs + s * 8, db + s * 128, idO, j > 1 || s > 0);
-                    if (!rest && !bar_wait(&m.pready[T][1], parity, gave_up)) return false;
+                    if (!rest && !bar_wait(&m.pready[T][1], parity, gave_up, a.tries)) return false;
                     tmem_fence_after();
 #pragma unroll
                     for (int s = 4; s < 8; ++s) umma_ts(tmem + co, tmem + cs + s * 8, db + s * 128, idO, true);
@@ -304,12 +322,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 }
                 ready = false;
                 if (j >= mine) return true;
-                if (j == 0 && !bar_wait(&m.qfull[T], items++ & 1, gave_up)) return false;
+                if (j == 0 && !bar_wait(&m.qfull[T], items++ & 1, gave_up, a.tries)) return false;
                 const uint32_t da = umma_desc(qa + T * kKChunks * kSlotB, 16);
 #pragma unroll
                 for (int c = 0; c < kKChunks; ++c) {
                     const uint32_t at = kstart + c, slot = at % kKSlots;
-                    if (first && !keys && !bar_wait(&m.kfull[slot], (at / kKSlots) & 1, gave_up)) return false;
+                    if (first && !keys && !bar_wait(&m.kfull[slot], (at / kKSlots) & 1, gave_up, a.tries)) return false;
                     if (c + 1 < kKChunks) {
                         keys = T == 0 && bar_passed(&m.kfull[(at + 1) % kKSlots], ((at + 1) / kKSlots) & 1);
                     } else {
@@ -361,7 +379,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 #pragma unroll 1
                     for (int c = 0; ok && c < kKChunks; ++c, ++kpos) {
                         const uint32_t slot = kpos % kKSlots;
-                        ok = bar_wait(&m.kempty[slot], ((kpos / kKSlots) & 1) ^ 1, gave_up);
+                        ok = bar_wait(&m.kempty[slot], ((kpos / kKSlots) & 1) ^ 1, gave_up, a.tries);
                         if (!ok) break;
                         uint8_t *dst = psm + kOffK + slot * kSlotB;
                         mbar_arrive_expect_tx(&m.kfull[slot], kSlotB);
@@ -369,7 +387,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                         else tma_box3(dst, &mapkr, 0, 0, y, &m.kfull[slot], pol);
                     }
                     const uint32_t slot = vpos % kVSlots;
-                    ok = ok && bar_wait(&m.vempty[slot], ((vpos / kVSlots) & 1) ^ 1, gave_up);
+                    ok = ok && bar_wait(&m.vempty[slot], ((vpos / kVSlots) & 1) ^ 1, gave_up, a.tries);
                     if (!ok) break;
                     uint8_t *dst = psm + kOffV + slot * 2 * kSlotB;
                     mbar_arrive_expect_tx(&m.vfull[slot], 2 * kSlotB);
@@ -397,7 +415,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 #pragma unroll 1
                 for (int tile = 0; tile < 2; ++tile) {
                     if ((tile ? n1 : n0) == 0 || !ok) continue;
-                    ok = bar_wait<kItemTries>(&m.qempty[tile], ((used >> tile) & 1) ^ 1, gave_up);
+                    ok = bar_wait(&m.qempty[tile], ((used >> tile) & 1) ^ 1, gave_up, a.item_tries);
                     used ^= 1u << tile;
                     if (!ok) continue;
                     uint64_t *full = &m.qfull[tile];
@@ -416,25 +434,14 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
         __syncwarp();
     } else {
-        // -------------------------- items, and the flags --------------------------
+        // -------------------------------- items --------------------------------
         reg_share_less<88>();
-        auto range = [&](int b, int &q0, int &nq, int &k0, int &nk) {
-            q0 = a.q_starts[b];
-            const int q1 = a.q_starts[b + 1], k1 = a.k_starts[b + 1];
-            k0 = a.k_starts[b];
-            nq = q1 - q0;
-            nk = k1 - k0;
-            return q0 >= 0 && q1 >= q0 && q1 <= a.total_q && k0 >= 0 && k1 >= k0 && k1 <= a.total_k && nq <= a.max_q_len;
-        };
         int q0, nq, k0, nk;
-        if (a.flags)
-            for (int b = blockIdx.x * 32 + lane; b < a.B; b += gridDim.x * 32)
-                a.flags[b] = range(b, q0, nq, k0, nk) ? 0 : PFKV_FLAG_BAD_LENGTH;
         // A lane a number (dense), or a number of the CTA's own turns: with a max_q_len far above
         // the lengths most numbers stand for no item.
         int i = 0;
         auto publish = [&](const Item &it) {
-            if (!bar_wait<kItemTries>(&m.iempty[i % kItems], ((i / kItems) & 1) ^ 1, gave_up)) return false;
+            if (!bar_wait(&m.iempty[i % kItems], ((i / kItems) & 1) ^ 1, gave_up, a.item_tries)) return false;
             m.item[i % kItems] = it;
             bar_arrive(&m.ifull[i % kItems]);
             return true;
@@ -454,7 +461,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             if (there) {
                 it.b = (int)(pair / a.H);
                 it.h = (int)(pair - (long long)it.b * a.H);
-                there = range(it.b, q0, nq, k0, nk) && t * kItemRows < nq;
+                there = request_rows(a, it.b, q0, nq, k0, nk) && t * kItemRows < nq;
             }
             if (there) {
                 it.q0 = q0 + t * kItemRows;
@@ -489,6 +496,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         __syncwarp();
     }
     __syncthreads();
+    // After a wait gave up, items of this CTA are left unwritten; which ones is not kept, and
+    // every request of the call is flagged.
+    if (*gave_up && a.flags)
+        for (int b = tid; b < a.B; b += kPreThreads) atomic_or_byte(a.flags, b, PFKV_FLAG_DEVICE_TIMEOUT);
     tmem_fence_after();
     if (warp == 8) tmem_free512<1>(tmem);
 }
@@ -529,6 +540,11 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, int num_sms, cudaS
     d.items = (pairs + d.pairs - 1) / d.pairs * d.pairs * d.tiles;
     d.dense = d.items <= 16LL * num_sms;
     const unsigned grid = (unsigned)max(1LL, min(d.items, (long long)num_sms));
+    if (a.flags) {
+        const unsigned ctas = (unsigned)min((a.B + kFlagThreads - 1LL) / kFlagThreads, 4LL * num_sms);
+        e = launch_pdl(latent_prefill_flags_kernel, dim3(ctas), dim3(kFlagThreads), 0, s, a);
+        if (e != cudaSuccess) return e;
+    }
     // a negative scale is the operands' sign: the softmax works with its magnitude
     const uint32_t idS = umma_idesc(kQTile, kKeys, true, false, false) | (a.sm_scale < 0.f ? 1u << 13 : 0u);
     return launch_pdl(latent_prefill_kernel, dim3(grid), dim3(kPreThreads), kPreSmem, s, qn, qr, kn, kr, v, a, d, idS,
@@ -538,7 +554,8 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, int num_sms, cudaS
 cudaError_t preload_latent_prefill() {
     const cudaError_t e =
         cudaFuncSetAttribute(latent_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPreSmem);
-    return e == cudaSuccess ? preload_kernel(latent_prefill_kernel) : e;
+    const cudaError_t f = e == cudaSuccess ? preload_kernel(latent_prefill_kernel) : e;
+    return f == cudaSuccess ? preload_kernel(latent_prefill_flags_kernel) : f;
 }
 
 }  // namespace pfkv

@@ -6,7 +6,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include "pfkv_internal.cuh"
+#include "latent_internal.cuh"
 
 namespace pfkv {
 namespace {
@@ -170,17 +170,15 @@ __device__ __forceinline__ void bar_arrive_at(uint64_t *bar, uint32_t rank) {
 }
 
 // Waits that give up.  A try sleeps until the phase completes, or for about kSleepNs
-// at most; after kTries of them (0.40 s, measured: 4 us a try) `gave_up` is
+// at most; after `tries` of them (kTries: 0.40 s, measured: 4 us a try) `gave_up` is
 // set, every later wait of the CTA returns soon, and the roles run to their end
 // without issuing copies or products.  Returns false then.  (Short on purpose: with
 // five roles at work the instruction cache is what is scarce, and a wait is inlined
 // in thirty places.)
 constexpr uint32_t kSleepNs = 20000;
-constexpr int kTries = 100000;
-template <int Tries = kTries>
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *gave_up) {
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *gave_up, int tries = kTries) {
 #pragma unroll 1
-    for (int i = 0; i < Tries; ++i) {
+    for (int i = 0; i < tries; ++i) {
         uint32_t ok;
         asm volatile(
             "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"

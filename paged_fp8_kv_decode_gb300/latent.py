@@ -22,7 +22,7 @@ PFKV_LATENT_VDIM = 128
 
 # every symbol include/pfkv_latent.h declares
 EXPORTED = ("pfkv_latent_append", "pfkv_latent_gather", "pfkv_latent_decode_workspace_size",
-            "pfkv_latent_decode_attn", "pfkv_latent_prefill_attn")
+            "pfkv_latent_decode_attn", "pfkv_latent_prefill_attn", "pfkv_selftest_latent_prefill")
 
 
 class _CLatentCache(ctypes.Structure):
@@ -78,6 +78,7 @@ def lib() -> ctypes.CDLL:
                                               rows, P, P]
         L.pfkv_latent_prefill_attn.argtypes = [I32, I32, P, P, I64, I64, I32, rows, rows, rows,
                                                rows, rows, F, I32, rows, P, P]
+        L.pfkv_selftest_latent_prefill.argtypes = [I32, *L.pfkv_latent_prefill_attn.argtypes]
         for name in EXPORTED:
             getattr(L, name).restype = ctypes.c_int
         L._latent_calls = True
@@ -166,6 +167,19 @@ def pfkv_latent_prefill_attn(q_nope: torch.Tensor, q_rope: torch.Tensor, k_nope:
     """Packed rows: q_nope, out: bf16 [rows][H][128], q_rope: [rows][H][64],
     k_nope, v: [key rows][H][128], k_rope: [key rows][64]; q_starts, k_starts:
     int32 [B + 1]; any strides that leave rows contiguous; the rows in device memory."""
+    _prefill((), q_nope, q_rope, k_nope, k_rope, v, q_starts, k_starts, max_q_len, sm_scale, causal,
+             out, flags, stream)
+
+
+def pfkv_selftest_latent_prefill(tries: int, *args, flags: Optional[torch.Tensor] = None,
+                                 stream=None) -> None:
+    """pfkv_latent_prefill_attn (whose positional arguments follow) with waits that
+    give up after ``tries`` tries."""
+    _prefill((int(tries),), *args, flags, stream)
+
+
+def _prefill(tries, q_nope, q_rope, k_nope, k_rope, v, q_starts, k_starts, max_q_len, sm_scale,
+             causal, out, flags, stream) -> None:
     (Tq, H), Tk = q_nope.shape[:2], k_nope.shape[0]
     if (q_nope.shape[:2] != q_rope.shape[:2] or q_nope.shape[:2] != out.shape[:2]
             or k_nope.shape[:2] != v.shape[:2] or k_nope.shape[1] != H or k_rope.shape[0] != Tk
@@ -178,8 +192,8 @@ def pfkv_latent_prefill_attn(q_nope: torch.Tensor, q_rope: torch.Tensor, k_nope:
         (q_nope, True, "q_nope", PFKV_LATENT_NOPE), (q_rope, True, "q_rope", PFKV_LATENT_ROPE),
         (k_nope, True, "k_nope", PFKV_LATENT_NOPE), (k_rope, False, "k_rope", PFKV_LATENT_ROPE),
         (v, True, "v", PFKV_LATENT_VDIM), (out, True, "out", PFKV_LATENT_VDIM))]
-    B._check(lib().pfkv_latent_prefill_attn(
-        int(q_starts.numel()) - 1, H, R._i32(q_starts, "q_starts"), R._i32(k_starts, "k_starts"),
+    name = "pfkv_selftest_latent_prefill" if tries else "pfkv_latent_prefill_attn"
+    B._check(getattr(lib(), name)(
+        *tries, int(q_starts.numel()) - 1, H, R._i32(q_starts, "q_starts"), R._i32(k_starts, "k_starts"),
         Tq, Tk, int(max_q_len), *[ctypes.byref(r) for r in rows[:5]], float(sm_scale),
-        int(bool(causal)), ctypes.byref(rows[5]), B._ptr(flags), B._stream(stream)),
-        "pfkv_latent_prefill_attn")
+        int(bool(causal)), ctypes.byref(rows[5]), B._ptr(flags), B._stream(stream)), name)

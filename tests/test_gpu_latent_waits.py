@@ -1,0 +1,53 @@
+"""Waits inside the attention kernels that give up: the call ends, every request of it
+that may lack rows is flagged, and the next call is sound.  The limit is an argument of
+the self-test entry points, so no wait has to last."""
+import pytest
+import torch
+
+import test_gpu_latent_prefill as P
+from latent_cases import SCALE, flags_for, gen, i32
+from paged_fp8_kv_decode_gb300 import binding as B
+from paged_fp8_kv_decode_gb300 import latent as L
+
+pytestmark = pytest.mark.gpu
+
+NEVER = 1000                                         # 4 ms: not in sound calls of microseconds
+
+
+def prefill(tries, x, qs, ks, max_q, causal=True):
+    out = torch.full(x["qn"].shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    fl = flags_for(len(qs) - 1)
+    fl.fill_(0x55)
+    L.pfkv_selftest_latent_prefill(tries, x["qn"], x["qr"], x["kn"], x["kr"], x["v"], i32(qs), i32(ks), max_q, SCALE, causal,
+                                   out, flags=fl)
+    torch.cuda.synchronize()
+    assert (fl[len(qs) - 1:] == 0x55).all()
+    return out, fl[:len(qs) - 1].tolist()
+
+
+def test_prefill_flags_all_that_a_wait_left_unwritten():
+    g = gen(91)
+    nq = [300, 1, 64, 0, 700] * 40                   # several items a CTA
+    qs = P.starts_of(nq)
+    x = P.inputs(g, sum(nq), sum(nq), 8)
+    want, fl = P.run(x, qs, qs, max(nq))
+    assert not any(fl)
+    for tries in (0, NEVER):
+        out, fl = prefill(tries, x, qs, qs, max(nq))
+        assert fl == [0 if tries else B.PFKV_FLAG_DEVICE_TIMEOUT] * len(nq)
+        assert torch.equal(out, want) if tries else (out == 7.0).all()
+    bad = list(qs)
+    bad[3] = -5                                      # two requests whose rows are refused besides
+    _, fl = prefill(0, x, bad, qs, max(nq))
+    assert fl[:5] == [8, 8, 12, 12, 8]
+    out, fl = P.run(x, qs, qs, max(nq))              # the call after it
+    assert not any(fl) and torch.equal(out, want)
+
+
+def test_prefill_refuses_a_limit_beyond_its_own():
+    g = gen(92)
+    x = P.inputs(g, 5, 5, 1)
+    for tries in (-1, 100001):
+        with pytest.raises(B.PfkvError) as e:
+            prefill(tries, x, [0, 5], [0, 5], 5)
+        assert e.value.status == B.PFKV_ERR_INVALID_ARG
