@@ -186,8 +186,8 @@ pfkv_status pfkv_latent_prefill_attn(int32_t batch, int32_t num_heads, const int
 
 /*
  * pfkv_selftest_latent_prefill -- pfkv_latent_prefill_attn with waits that give up
- * after `tries` tries (0 .. 100000, which is what the call itself takes; about 4 us
- * each), so that a test can let them run out: the call ends, its requests are flagged
+ * after `tries` tries (0 .. 100000, which is what the call itself takes; 0.2 to 4 us
+ * each; 1000 times as many for waits that last as long as a tile's work), so that a test can let them run out: the call ends, its requests are flagged
  * PFKV_FLAG_DEVICE_TIMEOUT, and the context stays usable.
  */
 pfkv_status pfkv_selftest_latent_prefill(int32_t tries, int32_t batch, int32_t num_heads,

@@ -290,7 +290,6 @@ pfkv_status pfkv_selftest_latent_prefill(int32_t tries, int32_t batch, int32_t n
     a.causal = causal != 0;
     a.sm_scale = sm_scale;
     a.tries = tries;
-    a.item_tries = 100 * tries;
     return launch_latent_prefill(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PFKV_OK : PFKV_ERR_CUDA;
 }
 

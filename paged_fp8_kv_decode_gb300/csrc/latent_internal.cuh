@@ -21,6 +21,9 @@ pfkv_status check_latent(const pfkv_latent_cache *c, const pfkv_pages *p);
 
 // Tries of a wait inside the attention kernels (umma.cuh), unless a self-test asks for fewer.
 constexpr int kTries = 100000;
+// Of one that lasts as long as an item of a prompt (436 million keys, all that memory holds, take
+// 6 s): 20 s at least.  It ends as soon as another wait of its CTA gives up.
+constexpr int kItemTries = 1000 * kTries;
 
 struct RowsArg {
     __nv_bfloat16 *p;
@@ -99,7 +102,7 @@ struct LatentPrefillArgs {
     uint8_t *flags;
     int B, H, max_q_len, causal;
     float sm_scale;
-    int tries, item_tries;  // of a wait, and of one that lasts as long as an item
+    int tries;  // of a wait
 };
 
 size_t latent_decode_workspace(int B, int H, int kq, int max_seq_len, int num_sms);

@@ -103,6 +103,8 @@ __global__ void __launch_bounds__(kFlagThreads) latent_prefill_flags_kernel(Late
         a.flags[b] = request_rows(a, (int)b, q0, nq, k0, nk) ? 0 : PFKV_FLAG_BAD_LENGTH;
 }
 
+// Selftest: waits of as many tries as the call says (as arguments the limits cost 0.7 us a call).
+template <bool Selftest>
 __global__ void __launch_bounds__(kPreThreads, 1)
     latent_prefill_kernel(const __grid_constant__ CUtensorMap mapqn, const __grid_constant__ CUtensorMap mapqr,
                           const __grid_constant__ CUtensorMap mapkn, const __grid_constant__ CUtensorMap mapkr,
@@ -143,9 +145,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     pdl_enter();
     const uint32_t tmem = m.tmem;
     volatile uint32_t *const gave_up = &m.gave_up;
+    const int tries = Selftest ? a.tries : kTries, item_tries = Selftest ? a.tries * (kItemTries / kTries) : kItemTries;
     // Waits for item number i of this CTA; false when there is none, or a wait has given up.
     auto item_ready = [&](int i) {
-        return bar_wait(&m.ifull[i % kItems], (i / kItems) & 1, gave_up, a.tries) && m.item[i % kItems].b >= 0;
+        return bar_wait(&m.ifull[i % kItems], (i / kItems) & 1, gave_up, item_tries) && m.item[i % kItems].b >= 0;
     };
 
     if (warp < 8) {
@@ -166,7 +169,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             float ref = kMinusInf, sum = 0.f;
             bool ok = true;
             for (int j = 0; j < steps; ++j, ++done) {
-                ok = bar_wait(&m.sfull[tile], done & 1, gave_up, a.tries);
+                // an item's first scores come when the other tile is done with the item before it
+                ok = bar_wait(&m.sfull[tile], done & 1, gave_up, item_tries);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 tmem_fence_after();
                 float x[4][32];
@@ -209,7 +213,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                     // key rows past the request's last may hold anything, NaN among it, and
                     // meet weights of zero: V's are zeroed where they lie
                     const uint32_t pos = base_pos + j;
-                    ok = bar_wait(&m.vfull[pos % kVSlots], (pos / kVSlots) & 1, gave_up, a.tries);
+                    ok = bar_wait(&m.vfull[pos % kVSlots], (pos / kVSlots) & 1, gave_up, tries);
                     uint4 *v = reinterpret_cast<uint4 *>(psm + kOffV + (pos % kVSlots) * 2 * kSlotB);
 #pragma unroll 1
                     for (int e = (nk - j * kKeys) * 8 + r; e < kKeys * 8; e += kQTile) {
@@ -247,7 +251,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 sum += s2.x + s2.y;
             }
             if (steps > 0) {
-                ok = bar_wait(&m.odone[tile], outs++ & 1, gave_up, a.tries) && ok;
+                ok = bar_wait(&m.odone[tile], outs++ & 1, gave_up, tries) && ok;
                 tmem_fence_after();
             }
             ok = __all_sync(0xffffffffu, ok);
@@ -306,14 +310,14 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 bool keys = T == 0 && bar_passed(&m.kfull[kstart % kKSlots], (kstart / kKSlots) & 1);
                 if (j > 0 && j <= mine) {
                     const uint32_t pos = vpos + j - 1, slot = pos % kVSlots, parity = weighed++ & 1;
-                    if (!ready && !bar_wait(&m.pready[T][0], parity, gave_up, a.tries)) return false;
-                    if ((T == 0 ? !ready : j > n0) && !bar_wait(&m.vfull[slot], (pos / kVSlots) & 1, gave_up, a.tries)) return false;
+                    if (!ready && !bar_wait(&m.pready[T][0], parity, gave_up, tries)) return false;
+                    if ((T == 0 ? !ready : j > n0) && !bar_wait(&m.vfull[slot], (pos / kVSlots) & 1, gave_up, tries)) return false;
                     const bool rest = bar_passed(&m.pready[T][1], parity);
                     tmem_fence_after();
                     const uint32_t db = umma_desc(va + slot * 2 * kSlotB, kSlotB);
 #pragma unroll
                     for (int s = 0; s < 4; ++s) umma_ts(tmem + co, tmem + cs + s * 8, db + s * 128, idO, j > 1 || s > 0);
-                    if (!rest && !bar_wait(&m.pready[T][1], parity, gave_up, a.tries)) return false;
+                    if (!rest && !bar_wait(&m.pready[T][1], parity, gave_up, tries)) return false;
                     tmem_fence_after();
 #pragma unroll
                     for (int s = 4; s < 8; ++s) umma_ts(tmem + co, tmem + cs + s * 8, db + s * 128, idO, true);
@@ -322,12 +326,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 }
                 ready = false;
                 if (j >= mine) return true;
-                if (j == 0 && !bar_wait(&m.qfull[T], items++ & 1, gave_up, a.tries)) return false;
+                if (j == 0 && !bar_wait(&m.qfull[T], items++ & 1, gave_up, tries)) return false;
                 const uint32_t da = umma_desc(qa + T * kKChunks * kSlotB, 16);
 #pragma unroll
                 for (int c = 0; c < kKChunks; ++c) {
                     const uint32_t at = kstart + c, slot = at % kKSlots;
-                    if (first && !keys && !bar_wait(&m.kfull[slot], (at / kKSlots) & 1, gave_up, a.tries)) return false;
+                    if (first && !keys && !bar_wait(&m.kfull[slot], (at / kKSlots) & 1, gave_up, tries)) return false;
                     if (c + 1 < kKChunks) {
                         keys = T == 0 && bar_passed(&m.kfull[(at + 1) % kKSlots], ((at + 1) / kKSlots) & 1);
                     } else {
@@ -379,7 +383,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 #pragma unroll 1
                     for (int c = 0; ok && c < kKChunks; ++c, ++kpos) {
                         const uint32_t slot = kpos % kKSlots;
-                        ok = bar_wait(&m.kempty[slot], ((kpos / kKSlots) & 1) ^ 1, gave_up, a.tries);
+                        ok = bar_wait(&m.kempty[slot], ((kpos / kKSlots) & 1) ^ 1, gave_up, tries);
                         if (!ok) break;
                         uint8_t *dst = psm + kOffK + slot * kSlotB;
                         mbar_arrive_expect_tx(&m.kfull[slot], kSlotB);
@@ -387,7 +391,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                         else tma_box3(dst, &mapkr, 0, 0, y, &m.kfull[slot], pol);
                     }
                     const uint32_t slot = vpos % kVSlots;
-                    ok = ok && bar_wait(&m.vempty[slot], ((vpos / kVSlots) & 1) ^ 1, gave_up, a.tries);
+                    ok = ok && bar_wait(&m.vempty[slot], ((vpos / kVSlots) & 1) ^ 1, gave_up, tries);
                     if (!ok) break;
                     uint8_t *dst = psm + kOffV + slot * 2 * kSlotB;
                     mbar_arrive_expect_tx(&m.vfull[slot], 2 * kSlotB);
@@ -415,7 +419,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 #pragma unroll 1
                 for (int tile = 0; tile < 2; ++tile) {
                     if ((tile ? n1 : n0) == 0 || !ok) continue;
-                    ok = bar_wait(&m.qempty[tile], ((used >> tile) & 1) ^ 1, gave_up, a.item_tries);
+                    ok = bar_wait(&m.qempty[tile], ((used >> tile) & 1) ^ 1, gave_up, item_tries);
                     used ^= 1u << tile;
                     if (!ok) continue;
                     uint64_t *full = &m.qfull[tile];
@@ -441,7 +445,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         // the lengths most numbers stand for no item.
         int i = 0;
         auto publish = [&](const Item &it) {
-            if (!bar_wait(&m.iempty[i % kItems], ((i / kItems) & 1) ^ 1, gave_up, a.item_tries)) return false;
+            if (!bar_wait(&m.iempty[i % kItems], ((i / kItems) & 1) ^ 1, gave_up, item_tries)) return false;
             m.item[i % kItems] = it;
             bar_arrive(&m.ifull[i % kItems]);
             return true;
@@ -547,15 +551,18 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, int num_sms, cudaS
     }
     // a negative scale is the operands' sign: the softmax works with its magnitude
     const uint32_t idS = umma_idesc(kQTile, kKeys, true, false, false) | (a.sm_scale < 0.f ? 1u << 13 : 0u);
-    return launch_pdl(latent_prefill_kernel, dim3(grid), dim3(kPreThreads), kPreSmem, s, qn, qr, kn, kr, v, a, d, idS,
+    auto *const kernel = a.tries == kTries ? latent_prefill_kernel<false> : latent_prefill_kernel<true>;
+    return launch_pdl(kernel, dim3(grid), dim3(kPreThreads), kPreSmem, s, qn, qr, kn, kr, v, a, d, idS,
                       qn_h, qr_h, kn_h, v_h);
 }
 
 cudaError_t preload_latent_prefill() {
-    const cudaError_t e =
-        cudaFuncSetAttribute(latent_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPreSmem);
-    const cudaError_t f = e == cudaSuccess ? preload_kernel(latent_prefill_kernel) : e;
-    return f == cudaSuccess ? preload_kernel(latent_prefill_flags_kernel) : f;
+    cudaError_t e = preload_kernel(latent_prefill_flags_kernel);
+    for (auto *const kernel : {latent_prefill_kernel<false>, latent_prefill_kernel<true>}) {
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPreSmem);
+        if (e == cudaSuccess) e = preload_kernel(kernel);
+    }
+    return e;
 }
 
 }  // namespace pfkv

@@ -170,11 +170,12 @@ __device__ __forceinline__ void bar_arrive_at(uint64_t *bar, uint32_t rank) {
 }
 
 // Waits that give up.  A try sleeps until the phase completes, or for about kSleepNs
-// at most; after `tries` of them (kTries: 0.40 s, measured: 4 us a try) `gave_up` is
-// set, every later wait of the CTA returns soon, and the roles run to their end
+// at most; after `tries` of them `gave_up` is set, every later wait of the CTA returns soon, and the roles run to their end
 // without issuing copies or products.  Returns false then.  (Short on purpose: with
 // five roles at work the instruction cache is what is scarce, and a wait is inlined
-// in thirty places.)
+// in thirty places.  So it counts tries, not time: measured, a try lasts 4 us in a CTA that
+// does nothing else, 0.2 to 0.4 us in one at work, where other barriers' phases wake it;
+// kTries of them are 20 ms at least, for waits that last microseconds.)
 constexpr uint32_t kSleepNs = 20000;
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *gave_up, int tries = kTries) {
 #pragma unroll 1

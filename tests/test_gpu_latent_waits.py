@@ -11,7 +11,7 @@ from paged_fp8_kv_decode_gb300 import latent as L
 
 pytestmark = pytest.mark.gpu
 
-NEVER = 1000                                         # 4 ms: not in sound calls of microseconds
+NEVER = 1000                                         # 0.2 ms at least: not in sound calls of microseconds
 
 
 def prefill(tries, x, qs, ks, max_q, causal=True):
@@ -51,3 +51,21 @@ def test_prefill_refuses_a_limit_beyond_its_own():
         with pytest.raises(B.PfkvError) as e:
             prefill(tries, x, [0, 5], [0, 5], 5)
         assert e.value.status == B.PFKV_ERR_INVALID_ARG
+
+
+def test_prefill_waits_that_last_as_long_as_an_item():
+    """128 queries over a million keys have no second tile: its warps wait for the next
+    item's scores, and that item for its place, while the first tile works for
+    milliseconds.  A limit of 300 tries (1.2 ms at most) does not count there."""
+    g = gen(93)
+    H, nq, nk = 160, [128, 200], [1 << 20, 300]      # more pairs than multiprocessors: both on one CTA
+    qs, ks = P.starts_of(nq), P.starts_of(nk)
+    x = P.inputs(g, sum(nq), sum(nk), 1)
+    x = {n: t if n == "kr" else t.expand(-1, H, -1) for n, t in x.items()}
+    want = torch.zeros(sum(nq), H, 128, dtype=torch.bfloat16, device="cuda")
+    _, fl = P.run(x, qs, ks, max(nq), out=want)
+    assert not any(fl)
+    P.check(x, (128, 328), (1 << 20, (1 << 20) + 300), want, heads=(0, 159))
+    out, fl = prefill(300, x, qs, ks, max(nq))
+    assert fl == [0, 0]
+    assert torch.equal(out, want)
