@@ -170,7 +170,9 @@ pfkv_status pfkv_latent_decode_attn(const pfkv_latent_cache *cache, const pfkv_p
  *   flags   : uint8 [batch], written; PFKV_FLAG_DEVICE_TIMEOUT in all of them where a
  *             wait inside the kernel gave up (any row may then be unwritten); may be NULL
  *
- * A query that sees no key gives a zero row.  A request whose rows are not
+ * A query that sees no key gives a zero row; keys and values that a query does not see
+ * do not reach its row, whatever they hold (tiles of queries in which one that is not
+ * finite might have are computed again, which costs their time twice).  A request whose rows are not
  * within the arrays is flagged and nothing of it is written.  Rows outside every
  * request's range are left as they were.  Arithmetic: tensor cores with fp32
  * accumulation, softmax statistics in fp32, a weight rounded once to bf16 where it
@@ -187,7 +189,8 @@ pfkv_status pfkv_latent_prefill_attn(int32_t batch, int32_t num_heads, const int
 /*
  * pfkv_selftest_latent_prefill -- pfkv_latent_prefill_attn with waits that give up
  * after `tries` tries (0 .. 100000, which is what the call itself takes; 0.2 to 4 us
- * each; 1000 times as many for waits that last as long as a tile's work), so that a test can let them run out: the call ends, its requests are flagged
+ * each; 1000 times as many for waits that last as long as a tile's work), so that a
+ * test can let them run out: the call ends, its requests are flagged
  * PFKV_FLAG_DEVICE_TIMEOUT, and the context stays usable.
  */
 pfkv_status pfkv_selftest_latent_prefill(int32_t tries, int32_t batch, int32_t num_heads,

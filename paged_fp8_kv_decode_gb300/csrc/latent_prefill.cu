@@ -62,6 +62,7 @@ struct Item {
     int k0, nk;      // the request's first key row and key rows
     int sees0;       // keys that the item's first query sees (each further one sees one more if causal)
     int n0, n1;      // steps of the two tiles
+    bool careful;    // done again: values that a row must not see may not be finite
 };
 
 struct PreMisc {
@@ -69,6 +70,8 @@ struct PreMisc {
     uint64_t qfull[2], qempty[2], sfull[2], pready[2][2], odone[2];
     uint64_t ifull[kItems], iempty[kItems], drain;
     Item item[kItems];
+    uint32_t redo[kItems];     // a row that does not see every key came out not finite
+    uint32_t unsound[kItems];  // careful: values were not finite, and zeroed
     uint32_t tmem, gave_up;
 };
 constexpr size_t kPreSmem = kOffPre + sizeof(PreMisc);
@@ -82,6 +85,61 @@ struct Deal {
     bool dense;    // numbers that stand for an item are dealt out, rather than all numbers
     long long items;
 };
+
+// Which of two bf16 values are not finite: the upper bit of each.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+
+// Values that a row must not see meet its weight of zero in the product, which is harmless where
+// they are finite.  Looking for others costs 1 to 2 us an item, so it is left to items that are
+// done again because they came out not finite: what is not finite from the first hidden key on is
+// zeroed by the tile that uses a step first, and given at the end to the rows that see it.  (Calls,
+// not inlined: 0.9 us for short prompts.)
+
+// Row r of the V of step number `pos`.
+__device__ __noinline__ void zero_odd_values(PreMisc &m, uint8_t *values, uint32_t pos, int r, uint32_t *odd, int tries) {
+    if (!bar_wait(&m.vfull[pos % kVSlots], (pos / kVSlots) & 1, &m.gave_up, tries)) return;
+    uint32_t *v = reinterpret_cast<uint32_t *>(values + (pos % kVSlots) * 2 * kSlotB) + r * 32;
+    bool any = false;
+#pragma unroll 1
+    for (int c = 0; c < 64; ++c) {  // words; each lane starts at another, or all would read the same bank
+        uint32_t *w = v + (c >> 5) * (kSlotB / 4) + ((c + r) & 31);
+        const uint32_t bad = not_finite(*w);
+        if (bad == 0) continue;
+        if (!any) *static_cast<volatile uint32_t *>(odd) = 1u;
+        any = true;
+        *w &= ~((bad >> 15) * 0xFFFFu);
+    }
+    if (any) fence_proxy_async_smem();
+}
+
+// Adds to a row's results, `o` in tensor memory, what is not finite in the values of keys k0 .. k1 - 1.
+__device__ __noinline__ void add_odd_values(const __nv_bfloat16 *v, long long stride, int k0, int k1, uint32_t o) {
+#pragma unroll 1
+    for (int g = 0; g < 8; ++g) {
+        float x[16];
+        tmem_ld16(o + g * 16, x);
+        tmem_wait_ld();
+#pragma unroll 1
+        for (int j = k0; j < k1; ++j) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(v + j * stride + g * 16);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const uint4 w = src[c];
+                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t bad = not_finite(u[k]);
+                    const float2 y = bf16x2_to_float2(u[k]);
+                    if (bad & 0x8000u) x[c * 8 + 2 * k] += y.x;
+                    if (bad & 0x80000000u) x[c * 8 + 2 * k + 1] += y.y;
+                }
+            }
+        }
+        __syncwarp();
+        tmem_st16(o + g * 16, x);
+    }
+    tmem_wait_st();
+}
 
 // The rows of request b; false where they are not within the arrays or the bound.
 __device__ __forceinline__ bool request_rows(const LatentPrefillArgs &a, int b, int &q0, int &nq, int &k0, int &nk) {
@@ -169,6 +227,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             float ref = kMinusInf, sum = 0.f;
             bool ok = true;
             for (int j = 0; j < steps; ++j, ++done) {
+                if (it.careful && (j + 1) * kKeys > it.sees0 && (tile == 0 || j >= it.n0) && j * kKeys + r >= it.sees0 &&
+                    j * kKeys + r < nk)
+                    zero_odd_values(m, psm + kOffV, base_pos + j, r, &m.unsound[i % kItems], tries);
                 // an item's first scores come when the other tile is done with the item before it
                 ok = bar_wait(&m.sfull[tile], done & 1, gave_up, item_tries);
                 if (!__all_sync(0xffffffffu, ok)) break;
@@ -258,6 +319,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             const float inv = sum > 0.f ? __fdiv_rn(1.f, sum) : sum;  // zero and NaN stay
             const int row = tile * kQTile + r;
             const bool live = row < it.nq;
+            if (it.careful && __any_sync(0xffffffffu, ok && *static_cast<volatile uint32_t *>(&m.unsound[i % kItems]) != 0u))
+                add_odd_values(a.v.p + (long long)it.k0 * a.v.st + (long long)it.h * a.v.sh, a.v.st, max(it.sees0, 0),
+                               row < it.nq ? sees : 0, co);
+            float2 odd = make_float2(0.f, 0.f);  // NaN once a result was not finite
             __nv_bfloat16 *out = a.out.p + (long long)(it.q0 + row) * a.out.st + (long long)it.h * a.out.sh;
 #pragma unroll 1
             for (int g = 0; g < 4; ++g) {
@@ -267,6 +332,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                     tmem_wait_ld();
                 }
                 if (!live || !ok) continue;
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) odd = fma2(make_float2(o[e], o[e + 1]), make_float2(0.f, 0.f), odd);
 #pragma unroll
                 for (int e = 0; e < 32; e += 8) {
                     uint32_t u[4];
@@ -281,6 +348,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 }
             }
             base_pos += max(it.n0, it.n1);
+            if (sees < nk && sees > 0 && !it.careful && live && odd.x + odd.y != 0.f)
+                *static_cast<volatile uint32_t *>(&m.redo[i % kItems]) = 1u;
             tmem_fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive(&m.iempty[i % kItems]);
@@ -444,10 +513,29 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         // A lane a number (dense), or a number of the CTA's own turns: with a max_q_len far above
         // the lengths most numbers stand for no item.
         int i = 0;
-        auto publish = [&](const Item &it) {
-            if (!bar_wait(&m.iempty[i % kItems], ((i / kItems) & 1) ^ 1, gave_up, item_tries)) return false;
+        // Waits until the place of number n is free; then its last item's redo flag stands.
+        auto is_free = [&](int n) { return bar_wait(&m.iempty[n % kItems], ((n / kItems) & 1) ^ 1, gave_up, item_tries); };
+        auto put = [&](const Item &it) {
             m.item[i % kItems] = it;
+            m.redo[i % kItems] = m.unsound[i % kItems] = 0u;
             bar_arrive(&m.ifull[i % kItems]);
+            ++i;
+        };
+        // Done by one lane: numbers i, and the item in the place of number n (free, as is that of i)
+        // once more before it if it came out not finite.
+        auto again = [&](int n) {
+            if (n < kItems || !*static_cast<volatile uint32_t *>(&m.redo[n % kItems])) return false;
+            Item it = m.item[n % kItems];
+            it.careful = true;
+            m.redo[n % kItems] = 0u;
+            put(it);
+            return true;
+        };
+        auto publish = [&](const Item &it) {
+            do {
+                if (!is_free(i)) return false;
+            } while (again(i));
+            put(it);
             return true;
         };
         bool ok = true;
@@ -488,14 +576,20 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 there = there && ((round & 1) ? gridDim.x - 1 - place : place) == blockIdx.x;
                 dealt += __popc(all);
             }
-            for (uint32_t left = __ballot_sync(0xffffffffu, there); ok && left; left &= left - 1, ++i) {
+            for (uint32_t left = __ballot_sync(0xffffffffu, there); ok && left; left &= left - 1) {
                 const int from = __ffs(left) - 1;
                 ok = __all_sync(0xffffffffu, lane != from || publish(it));
+                i = __shfl_sync(0xffffffffu, i, from);
             }
         }
         if (lane == 0 && ok) {
             it.b = -1;
-            publish(it);
+            // no more, once no item is to be done again
+            for (int n = i; a.causal && ok && n < i + kItems; ++n) {
+                ok = is_free(n);
+                if (ok && again(n)) n = i - 1;
+            }
+            if (ok) publish(it);
         }
         __syncwarp();
     }
