@@ -126,7 +126,7 @@ pfkv_status pfkv_latent_gather(const pfkv_latent_cache *cache, const pfkv_pages 
  * seq_lens[b]; a row that attends to none is zero.  Every live page id, and its
  * tag when tags are tracked, is checked; a request with a mismatch or a bad
  * length is flagged and all of its rows are zero.  Slots past a request's last
- * token are never used, whatever they hold.
+ * token, and tokens that a row does not see, do not reach it, whatever they hold.
  *
  * Arithmetic: both products run on the tensor cores with fp32 accumulation.
  * BF16 pools: q, c, r are exact; a softmax weight is rounded once to bf16.  FP8

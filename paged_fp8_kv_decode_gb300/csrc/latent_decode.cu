@@ -88,8 +88,13 @@ constexpr float kNegInf = -INFINITY;
 // What the roles need to know of a tile.
 struct Tile {
     int id[kTilePages];      // physical pages, -1 for one that is not to be read
-    float z[kTilePages], lz[kTilePages], iz[kTilePages];  // scales, their logarithms and reciprocals     // FP8: their scales
+    float z[kTilePages], lz[kTilePages], iz[kTilePages];  // FP8: scales, their logarithms and reciprocals
     int b, block, left;      // request, row block, the request's tokens from this tile's first on
+    // Of those, the ones that some row of the block sees: a value past them is taken for zero (it
+    // would meet weights of zero, harmless where it is finite).  And the ones before the first
+    // that a row does not see and that is not finite (else as many as are held): past them, what is
+    // not finite is zero; rows that see it have it in their scores.
+    int held, sound;
     uint32_t flags;
 };
 constexpr uint32_t kFirst = 1, kLast = 2, kWhole = 4, kBegins = 8;  // of the part of a (request, row block)
@@ -241,6 +246,62 @@ __device__ __forceinline__ void convert_query(uint8_t *q, int r, int part, float
             *piece(q + (part * 2 + (j >> 3)) * kChunkB, r, (j + u) & 7) =
                 make_uint4(scaled_half2(w[u].x, inv), scaled_half2(w[u].y, inv), scaled_half2(w[u].z, inv),
                            scaled_half2(w[u].w, inv));
+    }
+}
+
+// What a block's rows see in part (num_query_tokens > 1) is looked at before it is used, as a
+// weight of zero does not hide a value that is not finite.  (Inlined: the roles that do it have 64
+// and 88 registers, and a call may take any of the kernel's 96.)
+
+// Whether tokens k0 .. k1 - 1 of a tile, whose page ids the lanes from `lane0` on hold, have such a latent.
+template <bool FP8>
+__device__ __forceinline__ bool odd_latents(const void *pages, int id, int lane0, int k0, int k1, int lane) {
+    uint32_t odd = 0;
+#pragma unroll 4
+    for (int k = k0; k < k1; ++k) {
+        const int page = __shfl_sync(0xffffffffu, id, lane0 + k / kPage);
+        const uint4 *c = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(pages) +
+                                                         ((long long)max(page, 0) * kPage + k % kPage) * (kDC * (FP8 ? 1 : 2)));
+        const uint4 w = c[lane];
+        if constexpr (FP8) {
+            odd |= e4m3_nan(w.x) | e4m3_nan(w.y) | e4m3_nan(w.z) | e4m3_nan(w.w);
+        } else {
+            const uint4 u = c[lane + 32];
+            odd |= not_finite(w.x) | not_finite(w.y) | not_finite(w.z) | not_finite(w.w);
+            odd |= not_finite(u.x) | not_finite(u.y) | not_finite(u.z) | not_finite(u.w);
+        }
+    }
+    return __any_sync(0xffffffffu, odd != 0u);
+}
+
+// BF16: rows 16 full .. rows - 1 of a tile's V, without what is not finite from row `sound` on (a
+// lane's pieces are those that it stored as zeros before).
+__device__ __forceinline__ void copy_sound_latents(const void *pages, const Tile &ti, uint8_t *v, int full, int sound, int rows,
+                                                int x, int lane) {
+#pragma unroll 1
+    for (int e = lane; e < (rows - full * kPage) * 16; e += 32) {
+        const int r = full * kPage + (e >> 4), c = e & 15, id = ti.id[r / kPage];
+        if (id < 0) continue;
+        uint4 w = static_cast<const uint4 *>(pages)[((long long)id * kPage + (r & 15)) * (kDC / 8) + x / 8 + c];
+        if (r >= sound) {
+            w.x &= ~((not_finite(w.x) >> 15) * 0xFFFFu);
+            w.y &= ~((not_finite(w.y) >> 15) * 0xFFFFu);
+            w.z &= ~((not_finite(w.z) >> 15) * 0xFFFFu);
+            w.w &= ~((not_finite(w.w) >> 15) * 0xFFFFu);
+        }
+        *piece(v + (r >> 4) * 4096 + (c >> 3) * 2048, r & 15, c & 7) = w;
+    }
+}
+
+// FP8: the same to a lane's converted values, rows 8 u + r_in of a chunk from row `sound` on (NaN
+// codes have become the f16 of all ones).
+__device__ __forceinline__ void zero_odd_values(uint8_t *chunk, int pc, int r_in, int sound) {
+#pragma unroll 1
+    for (int u = 0; u < 32; ++u) {
+        const int r = (u >> 1) * 8 + r_in;
+        if (r < sound) continue;
+        uint32_t *w = reinterpret_cast<uint32_t *>(piece(chunk, r, 2 * pc + (u & 1)));
+        for (int i = 0; i < 4; ++i) w[i] &= ~((((w[i] & 0x7C007C00u) + 0x04000400u) >> 15 & 0x00010001u) * 0xFFFFu);
     }
 }
 
@@ -741,8 +802,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; !FP8 && t < N; ++t) {
             if (!__all_sync(0xffffffffu, looked_up(t))) break;
             const Tile &ti = m.tile[t % kRing];
-            const int left = ti.left;
-            const int full = min(kTilePages, left / kPage);  // pages without a slot past the last token
+            const int held = ti.held, sound = ti.sound;
+            const int full = min(kTilePages, max(0, sound) / kPage);  // pages whose slots are all taken as they are
 #pragma unroll 1
             for (int nb = 0; nb < 2; ++nb) {
                 if (!__all_sync(0xffffffffu, bar_wait(&m.vempty[nb], (t & 1) ^ 1, gave_up))) break;
@@ -770,17 +831,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 if (full < kTilePages) {
-                    // the page that the last token is in, and zeros for every slot past it:
-                    // those may hold anything, NaN among it, and meet weights of zero
-                    const int id = left % kPage ? ti.id[full] : -1;
+                    // the pages behind those, and zeros for every slot past the last token that is
+                    // held: those may hold anything, NaN among it, and meet weights of zero
+                    const int id = sound == held && held % kPage ? ti.id[full] : -1;
                     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
                     for (int e = lane; e < (kTile - full * kPage) * 16; e += 32) {
                         const int r = full * kPage + (e >> 4), c = e & 15;  // row, 16-byte piece of its 256
                         uint4 w = zero;
-                        if (r < left && id >= 0)
+                        if (r < held && id >= 0)
                             w = reinterpret_cast<const uint4 *>(a.pool.c_pages)[((long long)id * kPage + (r & 15)) * (kDC / 8) + x / 8 + c];
                         *piece(dst + (r >> 4) * 4096 + (c >> 3) * 2048, r & 15, c & 7) = w;
                     }
+                    if (sound < held) copy_sound_latents(a.pool.c_pages, ti, dst, full, sound, min(kTile, held), x, lane);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) bar_arrive_at(&m.vfull[nb], 0);
@@ -798,6 +860,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         int t = 0;
         while (walk.next(a, blocks, s)) {
             uint32_t bits = 0;
+            int seen_all = s.n, seen_any = s.n;  // tokens that all rows of the block see, and that one does
+            if (a.kq > 1) {
+                seen_all += 1 - a.kq + s.block * kRowBlock / a.H;
+                seen_any += min(0, 1 - a.kq + (s.block * kRowBlock + kRowBlock - 1) / a.H);
+            }
             for (int at = s.t0; at < s.t1; at += 2) {
                 const int tile = at + i, lp = tile * kTilePages + pg;
                 int id = -1;
@@ -812,6 +879,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bits |= bad;
                 if (id >= 0 && FP8) z = a.pool.c_scale[id];
                 for (int j = 0; j < min(2, s.t1 - at); ++j, ++t) {
+                    const int first = (at + j) * kTile, held = seen_any - first;
+                    int sound = held;
+                    if (seen_all < seen_any && seen_any > first && seen_all < first + kTile &&
+                        odd_latents<FP8>(a.pool.c_pages, id, j * 8, max(0, seen_all - first), min(kTile, held), lane))
+                        sound = seen_all - first;
                     Tile &ti = m.tile[t % kRing];
                     if (!__all_sync(0xffffffffu, bar_wait(&m.mempty[t % kRing], ((t / kRing) & 1) ^ 1, gave_up))) continue;
                     if (lane < 16 && i == j) {
@@ -826,6 +898,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ti.b = s.b;
                             ti.block = s.block;
                             ti.left = s.n - tile * kTile;
+                            ti.held = held;
+                            ti.sound = sound;
                             ti.flags = (tile == s.t0 ? kFirst : 0u) | (tile + 1 == s.t1 ? kLast : 0u) |
                                        (s.t1 - s.t0 == s.tiles ? kWhole : 0u) | (s.t0 == 0 ? kBegins : 0u);
                         }
@@ -903,11 +977,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t at = smem_addr(dst) + r_in * 128 + (((2 * pc) ^ r_in) << 4);
         reg_share_less<88>();
         uint4 raw[16];
-        int left = 0;
+        int held = 0, sound = 0;
         auto load = [&](int t) {
             const bool ok = t < N && looked_up(t);
             const Tile &ti = m.tile[t % kRing];
-            left = ok ? ti.left : 0;
+            held = ok ? ti.held : 0;
+            sound = ok ? ti.sound : 0;
 #pragma unroll
             for (int i = 0; i < kTilePages; ++i) {
                 const uint8_t *page = src + (long long)(kPage * kDC) * (ok ? max(0, ti.id[i]) : 0);
@@ -917,10 +992,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         load(0);
         for (int t = 0; t < N; ++t) {
-            if (left < kTile) {
+            if (held < kTile) {
 #pragma unroll
                 for (int u = 0; u < 16; ++u)
-                    if (u * 8 + r_in >= left) raw[u] = make_uint4(0u, 0u, 0u, 0u);
+                    if (u * 8 + r_in >= held) raw[u] = make_uint4(0u, 0u, 0u, 0u);
             }
             bar_wait(&m.vempty[s >> 1], (t & 1) ^ 1, gave_up);
 #pragma unroll
@@ -928,6 +1003,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 store_shared(at + u * 1024, cvt_e4m3x8(raw[u].x, raw[u].y));
                 store_shared((at ^ 16u) + u * 1024, cvt_e4m3x8(raw[u].z, raw[u].w));
             }
+            if (sound < held) zero_odd_values(dst, pc, r_in, sound);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) bar_arrive_at(&m.vfull[s >> 1], 0);

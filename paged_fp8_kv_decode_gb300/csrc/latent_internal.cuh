@@ -60,6 +60,11 @@ __device__ __forceinline__ uint32_t latent_entry_bits(const LatentPool &a, int i
     return 0u;
 }
 
+// Which of two bf16 values are not finite: the upper bit of each.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+// Which of four e4m3 codes are NaN (the format has no infinities): the upper bit of each.
+__device__ __forceinline__ uint32_t e4m3_nan(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
 // Two fp32 operations an instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;

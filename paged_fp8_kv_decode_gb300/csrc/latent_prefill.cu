@@ -86,9 +86,6 @@ struct Deal {
     long long items;
 };
 
-// Which of two bf16 values are not finite: the upper bit of each.
-__device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
-
 // Values that a row must not see meet its weight of zero in the product, which is harmless where
 // they are finite.  Looking for others costs 1 to 2 us an item, so it is left to items that are
 // done again because they came out not finite: what is not finite from the first hidden key on is

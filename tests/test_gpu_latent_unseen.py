@@ -3,8 +3,9 @@ that see them, as they are, and no other row."""
 import pytest
 import torch
 
+import test_gpu_latent_decode as D
 import test_gpu_latent_prefill as P
-from latent_cases import BF16, SCALE, close, gen, rows, score_error, softmax_attend
+from latent_cases import (BF16, PAGE, SCALE, close, gen, latent_pool, rows, score_error, softmax_attend, tables)
 
 pytestmark = pytest.mark.gpu
 
@@ -91,3 +92,37 @@ def test_prefill_of_many_prompts():
                 want[qs[b] + at:qs[b + 1], h, h] = 0.0
                 out[qs[b] + at:qs[b + 1], h, h] = 0.0
     assert torch.equal(out, want)                    # all else has the same bits
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("H,kq", [(16, 3), (128, 2), (128, 4), (1, 7), (64, 2), (3, 40), (1, 200), (5, 130)])
+@pytest.mark.parametrize("back", [0, 1])
+def test_decode(H, kq, back, fp8):
+    """A latent that is not finite in the last candidate, or the one before it: the rows of
+    earlier candidates have the bits that they have without it, later ones are NaN."""
+    if back >= kq:
+        return
+    g = gen(96)
+    lens = [128, 129, 130, 200, 256, 16, 3, 2, 1, 700, 0, 384, 145] * 2
+    bt, num = tables([(n + PAGE - 1) // PAGE for n in lens], seed=H + kq)
+    cache = latent_pool(g, num, fp8)
+    qc, qr = rows(g, len(lens), kq, H, 512, outliers=0), rows(g, len(lens), kq, H, 64, outliers=0)
+    want, fl = D.run(cache, bt, lens, qc, qr)
+    assert not any(fl)
+    D.check(cache, bt, lens, qc, qr, want)
+    for b, n in enumerate(lens):
+        if n - 1 - back >= 0:
+            j = n - 1 - back
+            page = int(bt[b, j // PAGE])
+            bad = (0x7F, 0xFF)[b % 2] if fp8 else (NAN, INF, -NAN)[b % 3]
+            cache.c_pages[page, j % PAGE, (37 * b) % 512] = bad
+            if not fp8:                              # a score of -inf would hide it: NaN beside it
+                cache.c_pages[page, j % PAGE, (37 * b + 1) % 512] = NAN
+    out, fl = D.run(cache, bt, lens, qc, qr)
+    assert not any(fl)
+    for b, n in enumerate(lens):
+        for t in range(kq):
+            if n - kq + 1 + t > n - 1 - back >= 0:
+                assert out[b, t].isnan().all(), (b, t)
+            else:
+                assert torch.equal(out[b, t], want[b, t]), (b, t, n)
