@@ -877,7 +877,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (bad) id = -1;  // not read; the merge kernel flags and zeroes the request
                 }
                 bits |= bad;
-                if (id >= 0 && FP8) z = a.pool.c_scale[id];
+                if (id >= 0 && FP8) {
+                    z = a.pool.c_scale[id];
+                    if (z < 7.888609052210118e-31f) z = 7.888609052210118e-31f;  // 2^-100
+                }
                 for (int j = 0; j < min(2, s.t1 - at); ++j, ++t) {
                     const int first = (at + j) * kTile, held = seen_any - first;
                     int sound = held;
@@ -890,9 +893,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ti.id[pg] = id;
                         ti.z[pg] = z;
                         if constexpr (FP8) {
-                            const float zc = fmaxf(z, 7.888609052210118e-31f);  // 2^-100
-                            ti.lz[pg] = __log2f(zc);
-                            ti.iz[pg] = __frcp_rn(zc);
+                            ti.lz[pg] = __log2f(z);
+                            ti.iz[pg] = __frcp_rn(z);
                         }
                         if (pg == 0) {
                             ti.b = s.b;
