@@ -93,7 +93,8 @@ pfkv_status pfkv_latent_append(const pfkv_latent_cache *cache, const pfkv_pages 
  *   c_out      : bf16, row i at c_out + i * c_stride (latent_dim elements);
  *                FP8 pools: e4m3 value x page scale, rounded to bf16
  *   r_out      : bf16, row i at r_out + i * r_stride (rope_dim elements)
- *                strides >= the row and multiples of 8
+ *                strides >= the row and multiples of 8; with total_rows 0 the arrays
+ *                may be NULL
  *   flags      : uint8 [batch] or NULL; bits are OR-ed in, never cleared
  *
  * A request whose length or rows are out of range is flagged

@@ -58,7 +58,8 @@ typedef struct pfkv_rows {
  *                    (len_stride_h 0, else PFKV_ERR_INVALID_ARG)
  *   row_starts     : int32 [batch + 1], or NULL for padded rows: packed rows,
  *                    request b holding rows row_starts[b] .. row_starts[b+1] - 1
- *   total_rows     : packed: rows that the arrays hold.  A request whose range is
+ *   total_rows     : packed: rows that the arrays hold (0: the arrays are not read and
+ *                    their data may be NULL).  A request whose range is
  *                    not within [0, total_rows] or longer than T is flagged
  *                    PFKV_FLAG_BAD_LENGTH and nothing of it is read or written.
  */

@@ -158,10 +158,13 @@ pfkv_status pfkv_latent_gather(const pfkv_latent_cache *cache, const pfkv_pages 
     if (st != PFKV_OK) return st;
     if (max_seq_len < 0 || total_rows < 0) return PFKV_ERR_INVALID_ARG;
     if (pages->batch == 0 || max_seq_len == 0) return PFKV_OK;
-    if (!row_starts || !c_out || !r_out) return PFKV_ERR_INVALID_ARG;
-    if (c_stride < PFKV_LATENT_DIM || r_stride < PFKV_LATENT_ROPE) return PFKV_ERR_INVALID_ARG;
-    if (!aligned(row_starts, 4) || !aligned(c_out, 16) || !aligned(r_out, 16) || ((c_stride | r_stride) & 7))
-        return PFKV_ERR_ALIGNMENT;
+    if (!row_starts) return PFKV_ERR_INVALID_ARG;
+    if (!aligned(row_starts, 4)) return PFKV_ERR_ALIGNMENT;
+    if (total_rows > 0) {
+        if (!c_out || !r_out) return PFKV_ERR_INVALID_ARG;
+        if (c_stride < PFKV_LATENT_DIM || r_stride < PFKV_LATENT_ROPE) return PFKV_ERR_INVALID_ARG;
+        if (!aligned(c_out, 16) || !aligned(r_out, 16) || ((c_stride | r_stride) & 7)) return PFKV_ERR_ALIGNMENT;
+    }
     if (flags && !aligned(flags, 4)) return PFKV_ERR_ALIGNMENT;
     const long long tiles = ((long long)max_seq_len + kPage - 1) / kPage;
     if (tiles * pages->batch > 0x7fffffffLL) return PFKV_ERR_UNSUPPORTED;
@@ -257,9 +260,7 @@ pfkv_status pfkv_selftest_latent_prefill(int32_t tries, int32_t batch, int32_t n
     if (flags && !aligned(flags, 4)) return PFKV_ERR_ALIGNMENT;
     // arrays without rows are not read; rows that share an address cannot be copied as a box
     auto check = [](const pfkv_rows *r, bool use_h, int64_t rows) {
-        if (!r) return PFKV_ERR_INVALID_ARG;
-        if (rows == 0) return PFKV_OK;
-        const pfkv_status st = check_rows(r, false, use_h);
+        const pfkv_status st = check_rows(r, false, use_h, rows);
         return st == PFKV_OK && rows > 1 && r->stride_t == 0 ? PFKV_ERR_UNSUPPORTED : st;
     };
     pfkv_status st = check(q_nope, true, total_q);

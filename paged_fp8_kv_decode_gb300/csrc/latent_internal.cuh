@@ -14,8 +14,8 @@ pfkv_status device_check(int *num_sms);
 pfkv_status check_cache(const pfkv_cache *c);
 pfkv_status check_pages(const pfkv_cache *c, const pfkv_pages *p);
 // host checks (rope.cu)
-// A pfkv_rows whose rows exist: data, alignment, strides (those in use).
-pfkv_status check_rows(const pfkv_rows *r, bool use_b, bool use_h);
+// A pfkv_rows of so many rows: data, alignment, strides (those in use); without rows it is not read.
+pfkv_status check_rows(const pfkv_rows *r, bool use_b, bool use_h, int64_t rows = 1);
 // host checks (latent.cu)
 pfkv_status check_latent(const pfkv_latent_cache *c, const pfkv_pages *p);
 

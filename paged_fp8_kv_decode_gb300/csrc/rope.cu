@@ -628,13 +628,16 @@ pfkv_status check_tokens(const pfkv_new_tokens *t, const pfkv_pages *p, const pf
     return PFKV_OK;
 }
 
+// Rows that the arrays of new tokens hold, as far as it is known here.
+int64_t new_rows(const pfkv_new_tokens *t) { return t->row_starts ? t->total_rows : 1; }
+
 // Queries: both arrays or neither.
-pfkv_status check_queries(const pfkv_rows *q, const pfkv_rows *out, int heads, bool use_b) {
+pfkv_status check_queries(const pfkv_rows *q, const pfkv_rows *out, int heads, bool use_b, int64_t rows) {
     if ((q == nullptr) != (out == nullptr)) return PFKV_ERR_INVALID_ARG;
     if (!q) return PFKV_OK;
     if (heads <= 0) return PFKV_ERR_INVALID_ARG;
-    pfkv_status st = check_rows(q, use_b, true);
-    if (st == PFKV_OK) st = check_rows(out, use_b, true);
+    pfkv_status st = check_rows(q, use_b, true, rows);
+    if (st == PFKV_OK) st = check_rows(out, use_b, true, rows);
     return st;
 }
 
@@ -647,8 +650,10 @@ TurnArgs turn_args(const pfkv_rope *r) { return TurnArgs{r->inv_freq, r->rot_dim
 
 }  // namespace
 
-pfkv_status check_rows(const pfkv_rows *r, bool use_b, bool use_h) {
-    if (!r || !r->data) return PFKV_ERR_INVALID_ARG;
+pfkv_status check_rows(const pfkv_rows *r, bool use_b, bool use_h, int64_t rows) {
+    if (!r) return PFKV_ERR_INVALID_ARG;
+    if (rows == 0) return PFKV_OK;
+    if (!r->data) return PFKV_ERR_INVALID_ARG;
     const int64_t sb = use_b ? r->stride_b : 0, sh = use_h ? r->stride_h : 0;
     if (sb < 0 || r->stride_t < 0 || sh < 0) return PFKV_ERR_INVALID_ARG;
     if (!aligned(r->data, 16) || ((sb | r->stride_t | sh) & 7)) return PFKV_ERR_ALIGNMENT;
@@ -683,9 +688,10 @@ pfkv_status pfkv_rope_append(const pfkv_cache *cache, const pfkv_pages *pages, c
     if (st == PFKV_OK) st = check_tokens(tokens, pages, rope);
     if (st != PFKV_OK || pages->batch == 0) return st;
     const bool use_b = tokens->row_starts == nullptr;
-    st = check_rows(k_new, use_b, true);
-    if (st == PFKV_OK) st = check_rows(v_new, use_b, true);
-    if (st == PFKV_OK) st = check_queries(q, q_out, num_q_heads, use_b);
+    const int64_t n = new_rows(tokens);
+    st = check_rows(k_new, use_b, true, n);
+    if (st == PFKV_OK) st = check_rows(v_new, use_b, true, n);
+    if (st == PFKV_OK) st = check_queries(q, q_out, num_q_heads, use_b, n);
     if (st != PFKV_OK) return st;
     if (flags && !aligned(flags, 4)) return PFKV_ERR_ALIGNMENT;
     const long long tiles = ((long long)tokens->num_new_tokens + 30) / kPage;  // ceil((T + 15) / 16)
@@ -742,9 +748,10 @@ pfkv_status pfkv_latent_append(const pfkv_latent_cache *cache, const pfkv_pages 
     if (st == PFKV_OK) st = check_tokens(tokens, pages, rope);
     if (st != PFKV_OK || pages->batch == 0) return st;
     const bool use_b = tokens->row_starts == nullptr;
-    st = check_rows(c_new, use_b, false);
-    if (st == PFKV_OK) st = check_rows(r_new, use_b, false);
-    if (st == PFKV_OK) st = check_queries(q, q_out, num_q_heads, use_b);
+    const int64_t n = new_rows(tokens);
+    st = check_rows(c_new, use_b, false, n);
+    if (st == PFKV_OK) st = check_rows(r_new, use_b, false, n);
+    if (st == PFKV_OK) st = check_queries(q, q_out, num_q_heads, use_b, n);
     if (st != PFKV_OK) return st;
     if (flags && !aligned(flags, 4)) return PFKV_ERR_ALIGNMENT;
     const long long tiles = ((long long)tokens->num_new_tokens + 30) / kPage;
