@@ -49,16 +49,15 @@ class LatentCache:
     def dtype(self) -> int:
         return B.PFKV_KV_BF16 if self.c_pages.dtype == torch.bfloat16 else B.PFKV_KV_FP8_E4M3
 
-    def c_struct(self) -> _CLatentCache:
+    def c_struct(self, dev: int) -> _CLatentCache:
         c, r = self.c_pages, self.r_pages
-        R._here(c)
         NP, PS, D = c.shape
         rNP, rPS, rD = r.shape
         if (rNP != NP or rPS != PS or r.dtype != torch.bfloat16 or not r.is_contiguous()
                 or not c.is_contiguous()):
             raise ValueError("c_pages [pages][16][512] and bfloat16 r_pages [pages][16][64], contiguous")
-        return _CLatentCache(NP, PS, D, rD, self.dtype, B._ptr(c), B._ptr(r), B._ptr(self.c_scale),
-                             B._ptr(self.page_tags))
+        return _CLatentCache(NP, PS, D, rD, self.dtype, R._ptr(c, dev), R._ptr(r, dev),
+                             R._ptr(self.c_scale, dev), R._ptr(self.page_tags, dev))
 
 
 def lib() -> ctypes.CDLL:
@@ -96,19 +95,20 @@ def pfkv_latent_append(cache: LatentCache, pages: B.Pages, rope: R.Rope, positio
     """c_new: bf16 [B][T][512], r_new: bf16 [B][T][64] (padded), or [rows][512]
     and [rows][64] with row_starts and max_new_tokens; q, q_out: bf16
     [B][T][H][64] or [rows][H][64]; the rest as in pfkv_rope_append."""
+    dev = R._current()
     packed = row_starts is not None
     tok = R._new_tokens(c_new, pages.batch, positions, new_lens, rope_positions, row_starts,
-                        max_new_tokens)
+                        max_new_tokens, dev)
     if c_new.shape[:-1] != r_new.shape[:-1]:
         raise ValueError("c_new and r_new: rows for the same tokens")
-    c = R._rows(c_new, packed, False, "c_new", cache.c_pages.shape[2])
-    r = R._rows(r_new, packed, False, "r_new", cache.r_pages.shape[2])
-    qr, qo, hq = R._queries(q, q_out, c_new, packed, cache.r_pages.shape[2])
-    k, p, t = cache.c_struct(), pages.c_struct(), rope.c_struct()
+    c = R._rows(c_new, packed, False, "c_new", cache.c_pages.shape[2], dev)
+    r = R._rows(r_new, packed, False, "r_new", cache.r_pages.shape[2], dev)
+    qr, qo, hq = R._queries(q, q_out, c_new, packed, cache.r_pages.shape[2], dev)
+    k, p, t = cache.c_struct(dev), R._pages(pages, dev), rope.c_struct(dev)
     B._check(lib().pfkv_latent_append(ctypes.byref(k), ctypes.byref(p), ctypes.byref(t),
                                       ctypes.byref(tok), ctypes.byref(c), ctypes.byref(r),
-                                      R._ref(qr), R._ref(qo), hq, B._ptr(flags),
-                                      B._stream(stream)), "pfkv_latent_append")
+                                      R._ref(qr), R._ref(qo), hq, R._ptr(flags, dev),
+                                      R._stream(stream, dev)), "pfkv_latent_append")
 
 
 def pfkv_latent_gather(cache: LatentCache, pages: B.Pages, row_starts: torch.Tensor,
@@ -116,20 +116,23 @@ def pfkv_latent_gather(cache: LatentCache, pages: B.Pages, row_starts: torch.Ten
                        flags: Optional[torch.Tensor] = None, stream=None) -> None:
     """row_starts: int32 [B + 1]; c_out: bf16 [rows][512], r_out: bf16
     [rows][64], rows of any stride."""
-    c = R._rows(c_out, True, False, "c_out", cache.c_pages.shape[2])
-    r = R._rows(r_out, True, False, "r_out", cache.r_pages.shape[2])
+    dev = R._current()
+    c = R._rows(c_out, True, False, "c_out", cache.c_pages.shape[2], dev)
+    r = R._rows(r_out, True, False, "r_out", cache.r_pages.shape[2], dev)
     if c_out.shape[0] != r_out.shape[0] or row_starts.numel() != pages.batch + 1:
         raise ValueError("as many rows of c_out as of r_out, and batch + 1 row_starts")
-    k, p = cache.c_struct(), pages.c_struct()
+    k, p = cache.c_struct(dev), R._pages(pages, dev)
     B._check(lib().pfkv_latent_gather(ctypes.byref(k), ctypes.byref(p),
-                                      R._i32(row_starts, "row_starts"), c_out.shape[0],
+                                      R._i32(row_starts, "row_starts", dev), c_out.shape[0],
                                       int(max_seq_len), c.data, c.stride_t, r.data, r.stride_t,
-                                      B._ptr(flags), B._stream(stream)), "pfkv_latent_gather")
+                                      R._ptr(flags, dev), R._stream(stream, dev)),
+             "pfkv_latent_gather")
 
 
 def pfkv_latent_decode_workspace_size(cache: LatentCache, pages: B.Pages, num_q_heads: int,
                                       num_query_tokens: int, max_seq_len: int) -> int:
-    k, p = cache.c_struct(), pages.c_struct()
+    dev = R._current()
+    k, p = cache.c_struct(dev), R._pages(pages, dev)
     n = ctypes.c_size_t(0)
     B._check(lib().pfkv_latent_decode_workspace_size(ctypes.byref(k), ctypes.byref(p),
                                                      int(num_q_heads), int(num_query_tokens),
@@ -148,15 +151,16 @@ def pfkv_latent_decode_attn(cache: LatentCache, pages: B.Pages, q_c: torch.Tenso
     if (q_c.shape != out.shape or q_c.shape[:-1] != q_r.shape[:-1]
             or q_c.shape[0] != pages.batch):
         raise ValueError("q_c and out [B][kq][H][512], q_r [B][kq][H][64]")
-    qc = R._rows(q_c, False, True, "q_c", cache.c_pages.shape[2])
-    qr = R._rows(q_r, False, True, "q_r", cache.r_pages.shape[2])
-    o = R._rows(out, False, True, "out", cache.c_pages.shape[2])
-    k, p = cache.c_struct(), pages.c_struct()
+    dev = R._current()
+    qc = R._rows(q_c, False, True, "q_c", cache.c_pages.shape[2], dev)
+    qr = R._rows(q_r, False, True, "q_r", cache.r_pages.shape[2], dev)
+    o = R._rows(out, False, True, "out", cache.c_pages.shape[2], dev)
+    k, p = cache.c_struct(dev), R._pages(pages, dev)
     B._check(lib().pfkv_latent_decode_attn(
         ctypes.byref(k), ctypes.byref(p), ctypes.byref(qc), ctypes.byref(qr), q_c.shape[2],
-        q_c.shape[1], float(sm_scale), int(max_seq_len), B._ptr(workspace),
-        workspace.nbytes, ctypes.byref(o), B._ptr(flags),
-        B._stream(stream)), "pfkv_latent_decode_attn")
+        q_c.shape[1], float(sm_scale), int(max_seq_len), R._ptr(workspace, dev),
+        workspace.nbytes, ctypes.byref(o), R._ptr(flags, dev),
+        R._stream(stream, dev)), "pfkv_latent_decode_attn")
 
 
 def pfkv_latent_prefill_attn(q_nope: torch.Tensor, q_rope: torch.Tensor, k_nope: torch.Tensor,
@@ -185,15 +189,16 @@ def _prefill(tries, q_nope, q_rope, k_nope, k_rope, v, q_starts, k_starts, max_q
             or k_nope.shape[:2] != v.shape[:2] or k_nope.shape[1] != H or k_rope.shape[0] != Tk
             or q_starts.numel() != k_starts.numel() or q_starts.numel() < 1):
         raise ValueError("query rows [Tq][H], key rows [Tk][H], and batch + 1 starts of both")
-    R._here(q_nope)
+    dev = R._current()
     if not (q_nope.is_cuda and q_rope.is_cuda and k_nope.is_cuda and k_rope.is_cuda and v.is_cuda):
         raise ValueError("rows in device memory")
-    rows = [R._rows(t, True, h, n, d) for t, h, n, d in (
+    rows = [R._rows(t, True, h, n, d, dev) for t, h, n, d in (
         (q_nope, True, "q_nope", PFKV_LATENT_NOPE), (q_rope, True, "q_rope", PFKV_LATENT_ROPE),
         (k_nope, True, "k_nope", PFKV_LATENT_NOPE), (k_rope, False, "k_rope", PFKV_LATENT_ROPE),
         (v, True, "v", PFKV_LATENT_VDIM), (out, True, "out", PFKV_LATENT_VDIM))]
     name = "pfkv_selftest_latent_prefill" if tries else "pfkv_latent_prefill_attn"
     B._check(getattr(lib(), name)(
-        *tries, int(q_starts.numel()) - 1, H, R._i32(q_starts, "q_starts"), R._i32(k_starts, "k_starts"),
+        *tries, int(q_starts.numel()) - 1, H, R._i32(q_starts, "q_starts", dev),
+        R._i32(k_starts, "k_starts", dev),
         Tq, Tk, int(max_q_len), *[ctypes.byref(r) for r in rows[:5]], float(sm_scale),
-        int(bool(causal)), ctypes.byref(rows[5]), B._ptr(flags), B._stream(stream)), name)
+        int(bool(causal)), ctypes.byref(rows[5]), R._ptr(flags, dev), R._stream(stream, dev)), name)

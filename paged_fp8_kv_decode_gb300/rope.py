@@ -43,17 +43,45 @@ class Rope:
     interleaved: bool = False
     scale: float = 1.0
 
-    def c_struct(self) -> _CRope:
+    def c_struct(self, dev: int) -> _CRope:
         if self.inv_freq.dtype != torch.float32 or not self.inv_freq.is_contiguous():
             raise ValueError("inv_freq: contiguous float32")
-        return _CRope(B._ptr(self.inv_freq), 2 * self.inv_freq.numel(), int(bool(self.interleaved)),
+        return _CRope(_ptr(self.inv_freq, dev), 2 * self.inv_freq.numel(), int(bool(self.interleaved)),
                       float(self.scale))
 
 
 _BF16, _I32, _byref = torch.bfloat16, torch.int32, ctypes.byref
 
 
-def _rows(x: torch.Tensor, packed: bool, heads: bool, name: str, dim: int) -> _CRows:
+def _current() -> int:
+    """The kernels run on the current device, whose stream `None` stands for: device
+    memory of any argument of a call is that device's."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+
+
+def _ptr(t, dev: int) -> Optional[int]:
+    """binding._ptr of memory of device `dev` or of the host."""
+    if t is None or t.__class__ is int:
+        return t
+    d = t.get_device()
+    if d == dev and d >= 0:
+        return t.data_ptr()
+    if d >= 0:
+        raise ValueError("tensors of another device than the current one")
+    return B._ptr(t)
+
+
+def _stream(stream, dev: int) -> Optional[int]:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else B._stream(stream)
+
+
+def _pages(p: B.Pages, dev: int) -> B._CPages:
+    return B._CPages(p.batch, p.max_pages, _ptr(p.block_tables, dev), p.bt_stride_b, p.bt_stride_h,
+                     _ptr(p.seq_lens, dev), p.len_stride_b, p.len_stride_h,
+                     _ptr(p.expected_tags, dev))
+
+
+def _rows(x: torch.Tensor, packed: bool, heads: bool, name: str, dim: int, dev: int) -> _CRows:
     """bf16 rows as the C ABI takes them: [B][T][H][D] padded or [rows][H][D]
     packed, without H where the rows are shared by all heads; any strides that
     leave a row's elements contiguous."""
@@ -63,26 +91,20 @@ def _rows(x: torch.Tensor, packed: bool, heads: bool, name: str, dim: int) -> _C
         raise ValueError(f"{name}: bfloat16 tensor of {want} dimensions with contiguous rows")
     if x.size(-1) != dim:
         raise ValueError(f"{name}: rows of {dim} elements")
-    p = x.data_ptr() if x.is_cuda else B._ptr(x)
+    p = _ptr(x, dev)
     if packed:
         return _CRows(p, 0, s[0], s[1] if heads else 0)
     return _CRows(p, s[0], s[1], s[2] if heads else 0)
 
 
-def _here(x: torch.Tensor) -> None:
-    """The kernels run on the current device, whose stream `None` stands for."""
-    if x.is_cuda and x.get_device() != torch.cuda.current_device():
-        raise ValueError("tensors of another device than the current one")
-
-
-def _i32(t: Optional[torch.Tensor], name: str):
+def _i32(t: Optional[torch.Tensor], name: str, dev: int):
     if t is not None and t.dtype != _I32:
         raise ValueError(f"{name}: int32")
-    return B._ptr(t)
+    return _ptr(t, dev)
 
 
 def _new_tokens(first: torch.Tensor, batch: int, positions, new_lens, rope_positions, row_starts,
-                max_new_tokens) -> _CNewTokens:
+                max_new_tokens, dev: int) -> _CNewTokens:
     """`first`: the tensor of new rows that gives T or the number of rows."""
     if row_starts is None:
         if first.shape[0] != batch:
@@ -96,11 +118,12 @@ def _new_tokens(first: torch.Tensor, batch: int, positions, new_lens, rope_posit
         if row_starts.numel() != batch + 1:
             raise ValueError("row_starts: batch + 1 entries")
         T, total = int(max_new_tokens), first.shape[0]
-    return _CNewTokens(T, _i32(positions, "positions"), _i32(new_lens, "new_lens"),
-                       _i32(rope_positions, "rope_positions"), _i32(row_starts, "row_starts"), total)
+    return _CNewTokens(T, _i32(positions, "positions", dev), _i32(new_lens, "new_lens", dev),
+                       _i32(rope_positions, "rope_positions", dev),
+                       _i32(row_starts, "row_starts", dev), total)
 
 
-def _queries(q, q_out, first, packed, dim):
+def _queries(q, q_out, first, packed, dim, dev):
     """(q rows, q_out rows, heads), or three empty ones without queries."""
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out: both or neither")
@@ -109,7 +132,8 @@ def _queries(q, q_out, first, packed, dim):
     lead = 1 if packed else 2
     if q.shape != q_out.shape or q.shape[:lead] != first.shape[:lead]:
         raise ValueError("q and q_out: rows for the same tokens as the new keys")
-    return _rows(q, packed, True, "q", dim), _rows(q_out, packed, True, "q_out", dim), q.shape[-2]
+    return (_rows(q, packed, True, "q", dim, dev), _rows(q_out, packed, True, "q_out", dim, dev),
+            q.shape[-2])
 
 
 def _ref(s):
@@ -143,17 +167,20 @@ def pfkv_rope_append(cache: B.Cache, pages: B.Pages, rope: Rope, positions: torc
     query heads (q_out may be q); positions, new_lens int32 with the length
     strides of ``pages``, rope_positions int32 [B]; flags uint8
     [>= round_up(B, 4)] (OR-ed)."""
-    _here(cache.k_pages)
+    dev = _current()
     packed = row_starts is not None
-    _, heads, _, D = cache.k_pages.shape
+    NP, heads, PS, D = cache.k_pages.shape
     tok = _new_tokens(k_new, pages.batch, positions, new_lens, rope_positions, row_starts,
-                      max_new_tokens)
+                      max_new_tokens, dev)
     if k_new.shape != v_new.shape or k_new.shape[-2] != heads:
         raise ValueError("k_new and v_new: one row per kv head")
-    k, v = _rows(k_new, packed, True, "k_new", D), _rows(v_new, packed, True, "v_new", D)
-    qr, qo, hq = _queries(q, q_out, k_new, packed, D)
-    c, p, r = cache.c_struct(), pages.c_struct(), rope.c_struct()
+    k = _rows(k_new, packed, True, "k_new", D, dev)
+    v = _rows(v_new, packed, True, "v_new", D, dev)
+    qr, qo, hq = _queries(q, q_out, k_new, packed, D, dev)
+    c = B._CCache(NP, heads, PS, D, cache.dtype, _ptr(cache.k_pages, dev), _ptr(cache.v_pages, dev),
+                  _ptr(cache.k_scale, dev), _ptr(cache.v_scale, dev), _ptr(cache.page_tags, dev))
+    p, r = _pages(pages, dev), rope.c_struct(dev)
     B._check(lib().pfkv_rope_append(_byref(c), _byref(p), _byref(r),
                                     _byref(tok), _byref(k), _byref(v), _ref(qr),
-                                    _ref(qo), hq, B._ptr(flags), B._stream(stream)),
+                                    _ref(qo), hq, _ptr(flags, dev), _stream(stream, dev)),
              "pfkv_rope_append")
