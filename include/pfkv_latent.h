@@ -116,6 +116,7 @@ pfkv_status pfkv_latent_gather(const pfkv_latent_cache *cache, const pfkv_pages 
  *          num_q_heads: queries times the key up-projection
  *   q_r  : rows of rope_dim elements: the queries' rotated parts, turned
  *   out  : rows of latent_dim elements: sum_j softmax_j c_j, rounded to bf16
+ *   cache: the pages are device memory (tensor copies fetch them)
  *   num_q_heads x num_query_tokens: any count >= 1 (up to 2^20 rows a request)
  *   max_seq_len: host-known upper bound of every seq_lens entry
  *   workspace  : >= pfkv_latent_decode_workspace_size(...) bytes, 256-byte

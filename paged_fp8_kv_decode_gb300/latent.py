@@ -53,9 +53,9 @@ class LatentCache:
         c, r = self.c_pages, self.r_pages
         NP, PS, D = c.shape
         rNP, rPS, rD = r.shape
-        if (rNP != NP or rPS != PS or r.dtype != torch.bfloat16 or not r.is_contiguous()
-                or not c.is_contiguous()):
+        if rNP != NP or rPS != PS or r.dtype != torch.bfloat16 or not r.is_contiguous():
             raise ValueError("c_pages [pages][16][512] and bfloat16 r_pages [pages][16][64], contiguous")
+        R._pool(c, self.c_scale, self.page_tags, NP)
         return _CLatentCache(NP, PS, D, rD, self.dtype, R._ptr(c, dev), R._ptr(r, dev),
                              R._ptr(self.c_scale, dev), R._ptr(self.page_tags, dev))
 
@@ -147,7 +147,10 @@ def pfkv_latent_decode_attn(cache: LatentCache, pages: B.Pages, q_c: torch.Tenso
                             flags: Optional[torch.Tensor] = None, stream=None) -> None:
     """q_c, out: bf16 [B][kq][H][512], q_r: bf16 [B][kq][H][64], any strides
     that leave rows contiguous: the last kq tokens of every request; workspace:
-    uint8 of at least pfkv_latent_decode_workspace_size(...) bytes."""
+    uint8 of at least pfkv_latent_decode_workspace_size(...) bytes.  The pool is in
+    device memory (tensor copies fetch it)."""
+    if not (cache.c_pages.is_cuda and cache.r_pages.is_cuda):
+        raise ValueError("a pool in device memory")
     if (q_c.shape != out.shape or q_c.shape[:-1] != q_r.shape[:-1]
             or q_c.shape[0] != pages.batch):
         raise ValueError("q_c and out [B][kq][H][512], q_r [B][kq][H][64]")

@@ -71,6 +71,25 @@ def _ptr(t, dev: int) -> Optional[int]:
     return B._ptr(t)
 
 
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_TAGS = (_I32, torch.uint32)
+
+
+def _pool(pages: torch.Tensor, scale, tags, units: int) -> None:
+    """One pool's tensors: bfloat16, or e4m3 codes with a float32 scale a unit; a tag a unit."""
+    if pages.dtype != _BF16:
+        if pages.dtype not in _CODES:
+            raise ValueError("pages: bfloat16, or uint8 for e4m3 codes")
+        if (scale is None or scale.dtype != torch.float32 or scale.numel() < units
+                or not scale.is_contiguous()):
+            raise ValueError("pages of e4m3 codes need a contiguous float32 scale each")
+    if tags is not None and (tags.dtype not in _TAGS or tags.numel() < units
+                             or not tags.is_contiguous()):
+        raise ValueError("page_tags: contiguous int32, one each")
+    if not pages.is_contiguous():
+        raise ValueError("pages: contiguous")
+
+
 def _stream(stream, dev: int) -> Optional[int]:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else B._stream(stream)
 
@@ -170,6 +189,10 @@ def pfkv_rope_append(cache: B.Cache, pages: B.Pages, rope: Rope, positions: torc
     dev = _current()
     packed = row_starts is not None
     NP, heads, PS, D = cache.k_pages.shape
+    if cache.v_pages.shape != cache.k_pages.shape or cache.v_pages.dtype != cache.k_pages.dtype:
+        raise ValueError("k_pages and v_pages: alike")
+    _pool(cache.k_pages, cache.k_scale, cache.page_tags, NP * heads)
+    _pool(cache.v_pages, cache.v_scale, None, NP * heads)
     tok = _new_tokens(k_new, pages.batch, positions, new_lens, rope_positions, row_starts,
                       max_new_tokens, dev)
     if k_new.shape != v_new.shape or k_new.shape[-2] != heads:
