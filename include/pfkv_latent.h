@@ -189,12 +189,19 @@ pfkv_status pfkv_latent_prefill_attn(int32_t batch, int32_t num_heads, const int
                                      void *stream);
 
 /*
- * pfkv_selftest_latent_prefill -- pfkv_latent_prefill_attn with waits that give up
- * after `tries` tries (0 .. 100000, which is what the call itself takes; 0.2 to 4 us
- * each; 1000 times as many for waits that last as long as a tile's work), so that a
- * test can let them run out: the call ends, its requests are flagged
- * PFKV_FLAG_DEVICE_TIMEOUT, and the context stays usable.
+ * pfkv_selftest_latent_decode, pfkv_selftest_latent_prefill -- the two attention calls
+ * with waits that give up after `tries` tries (0 .. 100000, which is what the calls
+ * themselves take; 0.2 to 4 us each; 1000 times as many for waits that last as long as
+ * a tile's work), so that a test can let them run out: the call ends, requests are
+ * flagged PFKV_FLAG_DEVICE_TIMEOUT (and their rows zero: decode), and the context stays
+ * usable.
  */
+pfkv_status pfkv_selftest_latent_decode(int32_t tries, const pfkv_latent_cache *cache,
+                                        const pfkv_pages *pages, const pfkv_rows *q_c,
+                                        const pfkv_rows *q_r, int32_t num_q_heads,
+                                        int32_t num_query_tokens, float sm_scale,
+                                        int32_t max_seq_len, void *workspace, size_t workspace_bytes,
+                                        const pfkv_rows *out, uint8_t *flags, void *stream);
 pfkv_status pfkv_selftest_latent_prefill(int32_t tries, int32_t batch, int32_t num_heads,
                                          const int32_t *q_starts, const int32_t *k_starts,
                                          int64_t total_q, int64_t total_k, int32_t max_q_len,

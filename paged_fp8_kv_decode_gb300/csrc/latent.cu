@@ -205,6 +205,15 @@ pfkv_status pfkv_latent_decode_attn(const pfkv_latent_cache *cache, const pfkv_p
                                     const pfkv_rows *q_r, int32_t num_q_heads, int32_t num_query_tokens,
                                     float sm_scale, int32_t max_seq_len, void *workspace, size_t workspace_bytes,
                                     const pfkv_rows *out, uint8_t *flags, void *stream) {
+    return pfkv_selftest_latent_decode(kTries, cache, pages, q_c, q_r, num_q_heads, num_query_tokens, sm_scale,
+                                       max_seq_len, workspace, workspace_bytes, out, flags, stream);
+}
+
+pfkv_status pfkv_selftest_latent_decode(int32_t tries, const pfkv_latent_cache *cache, const pfkv_pages *pages,
+                                        const pfkv_rows *q_c, const pfkv_rows *q_r, int32_t num_q_heads,
+                                        int32_t num_query_tokens, float sm_scale, int32_t max_seq_len, void *workspace,
+                                        size_t workspace_bytes, const pfkv_rows *out, uint8_t *flags, void *stream) {
+    if (tries < 0 || tries > kTries) return PFKV_ERR_INVALID_ARG;
     pfkv_status st = check_decode(cache, pages, num_q_heads, num_query_tokens, max_seq_len);
     if (st != PFKV_OK) return st;
     if (!std::isfinite(sm_scale)) return PFKV_ERR_INVALID_ARG;
@@ -233,6 +242,7 @@ pfkv_status pfkv_latent_decode_attn(const pfkv_latent_cache *cache, const pfkv_p
     a.max_seq_len = max_seq_len;
     a.sm_scale = sm_scale;
     a.workspace = workspace;
+    a.tries = tries;
     return launch_latent_decode(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PFKV_OK : PFKV_ERR_CUDA;
 }
 

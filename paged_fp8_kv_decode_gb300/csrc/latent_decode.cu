@@ -316,7 +316,8 @@ __device__ __forceinline__ bool bar_any(int id, bool says) {
     return r != 0;
 }
 
-template <bool FP8>
+// Selftest: waits of as many tries as the call says.
+template <bool FP8, bool Selftest>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_split_kernel(const __grid_constant__ CUtensorMap mapc, const __grid_constant__ CUtensorMap mapr,
                         const __grid_constant__ CUtensorMap mapk,
@@ -432,9 +433,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int N = (int)(m.x1 - m.x0);  // tiles of this cluster: every role counts them
     const uint32_t tmem = m.tmem;
     volatile uint32_t *const gave_up = &m.gave_up;
+    const int tries = Selftest ? a.tries : kTries;
     // Waits until tile t is looked up; false when a wait of this CTA has given up
     // (the entry may then be anything, and is not used).
-    auto looked_up = [&](int t) { return bar_wait(&m.mfull[t % kRing], (t / kRing) & 1, gave_up); };
+    auto looked_up = [&](int t) { return bar_wait(&m.mfull[t % kRing], (t / kRing) & 1, gave_up, tries); };
 
     // Registers of the five warpgroups, of 5 x 96 at launch: 2 x 120 + 64 + 2 x 88.  No role
     // may spill: with 230 KB of shared memory there is next to no L1 to catch it.
@@ -510,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     iz[i] = ti.iz[part * 2 + i];
                 }
             }
-            bar_wait(&m.sfull[t & 1], (t >> 1) & 1, gave_up);
+            bar_wait(&m.sfull[t & 1], (t >> 1) & 1, gave_up, tries);
             tmem_fence_after();
             float x[32];
             float top = kNegInf;
@@ -584,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (t > 0) {
-                bar_wait(&m.pvdone, (t - 1) & 1, gave_up);  // P is free, O is at rest
+                bar_wait(&m.pvdone, (t - 1) & 1, gave_up, tries);  // P is free, O is at rest
                 tmem_fence_after();
             }
             if (any_live) {
@@ -612,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (t + 1 < N && looked_up(t + 1)) fetch_queries(m.tile[(t + 1) % kRing].b, m.tile[(t + 1) % kRing].block);
                 const bool whole = (flags & kWhole) != 0;
                 const int slot = w * 2 + ((flags & kBegins) ? 1 : 0);
-                const bool done = bar_wait(&m.pvdone, t & 1, gave_up);
+                const bool done = bar_wait(&m.pvdone, t & 1, gave_up, tries);
                 tmem_fence_after();
                 float (&sums)[4][kRowsCta] = m.xm[(t & 1) ^ 1];  // read before this tile's first barrier
                 sums[part][r] = sum;
@@ -692,11 +694,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t idR = umma_idesc(kRowBlock, kTile, true, false, false);
             constexpr uint32_t idO = umma_idesc(kRowBlock, 256, !FP8, false, true);
             auto values = [&](int t, bool first) {
-                const bool ok = bar_wait(&m.pready, t & 1, gave_up);
+                const bool ok = bar_wait(&m.pready, t & 1, gave_up, tries);
                 const uint32_t da = umma_desc(pa, 16);
 #pragma unroll 1
                 for (int nb = 0; nb < 2; ++nb) {
-                    if (!bar_wait(&m.vfull[nb], t & 1, gave_up) || !ok) continue;
+                    if (!bar_wait(&m.vfull[nb], t & 1, gave_up, tries) || !ok) continue;
                     tmem_fence_after();
                     const uint32_t db = umma_desc(va + nb * 2 * kVChunkB, kVLbo<FP8>);
 #pragma unroll
@@ -717,12 +719,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool first = (flags & kFirst) != 0;
                 // the products of the tile before this one's scores when Q changes between them
                 if (t > 0 && first) values(t - 1, pfirst);
-                if (first) bar_wait(&m.qfull, seg & 1, gave_up);
+                if (first) bar_wait(&m.qfull, seg & 1, gave_up, tries);
                 const uint32_t cs = tmem + kColS + (t & 1) * 128;
                 // The rotated keys come first: their one slot is refilled by TMA, which then has
                 // the rest of the tile's time.  (Loops over stages stay loops: unrolled, their
                 // descriptors cost the registers that the other roles need.)
-                bool ok = bar_wait(&m.kfull[4], t & 1, gave_up);
+                bool ok = bar_wait(&m.kfull[4], t & 1, gave_up, tries);
                 uint32_t da = umma_desc(qa, 16), db = umma_desc(ka, 16);
                 if (ok) {
                     tmem_fence_after();
@@ -734,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c, da += 2 * kChunkB >> 4, db += 2 * kChunkB >> 4) {
-                    ok = bar_wait(&m.kfull[c], t & 1, gave_up) && ok;
+                    ok = bar_wait(&m.kfull[c], t & 1, gave_up, tries) && ok;
                     if (!ok) continue;
                     tmem_fence_after();
 #pragma unroll
@@ -767,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < kTilePages; ++i) pages += ti.id[i] >= 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) id[i] = ti.id[rank * 4 + i];
-                if (!bar_wait(&m.kempty[4], (t & 1) ^ 1, gave_up)) break;
+                if (!bar_wait(&m.kempty[4], (t & 1) ^ 1, gave_up, tries)) break;
                 // The odd CTA arrives too, with its ids in registers: where its four pages are
                 // past the last token its bytes hold nothing up, and the ring's entry and the
                 // barriers' phases would go on without it.
@@ -779,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (!FP8) {
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
-                        if (!bar_wait(&m.kempty[c], (t & 1) ^ 1, gave_up)) break;
+                        if (!bar_wait(&m.kempty[c], (t & 1) ^ 1, gave_up, tries)) break;
                         if (rank == 0) mbar_arrive_expect_tx(&m.kfull[c], pages * 4096u);
                         else bar_arrive_at(&m.kfull[c], 0);
                         uint8_t *dst = k + 2 * c * kChunkB;
@@ -806,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int full = min(kTilePages, max(0, sound) / kPage);  // pages whose slots are all taken as they are
 #pragma unroll 1
             for (int nb = 0; nb < 2; ++nb) {
-                if (!__all_sync(0xffffffffu, bar_wait(&m.vempty[nb], (t & 1) ^ 1, gave_up))) break;
+                if (!__all_sync(0xffffffffu, bar_wait(&m.vempty[nb], (t & 1) ^ 1, gave_up, tries))) break;
                 uint8_t *dst = v + nb * 2 * kVChunkB;
                 const int x = (nb * 4 + (int)rank * 2) * 64;
                 if (elect_one()) {
@@ -888,7 +890,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         odd_latents<FP8>(a.pool.c_pages, id, j * 8, max(0, seen_all - first), min(kTile, held), lane))
                         sound = seen_all - first;
                     Tile &ti = m.tile[t % kRing];
-                    if (!__all_sync(0xffffffffu, bar_wait(&m.mempty[t % kRing], ((t / kRing) & 1) ^ 1, gave_up))) continue;
+                    if (!__all_sync(0xffffffffu, bar_wait(&m.mempty[t % kRing], ((t / kRing) & 1) ^ 1, gave_up, tries))) continue;
                     if (lane < 16 && i == j) {
                         ti.id[pg] = id;
                         ti.z[pg] = z;
@@ -957,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int u = 0; u < 16; ++u)
                     if (u * 4 + r_in >= left) raw[u] = make_uint4(0u, 0u, 0u, 0u);
             }
-            bar_wait(&m.kempty[j], (t & 1) ^ 1, gave_up);
+            bar_wait(&m.kempty[j], (t & 1) ^ 1, gave_up, tries);
 #pragma unroll
             for (int u = 0; u < 16; ++u) {
                 const uint32_t to = at[u & 1] + u * 512;
@@ -999,7 +1001,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int u = 0; u < 16; ++u)
                     if (u * 8 + r_in >= held) raw[u] = make_uint4(0u, 0u, 0u, 0u);
             }
-            bar_wait(&m.vempty[s >> 1], (t & 1) ^ 1, gave_up);
+            bar_wait(&m.vempty[s >> 1], (t & 1) ^ 1, gave_up, tries);
 #pragma unroll
             for (int u = 0; u < 16; ++u) {  // row u * 8 + r_in
                 store_shared(at + u * 1024, cvt_e4m3x8(raw[u].x, raw[u].y));
@@ -1236,7 +1238,8 @@ cudaError_t launch_split(const CUtensorMap &mapc, const CUtensorMap &mapr, const
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, latent_split_kernel<FP8>, mapc, mapr, mapk, a, R, blocks, clusters, parts);
+    auto *const kernel = a.tries == kTries ? latent_split_kernel<FP8, false> : latent_split_kernel<FP8, true>;
+    return cudaLaunchKernelEx(&cfg, kernel, mapc, mapr, mapk, a, R, blocks, clusters, parts);
 }
 
 }  // namespace
@@ -1278,9 +1281,10 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs &a, int num_sms, cudaStr
 }
 
 cudaError_t preload_latent_decode() {
-    cudaError_t e = cudaFuncSetAttribute(latent_split_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(latent_split_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    cudaError_t e = cudaSuccess;
+    for (auto *const kernel : {latent_split_kernel<true, false>, latent_split_kernel<false, false>,
+                               latent_split_kernel<true, true>, latent_split_kernel<false, true>})
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (e == cudaSuccess) e = preload_kernel(latent_merge_kernel<1>);
     if (e == cudaSuccess) e = preload_kernel(latent_merge_kernel<4>);
     return e;

@@ -98,6 +98,7 @@ struct LatentDecodeArgs {
     int B, H, kq, max_seq_len;
     float sm_scale;
     void *workspace;
+    int tries;  // of a wait
 };
 
 struct LatentPrefillArgs {

@@ -22,7 +22,8 @@ PFKV_LATENT_VDIM = 128
 
 # every symbol include/pfkv_latent.h declares
 EXPORTED = ("pfkv_latent_append", "pfkv_latent_gather", "pfkv_latent_decode_workspace_size",
-            "pfkv_latent_decode_attn", "pfkv_latent_prefill_attn", "pfkv_selftest_latent_prefill")
+            "pfkv_latent_decode_attn", "pfkv_latent_prefill_attn", "pfkv_selftest_latent_decode",
+            "pfkv_selftest_latent_prefill")
 
 
 class _CLatentCache(ctypes.Structure):
@@ -75,6 +76,7 @@ def lib() -> ctypes.CDLL:
                                                         ctypes.POINTER(Z)]
         L.pfkv_latent_decode_attn.argtypes = [cache, pages, rows, rows, I32, I32, F, I32, P, Z,
                                               rows, P, P]
+        L.pfkv_selftest_latent_decode.argtypes = [I32, *L.pfkv_latent_decode_attn.argtypes]
         L.pfkv_latent_prefill_attn.argtypes = [I32, I32, P, P, I64, I64, I32, rows, rows, rows,
                                                rows, rows, F, I32, rows, P, P]
         L.pfkv_selftest_latent_prefill.argtypes = [I32, *L.pfkv_latent_prefill_attn.argtypes]
@@ -149,6 +151,18 @@ def pfkv_latent_decode_attn(cache: LatentCache, pages: B.Pages, q_c: torch.Tenso
     that leave rows contiguous: the last kq tokens of every request; workspace:
     uint8 of at least pfkv_latent_decode_workspace_size(...) bytes.  The pool is in
     device memory (tensor copies fetch it)."""
+    _decode((), cache, pages, q_c, q_r, sm_scale, max_seq_len, workspace, out, flags, stream)
+
+
+def pfkv_selftest_latent_decode(tries: int, *args, flags: Optional[torch.Tensor] = None,
+                                stream=None) -> None:
+    """pfkv_latent_decode_attn (whose positional arguments follow) with waits that give
+    up after ``tries`` tries."""
+    _decode((int(tries),), *args, flags, stream)
+
+
+def _decode(tries, cache, pages, q_c, q_r, sm_scale, max_seq_len, workspace, out, flags,
+            stream) -> None:
     if not (cache.c_pages.is_cuda and cache.r_pages.is_cuda):
         raise ValueError("a pool in device memory")
     if (q_c.shape != out.shape or q_c.shape[:-1] != q_r.shape[:-1]
@@ -159,11 +173,12 @@ def pfkv_latent_decode_attn(cache: LatentCache, pages: B.Pages, q_c: torch.Tenso
     qr = R._rows(q_r, False, True, "q_r", cache.r_pages.shape[2], dev)
     o = R._rows(out, False, True, "out", cache.c_pages.shape[2], dev)
     k, p = cache.c_struct(dev), R._pages(pages, dev)
-    B._check(lib().pfkv_latent_decode_attn(
-        ctypes.byref(k), ctypes.byref(p), ctypes.byref(qc), ctypes.byref(qr), q_c.shape[2],
+    name = "pfkv_selftest_latent_decode" if tries else "pfkv_latent_decode_attn"
+    B._check(getattr(lib(), name)(
+        *tries, ctypes.byref(k), ctypes.byref(p), ctypes.byref(qc), ctypes.byref(qr), q_c.shape[2],
         q_c.shape[1], float(sm_scale), int(max_seq_len), R._ptr(workspace, dev),
         workspace.nbytes, ctypes.byref(o), R._ptr(flags, dev),
-        R._stream(stream, dev)), "pfkv_latent_decode_attn")
+        R._stream(stream, dev)), name)
 
 
 def pfkv_latent_prefill_attn(q_nope: torch.Tensor, q_rope: torch.Tensor, k_nope: torch.Tensor,

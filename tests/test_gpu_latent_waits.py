@@ -4,8 +4,9 @@ the self-test entry points, so no wait has to last."""
 import pytest
 import torch
 
+import test_gpu_latent_decode as D
 import test_gpu_latent_prefill as P
-from latent_cases import SCALE, flags_for, gen, i32
+from latent_cases import PAGE, SCALE, flags_for, gen, i32, latent_pool, pages, rows, tables
 from paged_fp8_kv_decode_gb300 import binding as B
 from paged_fp8_kv_decode_gb300 import latent as L
 
@@ -69,3 +70,34 @@ def test_prefill_waits_that_last_as_long_as_an_item():
     out, fl = prefill(300, x, qs, ks, max(nq))
     assert fl == [0, 0]
     assert torch.equal(out, want)
+
+
+def decode(tries, cache, bt, lens, qc, qr):
+    Bn, kq, H, _ = qc.shape
+    pg = pages(bt, i32(lens))
+    ws = torch.empty(L.pfkv_latent_decode_workspace_size(cache, pg, H, kq, max(lens)), dtype=torch.uint8, device="cuda")
+    ws.fill_(0xFF)
+    out, fl = torch.full_like(qc, 7.0), flags_for(Bn)
+    fl.fill_(0x55)
+    L.pfkv_selftest_latent_decode(tries, cache, pg, qc, qr, SCALE, max(lens), ws, out, flags=fl)
+    torch.cuda.synchronize()
+    return out, fl[:Bn].tolist()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("H,kq", [(16, 1), (128, 2)])
+def test_decode_flags_and_zeroes_what_a_wait_left(H, kq, fp8):
+    g = gen(99)
+    lens = [300, 1, 0, 5000, 64, 129] * 6
+    bt, num = tables([(n + PAGE - 1) // PAGE for n in lens], seed=6)
+    cache = latent_pool(g, num, fp8)
+    qc, qr = rows(g, len(lens), kq, H, 512, outliers=0), rows(g, len(lens), kq, H, 64, outliers=0)
+    want, fl = D.run(cache, bt, lens, qc, qr)
+    assert not any(fl)
+    out, fl = decode(0, cache, bt, lens, qc, qr)
+    assert fl == [B.PFKV_FLAG_DEVICE_TIMEOUT if n else 0 for n in lens]
+    assert not out.any()
+    out, fl = decode(NEVER, cache, bt, lens, qc, qr)
+    assert not any(fl) and torch.equal(out, want)
+    out, fl = D.run(cache, bt, lens, qc, qr)
+    assert not any(fl) and torch.equal(out, want)
