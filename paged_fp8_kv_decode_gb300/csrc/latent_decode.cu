@@ -7,7 +7,8 @@
 // 2 R (576 + 512) operations a token for 1,152 bytes (BF16) or 640 (FP8): at 128
 // rows 242 or 435 operations a byte, where this GPU turns from memory-bound to
 // tensor-bound (288 at the measured rates).  So both products run on the
-// fifth-generation tensor cores, and every latent is to be read from HBM once.
+// fifth-generation tensor cores, and every latent is to be read from HBM once for up to
+// 128 rows (each further block of 128 reads it again).
 //
 // Why a pair of CTAs.  A row's result is 512 fp32 values: 128 rows of it fill a
 // streaming multiprocessor's whole tensor memory, and the scores have no room.
@@ -20,7 +21,7 @@
 // A tile is 128 tokens (8 pages).  For S each CTA brings 64 of them (K: nine
 // chunks of 64 values, 8 KB each); for O each brings all 128 tokens of 256 of the
 // values (V: four chunks, 16 KB each), as V's columns are split between the
-// CTAs.  Each latent is thus read from HBM once, and from L2 twice.  Shared
+// CTAs.  A block's rows thus read each latent from HBM once, and from L2 twice.  Shared
 // memory (Q 72 KB, K 72 KB, V 64 KB, P 16 KB) leaves no room for second buffers;
 // instead every stage's slot is refilled as soon as its last product has completed,
 // and an L2 prefetch runs ahead of that.
@@ -37,11 +38,15 @@
 // written out directly; parts of a pair go to the workspace (normalised rows and
 // their log2-sum-exp) and a second kernel merges them.
 //
-// Measured: a tile takes 1.82 us with BF16 pages (6.2 TB/s over 76 clusters, 91% of a
-// copy) and 2.35 us with FP8 ones, where 400 KB pass through shared memory a tile
+// Measured: a tile takes 1.85 us with BF16 pages (6.1 TB/s over 76 clusters, 90% of a
+// copy) and 2.45 us with FP8 ones, where 400 KB pass through shared memory a tile
 // (converted K and V stored, operands read, weights): 1.6 us at 128 bytes a cycle, and
 // the softmax's chain (scores read, maxima exchanged, weights stored when the last
 // products have ended) is 1.9 us long.  A call has 20-24 us besides: start 8, a part's end 4-6, merge 5.
+//
+// Tokens that a row does not see have weights of zero.  So that values which are not finite do
+// not reach it, a tile's tokens past the last that any row of the block sees are zero in the
+// second product, and those that only some rows see (several query tokens) are looked at.
 //
 // Roles of a CTA's twenty warps: 0-7 softmax and output (four threads a row); 8, in
 // the even CTA, issues the pair's products; 9 and 10 load rotated keys, K and V by TMA

@@ -21,10 +21,13 @@
 // What bounds it: one thread issues all products of the CTA, and they need it to be
 // quick.  A wait between two groups of them, satisfied or not, costs the tensor cores
 // about 140 cycles, and loops and descriptors in 64 bits as much again: 4,096 tokens of
-// 128 heads took 704 us with those, 477 us with barriers asked a group ahead and straight
+// 128 heads took 704 us with those, 480 us with barriers asked a group ahead and straight
 // code.  Then shared memory: S reads 128 bytes a cycle, all there is, and the copies of
 // K and V write beside it (1.39 us a pair of steps without them, 1.64 with them; the
-// whole kernel 1.75).  That is 1,440 TFLOP/s.
+// whole kernel 1.75).  That is 1,430 TFLOP/s.
+//
+// A row that does not see every key and comes out not finite has its item done once more, with
+// care for the values that it must not see (below).
 //
 // The kernel is persistent.  Work items are ordered so that the CTAs at work share
 // the K and V of few heads (about two rounds of items a group of heads, or all heads
@@ -32,7 +35,8 @@
 // that change direction, so that each CTA gets long and short ones.
 //
 // Roles of a CTA's twelve warps: 0-3 and 4-7 softmax and output of the two tiles; 8
-// issues the products; 9 loads K and V, 10 loads Q (TMA); 11 looks up items.  The flags are written by a launch before it.
+// issues the products; 9 loads K and V, 10 loads Q (TMA); 11 looks up items.  The flags are written by a
+// launch before it.
 #include "latent_internal.cuh"
 #include "umma.cuh"
 
@@ -628,7 +632,8 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, int num_sms, cudaS
     // heads (256 MiB): 502 us, 438 in groups.
     // Where there are few numbers, every CTA can look through all of them (32 a step of the
     // looking warp) and items alone are dealt out, which evens out ragged lengths: 5 prompts
-    // of up to 777 tokens, 16 heads, 26.5 us, 33.9 with all numbers dealt.
+    // of up to 777 tokens, 16 heads, 26.5 us, 33.9 with all numbers dealt (29.6 now, with the
+    // flags' launch and the list's end behind the last result).
     const bool fits = a.total_k * a.H * (PFKV_LATENT_NOPE + PFKV_LATENT_VDIM) * 2 <= (192LL << 20) &&
                       pairs <= (1LL << 30) / max(1, d.tiles);  // numbers within a group are 32-bit
     d.pairs = (int)min(pairs, fits ? pairs : (2LL * num_sms + d.tiles - 1) / max(1, d.tiles));

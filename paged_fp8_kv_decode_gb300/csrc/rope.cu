@@ -324,9 +324,11 @@ __device__ __forceinline__ UnitSpan unit_span(int p0, int n, int k, int max_page
 // head, K or V, its bf16 words held in registers between the absolute maximum and
 // the encoding, so that each element is read once) or a group of query rows.
 //
-// 16,752 tokens, 32 query and 8 kv heads of 128, FP8: 377 MB in 85 us (4.4 TB/s).  The
-// queries' part takes what a copy of them takes (43 us); keys and values (37 us) are
-// bound by instructions (turning, maximum, codes), not by their 103 MB.
+// 16,752 tokens, 32 query and 8 kv heads of 128, FP8: 377 MB in 86 us (4.4 TB/s).  The
+// queries alone take what a copy of them takes (43 us).  Keys and values alone take 37 us
+// for 103 MB: turning, maximum and codes are 23 instructions an element and lane, and half of
+// the issue slots are used: 24 warps a multiprocessor leave latencies open, and the CTAs are
+// 3.4 rounds of those that fit.  In one call the two parts add up.
 // --------------------------------------------------------------------------
 template <int D, bool FP8>
 __device__ __forceinline__ void append_turned_unit(const RopeAppendArgs &a, const Span &sp, const Trig &tr, int tlo,

@@ -50,7 +50,8 @@ class LatentCache:
     def dtype(self) -> int:
         return B.PFKV_KV_BF16 if self.c_pages.dtype == torch.bfloat16 else B.PFKV_KV_FP8_E4M3
 
-    def c_struct(self, dev: int) -> _CLatentCache:
+    def c_struct(self, dev: Optional[int] = None) -> _CLatentCache:
+        dev = R._current() if dev is None else dev
         c, r = self.c_pages, self.r_pages
         NP, PS, D = c.shape
         rNP, rPS, rD = r.shape

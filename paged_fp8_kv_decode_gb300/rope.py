@@ -43,7 +43,8 @@ class Rope:
     interleaved: bool = False
     scale: float = 1.0
 
-    def c_struct(self, dev: int) -> _CRope:
+    def c_struct(self, dev: Optional[int] = None) -> _CRope:
+        dev = _current() if dev is None else dev
         if self.inv_freq.dtype != torch.float32 or not self.inv_freq.is_contiguous():
             raise ValueError("inv_freq: contiguous float32")
         return _CRope(_ptr(self.inv_freq, dev), 2 * self.inv_freq.numel(), int(bool(self.interleaved)),

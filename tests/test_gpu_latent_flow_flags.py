@@ -50,3 +50,27 @@ def test_flags_of_every_call(refused, fp8):
     assert flags(lambda fl: L.pfkv_latent_decode_attn(cache, tables_of(more), qc, one[2], SCALE, 102, ws, o, flags=fl)) == want
     for b in range(Bn):
         assert o[b].any() == (b != refused)
+
+
+def test_flags_of_a_replayed_graph():
+    """A captured prompt call writes its flags at every replay, whatever they held."""
+    g = gen(107)
+    x = {k: rows(g, 60, *s, outliers=0) for k, s in dict(qn=(4, 128), qr=(4, 64), kn=(4, 128), kr=(64,), v=(4, 128)).items()}
+    qs, out, fl = i32([0, 20, 60]), torch.zeros(60, 4, 128, dtype=torch.bfloat16, device="cuda"), flags_for(2)
+    call = lambda: L.pfkv_latent_prefill_attn(x["qn"], x["qr"], x["kn"], x["kr"], x["v"], qs, qs, 50, SCALE, True, out, flags=fl)  # noqa: E731
+    call()
+    want = out.clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        call()
+    for starts, flags in (([0, 20, 60], [0, 0]), ([0, 20, 61], [0, 4]), ([0, 51, 60], [4, 0]), ([0, 20, 60], [0, 0])):
+        fl.fill_(0x55)
+        out.fill_(7.0)
+        qs.copy_(i32(starts))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert fl[:2].tolist() == flags and (fl[2:] == 0x55).all()
+        if starts == [0, 20, 60]:
+            assert torch.equal(out, want)
