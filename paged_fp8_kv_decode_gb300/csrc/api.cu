@@ -6,8 +6,10 @@
 #include <cstdint>
 #include <cstring>
 
+#include "evict_internal.cuh"
 #include "latent_internal.cuh"
 #include "pfkv_internal.cuh"
+#include "prefix_internal.cuh"
 
 namespace pfkv {
 namespace {
@@ -53,6 +55,8 @@ pfkv_status device_check(int *num_sms) {
             if (e == cudaSuccess) e = preload_latent();
             if (e == cudaSuccess) e = preload_latent_decode();
             if (e == cudaSuccess) e = preload_latent_prefill();
+            if (e == cudaSuccess) e = preload_prefix();
+            if (e == cudaSuccess) e = preload_evict();
             if (e != cudaSuccess) {
                 cudaGetLastError();
                 return PFKV_ERR_CUDA;
