@@ -81,6 +81,23 @@ pfkv_status pfkv_prefix_decode_attn(const pfkv_cache *cache, const pfkv_pages *p
                                     int64_t mass_stride_b, int64_t mass_stride_h, uint8_t *flags,
                                     void *stream);
 
+/*
+ * pfkv_selftest_prefix_decode -- the call with waits that give up after `tries` tries
+ * (0 .. 100000, which is what the call itself takes; 0.2 to 4 us each; 1000 times as many for
+ * waits that last as long as a segment's work), so that a test can let them run out: the call
+ * ends, every request with a prefix is flagged PFKV_FLAG_DEVICE_TIMEOUT and its rows are zero,
+ * and the context stays usable.
+ */
+pfkv_status pfkv_selftest_prefix_decode(int32_t tries, const pfkv_cache *cache,
+                                        const pfkv_pages *pages, const pfkv_pages *prefixes,
+                                        int32_t batch, const int32_t *prefix_of, const pfkv_rows *q,
+                                        int32_t num_q_heads, int32_t num_query_tokens,
+                                        float sm_scale, int32_t max_seq_len, int32_t max_prefix_len,
+                                        void *workspace, size_t workspace_bytes,
+                                        const pfkv_rows *out, float *attn_mass,
+                                        int64_t mass_stride_b, int64_t mass_stride_h,
+                                        uint8_t *flags, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

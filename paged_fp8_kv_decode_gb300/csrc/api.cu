@@ -173,9 +173,11 @@ pfkv_status append_args(const pfkv_cache *cache, const pfkv_pages *pages, const 
     return PFKV_OK;
 }
 
+}  // namespace
+
 pfkv_status make_plan(const pfkv_cache *c, const pfkv_pages *p, int32_t num_q_heads,
                       int32_t split_tokens, int32_t max_seq_len, int num_sms, DecodePlan *plan,
-                      bool mass = false, int32_t kq = 1, bool cuda_cores = false) {
+                      bool mass, int32_t kq, bool cuda_cores) {
     const pfkv_status st = check_decode_args(c, num_q_heads, split_tokens, max_seq_len);
     if (st != PFKV_OK) return st;
     if (kq < 1 || (long long)p->batch * kq > 0x7fffffffLL) return PFKV_ERR_INVALID_ARG;
@@ -254,7 +256,24 @@ pfkv_status make_plan(const pfkv_cache *c, const pfkv_pages *p, int32_t num_q_he
     return PFKV_OK;
 }
 
-}  // namespace
+// The arguments of the request group starting at request r0: every
+// per-request pointer moved to the group's first request.
+DecodeArgs group_args(const DecodeArgs &a, const DecodePlan &p, int r0) {
+    DecodeArgs g = a;
+    const long long v0 = (long long)r0 * p.kq;  // first virtual request
+    g.q = a.q + v0 * p.Hq * p.D;
+    g.out = a.out + v0 * p.Hq * p.D;
+    if (a.flags) g.flags = a.flags + r0;
+    g.block_tables = a.block_tables + (long long)r0 * a.bt_sb;
+    g.seq_lens = a.seq_lens + (long long)r0 * a.len_sb;
+    if (a.expected_tags) g.expected_tags = a.expected_tags + (long long)r0 * a.bt_sb;
+    if (a.hflags) g.hflags = a.hflags + (long long)r0 * p.Hkv * p.htiles;
+    if (a.mscore) g.mscore = a.mscore + v0 * p.Hkv * (long long)a.mlen * p.G;
+    if (a.lse_fin) g.lse_fin = a.lse_fin + v0 * p.Hq;
+    if (a.rflags) g.rflags = a.rflags + r0;
+    return g;
+}
+
 }  // namespace pfkv
 
 using namespace pfkv;
@@ -321,24 +340,6 @@ pfkv_status pfkv_decode_workspace_size(const pfkv_cache *cache, const pfkv_pages
 }  // extern "C"
 
 namespace {
-
-// The arguments of the request group starting at request r0: every
-// per-request pointer moved to the group's first request.
-DecodeArgs group_args(const DecodeArgs &a, const DecodePlan &p, int r0) {
-    DecodeArgs g = a;
-    const long long v0 = (long long)r0 * p.kq;  // first virtual request
-    g.q = a.q + v0 * p.Hq * p.D;
-    g.out = a.out + v0 * p.Hq * p.D;
-    if (a.flags) g.flags = a.flags + r0;
-    g.block_tables = a.block_tables + (long long)r0 * a.bt_sb;
-    g.seq_lens = a.seq_lens + (long long)r0 * a.len_sb;
-    if (a.expected_tags) g.expected_tags = a.expected_tags + (long long)r0 * a.bt_sb;
-    if (a.hflags) g.hflags = a.hflags + (long long)r0 * p.Hkv * p.htiles;
-    if (a.mscore) g.mscore = a.mscore + v0 * p.Hkv * (long long)a.mlen * p.G;
-    if (a.lse_fin) g.lse_fin = a.lse_fin + v0 * p.Hq;
-    if (a.rflags) g.rflags = a.rflags + r0;
-    return g;
-}
 
 struct MassOut {
     float *mass;

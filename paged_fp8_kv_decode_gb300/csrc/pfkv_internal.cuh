@@ -210,6 +210,12 @@ __device__ __forceinline__ bool request_rejected_cta(const DecodeArgs &a, int b,
     return __syncthreads_or(f) != 0;
 }
 
+// The launch plan of an attention call, and the arguments of one of its request groups (api.cu)
+pfkv_status make_plan(const pfkv_cache *c, const pfkv_pages *p, int32_t num_q_heads, int32_t split_tokens,
+                      int32_t max_seq_len, int num_sms, DecodePlan *plan, bool mass = false, int32_t kq = 1,
+                      bool cuda_cores = false);
+DecodeArgs group_args(const DecodeArgs &a, const DecodePlan &p, int r0);
+
 // launchers (defined in the .cu files)
 cudaError_t launch_kv_append(const AppendArgs &a, int B, cudaStream_t s);
 cudaError_t launch_validate(const DecodeArgs &a, const DecodePlan &p, cudaStream_t s);

@@ -1,9 +1,10 @@
 // prefix.cu -- pfkv_prefix_decode_attn: attention of a batch whose requests share
 // prefixes (declared in pfkv_prefix.h).
 //
-// The plainest form: one launch checks every request's lengths and table entries, a
-// second attends, a CTA a (query token, kv head), over the prefix's and the request's
-// own tokens with a running maximum and sum a warp.
+// Four launches.  The plan checks every table, sorts the requests by their prefix and cuts the
+// work of the prefixes into equal shares (below).  The split kernel of pfkv_paged_decode_attn
+// (decode_pers.cuh) attends over the requests' own tokens, and the kernel of prefix_attn.cu over the
+// prefixes; both leave normalised partial results with their log2-sum-exp, which the merge joins.
 #include <cmath>
 
 #include "prefix_internal.cuh"
@@ -11,7 +12,36 @@
 namespace pfkv {
 namespace {
 
-constexpr int kCheckThreads = 256, kAttnWarps = 4;
+// --------------------------------------------------------------------------
+// The plan: the first CTA counts the requests of every prefix and cuts the work into
+// segments and partial results; the others check one tile of a table row each, like
+// validate_kernel, with the tags as far as they are tracked, or pack the queries.  It waits for
+// its predecessor before it lets the next kernel start, so the call's inputs are final then.
+// --------------------------------------------------------------------------
+// Exclusive sum over the block of one number a thread; the total in *total.  Ends synchronised.
+__device__ __forceinline__ int block_sum_before(int v, int *part, int *total) {
+    const int tid = threadIdx.x;
+    __syncthreads();
+    part[tid] = v;
+    __syncthreads();
+    if (tid < 32) {
+        int carry = 0;
+        for (int at = 0; at < kValThreads; at += 32) {
+            const int x0 = part[at + tid];
+            int x = x0;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, off);
+                if (tid >= off) x += y;
+            }
+            part[at + tid] = carry + x - x0;
+            carry += __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (tid == 0) *total = carry;
+    }
+    __syncthreads();
+    return part[tid];
+}
 
 // Tokens of row i for head h; -1 where a bound does not hold.
 __device__ __forceinline__ int table_len(const PrefixTables &t, int i, int h) {
@@ -19,197 +49,386 @@ __device__ __forceinline__ int table_len(const PrefixTables &t, int i, int h) {
     return n < 0 || n > t.max_len || (long long)n > (long long)t.max_pages * kPage ? -1 : n;
 }
 
-__device__ uint32_t table_bits(const PrefixArgs &a, const PrefixTables &t, int i) {
-    uint32_t bits = 0u;
-    for (int h = 0; h < a.Hkv; ++h) {
-        const int n = table_len(t, i, h);
-        if (n < 0) bits |= PFKV_FLAG_BAD_LENGTH;
-        for (int p = threadIdx.x; p < (n + kPage - 1) / kPage; p += blockDim.x) {
-            const long long e = (long long)i * t.bt_sb + (long long)h * t.bt_sh + p;
-            const int id = t.block_tables[e];
-            if (id < 0 || id >= a.num_pages) bits |= PFKV_FLAG_BAD_PAGE;
-            else if (a.page_tags && a.page_tags[(long long)id * a.Hkv + h] != t.expected_tags[e]) bits |= PFKV_FLAG_TAG_MISMATCH;
-        }
-    }
-    return bits;
-}
+constexpr int kPlanChunk = 2048;
 
-__global__ void __launch_bounds__(kCheckThreads) prefix_check_kernel(PrefixArgs a) {
-    pdl_enter();
-    const int b = blockIdx.x, p = a.prefix_of[b];
-    uint32_t bits = 0u;
-    if (p < -1 || p >= a.pre.count) bits = PFKV_FLAG_BAD_PAGE;
-    else if (p >= 0) bits = table_bits(a, a.pre, p);
-    if (a.own.count > 0) bits |= table_bits(a, a.own, b);
-    uint32_t all = 0u;
-    for (const uint32_t f : {PFKV_FLAG_BAD_LENGTH, PFKV_FLAG_BAD_PAGE, PFKV_FLAG_TAG_MISMATCH})
-        if (__syncthreads_or((bits & f) != 0u)) all |= f;
-    if (threadIdx.x == 0) {
-        a.rflags[b] = all;
-        if (a.flags) a.flags[b] = (uint8_t)all;
-    }
-}
-
-template <int D, bool FP8>
-__device__ __forceinline__ void row_values(const void *pool, long long row, float scale, float (&x)[D / 32]) {
-    const int lane = threadIdx.x & 31;
-    if constexpr (FP8) {
-        const uint8_t *p = static_cast<const uint8_t *>(pool) + row * D + lane * (D / 32);
-#pragma unroll
-        for (int i = 0; i < D / 32; i += 2) {
-            const float2 v = e4m3x2_to_float2(*reinterpret_cast<const uint16_t *>(p + i));
-            x[i] = v.x * scale;
-            x[i + 1] = v.y * scale;
-        }
-    } else {
-        const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(pool) + row * D + lane * (D / 32);
-#pragma unroll
-        for (int i = 0; i < D / 32; i += 2) {
-            const float2 v = bf16x2_to_float2(*reinterpret_cast<const uint32_t *>(p + i));
-            x[i] = v.x;
-            x[i + 1] = v.y;
-        }
-    }
-}
-
-template <int D, bool FP8, int G>
-__global__ void __launch_bounds__(kAttnWarps * 32) prefix_plain_kernel(PrefixArgs a) {
-    pdl_enter();
-    constexpr int V = D / 32;
-    __shared__ float s_m[kAttnWarps][G], s_l[kAttnWarps][G], s_o[kAttnWarps][G][D];
-    const int v = blockIdx.x, h = blockIdx.y, b = v / a.kq, t = v - b * a.kq;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long to = (long long)b * a.out.sb + (long long)t * a.out.st;
-    if (a.rflags[b]) {
-        for (int i = threadIdx.x; i < G * D; i += kAttnWarps * 32)
-            a.out.p[to + (long long)(h * G + i / D) * a.out.sh + i % D] = __float2bfloat16(0.f);
-        return;
-    }
-    float q[G][V], o[G][V], m[G], l[G];
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-        const __nv_bfloat16 *src = a.q.p + (long long)b * a.q.sb + (long long)t * a.q.st + (long long)(h * G + g) * a.q.sh;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            q[g][i] = __bfloat162float(src[lane * V + i]) * a.q_scale;
-            o[g][i] = 0.f;
-        }
-        m[g] = -INFINITY;
-        l[g] = 0.f;
-    }
-    // the score of one token of a unit for head g, in every lane
-    auto score = [&](const float (&k)[V], int g) {
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) s = fmaf(q[g][i], k[i], s);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        return s;
-    };
-    const int p = a.prefix_of[b];
-    const int seen = a.own.count > 0 ? max(0, table_len(a.own, b, h) - a.kq + 1 + t) : 0;
-    for (int part = 0; part < 2; ++part) {
-        const PrefixTables &tab = part ? a.own : a.pre;
-        const int row = part ? b : p, n = part ? seen : p >= 0 ? table_len(a.pre, p, h) : 0;
-        for (int page = warp; page < (n + kPage - 1) / kPage; page += kAttnWarps) {
-            const int id = tab.block_tables[(long long)row * tab.bt_sb + (long long)h * tab.bt_sh + page];
-            const long long unit = (long long)id * a.Hkv + h;
-            const float ks = FP8 ? a.k_scale[unit] : 1.f, vs = FP8 ? a.v_scale[unit] : 1.f;
-            for (int j = 0; j < min(kPage, n - page * kPage); ++j) {
-                float k[V], x[V];
-                row_values<D, FP8>(a.k_pages, unit * kPage + j, ks, k);
-                row_values<D, FP8>(a.v_pages, unit * kPage + j, vs, x);
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    const float s = score(k, g);
-                    const float top = fmaxf(m[g], s), down = m[g] == top ? 1.f : exp2f(m[g] - top), w = exp2f(s - top);
-                    m[g] = top;
-                    l[g] = l[g] * down + w;
-#pragma unroll
-                    for (int i = 0; i < V; ++i) o[g][i] = fmaf(w, x[i], o[g][i] * down);
-                }
+__device__ void plan_segments(const PrefixArgs &a) {
+    __shared__ int count[PFKV_PREFIX_MAX];  // requests of a prefix
+    __shared__ int of[kPlanChunk], part[kValThreads], total;
+    const int tid = threadIdx.x, lane = tid & 31, NP = a.pre.count;
+    if (tid == 0) a.head->timeout = 0u;
+    for (int p = tid; p < NP; p += kValThreads) count[p] = 0;
+    // positions, in the order of the batch: one warp takes 32 requests at a time
+    for (int b0 = 0; b0 < a.B; b0 += kPlanChunk) {
+        const int n = min(kPlanChunk, a.B - b0);
+        __syncthreads();
+        for (int i = tid; i < n; i += kValThreads) of[i] = a.prefix_of[b0 + i];
+        __syncthreads();
+        if (tid < 32) {
+            for (int i = lane; i - lane < n; i += 32) {
+                const int p = i < n ? of[i] : -1;
+                const bool valid = p >= 0 && p < NP;
+                const uint32_t same = __match_any_sync(0xffffffffu, valid ? p : -1 - lane);
+                const int rank = __popc(same & ((1u << lane) - 1u));
+                const int before = valid ? count[p] : 0;
+                __syncwarp();
+                if (valid && rank == 0) count[p] = before + __popc(same);
+                __syncwarp();
+                if (i < n) a.pos[b0 + i] = valid ? before + rank : -1;
             }
         }
     }
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-        if (lane == 0) {
-            s_m[warp][g] = m[g];
-            s_l[warp][g] = l[g];
+    __syncthreads();
+    // first members and first segments
+    const auto blocks = [&](int p) { return (int)(((long long)count[p] * a.kq * a.G + kPrefixBlock - 1) / kPrefixBlock); };
+    {
+        const int per = (NP + kValThreads - 1) / kValThreads, p0 = min(NP, tid * per), p1 = min(NP, p0 + per);
+        int members = 0, segs = 0;
+        for (int p = p0; p < p1; ++p) {
+            members += count[p];
+            segs += blocks(p) * a.Hkv;
         }
-#pragma unroll
-        for (int i = 0; i < V; ++i) s_o[warp][g][lane * V + i] = o[g][i];
+        members = block_sum_before(members, part, &total);
+        if (tid == 0) a.mstart[NP] = total;
+        segs = block_sum_before(segs, part, &total);
+        if (tid == 0) a.seg0[NP] = total;
+        for (int p = p0; p < p1; ++p) {
+            a.mstart[p] = members;
+            a.seg0[p] = segs;
+            members += count[p];
+            segs += blocks(p) * a.Hkv;
+        }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < G * D; i += kAttnWarps * 32) {
-        const int g = i / D;
-        float top = -INFINITY, sum = 0.f, x = 0.f;
-        for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, s_m[w][g]);
-        for (int w = 0; w < kAttnWarps; ++w) {
-            const float f = s_l[w][g] == 0.f ? 0.f : exp2f(s_m[w][g] - top);
-            sum += f * s_l[w][g];
-            x += f * s_o[w][g][i % D];
-        }
-        a.out.p[to + (long long)(h * G + g) * a.out.sh + i % D] = __float2bfloat16(sum == 0.f ? 0.f : x / sum);
+    for (int b = tid; b < a.B; b += kValThreads) {
+        const int p = a.prefix_of[b], at = a.pos[b];
+        if (at >= 0) a.members[a.mstart[p] + at] = b;
     }
-    if (!a.mass) return;
-    float lse[G];
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-        float top = -INFINITY, sum = 0.f;
-        for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, s_m[w][g]);
-        for (int w = 0; w < kAttnWarps; ++w) sum += s_l[w][g] == 0.f ? 0.f : exp2f(s_m[w][g] - top) * s_l[w][g];
-        lse[g] = top + log2f(sum);
+    // tiles, and rows of partial results
+    const int pairs = NP * a.Hkv, per = (pairs + kValThreads - 1) / kValThreads;
+    const int x0 = min(pairs, tid * per), x1 = min(pairs, x0 + per);
+    const auto tiles = [&](int x) {
+        const int p = x / a.Hkv;
+        return (max(0, table_len(a.pre, p, x - p * a.Hkv)) + kPrefixTile - 1) / kPrefixTile;
+    };
+    int mine = 0;
+    for (int x = x0; x < x1; ++x) mine += blocks(x / a.Hkv) * tiles(x);
+    int tile = block_sum_before(mine, part, &total);
+    const int U = total, W = min(a.ctas, U), tile_first = tile;
+    if (tid == 0) {
+        a.head->U = U;
+        a.head->W = W;
     }
-    float *mass = a.mass + (long long)b * a.mass_sb + (long long)h * a.mass_sh;
-    for (int page = warp; page < (seen + kPage - 1) / kPage; page += kAttnWarps) {
-        const int id = a.own.block_tables[(long long)b * a.own.bt_sb + (long long)h * a.own.bt_sh + page];
-        const long long unit = (long long)id * a.Hkv + h;
-        for (int j = 0; j < min(kPage, seen - page * kPage); ++j) {
-            float k[V], sum = 0.f;
-            row_values<D, FP8>(a.k_pages, unit * kPage + j, FP8 ? a.k_scale[unit] : 1.f, k);
-#pragma unroll
-            for (int g = 0; g < G; ++g) sum += exp2f(score(k, g) - lse[g]);
-            if (lane == 0) mass[page * kPage + j] += sum;
+    for (int pass = 0, base = 0; pass < 2; ++pass) {
+        int rows = 0;
+        tile = tile_first;
+        for (int x = x0; x < x1; ++x) {
+            const int p = x / a.Hkv, h = x - p * a.Hkv, nb = blocks(p);
+            if (nb == 0) continue;
+            const int n = tiles(x), R = (int)((long long)count[p] * a.kq * a.G), len = max(0, table_len(a.pre, p, h));
+            for (int rb = 0; rb < nb; ++rb) {
+                PrefixSeg s;
+                s.p = p;
+                s.h = h;
+                s.row0 = rb * kPrefixBlock;
+                s.rows = min(kPrefixBlock, R - s.row0);
+                s.tile0 = tile;
+                s.ntiles = n;
+                s.base = base + rows;
+                s.len = len;
+                if (pass) a.seg[a.seg0[p] + h * nb + rb] = s;
+                if (n > 0) rows += rows8(s.rows) * (pers_worker_of(tile + n - 1, U, W) - pers_worker_of(tile, U, W) + 1);
+                tile += n;
+            }
         }
+        if (pass == 0) base = block_sum_before(rows, part, &total);
     }
 }
 
-template <int D, bool FP8>
-cudaError_t launch_plain(const PrefixArgs &a, cudaStream_t s) {
-    const dim3 grid((unsigned)(a.B * a.kq), (unsigned)a.Hkv), block(kAttnWarps * 32);
+// Check bits of one tile of kValTile entries of table row i, head h; VMAX: and its pages' largest |V scale|.
+template <bool VMAX>
+__device__ void check_tile(const PrefixArgs &a, const PrefixTables &t, int ih, int tile, uint32_t *bits_out, float *vmax_out) {
+    const int i = ih / a.Hkv, h = ih - i * a.Hkv;
+    const int n = table_len(t, i, h), np = (n + kPage - 1) / kPage;
+    const int p0 = tile * kValTile + threadIdx.x;
+    const long long row = (long long)i * t.bt_sb + (long long)h * t.bt_sh;
+    int id[kValPer];
+    uint32_t want[kValPer], tag[kValPer];
+#pragma unroll
+    for (int j = 0; j < kValPer; ++j) {
+        const int p = p0 + j * kValThreads;
+        id[j] = p < t.max_pages ? t.block_tables[row + p] : 0;
+        want[j] = p < t.max_pages && a.page_tags ? t.expected_tags[row + p] : 0u;
+    }
+    uint32_t bits = n < 0 ? PFKV_FLAG_BAD_LENGTH : 0u;
+    float scale[kValPer];
+#pragma unroll
+    for (int j = 0; j < kValPer; ++j) {
+        const bool live = p0 + j * kValThreads < np, in_pool = id[j] >= 0 && id[j] < a.num_pages;
+        if (live && !in_pool) bits |= PFKV_FLAG_BAD_PAGE;
+        const long long unit = live && in_pool ? (long long)id[j] * a.Hkv + h : -1;
+        tag[j] = unit >= 0 && a.page_tags ? a.page_tags[unit] : want[j];
+        scale[j] = VMAX && unit >= 0 ? fabsf(a.v_scale[unit]) : 0.f;
+        if (unit < 0) want[j] = tag[j];
+    }
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < kValPer; ++j) {
+        if (tag[j] != want[j]) bits |= PFKV_FLAG_TAG_MISMATCH;
+        top = fmaxf(top, scale[j]);
+    }
+    __shared__ uint32_t all, most;
+    if (threadIdx.x == 0) all = most = 0u;
+    __syncthreads();
+    bits = __reduce_or_sync(0xffffffffu, bits);
+    const uint32_t high = __reduce_max_sync(0xffffffffu, __float_as_uint(top));  // not negative: ordered as numbers
+    if ((threadIdx.x & 31) == 0) {
+        if (bits) atomicOr(&all, bits);
+        if (VMAX) atomicMax(&most, high);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        bits_out[(long long)ih * t.htiles + tile] = all;
+        if (VMAX) vmax_out[(long long)ih * t.htiles + tile] = __uint_as_float(most);
+    }
+}
+
+constexpr int kPackPer = 4;  // 16-byte chunks a thread packs
+
+template <bool FP8>
+__global__ void __launch_bounds__(kValThreads) prefix_plan_kernel(PrefixArgs a, int D, int pre_tiles, int own_tiles) {
+    pdl_enter();
+    int x = blockIdx.x;
+    if (x == 0) {
+        plan_segments(a);
+        return;
+    }
+    x -= 1;
+    if (x < pre_tiles) {
+        check_tile<FP8>(a, a.pre, x / a.pre.htiles, x % a.pre.htiles, a.pre_bits, a.pre_vmax);
+        return;
+    }
+    x -= pre_tiles;
+    if (x < own_tiles) {
+        check_tile<false>(a, a.own, x / a.own.htiles, x % a.own.htiles, a.own_bits, nullptr);
+        return;
+    }
+    // queries as rows that follow each other
+    x -= own_tiles;
+    const int per = D / 8, Hq = a.Hkv * a.G;
+    const long long chunks = (long long)a.B * a.kq * Hq * per;
+#pragma unroll
+    for (int j = 0; j < kPackPer; ++j) {
+        const long long at = ((long long)x * kPackPer + j) * kValThreads + threadIdx.x;
+        if (at >= chunks) return;
+        const long long row = at / per;
+        const int c = (int)(at - row * per), hq = (int)(row % Hq);
+        const long long v = row / Hq;
+        const int b = (int)(v / a.kq), t = (int)(v - (long long)b * a.kq);
+        reinterpret_cast<uint4 *>(a.packed_q)[at] = *reinterpret_cast<const uint4 *>(
+            a.q.p + (long long)b * a.q.sb + (long long)t * a.q.st + (long long)hq * a.q.sh + c * 8);
+    }
+}
+
+// --------------------------------------------------------------------------
+// The merge: a CTA a (request, query token, kv head).  Its partial results are those that the
+// CTAs of the attention over the prefix left for its rows, and those that the workers of the own
+// tokens' split kernel left for its segment; out = sum 2^(lse - M) o / sum 2^(lse - M).
+// --------------------------------------------------------------------------
+constexpr int kMergeThreads = 256;
+
+template <int D, int G>
+__global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(PrefixArgs a, PrefixOwnRows own) {
+    constexpr int C4 = D / 4, TPR = G * C4, WAYS = kMergeThreads / TPR;
+    static_assert(WAYS >= 1 && TPR % 32 == 0 || TPR < 32, "whole warps a way");
+    __shared__ uint32_t s_flags;
+    __shared__ float s_m[WAYS][G], s_s[WAYS][G];
+    __shared__ float4 s_o[WAYS][TPR];
+    pdl_enter();
+    const int v = blockIdx.x / a.Hkv, h = blockIdx.x - v * a.Hkv, b = v / a.kq, t = v - b * a.kq;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) s_flags = 0u;
+    __syncthreads();
+    // the request's flags
+    const int p = a.prefix_of[b];
+    const bool member = p >= 0 && p < a.pre.count;
+    uint32_t f = p < -1 || p >= a.pre.count ? PFKV_FLAG_BAD_PAGE : 0u;
+    if (member) {
+        f |= a.head->timeout;
+        for (int i = tid; i < a.Hkv * a.pre.htiles; i += kMergeThreads) f |= a.pre_bits[(long long)p * a.Hkv * a.pre.htiles + i];
+    }
+    if (own.status)
+        for (int i = tid; i < a.Hkv * a.own.htiles; i += kMergeThreads) f |= a.own_bits[(long long)b * a.Hkv * a.own.htiles + i];
+    // own tokens: rows k + worker of the request's group of launches
+    long long own_row = 0;
+    int own_n = 0;
+    size_t shift = 0;
+    if (own.status) {
+        const int grp = b / own.greq, r0 = grp * own.greq, Bg = min(own.greq, a.B - r0);
+        shift = (size_t)grp * own.group_bytes;
+        const int *prefix = reinterpret_cast<const int *>(reinterpret_cast<const uint8_t *>(own.prefix) + shift);
+        const uint32_t *status = reinterpret_cast<const uint32_t *>(reinterpret_cast<const uint8_t *>(own.status) + shift);
+        const int U = prefix[Bg * a.kq * a.Hkv], W = min(own.workers, U);
+        // every segment of the request: a warp each
+        for (int i = warp; i < a.kq * a.Hkv; i += kMergeThreads / 32) {
+            const int k = (b - r0) * a.kq * a.Hkv + i, u0 = prefix[k], u1 = prefix[k + 1];
+            if (u1 == u0) continue;
+            const int w0 = pers_worker_of(u0, U, W), w1 = pers_worker_of(u1 - 1, U, W);
+            for (int w = w0 + lane; w <= w1; w += 32) f |= status[k + w];
+        }
+        const int k = ((b - r0) * a.kq + t) * a.Hkv + h, u0 = prefix[k], u1 = prefix[k + 1];
+        if (u1 > u0) {
+            const int w0 = pers_worker_of(u0, U, W);
+            own_row = k + w0;
+            own_n = pers_worker_of(u1 - 1, U, W) - w0 + 1;
+        }
+    }
+    f = __reduce_or_sync(0xffffffffu, f);
+    if (lane == 0 && f) atomicOr(&s_flags, f);
+    // the prefix's: one a CTA that touched the rows' segment
+    int pre_n = 0, pre_rows = 0, base = 0, block_row = 0;
+    if (member) {
+        const int R = (a.pos[b] * a.kq + t) * G;
+        const int nb = (int)(((long long)(a.mstart[p + 1] - a.mstart[p]) * a.kq * G + kPrefixBlock - 1) / kPrefixBlock);
+        const PrefixSeg sg = a.seg[a.seg0[p] + h * nb + R / kPrefixBlock];
+        if (sg.ntiles > 0) {
+            const int U = a.head->U, W = a.head->W;
+            pre_n = pers_worker_of(sg.tile0 + sg.ntiles - 1, U, W) - pers_worker_of(sg.tile0, U, W) + 1;
+            pre_rows = rows8(sg.rows);
+            base = sg.base;
+            block_row = R % kPrefixBlock;
+        }
+    }
+    __syncthreads();
+    const uint32_t flags = s_flags;
+    if (t == 0 && h == 0 && tid == 0) {
+        if (a.flags) a.flags[b] = (uint8_t)flags;
+        if (own.rflags) own.rflags[b] = (uint8_t)flags;
+    }
+    const int way = tid / TPR, e = tid - way * TPR, g = e / C4, c = e - g * C4;
+    const bool works = way < WAYS;
+    __nv_bfloat16 *out = a.out.p + (long long)b * a.out.sb + (long long)t * a.out.st;
+    if (flags) {
+        if (way == 0)
+            *reinterpret_cast<uint2 *>(out + (long long)(h * G + g) * a.out.sh + c * 4) = make_uint2(0u, 0u);
+        return;
+    }
+    const float *own_lse = reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(own.lse) + shift);
+    const float *own_o = reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(own.o) + shift);
+    float M = -INFINITY, S = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int n = works ? pre_n + own_n : 0;
+    constexpr int RB = 4;  // rows in flight
+    for (int j0 = way; j0 < n; j0 += RB * WAYS) {
+        float l[RB];
+        float4 x[RB];
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            const int j = j0 + r * WAYS;
+            l[r] = -INFINITY;
+            x[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (j < pre_n) {
+                const long long first = base + (long long)j * pre_rows;
+                l[r] = a.plse[first + block_row + g];
+                x[r] = reinterpret_cast<const float4 *>(a.po + first * D)[(long long)c * pre_rows + block_row + g];
+            } else if (j < n) {
+                const long long row = (own_row + j - pre_n) * G + g;
+                l[r] = own_lse[row];
+                x[r] = reinterpret_cast<const float4 *>(own_o + row * D)[c];
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            if (l[r] == -INFINITY) continue;  // no token
+            if (l[r] > M) {
+                const float down = exp2f(M - l[r]);
+                S *= down;
+                acc = make_float4(acc.x * down, acc.y * down, acc.z * down, acc.w * down);
+                M = l[r];
+            }
+            const float w = exp2f(l[r] - M);
+            S += w;
+            acc = make_float4(fmaf(w, x[r].x, acc.x), fmaf(w, x[r].y, acc.y), fmaf(w, x[r].z, acc.z), fmaf(w, x[r].w, acc.w));
+        }
+    }
+    if (WAYS > 1) {
+        if (works) {
+            if (c == 0) {
+                s_m[way][g] = M;
+                s_s[way][g] = S;
+            }
+            s_o[way][e] = acc;
+        }
+        __syncthreads();
+        if (way != 0) return;
+#pragma unroll
+        for (int w2 = 1; w2 < WAYS; ++w2) {
+            const float M2 = s_m[w2][g], S2 = s_s[w2][g];
+            const float4 y = s_o[w2][e];
+            if (S2 == 0.f) continue;
+            const float top = fmaxf(M, M2), f1 = M == top ? 1.f : exp2f(M - top), f2 = M2 == top ? 1.f : exp2f(M2 - top);
+            S = S * f1 + S2 * f2;
+            acc = make_float4(acc.x * f1 + y.x * f2, acc.y * f1 + y.y * f2, acc.z * f1 + y.z * f2, acc.w * f1 + y.w * f2);
+            M = top;
+        }
+    }
+    if (c == 0 && own.lse_fin) own.lse_fin[((long long)v * a.Hkv + h) * G + g] = S == 0.f ? -INFINITY : M + log2f(S);
+    const float inv = S == 0.f ? 0.f : 1.f / S;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+    *reinterpret_cast<uint2 *>(out + (long long)(h * G + g) * a.out.sh + c * 4) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+}
+
+template <int D>
+cudaError_t launch_merge_d(const PrefixArgs &a, const PrefixOwnRows &o, cudaStream_t s) {
+    const dim3 grid((unsigned)((long long)a.B * a.kq * a.Hkv)), block(kMergeThreads);
     switch (a.G) {
-        case 1: return launch_pdl(prefix_plain_kernel<D, FP8, 1>, grid, block, 0, s, a);
-        case 2: return launch_pdl(prefix_plain_kernel<D, FP8, 2>, grid, block, 0, s, a);
-        case 4: return launch_pdl(prefix_plain_kernel<D, FP8, 4>, grid, block, 0, s, a);
-        case 8: return launch_pdl(prefix_plain_kernel<D, FP8, 8>, grid, block, 0, s, a);
+        case 1: return launch_pdl(prefix_merge_kernel<D, 1>, grid, block, 0, s, a, o);
+        case 2: return launch_pdl(prefix_merge_kernel<D, 2>, grid, block, 0, s, a, o);
+        case 4: return launch_pdl(prefix_merge_kernel<D, 4>, grid, block, 0, s, a, o);
+        case 8: return launch_pdl(prefix_merge_kernel<D, 8>, grid, block, 0, s, a, o);
     }
     return cudaErrorInvalidValue;
 }
 
-}  // namespace
-
-cudaError_t launch_prefix(const PrefixArgs &a, int D, bool fp8, int num_sms, cudaStream_t s) {
-    const cudaError_t e = launch_pdl(prefix_check_kernel, dim3((unsigned)a.B), dim3(kCheckThreads), 0, s, a);
-    if (e != cudaSuccess) return e;
-    if (D == 128) return fp8 ? launch_plain<128, true>(a, s) : launch_plain<128, false>(a, s);
-    return fp8 ? launch_plain<64, true>(a, s) : launch_plain<64, false>(a, s);
+template <int D>
+cudaError_t preload_merge_d() {
+    cudaError_t e = preload_kernel(prefix_merge_kernel<D, 1>);
+    if (e == cudaSuccess) e = preload_kernel(prefix_merge_kernel<D, 2>);
+    if (e == cudaSuccess) e = preload_kernel(prefix_merge_kernel<D, 4>);
+    if (e == cudaSuccess) e = preload_kernel(prefix_merge_kernel<D, 8>);
+    return e;
 }
 
-cudaError_t preload_prefix() { return preload_kernel(prefix_check_kernel); }
+}  // namespace
+
+cudaError_t launch_prefix_plan(const PrefixArgs &a, int D, bool fp8, cudaStream_t s) {
+    const long long pre = (long long)a.pre.count * a.Hkv * a.pre.htiles, own = (long long)a.own.count * a.Hkv * a.own.htiles;
+    const long long chunks = a.packed_q ? (long long)a.B * a.kq * a.Hkv * a.G * (D / 8) : 0;
+    const long long pack = (chunks + kPackPer * kValThreads - 1) / (kPackPer * kValThreads);
+    const dim3 grid((unsigned)(1 + pre + own + pack)), block(kValThreads);
+    return launch_pdl(fp8 ? prefix_plan_kernel<true> : prefix_plan_kernel<false>, grid, block, 0, s, a, D, (int)pre, (int)own);
+}
+
+cudaError_t launch_prefix_merge(const PrefixArgs &a, const PrefixOwnRows &o, int D, cudaStream_t s) {
+    return D == 128 ? launch_merge_d<128>(a, o, s) : launch_merge_d<64>(a, o, s);
+}
+
+cudaError_t preload_prefix() {
+    cudaError_t e = preload_kernel(prefix_plan_kernel<false>);
+    if (e == cudaSuccess) e = preload_kernel(prefix_plan_kernel<true>);
+    if (e == cudaSuccess) e = preload_merge_d<128>();
+    if (e == cudaSuccess) e = preload_merge_d<64>();
+    if (e == cudaSuccess) e = preload_prefix_attn();
+    return e;
+}
 
 namespace {
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
-struct PrefixSizes {
-    size_t off_rflags, total;
-};
-
-// Arguments that size the workspace.
-pfkv_status prefix_sizes(const pfkv_cache *cache, const pfkv_pages *pages, const pfkv_pages *prefixes, int32_t batch,
-                         int32_t num_q_heads, int32_t kq, int32_t max_seq_len, int32_t max_prefix_len, bool mass,
-                         PrefixSizes *z) {
+// Checks of what sizes a call (no CUDA call).
+pfkv_status check_prefix(const pfkv_cache *cache, const pfkv_pages *pages, const pfkv_pages *prefixes, int32_t batch,
+                         int32_t num_q_heads, int32_t kq, int32_t max_seq_len, int32_t max_prefix_len, bool mass) {
     pfkv_status st = check_cache(cache);
     if (st != PFKV_OK) return st;
     if (batch < 0) return PFKV_ERR_INVALID_ARG;
@@ -231,15 +450,201 @@ pfkv_status prefix_sizes(const pfkv_cache *cache, const pfkv_pages *pages, const
     if (mass && !pages) return PFKV_ERR_INVALID_ARG;
     if (mass && kq != 1) return PFKV_ERR_UNSUPPORTED;
     if ((long long)batch * kq > 0x7fffffffLL / num_q_heads) return PFKV_ERR_UNSUPPORTED;
-    z->off_rflags = 0;
-    z->total = up256(sizeof(uint32_t) * (size_t)batch);
     return PFKV_OK;
+}
+
+int check_words(const pfkv_pages *p) { return max(1, (p->max_pages + kValTile - 1) / kValTile); }
+
+// Where everything lies in the workspace.
+struct Layout {
+    size_t head, pre_bits, pre_vmax, own_bits, pos, members, mstart, seg0, seg, plse, po, packed, own, mass, total;
+    size_t group_bytes;
+    DecodePlan plan;  // of the own tokens
+};
+
+pfkv_status lay_out(const pfkv_cache *c, const pfkv_pages *pages, const pfkv_pages *prefixes, int32_t batch,
+                    int32_t num_q_heads, int32_t kq, int32_t max_seq_len, int32_t max_prefix_len, bool mass, int sms,
+                    Layout *l) {
+    const long long H = c->num_kv_heads, NP = prefixes->batch, rows = (long long)batch * kq * (num_q_heads / H);
+    const int pre_words = NP > 0 ? check_words(prefixes) : 0, own_words = pages ? check_words(pages) : 0;
+    // segments, tiles and rows of partial results, at most
+    const long long S = NP > 0 ? H * (min(NP, (long long)batch) + rows / kPrefixBlock) : 0;
+    const long long tiles = ((long long)max_prefix_len + kPrefixTile - 1) / kPrefixTile;
+    if (S > 0x7fffffffLL || (tiles > 0 && S > 0x7fffffffLL / tiles)) return PFKV_ERR_UNSUPPORTED;
+    const long long partial = NP > 0 ? H * rows + 8 * S + (long long)sms * kPrefixBlock : 0;
+    const long long words = NP * H * pre_words + batch * H * own_words;
+    const long long pack = rows * H * c->head_dim / (8 * kPackPer * kValThreads) + 1;
+    if (partial > 0x7fffffffLL || words + pack + 1 > 0x7fffffffLL) return PFKV_ERR_UNSUPPORTED;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = up256(off + bytes);
+        return at;
+    };
+    l->head = take(sizeof(PrefixHead));
+    l->pre_bits = take(4 * (size_t)(NP * H * pre_words));
+    l->pre_vmax = take(c->dtype == PFKV_KV_FP8_E4M3 ? 4 * (size_t)(NP * H * pre_words) : 0);
+    l->own_bits = take(4 * (size_t)(batch * H * own_words));
+    l->pos = take(4 * (size_t)batch);
+    l->members = take(4 * (size_t)batch);
+    l->mstart = take(4 * (size_t)(NP + 1));
+    l->seg0 = take(4 * (size_t)(NP + 1));
+    l->seg = take(sizeof(PrefixSeg) * (size_t)S);
+    l->plse = take(4 * (size_t)partial);
+    l->po = take(4 * (size_t)partial * c->head_dim);
+    l->packed = take(pages ? 2 * (size_t)(rows * H) * c->head_dim : 0);
+    l->own = l->mass = off;
+    l->group_bytes = 0;
+    if (pages) {
+        const pfkv_status st = make_plan(c, pages, num_q_heads, 0, max_seq_len, sms, &l->plan, mass, kq);
+        if (st != PFKV_OK) return st;
+        if (l->plan.kind != 1 || l->plan.nchunks != 1) return PFKV_ERR_UNSUPPORTED;
+        // a group of launches keeps its results until the merge; the mass pass's arrays are the call's
+        l->group_bytes = l->plan.off_mscore - l->plan.off_prefix;
+        l->own = take(l->group_bytes * (size_t)l->plan.ngroups);
+        l->mass = take(l->plan.total - l->plan.off_mscore);
+    }
+    l->total = off;
+    return PFKV_OK;
+}
+
+// Whether the queries lie as the split kernel reads them.
+bool rows_follow(const pfkv_rows *q, int B, int kq, int Hq, int D) {
+    return (Hq == 1 || q->stride_h == D) && (kq == 1 || q->stride_t == (int64_t)Hq * D) &&
+           (B == 1 || q->stride_b == (int64_t)kq * Hq * D);
 }
 
 PrefixTables prefix_tables(const pfkv_pages *p, int max_len) {
     return PrefixTables{p->block_tables, (long long)p->bt_stride_b, (long long)p->bt_stride_h, p->seq_lens,
                         (long long)p->len_stride_b, (long long)p->len_stride_h, p->expected_tags, p->max_pages, max_len,
-                        p->batch};
+                        p->batch, check_words(p)};
+}
+
+pfkv_status prefix_attn(int tries, const pfkv_cache *cache, const pfkv_pages *pages, const pfkv_pages *prefixes,
+                        int32_t batch, const int32_t *prefix_of, const pfkv_rows *q, int32_t num_q_heads, int32_t kq,
+                        float sm_scale, int32_t max_seq_len, int32_t max_prefix_len, void *workspace,
+                        size_t workspace_bytes, const pfkv_rows *out, float *attn_mass, int64_t mass_stride_b,
+                        int64_t mass_stride_h, uint8_t *flags, void *stream) {
+    const bool mass = attn_mass != nullptr;
+    pfkv_status st = check_prefix(cache, pages, prefixes, batch, num_q_heads, kq, max_seq_len, max_prefix_len, mass);
+    if (st != PFKV_OK) return st;
+    if (!(sm_scale == sm_scale) || std::isinf(sm_scale)) return PFKV_ERR_INVALID_ARG;
+    if (batch == 0) return PFKV_OK;
+    if (!prefix_of) return PFKV_ERR_INVALID_ARG;
+    st = check_rows(q, true, true);
+    if (st == PFKV_OK) st = check_rows(out, true, true);
+    if (st != PFKV_OK) return st;
+    if (mass && (mass_stride_b < 0 || mass_stride_h < 0)) return PFKV_ERR_INVALID_ARG;
+    if (!aligned(prefix_of, 4) || !aligned(attn_mass, 4) || !aligned(flags, 4)) return PFKV_ERR_ALIGNMENT;
+    if (!workspace || workspace_bytes < sizeof(PrefixHead)) return PFKV_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return PFKV_ERR_ALIGNMENT;
+    int sms = 0;
+    st = device_check(&sms);
+    if (st != PFKV_OK) return st;
+    Layout l{};
+    st = lay_out(cache, pages, prefixes, batch, num_q_heads, kq, max_seq_len, max_prefix_len, mass, sms, &l);
+    if (st != PFKV_OK) return st;
+    if (workspace_bytes < l.total) return PFKV_ERR_WORKSPACE;
+
+    const int D = cache->head_dim;
+    const bool fp8 = cache->dtype == PFKV_KV_FP8_E4M3;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    PrefixArgs a{};
+    a.k_pages = cache->k_pages;
+    a.v_pages = cache->v_pages;
+    a.k_scale = cache->k_scale;
+    a.v_scale = cache->v_scale;
+    a.page_tags = cache->page_tags;
+    a.num_pages = cache->num_pages;
+    a.Hkv = cache->num_kv_heads;
+    a.G = num_q_heads / cache->num_kv_heads;
+    a.B = batch;
+    a.kq = kq;
+    if (pages) a.own = prefix_tables(pages, max_seq_len);
+    if (prefixes->batch > 0) a.pre = prefix_tables(prefixes, max_prefix_len);
+    a.prefix_of = prefix_of;
+    a.q = rows_arg(q);
+    a.out = rows_arg(out);
+    a.sm_scale = sm_scale;
+    a.flags = flags;
+    a.own_bits = reinterpret_cast<uint32_t *>(ws + l.own_bits);
+    a.pre_bits = reinterpret_cast<uint32_t *>(ws + l.pre_bits);
+    a.pre_vmax = reinterpret_cast<float *>(ws + l.pre_vmax);
+    a.head = reinterpret_cast<PrefixHead *>(ws + l.head);
+    a.pos = reinterpret_cast<int *>(ws + l.pos);
+    a.members = reinterpret_cast<int *>(ws + l.members);
+    a.mstart = reinterpret_cast<int *>(ws + l.mstart);
+    a.seg0 = reinterpret_cast<int *>(ws + l.seg0);
+    a.seg = reinterpret_cast<PrefixSeg *>(ws + l.seg);
+    a.plse = reinterpret_cast<float *>(ws + l.plse);
+    a.po = reinterpret_cast<float *>(ws + l.po);
+    const bool packs = pages && !rows_follow(q, batch, kq, num_q_heads, D);
+    a.packed_q = packs ? reinterpret_cast<__nv_bfloat16 *>(ws + l.packed) : nullptr;
+    a.ctas = sms;
+    a.tries = tries;
+    a.after_own = pages != nullptr;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (launch_prefix_plan(a, D, fp8, s) != cudaSuccess) return PFKV_ERR_CUDA;
+
+    DecodeArgs d{};
+    PrefixOwnRows own{};
+    if (pages) {
+        const DecodePlan &plan = l.plan;
+        uint8_t *part = ws + l.own - plan.off_prefix;  // of the plan's offsets
+        d.k_pages = cache->k_pages;
+        d.v_pages = cache->v_pages;
+        d.k_scale = cache->k_scale;
+        d.v_scale = cache->v_scale;
+        d.num_pages = cache->num_pages;
+        d.block_tables = pages->block_tables;
+        d.bt_sb = pages->bt_stride_b;
+        d.bt_sh = pages->bt_stride_h;
+        d.seq_lens = pages->seq_lens;
+        d.len_sb = pages->len_stride_b;
+        d.len_sh = pages->len_stride_h;
+        d.max_pages = pages->max_pages;
+        d.max_seq_len = max_seq_len;
+        d.q = packs ? a.packed_q : a.q.p;
+        d.q_scale = sm_scale * 1.4426950408889634f;  // log2(e): scores in log2 units
+        d.hflags = a.own_bits;
+        d.htiles = plan.htiles;
+        d.kq = kq;
+        d.status = reinterpret_cast<uint32_t *>(part + plan.off_status);
+        d.lse = reinterpret_cast<float *>(part + plan.off_lse);
+        d.o = reinterpret_cast<float *>(part + plan.off_o);
+        d.ws_prefix = reinterpret_cast<int *>(part + plan.off_prefix);
+        // the plan kernel checks tables and lengths as the validation kernel does; the split kernel may
+        // read queries before it has ended unless they are packed there
+        d.early = packs ? 0 : 1;
+        if (mass) {
+            uint8_t *m = ws + l.mass - plan.off_mscore;
+            d.mscore = reinterpret_cast<float *>(m + plan.off_mscore);
+            d.mlen = max_seq_len;
+            d.lse_fin = reinterpret_cast<float *>(m + plan.off_lsefin);
+            d.rflags = m + plan.off_rflags;
+            d.mass = attn_mass;
+            d.mass_sb = mass_stride_b;
+            d.mass_sh = mass_stride_h;
+        }
+        own = PrefixOwnRows{d.status, d.lse, d.o, d.ws_prefix, l.group_bytes, plan.greq, plan.workers, d.lse_fin, d.rflags};
+        for (int g = 0; g < plan.ngroups; ++g) {
+            DecodePlan pg = plan;
+            pg.Breq = min(plan.greq, plan.Breq - g * plan.greq);
+            pg.B = pg.Breq * kq;
+            DecodeArgs dg = group_args(d, plan, g * plan.greq);
+            const size_t shift = (size_t)g * l.group_bytes;
+            const auto moved = [&](auto *p) { return reinterpret_cast<decltype(p)>(reinterpret_cast<uint8_t *>(p) + shift); };
+            dg.status = moved(d.status);
+            dg.lse = moved(d.lse);
+            dg.o = moved(d.o);
+            dg.ws_prefix = moved(d.ws_prefix);
+            if (launch_split(dg, pg, s) != cudaSuccess) return PFKV_ERR_CUDA;
+        }
+    }
+    if (prefixes->batch > 0 && launch_prefix_attn(a, D, fp8, s) != cudaSuccess) return PFKV_ERR_CUDA;
+    if (launch_prefix_merge(a, own, D, s) != cudaSuccess) return PFKV_ERR_CUDA;
+    if (mass && launch_mass(d, l.plan, s) != cudaSuccess) return PFKV_ERR_CUDA;
+    return PFKV_OK;
 }
 
 }  // namespace
@@ -254,11 +659,17 @@ pfkv_status pfkv_prefix_decode_workspace_size(const pfkv_cache *cache, const pfk
                                               int32_t num_query_tokens, int32_t max_seq_len, int32_t max_prefix_len,
                                               int32_t with_mass, size_t *bytes) {
     if (!bytes) return PFKV_ERR_INVALID_ARG;
-    PrefixSizes z{};
-    const pfkv_status st = prefix_sizes(cache, pages, prefixes, batch, num_q_heads, num_query_tokens, max_seq_len,
-                                        max_prefix_len, with_mass != 0, &z);
+    pfkv_status st = check_prefix(cache, pages, prefixes, batch, num_q_heads, num_query_tokens, max_seq_len,
+                                  max_prefix_len, with_mass != 0);
     if (st != PFKV_OK) return st;
-    *bytes = z.total;
+    int sms = 0;
+    st = device_check(&sms);
+    if (st != PFKV_OK) return st;
+    Layout l{};
+    st = lay_out(cache, pages, prefixes, batch, num_q_heads, num_query_tokens, max_seq_len, max_prefix_len,
+                 with_mass != 0, sms, &l);
+    if (st != PFKV_OK) return st;
+    *bytes = l.total;
     return PFKV_OK;
 }
 
@@ -268,50 +679,21 @@ pfkv_status pfkv_prefix_decode_attn(const pfkv_cache *cache, const pfkv_pages *p
                                     int32_t max_prefix_len, void *workspace, size_t workspace_bytes,
                                     const pfkv_rows *out, float *attn_mass, int64_t mass_stride_b,
                                     int64_t mass_stride_h, uint8_t *flags, void *stream) {
-    PrefixSizes z{};
-    pfkv_status st = prefix_sizes(cache, pages, prefixes, batch, num_q_heads, num_query_tokens, max_seq_len,
-                                  max_prefix_len, attn_mass != nullptr, &z);
-    if (st != PFKV_OK) return st;
-    if (!(sm_scale == sm_scale) || std::isinf(sm_scale)) return PFKV_ERR_INVALID_ARG;
-    if (batch == 0) return PFKV_OK;
-    if (!prefix_of) return PFKV_ERR_INVALID_ARG;
-    st = check_rows(q, true, true);
-    if (st == PFKV_OK) st = check_rows(out, true, true);
-    if (st != PFKV_OK) return st;
-    if (attn_mass && (mass_stride_b < 0 || mass_stride_h < 0)) return PFKV_ERR_INVALID_ARG;
-    if (!aligned(prefix_of, 4) || !aligned(attn_mass, 4) || !aligned(flags, 4)) return PFKV_ERR_ALIGNMENT;
-    if (!workspace || workspace_bytes < z.total) return PFKV_ERR_WORKSPACE;
-    if (!aligned(workspace, 256)) return PFKV_ERR_ALIGNMENT;
-    int sms = 0;
-    st = device_check(&sms);
-    if (st != PFKV_OK) return st;
+    return prefix_attn(kTries, cache, pages, prefixes, batch, prefix_of, q, num_q_heads, num_query_tokens, sm_scale,
+                       max_seq_len, max_prefix_len, workspace, workspace_bytes, out, attn_mass, mass_stride_b,
+                       mass_stride_h, flags, stream);
+}
 
-    PrefixArgs a{};
-    a.k_pages = cache->k_pages;
-    a.v_pages = cache->v_pages;
-    a.k_scale = cache->k_scale;
-    a.v_scale = cache->v_scale;
-    a.page_tags = cache->page_tags;
-    a.num_pages = cache->num_pages;
-    a.Hkv = cache->num_kv_heads;
-    a.G = num_q_heads / cache->num_kv_heads;
-    a.B = batch;
-    a.kq = num_query_tokens;
-    if (pages) a.own = prefix_tables(pages, max_seq_len);
-    a.pre = prefix_tables(prefixes, max_prefix_len);
-    a.prefix_of = prefix_of;
-    a.q = rows_arg(q);
-    a.out = rows_arg(out);
-    a.q_scale = sm_scale * 1.4426950408889634f;  // log2(e): scores in log2 units
-    a.mass = attn_mass;
-    a.mass_sb = mass_stride_b;
-    a.mass_sh = mass_stride_h;
-    a.flags = flags;
-    a.rflags = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(workspace) + z.off_rflags);
-    return launch_prefix(a, cache->head_dim, cache->dtype == PFKV_KV_FP8_E4M3, sms, static_cast<cudaStream_t>(stream)) ==
-                   cudaSuccess
-               ? PFKV_OK
-               : PFKV_ERR_CUDA;
+pfkv_status pfkv_selftest_prefix_decode(int32_t tries, const pfkv_cache *cache, const pfkv_pages *pages,
+                                        const pfkv_pages *prefixes, int32_t batch, const int32_t *prefix_of,
+                                        const pfkv_rows *q, int32_t num_q_heads, int32_t num_query_tokens,
+                                        float sm_scale, int32_t max_seq_len, int32_t max_prefix_len, void *workspace,
+                                        size_t workspace_bytes, const pfkv_rows *out, float *attn_mass,
+                                        int64_t mass_stride_b, int64_t mass_stride_h, uint8_t *flags, void *stream) {
+    if (tries < 0 || tries > kTries) return PFKV_ERR_INVALID_ARG;
+    return prefix_attn(tries, cache, pages, prefixes, batch, prefix_of, q, num_q_heads, num_query_tokens, sm_scale,
+                       max_seq_len, max_prefix_len, workspace, workspace_bytes, out, attn_mass, mass_stride_b,
+                       mass_stride_h, flags, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,785 @@
+// prefix_attn.cu -- attention of all query rows of a prefix's requests over the prefix, by
+// the fifth-generation tensor cores (the middle part of pfkv_prefix_decode_attn).
+//
+// Mathematics.  For a prefix and kv head, with the rows of its requests (request, query token,
+// head of the group) as one matrix Q of R rows: S = Q K^T, P = softmax weights, O = P V.  A token
+// costs 4 R D operations and 2 D bytes an element of the pool: with 128 rows a BF16 pool is still
+// bound by memory (128 operations a byte, the machine has 282), with 256 rows both bind.
+//
+// A CTA takes a range of tiles of 128 tokens (see PrefixSeg) and leaves a partial result (rows
+// normalised, with their log2-sum-exp) for every segment that it touches.  Two groups of four
+// softmax warps work in turns, so that one's softmax runs under the other's products: on the two
+// halves of a block of more than 128 rows, both on every tile; or, with up to 128 rows, on every
+// second tile of the same rows, and their results are merged at the end.  Tensor memory holds S of
+// both (a group's weights overwrite its scores and are read from there as the A operand) and O of
+// both.
+//
+// BF16 pools: K and V come by TMA as the operands that they are; weights are bf16.
+// FP8 pools: K comes as it is too, and Q enters as a pair of e4m3 values (hi + lo, two products of
+// half the cost of one in 16 bits); two warps convert V to f16 (exact), and weights times their
+// unit's V scale are f16.  K's scales are applied to the scores, 16 columns at a time.
+//
+// Roles of the twelve warps: 0-3 and 4-7 softmax; 8 issues the products; 9 finds the segments, and
+// loads page ids, scales, K and V; 10 and 11 convert V (FP8).
+#include "prefix_internal.cuh"
+#include "umma.cuh"
+
+namespace pfkv {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kPages = kPrefixTile / kPage;  // pages of a tile
+constexpr int kInfo = 4;                     // tiles' scales kept ahead, a softmax group
+constexpr int kItems = 3;                    // segments found ahead
+constexpr uint32_t kColO = 256;
+constexpr float kGrowth = 8.f;
+constexpr float kMinusInf = -INFINITY;
+
+template <int D, bool FP8>
+struct Cfg {
+    static constexpr int ROWB = D * (FP8 ? 1 : 2);            // a token's row in the pool
+    static constexpr uint32_t KB = kPrefixTile * ROWB;        // a tile of K (and of V as loaded)
+    static constexpr uint32_t VB = kPrefixTile * D * 2;       // of V as the operand
+    static constexpr uint32_t HALF = kPrefixTile * 128;       // 64 16-bit columns of it
+    static constexpr uint32_t QB = 128 * D * 2;               // 128 query rows (FP8: hi, then lo)
+    static constexpr int NK = FP8 ? (D == 128 ? 4 : 6) : (D == 128 ? 3 : 4);
+    static constexpr int NV = FP8 ? (D == 128 ? 2 : 3) : (D == 128 ? 2 : 4);
+    static constexpr int NR = FP8 ? (D == 128 ? 2 : 4) : 0;   // V as loaded
+    static constexpr uint32_t OFF_K = 2 * QB, OFF_V = OFF_K + NK * KB, OFF_R = OFF_V + NV * VB;
+    static constexpr uint32_t OFF_MISC = OFF_R + NR * KB;
+    static constexpr int CPP = FP8 || D == 64 ? 1 : 2;        // copies a page (128 bytes of a row at most)
+    static constexpr uint32_t COPYB = kPage * ROWB / CPP;
+};
+
+struct Item {
+    int p, h;            // p < 0: no more
+    int row0, rows;      // query rows of the segment
+    int t0, nt;          // tiles of this CTA
+    int len;             // tokens of the prefix
+    int base;            // first row of the partial result
+    float vinv, vback;   // weights' factor beside the V scale, and what undoes it
+};
+
+// Scales of a tile's pages.
+struct Info {
+    float ks[kPages], vs[kPages];
+};
+
+struct Misc {
+    uint64_t kfull[6], kempty[6], vfull[4], vempty[4], rfull[4], rempty[4];
+    uint64_t qfull, sfull[2], pready[2][2], odone[2], merge, rest;
+    uint64_t tfull[2][kInfo], tempty[2][kInfo];
+    uint64_t ifull[kItems], iempty[kItems], drain;
+    Item item[kItems];
+    Info info[2][kInfo];
+    float ref1[128], sum1[128];
+    uint32_t tmem, gave_up;
+};
+template <int D, bool FP8>
+constexpr size_t smem_bytes() {
+    return Cfg<D, FP8>::OFF_MISC + sizeof(Misc);
+}
+static_assert(smem_bytes<128, true>() <= 232448 && smem_bytes<128, false>() <= 232448, "shared memory of one CTA");
+
+// D (+)= A B of 8-bit operands (both e4m3); `up` is the descriptors' upper word.
+template <uint32_t UP>
+__device__ __forceinline__ void umma_ss_f8(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\t"
+                 "mov.b64 b, {%2, %5};\n\ttcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "n"(UP)
+                 : "memory");
+}
+// Rows of 64 bytes with the 64-byte swizzle: 16-byte chunk c of row r at chunk c ^ (r / 2 & 3),
+// eight rows a 512-byte atom.
+constexpr uint32_t kDescUpper64 = (512u >> 4) | (1u << 14) | (4u << 29);
+
+__device__ __forceinline__ uint32_t pack16(float a, float b, bool bf16) {
+    if (bf16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Four e4m3 codes -> two f16 pairs.
+__device__ __forceinline__ uint2 e4m3x4_to_half4(uint32_t w) {
+    uint2 r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(r.x), "=r"(r.y)
+        : "r"(w));
+    return r;
+}
+
+// Selftest: waits of as many tries as the call says.
+template <int D, bool FP8, bool Selftest>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefix_attn_kernel(const __grid_constant__ CUtensorMap mapk, const __grid_constant__ CUtensorMap mapv, PrefixArgs a,
+                       uint32_t idS) {
+    using C = Cfg<D, FP8>;
+    extern __shared__ __align__(1024) uint8_t psm[];  // no static shared memory: the window's aligned base
+    Misc &m = *reinterpret_cast<Misc *>(psm + C::OFF_MISC);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < C::NK; ++i) {
+            mbar_init(&m.kfull[i], 1);
+            mbar_init(&m.kempty[i], 1);
+        }
+        for (int i = 0; i < C::NV; ++i) {
+            mbar_init(&m.vfull[i], FP8 ? 2 : 1);
+            mbar_init(&m.vempty[i], 1);
+        }
+        for (int i = 0; i < C::NR; ++i) {
+            mbar_init(&m.rfull[i], 1);
+            mbar_init(&m.rempty[i], 2);
+        }
+        mbar_init(&m.qfull, 8);
+        mbar_init(&m.merge, 4);
+        mbar_init(&m.rest, 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&m.sfull[i], 1);
+            mbar_init(&m.pready[i][0], 4);
+            mbar_init(&m.pready[i][1], 4);
+            mbar_init(&m.odone[i], 1);
+            for (int j = 0; j < kInfo; ++j) {
+                mbar_init(&m.tfull[i][j], 1);
+                mbar_init(&m.tempty[i][j], 4);
+            }
+        }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&m.ifull[i], 1);
+            mbar_init(&m.iempty[i], 9 + (FP8 ? 2 : 0));  // softmax warps, the issuing thread, the converting warps
+        }
+        mbar_init(&m.drain, 1);
+        m.gave_up = (smem_addr(psm) & 1023u) != 0u;  // nothing runs on a base that the swizzle cannot take
+        fence_mbar_init();
+    }
+    if (warp == 8) tmem_alloc512<1>(&m.tmem);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    // After the own tokens' split kernel, which started once the plan was complete and which this
+    // kernel does not read, only the end waits; the merge that follows needs both.
+    if (a.after_own) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    else pdl_enter();
+    const uint32_t tmem = m.tmem;
+    volatile uint32_t *const gave_up = &m.gave_up;
+    const int tries = Selftest ? a.tries : kTries, item_tries = Selftest ? a.tries * (kItemTries / kTries) : kItemTries;
+    auto item_ready = [&](int i) {
+        return bar_wait(&m.ifull[i % kItems], (i / kItems) & 1, gave_up, item_tries) && m.item[i % kItems].p >= 0;
+    };
+    // Steps of softmax group `g`: every tile, or every second one.
+    auto steps_of = [](const Item &it, int g) { return it.rows > 128 ? it.nt : (it.nt + 1 - g) / 2; };
+
+    if (warp < 8) {
+        // ----------------------- queries, softmax and results -----------------------
+        reg_share_more<208>();
+        const int grp = warp >> 2, r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t cs = lanes + grp * 128, co = lanes + kColO + grp * 128;
+        const float a2 = fmaxf(fabsf(a.sm_scale) * 1.4426950408889634f, 1.1754944e-38f);
+        uint32_t done = 0, outs = 0, merges = 0, base_pos = 0;
+        for (int i = 0; __all_sync(0xffffffffu, item_ready(i)); ++i) {
+            const Item &it = m.item[i % kItems];
+            const bool wide = it.rows > 128;
+            const int steps = steps_of(it, grp), nt = it.nt;
+            const int row = wide ? grp * 128 + r : r;
+            const bool live = row < it.rows;
+            const bool warp_live = (row & ~31) < it.rows;
+            bool ok = true;
+            // this row's query
+            float mul = a2;
+            if (live) {
+                const int R = it.row0 + row, per = a.kq * a.G, member = R / per, tg = R - member * per;
+                const int t = tg / a.G, g = tg - t * a.G;
+                const int b = a.members[a.mstart[it.p] + member];
+                const uint4 *src = reinterpret_cast<const uint4 *>(a.q.p + (long long)b * a.q.sb + (long long)t * a.q.st +
+                                                                   (long long)(it.h * a.G + g) * a.q.sh);
+                uint8_t *dst = psm + (wide ? grp : 0) * C::QB;
+                if constexpr (!FP8) {
+                    constexpr int N = D / 8;  // 16-byte chunks
+#pragma unroll
+                    for (int c = 0; c < N; ++c) {
+                        if (!wide && (c >= N / 2) != (grp == 1)) continue;
+                        *reinterpret_cast<uint4 *>(dst + (c >> 3) * C::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = src[c];
+                    }
+                } else {
+                    uint4 w[D / 8];
+                    uint32_t top = 0u;
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) {
+                        w[c] = src[c];
+                        const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) top = max(top, max((u[k] << 16) & 0x7fff0000u, u[k] & 0x7fff0000u));
+                    }
+                    // the largest element between 128 and 256: hi is within 2^-4 of an element, and their
+                    // difference, four bits, is exact in lo down to 2^-9; what is not finite spoils the row
+                    const int e = min(126, max(-119, (int)(top >> 23) - 127));
+                    float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+                    if (a.sm_scale < 0.f) up = -up;
+                    mul = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : a2 * __uint_as_float((uint32_t)(127 + e - 7) << 23);
+                    const int first = wide ? 0 : grp, last = wide ? 1 : grp;
+#pragma unroll 1
+                    for (int part = first; part <= last; ++part) {
+                        uint8_t *to = dst + part * (C::QB / 2);
+#pragma unroll
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t o[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint4 &ww = w[2 * c + (k >> 1)];
+                                const uint32_t x0 = (k & 1) ? ww.z : ww.x, x1 = (k & 1) ? ww.w : ww.y;
+                                const float2 f0 = bf16x2_to_float2(x0), f1 = bf16x2_to_float2(x1);
+                                const float2 y0 = make_float2(f0.x * up, f0.y * up), y1 = make_float2(f1.x * up, f1.y * up);
+                                uint32_t h0 = __nv_cvt_float2_to_fp8x2(y0, __NV_SATFINITE, __NV_E4M3);
+                                uint32_t h1 = __nv_cvt_float2_to_fp8x2(y1, __NV_SATFINITE, __NV_E4M3);
+                                if (part) {
+                                    const float2 z0 = e4m3x2_to_float2((uint16_t)h0), z1 = e4m3x2_to_float2((uint16_t)h1);
+                                    h0 = __nv_cvt_float2_to_fp8x2(make_float2(y0.x - z0.x, y0.y - z0.y), __NV_SATFINITE, __NV_E4M3);
+                                    h1 = __nv_cvt_float2_to_fp8x2(make_float2(y1.x - z1.x, y1.y - z1.y), __NV_SATFINITE, __NV_E4M3);
+                                }
+                                o[k] = h0 | (h1 << 16);
+                            }
+                            const int at = D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+                            *reinterpret_cast<uint4 *>(to + at) = make_uint4(o[0], o[1], o[2], o[3]);
+                        }
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&m.qfull);
+
+            float ref = kMinusInf, sum = 0.f;
+            for (int j = 0; j < steps; ++j, ++done) {
+                ok = bar_wait(&m.sfull[grp], done & 1, gave_up, tries);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tmem_fence_after();
+                const int tile = wide ? j : 2 * j + grp;
+                const int seen = it.len - (it.t0 + tile) * kPrefixTile;
+                const Info &inf = m.info[grp][done % kInfo];
+                if constexpr (FP8) {
+                    ok = bar_wait(&m.tfull[grp][done % kInfo], (done / kInfo) & 1, gave_up, tries);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                }
+                if (!FP8 && seen < kPrefixTile && (!wide || grp == 0)) {
+                    // tokens past the last may hold anything, NaN among it, and meet weights of zero: V's
+                    // are zeroed where they lie, by the group whose products use the tile first
+                    const uint32_t pos = base_pos + tile;
+                    ok = bar_wait(&m.vfull[pos % C::NV], (pos / C::NV) & 1, gave_up, tries);
+                    uint4 *v = reinterpret_cast<uint4 *>(psm + C::OFF_V + (pos % C::NV) * C::VB);
+#pragma unroll 1
+                    for (int e = seen * 8 + r; e < kPrefixTile * 8; e += 128) {
+                        v[e] = make_uint4(0u, 0u, 0u, 0u);
+                        if (D == 128) v[e + C::HALF / 16] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                }
+                if (warp_live) {
+                    float x[4][32];
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) tmem_ld32(cs + g * 32, x[g]);
+                    tmem_wait_ld();
+                    float f[kPages];  // factors of 16 columns each
+                    if constexpr (FP8) {
+#pragma unroll
+                        for (int p = 0; p < kPages; ++p) {
+                            const float k = inf.ks[p];
+                            if (k < 0.f) {  // the scores' sign
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) x[p >> 1][(p & 1) * 16 + e] = -x[p >> 1][(p & 1) * 16 + e];
+                            }
+                            f[p] = fabsf(k) * mul;
+                            if (f[p] < 1.1754944e-38f) f[p] = 1.1754944e-38f;  // hidden scores stay -inf; NaN stays
+                        }
+                    }
+                    if (seen < kPrefixTile) {
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (g * 32 + e >= seen) x[g][e] = kMinusInf;
+                        if constexpr (FP8) {  // what follows the last page has no scale
+#pragma unroll
+                            for (int p = 0; p < kPages; ++p)
+                                if (p * kPage >= seen) f[p] = mul;
+                        }
+                    }
+                    float tops[8];
+#pragma unroll
+                    for (int p = 0; p < 8; ++p) tops[p] = fmaxf(x[p >> 1][(p & 1) * 16], x[p >> 1][(p & 1) * 16 + 1]);
+#pragma unroll
+                    for (int e = 2; e < 16; e += 2)
+#pragma unroll
+                        for (int p = 0; p < 8; ++p)
+                            tops[p] = fmaxf(tops[p], fmaxf(x[p >> 1][(p & 1) * 16 + e], x[p >> 1][(p & 1) * 16 + e + 1]));
+                    if constexpr (FP8) {
+#pragma unroll
+                        for (int p = 0; p < 8; ++p) tops[p] *= f[p];
+                    }
+                    float top = fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])),
+                                      fmaxf(fmaxf(tops[4], tops[5]), fmaxf(tops[6], tops[7])));
+                    if constexpr (!FP8) top *= a2;
+                    float shrink = 1.f;
+                    if (top > ref + kGrowth || (ref == kMinusInf && top > kMinusInf)) {
+                        shrink = fast_exp2(ref - top);  // 0 when nothing was seen yet
+                        sum *= shrink;
+                        ref = top;
+                    }
+                    // the scores are here, so the products before them (O among them) are done
+                    if (j > 0 && __any_sync(0xffffffffu, shrink != 1.f)) {
+#pragma unroll 1
+                        for (int g = 0; g < D / 16; ++g) {
+                            float o[16];
+                            tmem_ld16(co + g * 16, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] *= shrink;
+                            tmem_st16(co + g * 16, o);
+                        }
+                    }
+                    const float base = ref == kMinusInf ? 0.f : -ref;
+                    const float2 base2 = make_float2(base, base);
+                    float2 sums[4] = {};
+                    // the weights of 64 tokens at a time: the products with the first half's V start
+                    // while the second half is computed
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                        for (int g = 2 * half; g < 2 * half + 2; ++g) {
+                            float w[16];  // packed pairs
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) {
+                                const int p = 2 * g + (e >> 4);
+                                const float fp = FP8 ? f[p] : a2;
+                                float2 y = fma2(make_float2(x[g][e], x[g][e + 1]), make_float2(fp, fp), base2);
+                                y = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                                sums[(e >> 1) & 3] = add2(sums[(e >> 1) & 3], y);
+                                if constexpr (FP8) {
+                                    const float z = p * kPage < seen ? inf.vs[p] * it.vinv : 0.f;
+                                    y = mul2(y, make_float2(z, z));
+                                }
+                                w[e >> 1] = __uint_as_float(pack16(y.x, y.y, !FP8));
+                            }
+                            tmem_st16(cs + g * 16, w);
+                        }
+                        tmem_wait_st();
+                        tmem_fence_before();
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(&m.pready[grp][half]);
+                    }
+                    const float2 s2 = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
+                    sum += s2.x + s2.y;
+                } else {
+                    __syncwarp();
+                    if (lane == 0) {
+                        bar_arrive(&m.pready[grp][0]);
+                        bar_arrive(&m.pready[grp][1]);
+                    }
+                }
+                if constexpr (FP8) {
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&m.tempty[grp][done % kInfo]);
+                }
+            }
+            if (steps > 0) {
+                ok = bar_wait(&m.odone[grp], outs++ & 1, gave_up, tries) && ok;
+                tmem_fence_after();
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            const bool both = !wide && nt > 1;  // two parts to merge
+            float4 *part = reinterpret_cast<float4 *>(psm);  // the queries' place: [D / 4][128] of group 1's O
+            if (both && grp == 1 && warp_live && ok) {
+#pragma unroll 1
+                for (int g = 0; g < D / 16; ++g) {
+                    float o[16];
+                    tmem_ld16(co + g * 16, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        part[(g * 4 + k) * 128 + r] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                }
+                m.ref1[r] = ref;
+                m.sum1[r] = sum;
+            }
+            if (both) {
+                if (grp == 1) {
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&m.merge);
+                } else {
+                    ok = bar_wait(&m.merge, merges & 1, gave_up, tries) && ok;
+                    ok = __all_sync(0xffffffffu, ok);
+                }
+                ++merges;
+            }
+            if ((wide || grp == 0) && warp_live && ok) {
+                float f0 = 1.f, f1 = 0.f;
+                if (both) {
+                    const float ref1 = m.ref1[r], sum1 = m.sum1[r];
+                    const float top = fmaxf(ref, ref1);
+                    f0 = ref == top ? 1.f : fast_exp2(ref - top);
+                    f1 = ref1 == top ? 1.f : fast_exp2(ref1 - top);
+                    sum = sum * f0 + sum1 * f1;
+                    ref = top;
+                }
+                const float inv = sum == 0.f ? 0.f : (FP8 ? it.vback : 1.f) / sum;
+                const int n8 = rows8(it.rows);
+                float4 *dst = reinterpret_cast<float4 *>(a.po + (long long)it.base * D) + row;
+                if (live) a.plse[it.base + row] = sum == 0.f ? kMinusInf : ref + log2f(sum);
+#pragma unroll 1
+                for (int g = 0; g < D / 16; ++g) {
+                    float o[16];
+                    __syncwarp();
+                    tmem_ld16(co + g * 16, o);
+                    tmem_wait_ld();
+                    if (!live) continue;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float4 y = make_float4(o[4 * k] * f0, o[4 * k + 1] * f0, o[4 * k + 2] * f0, o[4 * k + 3] * f0);
+                        if (both) {
+                            const float4 z = part[(g * 4 + k) * 128 + r];
+                            y = make_float4(fmaf(z.x, f1, y.x), fmaf(z.y, f1, y.y), fmaf(z.z, f1, y.z), fmaf(z.w, f1, y.w));
+                        }
+                        dst[(long long)(g * 4 + k) * n8] = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+                    }
+                }
+            }
+            base_pos += nt;
+            tmem_fence_before();
+            __syncwarp();
+            // Both groups are done with the queries' place and with O.
+            if (lane == 0) bar_arrive(&m.rest);
+            ok = bar_wait(&m.rest, i & 1, gave_up, tries) && ok;
+            if (lane == 0) bar_arrive(&m.iempty[i % kItems]);
+            if (!__all_sync(0xffffffffu, ok)) break;
+        }
+    } else if (warp == 8) {
+        // ------------------------------ products ------------------------------
+        reg_share_less<88>();
+        if (elect_one()) {
+            constexpr uint32_t idO = umma_idesc(128, D, !FP8, false, true);
+            const uint32_t qa = smem_addr(psm), ka = qa + C::OFF_K, va = qa + C::OFF_V;
+            uint32_t weighed[2] = {0, 0}, pos = 0;
+            bool ok = true;
+            for (int i = 0; ok && item_ready(i); ++i) {
+                const bool wide = m.item[i % kItems].rows > 128;
+                const int nt = m.item[i % kItems].nt;
+                const int n[2] = {steps_of(m.item[i % kItems], 0), steps_of(m.item[i % kItems], 1)};
+                bar_arrive(&m.iempty[i % kItems]);
+                ok = bar_wait(&m.qfull, i & 1, gave_up, item_tries);
+                // Step j of a group: O of its step j - 1, then S of step j.
+                auto step = [&](int T, int j) {
+                    const uint32_t cs = tmem + T * 128, co = tmem + kColO + T * 128;
+                    if (j > 0 && j <= n[T]) {
+                        const uint32_t at = pos + (wide ? j - 1 : 2 * (j - 1) + T), slot = at % C::NV, parity = weighed[T]++ & 1;
+                        if (!bar_wait(&m.vfull[slot], (at / C::NV) & 1, gave_up, tries)) return false;
+                        if (!bar_wait(&m.pready[T][0], parity, gave_up, tries)) return false;
+                        tmem_fence_after();
+                        const uint32_t db = umma_desc(va + slot * C::VB, C::HALF);
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) umma_ts(co, cs + s * 8, db + s * 128, idO, j > 1 || s > 0);
+                        if (!bar_wait(&m.pready[T][1], parity, gave_up, tries)) return false;
+                        tmem_fence_after();
+#pragma unroll
+                        for (int s = 4; s < 8; ++s) umma_ts(co, cs + s * 8, db + s * 128, idO, true);
+                        if (!wide || T == 1) umma_commit(&m.vempty[slot]);
+                        if (j == n[T]) umma_commit(&m.odone[T]);
+                    }
+                    if (j >= n[T]) return true;
+                    const uint32_t at = pos + (wide ? j : 2 * j + T), slot = at % C::NK;
+                    if (!bar_wait(&m.kfull[slot], (at / C::NK) & 1, gave_up, tries)) return false;
+                    tmem_fence_after();
+                    const uint32_t qt = qa + (wide ? T : 0) * C::QB;
+                    if constexpr (!FP8) {
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c) {
+                            const uint32_t da = umma_desc(qt + c * C::HALF, 16), db = umma_desc(ka + slot * C::KB + c * C::HALF, 16);
+#pragma unroll
+                            for (int s = 0; s < 4; ++s) umma_ss<1>(cs, da + 2 * s, db + 2 * s, idS, c > 0 || s > 0);
+                        }
+                    } else {
+                        constexpr uint32_t UP = D == 128 ? kDescUpper : kDescUpper64;
+                        const uint32_t db = umma_desc(ka + slot * C::KB, 16);
+#pragma unroll
+                        for (int part = 0; part < 2; ++part) {
+                            const uint32_t da = umma_desc(qt + part * (C::QB / 2), 16);
+#pragma unroll
+                            for (int s = 0; s < D / 32; ++s) umma_ss_f8<UP>(cs, da + 2 * s, db + 2 * s, idS, part > 0 || s > 0);
+                        }
+                    }
+                    if (!wide || T == 1) umma_commit(&m.kempty[slot]);
+                    umma_commit(&m.sfull[T]);
+                    return true;
+                };
+                const int most = max(n[0], n[1]);
+#pragma unroll 1
+                for (int j = 0; j <= most && ok; ++j) ok = step(0, j) && step(1, j);
+                pos += nt;
+            }
+            // nothing in flight when the CTA leaves
+            umma_commit(&m.drain);
+            bar_drain(&m.drain, 0);
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // ---------------------- segments, page ids, K and V ----------------------
+        reg_share_less<88>();
+        const uint64_t pol = l2_policy_evict_normal();
+        const int U = a.head->U, W = a.head->W;
+        const int c = blockIdx.x;
+        int x = c < W ? (int)(((long long)c * U + W - 1) / W) : 0;
+        const int x1 = c < W ? (int)(((long long)(c + 1) * U + W - 1) / W) : 0;
+        uint32_t pos = 0, info[2] = {0, 0};
+        int i = 0;
+        bool ok = true;
+        auto put = [&](const Item &it) {
+            ok = bar_wait(&m.iempty[i % kItems], ((i / kItems) & 1) ^ 1, gave_up, item_tries);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) return;
+            if (lane == 0) {
+                m.item[i % kItems] = it;
+                bar_arrive(&m.ifull[i % kItems]);
+            }
+            ++i;
+        };
+        // the last segment whose first tile is at most x, 32 candidates a step
+        int k = 0;
+        if (x < x1) {
+            int lo = 0, hi = a.seg0[a.pre.count];  // seg[lo].tile0 <= x; seg[hi] is past it
+            while (hi - lo > 1) {
+                const int width = (hi - lo + 31) / 32, at = lo + lane * width;
+                const bool below = at < hi && a.seg[at].tile0 <= x;
+                const int n = __popc(__ballot_sync(0xffffffffu, below));  // of ascending numbers: the first n
+                lo += (n - 1) * width;
+                hi = min(hi, lo + width);
+            }
+            k = lo;
+        }
+        while (ok && x < x1) {
+            const PrefixSeg sg = a.seg[k];
+            const int end = min(x1, sg.tile0 + sg.ntiles);
+            if (end <= x) {  // an empty segment
+                ++k;
+                continue;
+            }
+            // a prefix that failed a check is not read: its requests are flagged
+            const long long words = (long long)sg.p * a.Hkv * a.pre.htiles;
+            uint32_t bits = 0u;
+            for (int w = lane; w < a.Hkv * a.pre.htiles; w += 32) bits |= a.pre_bits[words + w];
+            if (__any_sync(0xffffffffu, bits != 0u)) {
+                x = end;
+                ++k;
+                continue;
+            }
+            Item it{};
+            it.p = sg.p;
+            it.h = sg.h;
+            it.row0 = sg.row0;
+            it.rows = sg.rows;
+            it.t0 = x - sg.tile0;
+            it.nt = end - x;
+            it.len = sg.len;
+            it.base = sg.base + (c - (int)((long long)sg.tile0 * W / U)) * rows8(sg.rows);
+            if constexpr (FP8) {
+                float top = 0.f;
+                for (int w = lane; w < a.pre.htiles; w += 32) top = fmaxf(top, a.pre_vmax[words + (long long)sg.h * a.pre.htiles + w]);
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                // scales over a power of two above the largest, and 2^7: f16's subnormals begin 2^-31 below
+                const int e = min(120, max(-112, (int)(__float_as_uint(top) >> 23) - 126));
+                it.vinv = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+                it.vback = __uint_as_float((uint32_t)(127 + e - 7) << 23);
+            }
+            put(it);
+            const bool wide = it.rows > 128;
+            const long long row = (long long)it.p * a.pre.bt_sb + (long long)it.h * a.pre.bt_sh;
+            const int npages = (it.len + kPage - 1) / kPage;
+            // 32 pages (four tiles) a round, one a lane; the next round's ids are on their way
+            int next_id = -1;
+            auto fetch = [&](int t) {
+                const int page = (it.t0 + t) * kPages + lane;
+                next_id = page < npages && t + (lane >> 3) < it.nt ? a.pre.block_tables[row + page] : -1;
+            };
+            fetch(0);
+            for (int t = 0; ok && t < it.nt; t += 4) {
+                const int id = next_id;
+                const bool there = id >= 0 && id < a.num_pages;
+                const int unit = there ? id * a.Hkv + it.h : -1;
+                float ks = 1.f, vs = 0.f;
+                if (FP8 && there) {
+                    ks = a.k_scale[unit];
+                    vs = a.v_scale[unit];
+                }
+                if (t + 4 < it.nt) fetch(t + 4);
+                for (int q = 0; ok && q < 4 && t + q < it.nt; ++q, ++pos) {
+                    const int copy = lane / kPages;  // of a page
+                    const int u = __shfl_sync(0xffffffffu, unit, q * kPages + lane % kPages);
+                    const bool mine = copy < C::CPP && u >= 0;
+                    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * C::COPYB;
+                    const int off = copy * C::HALF + lane % kPages * C::COPYB;
+                    const uint32_t kslot = pos % C::NK;
+                    ok = __all_sync(0xffffffffu, bar_wait(&m.kempty[kslot], ((pos / C::NK) & 1) ^ 1, gave_up, tries));
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&m.kfull[kslot], bytes);
+                    __syncwarp();
+                    if (mine) tma_box3(psm + C::OFF_K + kslot * C::KB + off, &mapk, copy * 64, 0, u, &m.kfull[kslot], pol);
+                    if constexpr (FP8) {
+#pragma unroll 1
+                        for (int g = 0; g < 2; ++g) {
+                            if (!wide && ((t + q) & 1) != g) continue;
+                            const uint32_t slot = info[g] % kInfo;
+                            ok = ok && bar_wait(&m.tempty[g][slot], ((info[g] / kInfo) & 1) ^ 1, gave_up, tries);
+                            ok = __all_sync(0xffffffffu, ok);
+                            if (!ok) break;
+                            if (lane / kPages == q) {
+                                m.info[g][slot].ks[lane % kPages] = ks;
+                                m.info[g][slot].vs[lane % kPages] = vs;
+                            }
+                            __syncwarp();
+                            if (lane == 0) bar_arrive(&m.tfull[g][slot]);
+                            ++info[g];
+                        }
+                        if (!ok) break;
+                        const uint32_t slot = pos % (C::NR > 0 ? C::NR : 1);
+                        ok = __all_sync(0xffffffffu, bar_wait(&m.rempty[slot], ((pos / (C::NR > 0 ? C::NR : 1)) & 1) ^ 1, gave_up, tries));
+                        if (!ok) break;
+                        if (lane == 0) mbar_arrive_expect_tx(&m.rfull[slot], bytes);
+                        __syncwarp();
+                        if (mine) tma_box3(psm + C::OFF_R + slot * C::KB + off, &mapv, 0, 0, u, &m.rfull[slot], pol);
+                    } else {
+                        const uint32_t slot = pos % C::NV;
+                        ok = __all_sync(0xffffffffu, bar_wait(&m.vempty[slot], ((pos / C::NV) & 1) ^ 1, gave_up, tries));
+                        if (!ok) break;
+                        if (lane == 0) mbar_arrive_expect_tx(&m.vfull[slot], bytes);
+                        __syncwarp();
+                        if (mine) tma_box3(psm + C::OFF_V + slot * C::VB + off, &mapv, copy * 64, 0, u, &m.vfull[slot], pol);
+                    }
+                }
+            }
+            x = end;
+            ++k;
+        }
+        if (ok) {
+            Item it{};
+            it.p = -1;
+            put(it);
+        }
+        if (*gave_up) {  // copies in flight are left time to land
+            const unsigned long long t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < kWaitLimitNs) {}
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------ V to f16 ------------------------------
+        reg_share_less<88>();
+        if constexpr (FP8) {
+            const int j = (warp - 10) * 32 + lane;
+            uint32_t pos = 0;
+            bool ok = true;
+            for (int i = 0; ok && __all_sync(0xffffffffu, item_ready(i)); ++i) {
+                const int nt = m.item[i % kItems].nt, t0 = m.item[i % kItems].t0, len = m.item[i % kItems].len;
+                __syncwarp();
+                if (lane == 0) bar_arrive(&m.iempty[i % kItems]);
+                for (int t = 0; ok && t < nt; ++t, ++pos) {
+                    const uint32_t rs = pos % C::NR, vslot = pos % C::NV;
+                    ok = bar_wait(&m.rfull[rs], (pos / C::NR) & 1, gave_up, tries) &&
+                         bar_wait(&m.vempty[vslot], ((pos / C::NV) & 1) ^ 1, gave_up, tries);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const int seen = len - (t0 + t) * kPrefixTile;
+                    const uint8_t *raw = psm + C::OFF_R + rs * C::KB;
+                    uint8_t *dst = psm + C::OFF_V + vslot * C::VB;
+                    constexpr int CH = D / 16, RP = 64 / CH;  // chunks a row, rows at a time
+                    const int ch = j % CH, r0 = j / CH, flip = ch >> 2;
+#pragma unroll 4
+                    for (int p = 0; p < kPrefixTile / RP; ++p) {
+                        const int r = p * RP + r0;
+                        const int at = D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
+                        uint4 w = *reinterpret_cast<const uint4 *>(raw + at);
+                        if (r >= seen) w = make_uint4(0u, 0u, 0u, 0u);  // whatever follows the last token
+                        const uint2 h0 = e4m3x4_to_half4(w.x), h1 = e4m3x4_to_half4(w.y), h2 = e4m3x4_to_half4(w.z), h3 = e4m3x4_to_half4(w.w);
+                        uint8_t *to = dst + (ch >> 2) * C::HALF + r * 128;
+                        const int d0 = 2 * (ch & 3);
+                        const uint4 lo = make_uint4(h0.x, h0.y, h1.x, h1.y), hi = make_uint4(h2.x, h2.y, h3.x, h3.y);
+                        // the two halves' lanes store their chunks in opposite order, on banks of their own
+                        *reinterpret_cast<uint4 *>(to + (((d0 + flip) ^ (r & 7)) << 4)) = flip ? hi : lo;
+                        *reinterpret_cast<uint4 *>(to + (((d0 + 1 - flip) ^ (r & 7)) << 4)) = flip ? lo : hi;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        bar_arrive(&m.vfull[vslot]);
+                        bar_arrive(&m.rempty[rs]);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+    if (tid == 0 && *gave_up) atomicOr(&a.head->timeout, PFKV_FLAG_DEVICE_TIMEOUT);
+    tmem_fence_after();
+    if (warp == 8) tmem_free512<1>(tmem);
+    if (a.after_own) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// A pool as [units][16][D], read in boxes of one unit's 16 rows of 128 bytes at most.
+cudaError_t pool_map(CUtensorMap *map, const void *pages, long long units, int D, bool fp8) {
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = umma_map_encoder();
+    if (!enc) return cudaErrorNotSupported;
+    const int el = fp8 ? 1 : 2;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, kPage, (cuuint64_t)units};
+    const cuuint64_t strides[2] = {(cuuint64_t)(D * el), (cuuint64_t)(kPage * D * el)};
+    const cuuint32_t box[3] = {(cuuint32_t)(fp8 ? D : 64), kPage, 1};
+    const cuuint32_t one[3] = {1, 1, 1};
+    const CUresult r = enc(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                           const_cast<void *>(pages), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           fp8 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int D, bool FP8>
+cudaError_t launch_d(const PrefixArgs &a, cudaStream_t s) {
+    CUtensorMap mk{}, mv{};
+    const long long units = (long long)a.num_pages * a.Hkv;
+    cudaError_t e = pool_map(&mk, a.k_pages, units, D, FP8);
+    if (e == cudaSuccess) e = pool_map(&mv, a.v_pages, units, D, FP8);
+    if (e != cudaSuccess) return e;
+    // the first product's instruction: both operands e4m3, or bf16 with A negated for a scale below
+    // zero (the softmax works with its magnitude; FP8 queries change sign as they are converted)
+    const uint32_t idS = FP8 ? (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24)
+                             : umma_idesc(128, 128, true, false, false) | (a.sm_scale < 0.f ? 1u << 13 : 0u);
+    auto *const kernel = a.tries == kTries ? prefix_attn_kernel<D, FP8, false> : prefix_attn_kernel<D, FP8, true>;
+    return launch_pdl(kernel, dim3((unsigned)a.ctas), dim3(kThreads), smem_bytes<D, FP8>(), s, mk, mv, a, idS);
+}
+
+template <int D, bool FP8>
+cudaError_t preload_d() {
+    cudaError_t e = cudaSuccess;
+    for (auto *const kernel : {prefix_attn_kernel<D, FP8, false>, prefix_attn_kernel<D, FP8, true>}) {
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D, FP8>());
+        if (e == cudaSuccess) e = preload_kernel(kernel);
+    }
+    return e;
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_attn(const PrefixArgs &a, int D, bool fp8, cudaStream_t s) {
+    if (D == 128) return fp8 ? launch_d<128, true>(a, s) : launch_d<128, false>(a, s);
+    return fp8 ? launch_d<64, true>(a, s) : launch_d<64, false>(a, s);
+}
+
+cudaError_t preload_prefix_attn() {
+    cudaError_t e = preload_d<128, true>();
+    if (e == cudaSuccess) e = preload_d<128, false>();
+    if (e == cudaSuccess) e = preload_d<64, true>();
+    if (e == cudaSuccess) e = preload_d<64, false>();
+    return e;
+}
+
+}  // namespace pfkv

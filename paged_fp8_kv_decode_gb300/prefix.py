@@ -18,7 +18,8 @@ from . import rope as R
 PFKV_PREFIX_MAX = 4096
 
 # every symbol include/pfkv_prefix.h declares
-EXPORTED: tuple = ("pfkv_prefix_decode_workspace_size", "pfkv_prefix_decode_attn")
+EXPORTED: tuple = ("pfkv_prefix_decode_workspace_size", "pfkv_prefix_decode_attn",
+                   "pfkv_selftest_prefix_decode")
 
 
 def lib() -> ctypes.CDLL:
@@ -32,6 +33,7 @@ def lib() -> ctypes.CDLL:
                                                         I32, ctypes.POINTER(Z)]
         L.pfkv_prefix_decode_attn.argtypes = [cache, pages, pages, I32, P, rows, I32, I32, F, I32, I32,
                                               P, Z, rows, P, I64, I64, P, P]
+        L.pfkv_selftest_prefix_decode.argtypes = [I32, *L.pfkv_prefix_decode_attn.argtypes]
         for name in EXPORTED:
             getattr(L, name).restype = ctypes.c_int
         L._prefix_calls = True
@@ -88,6 +90,19 @@ def pfkv_prefix_decode_attn(cache: B.Cache, pages: Optional[B.Pages], prefixes: 
     prefix_of int32 [B] (-1: none); attn_mass: float32 [B][Hkv][>= max_seq_len], added to;
     workspace: uint8 of at least pfkv_prefix_decode_workspace_size(...) bytes; flags uint8
     [>= round_up(B, 4)].  The pool is in device memory."""
+    _attn((), cache, pages, prefixes, prefix_of, q, sm_scale, max_seq_len, max_prefix_len, workspace, out,
+          attn_mass, flags, stream)
+
+
+def pfkv_selftest_prefix_decode(tries: int, *args, attn_mass: Optional[torch.Tensor] = None,
+                                flags: Optional[torch.Tensor] = None, stream=None) -> None:
+    """pfkv_prefix_decode_attn (whose positional arguments up to ``out`` follow) with waits that
+    give up after ``tries`` tries."""
+    _attn((int(tries),), *args, attn_mass, flags, stream)
+
+
+def _attn(tries, cache, pages, prefixes, prefix_of, q, sm_scale, max_seq_len, max_prefix_len, workspace, out,
+          attn_mass, flags, stream) -> None:
     dev = R._current()
     if q.dim() != 4 or q.shape != out.shape:
         raise ValueError("q and out: bfloat16 [B][kq][Hq][D]")
@@ -105,8 +120,9 @@ def pfkv_prefix_decode_attn(cache: B.Cache, pages: Optional[B.Pages], prefixes: 
                 or attn_mass.shape[2] < max_seq_len):
             raise ValueError("attn_mass: float32 [B][Hkv][>= max_seq_len] with unit stride along tokens")
         sb, sh = attn_mass.stride(0), attn_mass.stride(1)
-    B._check(lib().pfkv_prefix_decode_attn(
-        ctypes.byref(c), R._ref(p), ctypes.byref(x), batch, R._i32(prefix_of, "prefix_of", dev),
+    name = "pfkv_selftest_prefix_decode" if tries else "pfkv_prefix_decode_attn"
+    B._check(getattr(lib(), name)(
+        *tries, ctypes.byref(c), R._ref(p), ctypes.byref(x), batch, R._i32(prefix_of, "prefix_of", dev),
         ctypes.byref(rq), hq, kq, float(sm_scale), int(max_seq_len), int(max_prefix_len),
         R._ptr(workspace, dev), workspace.nbytes, ctypes.byref(ro), R._ptr(attn_mass, dev), sb, sh,
-        R._ptr(flags, dev), R._stream(stream, dev)), "pfkv_prefix_decode_attn")
+        R._ptr(flags, dev), R._stream(stream, dev)), name)
