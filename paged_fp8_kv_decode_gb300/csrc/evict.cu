@@ -10,9 +10,10 @@
 namespace pfkv {
 namespace {
 
-constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
-constexpr int kSelBins = 2048;            // 11 bits a digit
+constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
+constexpr int kSelBins = 256;             // eight bits a digit
 constexpr int kSelCluster = 8;            // CTAs a (request, kv head), at most
+constexpr int kGroup = 128;               // keys that a warp takes at a time
 constexpr int kSelSlice = 8192;           // totals that a CTA takes while there are CTAs to share with
 constexpr int kSelKeys = 48 * 1024;       // keys that a CTA keeps in shared memory, at most
 constexpr int kMoveWarps = 8;
@@ -47,10 +48,10 @@ __device__ __forceinline__ bool lengths(const EvictArgs &a, int b, int h, int &n
 // The selection.  A cluster of one to eight CTAs a (request, kv head), each with a slice of the
 // totals between the protected ends, which it reads once and keeps as ordered keys in shared
 // memory (what does not fit is read again).  The m-th largest key is found digit by digit, from
-// the top (11, 11 and 10 bits): every CTA counts its keys' digits, the counts are added up over the
-// cluster, and the digit is the one in which the m-th falls.  Then every warp counts, over its part
-// of the slice, the keys above the m-th and those equal to it; with the sums of the parts before
-// it, it knows where its kept tokens go: larger ones all, equal ones from the lowest index on.
+// the top, eight bits each: every CTA counts its keys' digits, the counts are added up over the
+// cluster, and the digit is the one in which the m-th falls.  Then every warp counts, over its part of the slice, the keys above the m-th and those equal to it;
+// with the sums of the parts before it, it knows where its kept tokens go: larger ones all, equal
+// ones from the lowest index on.
 // --------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t cta_of_cluster() {
     uint32_t r;
@@ -72,20 +73,20 @@ __device__ __forceinline__ int word_of_cta(const int *p, uint32_t rank) {
 }
 
 struct SelShared {
-    int hist[3][kSelBins];     // a digit's counts: one array a pass, so that one is read while the next is made
+    int hist[4][kSelBins];     // a digit's counts
     int warp_sum[kSelWarps], warp_eq[kSelWarps];
     int gt, eq;                // keys above and equal to the m-th in this CTA
     uint32_t bits;             // flag bits
     int digit, need;
 };
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, int ctas, int room) {
+__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs a, int ctas, int room) {
     extern __shared__ uint32_t keys[];
     __shared__ SelShared sm;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = ctas == 1 ? 0 : (int)cta_of_cluster();
     const int bh = blockIdx.x / ctas, b = bh / a.Hkv, h = bh - b * a.Hkv;
-    for (int i = tid; i < 3 * kSelBins; i += kSelThreads) sm.hist[0][i] = 0;
+    for (int i = tid; i < 4 * kSelBins; i += kSelThreads) sm.hist[0][i] = 0;
     if (tid == 0) sm.bits = 0u;
     pdl_enter();
     int n, k;
@@ -101,25 +102,56 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, 
     const int f = min(a.keep_first, k), l = min(a.keep_last, k - f), m = k - f - l;
     const int L = n - l - f;  // candidates
     // this CTA's slice of them, in whole warps' worth
-    const int per = ((L + ctas - 1) / ctas + 31) & ~31, s0 = min(L, rank * per), len = min(L, s0 + per) - s0;
+    const int per = ((L + ctas - 1) / ctas + kGroup - 1) / kGroup * kGroup, s0 = min(L, rank * per), len = min(L, s0 + per) - s0;
     const float *mass = a.mass + (long long)b * a.mass_sb + (long long)h * a.mass_sh + f + s0;
-    const int have = min(len, room);
-    auto key_at = [&](int j) { return j < have ? keys[j] : order_key(mass[j]); };
+    const int groups = (len + kGroup - 1) / kGroup, have = min(groups, room / kGroup);
+    // four keys that follow each other, of lane's place in a group; zero, which is below all keys, past the last
+    auto four_keys = [&](int g) {
+        if (g < have) return reinterpret_cast<const uint4 *>(keys)[g * 32 + lane];
+        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+        const int j = g * kGroup + lane * 4;
+        if (j < len) u.x = order_key(mass[j]);
+        if (j + 1 < len) u.y = order_key(mass[j + 1]);
+        if (j + 2 < len) u.z = order_key(mass[j + 2]);
+        if (j + 3 < len) u.w = order_key(mass[j + 3]);
+        return u;
+    };
     __syncthreads();  // the counts are zero
     if (m > 0 && m < L) {
-        // keys, and the first digit's counts
-#pragma unroll 4
-        for (int j = tid; j < len; j += kSelThreads) {
-            const uint32_t u = order_key(mass[j]);
-            if (j < have) keys[j] = u;
-            atomicAdd(&sm.hist[0][u >> 21], 1);
+        // keys, and the first digit's counts; the loads of kAhead groups are on their way together
+        constexpr int kAhead = 4;
+        for (int g0 = warp; g0 < groups; g0 += kAhead * kSelWarps) {
+            float x[kAhead][4];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = (g0 + i * kSelWarps) * kGroup + e * 32 + lane;
+                    x[i][e] = j < len ? mass[j] : 0.f;
+                }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int g = g0 + i * kSelWarps;
+                if (g >= groups) break;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = g * kGroup + e * 32 + lane;
+                    const uint32_t u = j < len ? order_key(x[i][e]) : 0u;
+                    if (g < have) keys[j] = u;
+                    atomicAdd(&sm.hist[0][u >> 24], 1);
+                }
+            }
         }
     }
     bits = __reduce_or_sync(0xffffffffu, bits);
     if (lane == 0 && bits) atomicOr(&sm.bits, bits);
     sync_cluster(ctas);
     bits = sm.bits;
-    for (int r = 0; r < ctas && ctas > 1; ++r) bits |= (uint32_t)word_of_cta(reinterpret_cast<const int *>(&sm.bits), r);
+    if (ctas > 1) {
+#pragma unroll
+        for (int r = 0; r < kSelCluster; ++r)  // all on their way at once
+            bits |= (uint32_t)word_of_cta(reinterpret_cast<const int *>(&sm.bits), min(r, ctas - 1));
+    }
     if (rank == 0 && tid == 0) a.status[bh] = make_int2((int)bits, k);
     int32_t *kept = a.kept + (long long)b * a.kept_sb + (long long)h * a.kept_sh;
     if (bits || m == 0 || m == L) {
@@ -134,59 +166,67 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, 
 
     uint32_t found = 0u;
     int need = m;
-    constexpr int kShift[3] = {21, 10, 0};
-#pragma unroll
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = kShift[pass];
+#pragma unroll 1
+    for (int pass = 0; pass < 4; ++pass) {
+        const int shift = 24 - 8 * pass;
         if (pass > 0) {
-            const uint32_t above = pass == 1 ? 0xffe00000u : 0xfffffc00u;
-            const uint32_t mask = pass == 1 ? 2047u : 1023u;
-            for (int j = tid; j < len; j += kSelThreads) {
-                const uint32_t u = key_at(j);
-                if ((u & above) == found) atomicAdd(&sm.hist[pass][(u >> shift) & mask], 1);
+            const uint32_t above = 0xffffffffu << (shift + 8);
+            auto count = [&](uint32_t u) {
+                if ((u & above) == found) atomicAdd(&sm.hist[pass][(u >> shift) & 255u], 1);
+            };
+#pragma unroll 2
+            for (int g = warp; g < groups; g += kSelWarps) {
+                const uint4 u = four_keys(g);
+                count(u.x);
+                count(u.y);
+                count(u.z);
+                count(u.w);
             }
             sync_cluster(ctas);
         }
-        // the digit: counts from the top, two bins a thread (thread 0 has the highest)
-        const int top = kSelBins - 1 - 2 * tid;
-        int c0 = 0, c1 = 0;
-        if (ctas == 1) {
-            c0 = sm.hist[pass][top];
-            c1 = sm.hist[pass][top - 1];
-        } else {
-            for (int r = 0; r < ctas; ++r) {
-                c0 += word_of_cta(&sm.hist[pass][top], r);
-                c1 += word_of_cta(&sm.hist[pass][top - 1], r);
-            }
-        }
-        int x = c0 + c1;
+        const int *const sum = sm.hist[pass];
+        // the digit: counts from the top, a bin a thread (thread 0 has the highest)
+        int c = 0, x = 0;
+        const int bin = kSelBins - 1 - tid;
+        if (tid < kSelBins) {
+            if (ctas == 1) c = sum[bin];
+            else {
+                int y[kSelCluster];
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, off);
-            if (lane >= off) x += y;
+                for (int r = 0; r < kSelCluster; ++r) y[r] = word_of_cta(&sum[bin], min(r, ctas - 1));
+#pragma unroll
+                for (int r = 0; r < kSelCluster; ++r) c += r < ctas ? y[r] : 0;
+            }
+            x = c;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, off);
+                if (lane >= off) x += y;
+            }
+            if (lane == 31) sm.warp_sum[warp] = x;
         }
-        if (lane == 31) sm.warp_sum[warp] = x;
         __syncthreads();
-        const int w = sm.warp_sum[lane];
-        const int before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0) + x - c0 - c1;
-        if (before < need && before + c0 + c1 >= need) {  // one thread
-            const bool second = before + c0 < need;
-            sm.digit = second ? top - 1 : top;
-            sm.need = need - before - (second ? c0 : 0);
+        if (tid < kSelBins) {
+            const int w = lane < kSelBins / 32 ? sm.warp_sum[lane] : 0;
+            const int before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0) + x - c;
+            if (before < need && before + c >= need) {  // one thread
+                sm.digit = bin;
+                sm.need = need - before;
+            }
         }
         __syncthreads();
         found |= (uint32_t)sm.digit << shift;
         need = sm.need;
     }
 
-    // where the kept ones go: a warp's part of the slice, 32 keys at a time
-    const int part = ((len + kSelWarps - 1) / kSelWarps + 31) & ~31;
-    const int p0 = min(len, warp * part), p1 = min(len, p0 + part);
+    // where the kept ones go: a warp's part of the slice, a group at a time
+    const int part = (groups + kSelWarps - 1) / kSelWarps, g0 = min(groups, warp * part), g1 = min(groups, g0 + part);
     int gt = 0, eq = 0;
-    for (int j = p0 + lane; j < p1; j += 32) {
-        const uint32_t u = key_at(j);
-        gt += u > found;
-        eq += u == found;
+#pragma unroll 2
+    for (int g = g0; g < g1; ++g) {
+        const uint4 u = four_keys(g);
+        gt += (u.x > found) + (u.y > found) + (u.z > found) + (u.w > found);
+        eq += (u.x == found) + (u.y == found) + (u.z == found) + (u.w == found);
     }
     gt = __reduce_add_sync(0xffffffffu, gt);
     eq = __reduce_add_sync(0xffffffffu, eq);
@@ -195,7 +235,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, 
         sm.warp_eq[warp] = eq;
     }
     __syncthreads();
-    const int wg = sm.warp_sum[lane], we = sm.warp_eq[lane];
+    const int wg = lane < kSelWarps ? sm.warp_sum[lane] : 0, we = lane < kSelWarps ? sm.warp_eq[lane] : 0;
     int at_gt = __reduce_add_sync(0xffffffffu, lane < warp ? wg : 0);
     int at_eq = __reduce_add_sync(0xffffffffu, lane < warp ? we : 0);
     if (ctas > 1) {
@@ -207,24 +247,52 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a, 
             }
         }
         sync_cluster(ctas);
-        for (int r = 0; r < rank; ++r) {
-            at_gt += word_of_cta(&sm.gt, r);
-            at_eq += word_of_cta(&sm.eq, r);
+        int y[2][kSelCluster];
+#pragma unroll
+        for (int r = 0; r < kSelCluster; ++r) {
+            y[0][r] = word_of_cta(&sm.gt, min(r, ctas - 1));
+            y[1][r] = word_of_cta(&sm.eq, min(r, ctas - 1));
+        }
+#pragma unroll
+        for (int r = 0; r < kSelCluster; ++r) {
+            at_gt += r < rank ? y[0][r] : 0;
+            at_eq += r < rank ? y[1][r] : 0;
         }
         // no CTA leaves while another reads its shared memory
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     }
     const uint32_t below = (1u << lane) - 1u;
-    for (int j0 = p0; j0 < p1; j0 += 32) {
-        const int j = j0 + lane;
-        const uint32_t u = j < p1 ? key_at(j) : 0u;
-        const uint32_t is_gt = __ballot_sync(0xffffffffu, j < p1 && u > found);
-        const uint32_t is_eq = __ballot_sync(0xffffffffu, j < p1 && u == found);
-        const int before_eq = at_eq + __popc(is_eq & below);
-        const bool keep = ((is_gt >> lane) & 1u) || (((is_eq >> lane) & 1u) && before_eq < need);
-        if (keep) kept[f + at_gt + __popc(is_gt & below) + min(before_eq, need)] = f + s0 + j;
-        at_gt += __popc(is_gt);
-        at_eq += __popc(is_eq);
+#pragma unroll 1
+    for (int g = g0; g < g1; ++g) {
+        const uint4 u4 = four_keys(g);
+        const uint32_t u[4] = {u4.x, u4.y, u4.z, u4.w};
+        uint32_t is_gt[4], is_eq[4];
+        int gt_before = at_gt, eq_before = at_eq;  // of this lane's four
+        int any = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            is_gt[e] = __ballot_sync(0xffffffffu, u[e] > found);
+            is_eq[e] = __ballot_sync(0xffffffffu, u[e] == found);
+            any |= is_eq[e];
+            gt_before += __popc(is_gt[e] & below);
+            at_gt += __popc(is_gt[e]);
+        }
+        if (any) {  // (equal ones are few)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                eq_before += __popc(is_eq[e] & below);
+                at_eq += __popc(is_eq[e]);
+            }
+        }
+        int32_t *const to = kept + f;
+        const int j = f + s0 + g * kGroup + lane * 4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool larger = u[e] > found, equal = u[e] == found;
+            if (larger || (equal && eq_before < need)) to[gt_before + min(eq_before, need)] = j + e;
+            gt_before += larger;
+            eq_before += equal;
+        }
     }
     if (ctas > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -267,32 +335,82 @@ __device__ __forceinline__ __half2 codes_to_half2(uint32_t two) {
     return *reinterpret_cast<__half2 *>(&h);
 }
 
-// New codes of a destination unit's rows, in registers as load_rows left them; `mine`: the scale of
-// row `lane` (lanes below `live`).  Returns the unit's new scale.
-//
-// The code of fl(fl(c s) / z) for old code c, old scale s and new scale z.  Taken as the code of
-// c fl(s / z): both are within 2^-23 (relative) of c s / z, so they differ at most if a border
-// between codes lies within 2^-21 of the product.  A code's significand is one of eight, and
-// borders are multiples of 1/16 of a power of two (of 1/8 and coarser below the normal range), so
-// eight products a row say whether any code of it comes near one; then all of the unit's codes are
-// taken by the definition.  A ratio within 2^-21 of one keeps every code.
+// The rows of a destination unit by the definition: code of fl(fl(c s) / z).  (A call, not inlined:
+// few units need it, and its registers would be every unit's.)
 template <int D>
-__device__ __forceinline__ float new_codes(uint4 (&w)[MoveCfg<D, true>::PASSES], float mine, int live, int lane) {
+__device__ __noinline__ float by_definition(void *pool, long long row, float mine, long long to, int live, int lane) {
     using C = MoveCfg<D, true>;
-    // absolute maxima of rows as codes (exact in f16), then of values
+    uint4 w[C::PASSES];
+    load_rows<D, true>(w, pool, row, live, lane);
+    float z[C::PASSES];
+    float top = 0.f;  // (a NaN is no maximum)
+#pragma unroll
+    for (int i = 0; i < C::PASSES; ++i) z[i] = __shfl_sync(0xffffffffu, mine, i * C::RPP + lane / C::LPR);
+#pragma unroll
+    for (int i = 0; i < C::PASSES; ++i) {
+        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const float2 x = e4m3x2_to_float2((uint16_t)(u[q >> 1] >> (16 * (q & 1))));
+            top = fmaxf(top, fmaxf(fabsf(x.x * z[i]), fabsf(x.y * z[i])));
+        }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    const float sound = top == 0.f ? 1.f : __fdiv_rn(top, 448.f);
+#pragma unroll
+    for (int i = 0; i < C::PASSES; ++i) {
+        uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float2 x0 = e4m3x2_to_float2((uint16_t)u[q]), x1 = e4m3x2_to_float2((uint16_t)(u[q] >> 16));
+            const float2 y0 = make_float2(__fdiv_rn(x0.x * z[i], sound), __fdiv_rn(x0.y * z[i], sound));
+            const float2 y1 = make_float2(__fdiv_rn(x1.x * z[i], sound), __fdiv_rn(x1.y * z[i], sound));
+            u[q] = (uint32_t)__nv_cvt_float2_to_fp8x2(y0, __NV_SATFINITE, __NV_E4M3) |
+                   (uint32_t)__nv_cvt_float2_to_fp8x2(y1, __NV_SATFINITE, __NV_E4M3) << 16;
+        }
+        w[i] = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    store_rows<D, true>(w, pool, to, live, lane);
+    return sound;
+}
+
+// Writes a destination unit's rows, in registers as load_rows left them, with new codes; `mine`: the
+// scale of row `lane` (lanes below `live`).  Returns the unit's new scale.
+//
+// The code of fl(fl(c s) / z) for old code c, old scale s and new scale z, in one of three ways:
+//
+// (1) As the code of c fl(s / z).  Both are within 2^-23 (relative) of c s / z, so the codes are the
+// same unless a border between codes lies within 2^-21 of the product.  With c = m 2^q, m = 8 .. 15 (a
+// subnormal c as a multiple of its own), and t = m s / z, borders are at odd multiples of 1/16 of t's
+// power of two; or, where the new code is subnormal, at odd multiples o < 16 of 2^-10, so that t is
+// a multiple of 1/8 of its power of two and below 8, or o (m even), 2 o (m = 8, 12) or 4 o (m = 8), where
+// c is subnormal.  Eight t a row say whether any code of it may come near a border.  A ratio
+// within 2^-21 of one keeps every code.  (Borders are met often: z is a code's value over 448, so
+// in the row of the largest, ratios are 14 / m.)
+// (2) Otherwise with a correctly rounded quotient, by Markstein's theorem (IBM J. Res. Dev. 34, 1990): two
+// corrections of x times the correctly rounded reciprocal of z.  Magnitudes: a sum would lose a
+// zero's sign.
+// (3) By divisions, for scales so small or large that (1) or (2) might not hold, and codes of NaN.
+template <int D>
+__device__ __forceinline__ float new_codes(uint4 (&w)[MoveCfg<D, true>::PASSES], void *pool, long long row, float mine,
+                                           long long to, int live, int lane) {
+    using C = MoveCfg<D, true>;
+    // absolute maxima of rows as codes, whose order is that of their values; then of values
     float top = 0.f;
+    uint32_t most = 0u;
     float z[C::PASSES];
 #pragma unroll
     for (int i = 0; i < C::PASSES; ++i) {
-        const int r = i * C::RPP + lane / C::LPR;
-        z[i] = __shfl_sync(0xffffffffu, mine, r);
-        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-        __half2 t = __float2half2_rn(0.f);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            t = __hmax2(t, __hmax2(__habs2(codes_to_half2(u[q] & 0xffffu)), __habs2(codes_to_half2(u[q] >> 16))));
-        const float2 t2 = __half22float2(t);
-        top = fmaxf(top, fabsf(fmaxf(t2.x, t2.y) * z[i]));
+        z[i] = __shfl_sync(0xffffffffu, mine, i * C::RPP + lane / C::LPR);
+        // the upper and the lower bytes of 16-bit halves
+        uint32_t hi = __vimax3_u16x2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu, w[i].z & 0x7fff7fffu);
+        uint32_t lo = __vimax3_u16x2(w[i].x & 0x007f007fu, w[i].y & 0x007f007fu, w[i].z & 0x007f007fu);
+        hi = __vimax3_u16x2(hi, w[i].w & 0x7fff7fffu, 0u) >> 8;
+        lo = __vimax3_u16x2(lo, w[i].w & 0x007f007fu, 0u);
+        const uint32_t code = max(max(hi & 0xffu, hi >> 16), max(lo & 0xffffu, lo >> 16));
+        most = max(most, code);
+        top = fmaxf(top, fabsf(e4m3x2_to_float2((uint16_t)code).x * z[i]));
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
@@ -301,92 +419,143 @@ __device__ __forceinline__ float new_codes(uint4 (&w)[MoveCfg<D, true>::PASSES],
     // lane + 16 has the other half
     const float from = __shfl_sync(0xffffffffu, mine, lane & 15);
     const float ratio = __fdiv_rn(from, scale);
-    bool near = !(from > 1e-24f && from < 1e30f && scale > 1e-24f && scale < 1e30f && ratio > 1e-20f && ratio < 1e20f);
+    const bool odd = !(from > 1e-24f && from < 1e30f && scale > 1e-24f && scale < 1e30f && ratio > 1e-20f && ratio < 1e20f);
+    bool near = false;
     if (!(fabsf(ratio - 1.f) <= 0x1p-21f)) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float y = ratio * (float)(8 + 4 * (lane >> 4) + e);
-            near |= ((__float_as_uint(y) + 16u) & 0x7ffffu) <= 32u;
+            const int sig = 8 + 4 * (lane >> 4) + e;
+            const float t = ratio * (float)sig;
+            const uint32_t u = __float_as_uint(t) + 16u;  // near: within 16 steps
+            if ((u & 0x7ffffu) > 32u) continue;           // of no multiple of 1/16
+            const int n = (int)(t + 0.5f);                // t itself where it matters below: 8 <= t < 61
+            const int twos = n & -n;
+            near |= (u & 0x80000u) != 0u || t < 7.9f || (t < 60.1f && twos <= (sig == 8 ? 4 : sig == 12 ? 2 : (sig & 1) ? 0 : 1));
         }
     }
-    const bool exact = __any_sync(0xffffffffu, (lane & 15) < live && near);
+    if (__any_sync(0xffffffffu, ((lane & 15) < live && odd) || most == 0x7fu))
+        return by_definition<D>(pool, row, mine, to, live, lane);
+    if (__any_sync(0xffffffffu, (lane & 15) < live && near)) {
+        const float inv = __frcp_rn(scale);
+        const float2 inv2 = make_float2(inv, inv), down = make_float2(-scale, -scale);
 #pragma unroll
-    for (int i = 0; i < C::PASSES; ++i) {
-        const float f = __shfl_sync(0xffffffffu, ratio, i * C::RPP + lane / C::LPR);
-        uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        for (int i = 0; i < C::PASSES; ++i) {
+            uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const float2 x0 = __half22float2(codes_to_half2(u[q] & 0xffffu)), x1 = __half22float2(codes_to_half2(u[q] >> 16));
-            float2 y0, y1;
-            if (!exact) {
-                y0 = mul2(x0, make_float2(f, f));
-                y1 = mul2(x1, make_float2(f, f));
-            } else {
-                y0 = make_float2(__fdiv_rn(x0.x * z[i], scale), __fdiv_rn(x0.y * z[i], scale));
-                y1 = make_float2(__fdiv_rn(x1.x * z[i], scale), __fdiv_rn(x1.y * z[i], scale));
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t size = u[q] & 0x7f7f7f7fu;
+                uint32_t code = u[q] & 0x80808080u;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const float2 x = mul2(__half22float2(codes_to_half2(size >> (16 * half))), make_float2(z[i], z[i]));
+                    float2 y = mul2(x, inv2);
+                    y = fma2(fma2(y, down, x), inv2, y);
+                    y = fma2(fma2(y, down, x), inv2, y);
+                    code |= (uint32_t)__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3) << (16 * half);
+                }
+                u[q] = code;
             }
-            u[q] = (uint32_t)__nv_cvt_float2_to_fp8x2(y0, __NV_SATFINITE, __NV_E4M3) |
-                   (uint32_t)__nv_cvt_float2_to_fp8x2(y1, __NV_SATFINITE, __NV_E4M3) << 16;
+            w[i] = make_uint4(u[0], u[1], u[2], u[3]);
         }
-        w[i] = make_uint4(u[0], u[1], u[2], u[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < C::PASSES; ++i) {
+            const float f = __shfl_sync(0xffffffffu, ratio, i * C::RPP + lane / C::LPR);
+            uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float2 y0 = mul2(__half22float2(codes_to_half2(u[q])), make_float2(f, f));
+                const float2 y1 = mul2(__half22float2(codes_to_half2(u[q] >> 16)), make_float2(f, f));
+                u[q] = (uint32_t)__nv_cvt_float2_to_fp8x2(y0, __NV_SATFINITE, __NV_E4M3) |
+                       (uint32_t)__nv_cvt_float2_to_fp8x2(y1, __NV_SATFINITE, __NV_E4M3) << 16;
+            }
+            w[i] = make_uint4(u[0], u[1], u[2], u[3]);
+        }
     }
+    store_rows<D, true>(w, pool, to, live, lane);
     return scale;
 }
 
+
+// A warp takes `each` units (at most kMoveUnits) of one (request, head), kMoveWarps apart.  What
+// leads to their rows (status, indices and new pages, then old pages) is loaded for all of them at
+// once, half a warp a unit: one after the other, these loads took most of a unit's time.
+constexpr int kMoveUnits = 4;
+
 template <int D, bool FP8>
-__global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(EvictArgs a, int units) {
+__global__ void __launch_bounds__(kMoveWarps * 32, FP8 ? 3 : 4) evict_move_kernel(EvictArgs a, int chunks, int each) {
     pdl_enter();
-    const long long x = (long long)blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    const long long bh = x / units;
-    if (bh >= (long long)a.B * a.Hkv) return;
-    const int u = (int)(x - bh * units), b = (int)(bh / a.Hkv), h = (int)(bh - (long long)b * a.Hkv);
+    using C = MoveCfg<D, FP8>;
+    const int bh = blockIdx.x / chunks, chunk = blockIdx.x - bh * chunks;
+    const int b = bh / a.Hkv, h = bh - b * a.Hkv;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slot = lane & 15;
+    const int u0 = chunk * each * kMoveWarps + warp;
     uint32_t bits = 0u;
     for (int i = lane; i < a.Hkv; i += 32) bits |= (uint32_t)a.status[(long long)b * a.Hkv + i].x;
-    bits = __reduce_or_sync(0xffffffffu, bits);
     const int k = a.status[bh].y;
-    if (u == 0 && lane == 0) {
+    const int32_t *kept = a.kept + (long long)b * a.kept_sb + (long long)h * a.kept_sh;
+    int from[kMoveUnits / 2], id[kMoveUnits / 2];
+#pragma unroll
+    for (int i = 0; i < kMoveUnits / 2; ++i) {
+        const int at = 2 * i + (lane >> 4), j = (u0 + at * kMoveWarps) * kPage + slot;
+        from[i] = at < each && j < a.max_keep ? kept[j] : 0;
+    }
+    // a new page a unit, in lane `unit`
+    const int up = u0 + min(lane, each - 1) * kMoveWarps;
+    const int new_id = up < a.dst.max_pages ? a.dst.block_tables[(long long)b * a.dst.bt_sb + (long long)h * a.dst.bt_sh + up] : 0;
+    bits = __reduce_or_sync(0xffffffffu, bits);
+    if (u0 == 0 && lane == 0) {
         if (h == 0 || a.len_sh != 0) a.new_lens[(long long)b * a.len_sb + (long long)h * a.len_sh] = bits ? 0 : k;
         if (h == 0 && a.flags) a.flags[b] = (uint8_t)bits;
     }
     if (bits) return;
-    const int j = u * kPage + (lane & 15), live = min(kPage, k - u * kPage);
-    int from = 0;
-    long long row = 0;
-    if (lane < live) {
-        from = a.kept[(long long)b * a.kept_sb + (long long)h * a.kept_sh + j];
-        const int id = a.src.block_tables[(long long)b * a.src.bt_sb + (long long)h * a.src.bt_sh + from / kPage];
-        row = ((long long)id * a.Hkv + h) * kPage + from % kPage;
+    const int32_t *table = a.src.block_tables + (long long)b * a.src.bt_sb + (long long)h * a.src.bt_sh;
+#pragma unroll
+    for (int i = 0; i < kMoveUnits / 2; ++i) {
+        const int at = 2 * i + (lane >> 4), j = (u0 + at * kMoveWarps) * kPage + slot;
+        const bool there = at < each && j < k;
+        id[i] = there ? table[from[i] / kPage] : -1;
+        if (a.new_mass && at < each && j < a.nm_len)
+            a.new_mass[(long long)b * a.nm_sb + (long long)h * a.nm_sh + j] =
+                there ? a.mass[(long long)b * a.mass_sb + (long long)h * a.mass_sh + from[i]] : 0.f;
     }
-    if (a.new_mass && lane < kPage && j < a.nm_len)
-        a.new_mass[(long long)b * a.nm_sb + (long long)h * a.nm_sh + j] =
-            lane < live ? a.mass[(long long)b * a.mass_sb + (long long)h * a.mass_sh + from] : 0.f;
-    if (live <= 0) return;
-    const int id = a.dst.block_tables[(long long)b * a.dst.bt_sb + (long long)h * a.dst.bt_sh + u];
-    const long long to = (long long)id * a.Hkv + h;
-    using C = MoveCfg<D, FP8>;
-    uint4 wk[C::PASSES], wv[C::PASSES];
-    load_rows<D, FP8>(wk, a.k_pages, row, live, lane);
-    load_rows<D, FP8>(wv, a.v_pages, row, live, lane);
-    if constexpr (FP8) {
-        const long long unit = row / kPage, first = __shfl_sync(0xffffffffu, unit, 0);
-        float ks = 0.f, vs = 0.f;
-        if (lane < live) {
-            ks = a.k_scale[unit];
-            vs = a.v_scale[unit];
-        }
-        // of one unit: bytes and scales as they are
-        if (!__all_sync(0xffffffffu, lane >= live || unit == first)) {
-            ks = new_codes<D>(wk, ks, live, lane);
-            vs = new_codes<D>(wv, vs, live, lane);
-        }
-        if (lane == 0) {
-            a.k_scale[to] = ks;
-            a.v_scale[to] = vs;
+#pragma unroll 1
+    for (int i = 0; i < each; ++i) {
+        const int u = u0 + i * kMoveWarps, live = min(kPage, k - u * kPage);
+        if (live <= 0) return;
+        static_assert(kMoveUnits == 4, "two registers of indices");
+        const int src = (i & 1) * 16 + slot;
+        const int page = __shfl_sync(0xffffffffu, i < 2 ? id[0] : id[1], src);
+        const int token = __shfl_sync(0xffffffffu, i < 2 ? from[0] : from[1], src);
+        const long long unit = (long long)page * a.Hkv + h, row = unit * kPage + token % kPage;
+        const long long to = (long long)__shfl_sync(0xffffffffu, new_id, i) * a.Hkv + h;
+        uint4 wk[C::PASSES], wv[C::PASSES];
+        load_rows<D, FP8>(wk, a.k_pages, row, live, lane);
+        load_rows<D, FP8>(wv, a.v_pages, row, live, lane);
+        if constexpr (FP8) {
+            const long long first = __shfl_sync(0xffffffffu, unit, 0);
+            float ks = 0.f, vs = 0.f;
+            if (lane < live) {
+                ks = a.k_scale[unit];
+                vs = a.v_scale[unit];
+            }
+            // of one unit: bytes and scales as they are
+            if (!__all_sync(0xffffffffu, lane >= live || unit == first)) {
+                ks = new_codes<D>(wk, a.k_pages, row, ks, to, live, lane);
+                vs = new_codes<D>(wv, a.v_pages, row, vs, to, live, lane);
+            } else {
+                store_rows<D, FP8>(wk, a.k_pages, to, live, lane);
+                store_rows<D, FP8>(wv, a.v_pages, to, live, lane);
+            }
+            if (lane == 0) {
+                a.k_scale[to] = ks;
+                a.v_scale[to] = vs;
+            }
+        } else {
+            store_rows<D, FP8>(wk, a.k_pages, to, live, lane);
+            store_rows<D, FP8>(wv, a.v_pages, to, live, lane);
         }
     }
-    store_rows<D, FP8>(wk, a.k_pages, to, live, lane);
-    store_rows<D, FP8>(wv, a.v_pages, to, live, lane);
 }
 
 }  // namespace
@@ -399,7 +568,7 @@ cudaError_t launch_evict(const EvictArgs &a, int D, bool fp8, int num_sms, cudaS
     while (ctas < kSelCluster && a.max_seq_len > ctas * kSelSlice &&
            (bh * ctas * 2 <= 2LL * num_sms || a.max_seq_len > ctas * kSelKeys))
         ctas *= 2;
-    const int room = min(kSelKeys, (a.max_seq_len + ctas - 1) / ctas + 32);
+    const int room = min(kSelKeys, ((a.max_seq_len + ctas - 1) / ctas + kGroup - 1) / kGroup * kGroup);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(bh * ctas));
     cfg.blockDim = dim3(kSelThreads);
@@ -416,11 +585,13 @@ cudaError_t launch_evict(const EvictArgs &a, int D, bool fp8, int num_sms, cudaS
     cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a, ctas, room);
     if (e != cudaSuccess) return e;
     const int units = max(1, (max(a.max_keep, a.new_mass ? a.nm_len : 0) + kPage - 1) / kPage);
-    const long long grid_x = (bh * units + kMoveWarps - 1) / kMoveWarps;
-    const dim3 grid((unsigned)grid_x), block(kMoveWarps * 32);
+    // one unit a warp while all warps run at once
+    const int each = (int)min((long long)kMoveUnits, max(1LL, bh * units / ((long long)num_sms * 32)));
+    const int chunks = (units + each * kMoveWarps - 1) / (each * kMoveWarps);
+    const dim3 grid((unsigned)(bh * chunks)), block(kMoveWarps * 32);
     auto *const kernel = D == 128 ? (fp8 ? evict_move_kernel<128, true> : evict_move_kernel<128, false>)
                                   : (fp8 ? evict_move_kernel<64, true> : evict_move_kernel<64, false>);
-    return launch_pdl(kernel, grid, block, 0, s, a, units);
+    return launch_pdl(kernel, grid, block, 0, s, a, chunks, each);
 }
 
 cudaError_t preload_evict() {
