@@ -114,10 +114,8 @@ __device__ void plan_segments(const PrefixArgs &a) {
     for (int x = x0; x < x1; ++x) mine += blocks(x / a.Hkv) * tiles(x);
     int tile = block_sum_before(mine, part, &total);
     const int U = total, W = min(a.ctas, U), tile_first = tile;
-    if (tid == 0) {
-        a.head->U = U;
-        a.head->W = W;
-    }
+    // CTAs without work; the others' ranges are written with the segment that holds their first tile
+    for (int c = W + tid; c < a.ctas; c += kValThreads) a.range[c] = PrefixRange{0, 0, 0, 0};
     for (int pass = 0, base = 0; pass < 2; ++pass) {
         int rows = 0;
         tile = tile_first;
@@ -135,8 +133,20 @@ __device__ void plan_segments(const PrefixArgs &a) {
                 s.ntiles = n;
                 s.base = base + rows;
                 s.len = len;
-                if (pass) a.seg[a.seg0[p] + h * nb + rb] = s;
-                if (n > 0) rows += rows8(s.rows) * (pers_worker_of(tile + n - 1, U, W) - pers_worker_of(tile, U, W) + 1);
+                s.pad[0] = s.pad[1] = 0;
+                s.first = n > 0 ? pers_worker_of(tile, U, W) : 0;
+                s.ctas = n > 0 ? pers_worker_of(tile + n - 1, U, W) - s.first + 1 : 0;
+                if (pass) {
+                    const int k = a.seg0[p] + h * nb + rb;
+                    a.seg[k] = s;
+                    // CTAs whose first tile is in this segment
+                    for (int c = s.first; c < s.first + s.ctas; ++c) {
+                        const int t0 = (int)(((long long)c * U + W - 1) / W);
+                        if (t0 >= tile && t0 < tile + n)
+                            a.range[c] = PrefixRange{t0, (int)(((long long)(c + 1) * U + W - 1) / W), k, 0};
+                    }
+                }
+                rows += rows8(s.rows) * s.ctas;
                 tile += n;
             }
         }
@@ -291,8 +301,7 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(PrefixArgs 
         const int nb = (int)(((long long)(a.mstart[p + 1] - a.mstart[p]) * a.kq * G + kPrefixBlock - 1) / kPrefixBlock);
         const PrefixSeg sg = a.seg[a.seg0[p] + h * nb + R / kPrefixBlock];
         if (sg.ntiles > 0) {
-            const int U = a.head->U, W = a.head->W;
-            pre_n = pers_worker_of(sg.tile0 + sg.ntiles - 1, U, W) - pers_worker_of(sg.tile0, U, W) + 1;
+            pre_n = sg.ctas;
             pre_rows = rows8(sg.rows);
             base = sg.base;
             block_row = R % kPrefixBlock;
@@ -457,7 +466,7 @@ int check_words(const pfkv_pages *p) { return max(1, (p->max_pages + kValTile - 
 
 // Where everything lies in the workspace.
 struct Layout {
-    size_t head, pre_bits, pre_vmax, own_bits, pos, members, mstart, seg0, seg, plse, po, packed, own, mass, total;
+    size_t head, pre_bits, pre_vmax, own_bits, pos, members, mstart, seg0, seg, range, plse, po, packed, own, mass, total;
     size_t group_bytes;
     DecodePlan plan;  // of the own tokens
 };
@@ -490,6 +499,7 @@ pfkv_status lay_out(const pfkv_cache *c, const pfkv_pages *pages, const pfkv_pag
     l->mstart = take(4 * (size_t)(NP + 1));
     l->seg0 = take(4 * (size_t)(NP + 1));
     l->seg = take(sizeof(PrefixSeg) * (size_t)S);
+    l->range = take(sizeof(PrefixRange) * (size_t)sms);
     l->plse = take(4 * (size_t)partial);
     l->po = take(4 * (size_t)partial * c->head_dim);
     l->packed = take(pages ? 2 * (size_t)(rows * H) * c->head_dim : 0);
@@ -576,6 +586,7 @@ pfkv_status prefix_attn(int tries, const pfkv_cache *cache, const pfkv_pages *pa
     a.mstart = reinterpret_cast<int *>(ws + l.mstart);
     a.seg0 = reinterpret_cast<int *>(ws + l.seg0);
     a.seg = reinterpret_cast<PrefixSeg *>(ws + l.seg);
+    a.range = reinterpret_cast<PrefixRange *>(ws + l.range);
     a.plse = reinterpret_cast<float *>(ws + l.plse);
     a.po = reinterpret_cast<float *>(ws + l.po);
     const bool packs = pages && !rows_follow(q, batch, kq, num_q_heads, D);

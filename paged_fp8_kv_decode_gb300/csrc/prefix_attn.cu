@@ -19,8 +19,10 @@
 // half the cost of one in 16 bits); two warps convert V to f16 (exact), and weights times their
 // unit's V scale are f16.  K's scales are applied to the scores, 16 columns at a time.
 //
-// Roles of the twelve warps: 0-3 and 4-7 softmax; 8 issues the products; 9 finds the segments, and
-// loads page ids, scales, K and V; 10 and 11 convert V (FP8).
+// Roles of the twelve warps: 0-3 and 4-7 softmax; 8 issues the products; 9 finds the segments and
+// loads K and the scales; 10 and 11 load the V of four pages of every tile each (FP8: and convert it).  A
+// page's slab of 2 KB is a copy, and a warp issues one in 67 cycles whatever its size (measured), so three
+// warps share them: one alone would feed 28 bytes a cycle.
 #include "prefix_internal.cuh"
 #include "umma.cuh"
 
@@ -66,7 +68,7 @@ struct Info {
 };
 
 struct Misc {
-    uint64_t kfull[6], kempty[6], vfull[4], vempty[4], rfull[4], rempty[4];
+    uint64_t kfull[6], kempty[6], vfull[4], vempty[4], rfull[2][4];
     uint64_t qfull, sfull[2], pready[2][2], odone[2], merge, rest;
     uint64_t tfull[2][kInfo], tempty[2][kInfo];
     uint64_t ifull[kItems], iempty[kItems], drain;
@@ -127,12 +129,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&m.kempty[i], 1);
         }
         for (int i = 0; i < C::NV; ++i) {
-            mbar_init(&m.vfull[i], FP8 ? 2 : 1);
+            mbar_init(&m.vfull[i], 2);
             mbar_init(&m.vempty[i], 1);
         }
         for (int i = 0; i < C::NR; ++i) {
-            mbar_init(&m.rfull[i], 1);
-            mbar_init(&m.rempty[i], 2);
+            mbar_init(&m.rfull[0][i], 1);
+            mbar_init(&m.rfull[1][i], 1);
         }
         mbar_init(&m.qfull, 8);
         mbar_init(&m.merge, 4);
@@ -149,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&m.ifull[i], 1);
-            mbar_init(&m.iempty[i], 9 + (FP8 ? 2 : 0));  // softmax warps, the issuing thread, the converting warps
+            mbar_init(&m.iempty[i], 11);  // softmax warps, the issuing thread, the warps of V
         }
         mbar_init(&m.drain, 1);
         m.gave_up = (smem_addr(psm) & 1023u) != 0u;  // nothing runs on a base that the swizzle cannot take
@@ -199,52 +201,57 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint8_t *dst = psm + (wide ? grp : 0) * C::QB;
                 if constexpr (!FP8) {
                     constexpr int N = D / 8;  // 16-byte chunks
-#pragma unroll
-                    for (int c = 0; c < N; ++c) {
-                        if (!wide && (c >= N / 2) != (grp == 1)) continue;
+                    const int c0 = wide || grp == 0 ? 0 : N / 2, c1 = wide || grp == 1 ? N : N / 2;
+#pragma unroll 4
+                    for (int c = c0; c < c1; ++c)
                         *reinterpret_cast<uint4 *>(dst + (c >> 3) * C::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = src[c];
-                    }
                 } else {
-                    uint4 w[D / 8];
+                    // (Loops, not straight code: this runs once a segment, and instructions that are met
+                    // for the first time cost more than the loops' tests.)
                     uint32_t top = 0u;
+#pragma unroll 1
+                    for (int c = 0; c < D / 8; c += 4) {
+                        uint4 w[4];
 #pragma unroll
-                    for (int c = 0; c < D / 8; ++c) {
-                        w[c] = src[c];
-                        const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+                        for (int k = 0; k < 4; ++k) w[k] = src[c + k];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) top = max(top, max((u[k] << 16) & 0x7fff0000u, u[k] & 0x7fff0000u));
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t hi = __vimax3_u16x2(w[k].x & 0x7fff7fffu, w[k].y & 0x7fff7fffu, w[k].z & 0x7fff7fffu);
+                            top = __vimax3_u16x2(top, hi, w[k].w & 0x7fff7fffu);
+                        }
                     }
+                    top = max(top << 16, top & 0x7fff0000u);
                     // the largest element between 128 and 256: hi is within 2^-4 of an element, and their
                     // difference, four bits, is exact in lo down to 2^-9; what is not finite spoils the row
                     const int e = min(126, max(-119, (int)(top >> 23) - 127));
                     float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
                     if (a.sm_scale < 0.f) up = -up;
                     mul = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : a2 * __uint_as_float((uint32_t)(127 + e - 7) << 23);
-                    const int first = wide ? 0 : grp, last = wide ? 1 : grp;
 #pragma unroll 1
-                    for (int part = first; part <= last; ++part) {
-                        uint8_t *to = dst + part * (C::QB / 2);
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint32_t hi[4], lo[4];
 #pragma unroll
-                        for (int c = 0; c < D / 16; ++c) {
-                            uint32_t o[4];
+                        for (int half = 0; half < 2; ++half) {
+                            const uint4 w = src[2 * c + half];
+                            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const uint4 &ww = w[2 * c + (k >> 1)];
-                                const uint32_t x0 = (k & 1) ? ww.z : ww.x, x1 = (k & 1) ? ww.w : ww.y;
-                                const float2 f0 = bf16x2_to_float2(x0), f1 = bf16x2_to_float2(x1);
-                                const float2 y0 = make_float2(f0.x * up, f0.y * up), y1 = make_float2(f1.x * up, f1.y * up);
-                                uint32_t h0 = __nv_cvt_float2_to_fp8x2(y0, __NV_SATFINITE, __NV_E4M3);
-                                uint32_t h1 = __nv_cvt_float2_to_fp8x2(y1, __NV_SATFINITE, __NV_E4M3);
-                                if (part) {
-                                    const float2 z0 = e4m3x2_to_float2((uint16_t)h0), z1 = e4m3x2_to_float2((uint16_t)h1);
-                                    h0 = __nv_cvt_float2_to_fp8x2(make_float2(y0.x - z0.x, y0.y - z0.y), __NV_SATFINITE, __NV_E4M3);
-                                    h1 = __nv_cvt_float2_to_fp8x2(make_float2(y1.x - z1.x, y1.y - z1.y), __NV_SATFINITE, __NV_E4M3);
+                            for (int k = 0; k < 4; k += 2) {
+                                uint32_t h[2], l[2];
+#pragma unroll
+                                for (int n = 0; n < 2; ++n) {
+                                    const float2 y = mul2(bf16x2_to_float2(u[k + n]), make_float2(up, up));
+                                    h[n] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+                                    const float2 z = e4m3x2_to_float2((uint16_t)h[n]);
+                                    l[n] = __nv_cvt_float2_to_fp8x2(make_float2(y.x - z.x, y.y - z.y), __NV_SATFINITE, __NV_E4M3);
                                 }
-                                o[k] = h0 | (h1 << 16);
+                                hi[2 * half + k / 2] = h[0] | (h[1] << 16);
+                                lo[2 * half + k / 2] = l[0] | (l[1] << 16);
                             }
-                            const int at = D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-                            *reinterpret_cast<uint4 *>(to + at) = make_uint4(o[0], o[1], o[2], o[3]);
                         }
+                        const int at = D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+                        // both groups work on the same rows, or each on its own
+                        if (wide || grp == 0) *reinterpret_cast<uint4 *>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        if (wide || grp == 1) *reinterpret_cast<uint4 *>(dst + C::QB / 2 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                 }
             }
@@ -524,13 +531,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp == 9) {
-        // ---------------------- segments, page ids, K and V ----------------------
+        // --------------------------- segments, scales and K ---------------------------
         reg_share_less<88>();
         const uint64_t pol = l2_policy_evict_normal();
-        const int U = a.head->U, W = a.head->W;
-        const int c = blockIdx.x;
-        int x = c < W ? (int)(((long long)c * U + W - 1) / W) : 0;
-        const int x1 = c < W ? (int)(((long long)(c + 1) * U + W - 1) / W) : 0;
+        const PrefixRange range = a.range[blockIdx.x];
+        int x = range.x0, k = range.seg;
+        const int x1 = range.x1;
         uint32_t pos = 0, info[2] = {0, 0};
         int i = 0;
         bool ok = true;
@@ -544,32 +550,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++i;
         };
-        // the last segment whose first tile is at most x, 32 candidates a step
-        int k = 0;
-        if (x < x1) {
-            int lo = 0, hi = a.seg0[a.pre.count];  // seg[lo].tile0 <= x; seg[hi] is past it
-            while (hi - lo > 1) {
-                const int width = (hi - lo + 31) / 32, at = lo + lane * width;
-                const bool below = at < hi && a.seg[at].tile0 <= x;
-                const int n = __popc(__ballot_sync(0xffffffffu, below));  // of ascending numbers: the first n
-                lo += (n - 1) * width;
-                hi = min(hi, lo + width);
-            }
-            k = lo;
-        }
         while (ok && x < x1) {
             const PrefixSeg sg = a.seg[k];
             const int end = min(x1, sg.tile0 + sg.ntiles);
             if (end <= x) {  // an empty segment
-                ++k;
-                continue;
-            }
-            // a prefix that failed a check is not read: its requests are flagged
-            const long long words = (long long)sg.p * a.Hkv * a.pre.htiles;
-            uint32_t bits = 0u;
-            for (int w = lane; w < a.Hkv * a.pre.htiles; w += 32) bits |= a.pre_bits[words + w];
-            if (__any_sync(0xffffffffu, bits != 0u)) {
-                x = end;
                 ++k;
                 continue;
             }
@@ -581,28 +565,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             it.t0 = x - sg.tile0;
             it.nt = end - x;
             it.len = sg.len;
-            it.base = sg.base + (c - (int)((long long)sg.tile0 * W / U)) * rows8(sg.rows);
-            if constexpr (FP8) {
-                float top = 0.f;
+            it.base = sg.base + ((int)blockIdx.x - sg.first) * rows8(sg.rows);
+            x = end;
+            ++k;
+            const bool wide = it.rows > 128;
+            // 32 pages (four tiles) a round, one a lane; the next round's ids are on their way
+            const int32_t *table = a.pre.block_tables + (long long)it.p * a.pre.bt_sb + (long long)it.h * a.pre.bt_sh;
+            const int npages = min((it.len + kPage - 1) / kPage, (it.t0 + it.nt) * kPages);
+            auto fetch = [&](int t) {
+                const int page = (it.t0 + t) * kPages + lane;
+                return page < npages ? table[page] : -1;
+            };
+            int next_id = fetch(0);
+            // a prefix that failed a check is not read: its requests are flagged
+            const long long words = (long long)sg.p * a.Hkv * a.pre.htiles;
+            uint32_t bits = 0u;
+            float top = 0.f;
+            for (int w = lane; w < a.Hkv * a.pre.htiles; w += 32) bits |= a.pre_bits[words + w];
+            if constexpr (FP8)
                 for (int w = lane; w < a.pre.htiles; w += 32) top = fmaxf(top, a.pre_vmax[words + (long long)sg.h * a.pre.htiles + w]);
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            if (__any_sync(0xffffffffu, bits != 0u)) continue;
+            if constexpr (FP8) {
+                top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // not negative: ordered as numbers
                 // scales over a power of two above the largest, and 2^7: f16's subnormals begin 2^-31 below
                 const int e = min(120, max(-112, (int)(__float_as_uint(top) >> 23) - 126));
                 it.vinv = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
                 it.vback = __uint_as_float((uint32_t)(127 + e - 7) << 23);
             }
             put(it);
-            const bool wide = it.rows > 128;
-            const long long row = (long long)it.p * a.pre.bt_sb + (long long)it.h * a.pre.bt_sh;
-            const int npages = (it.len + kPage - 1) / kPage;
-            // 32 pages (four tiles) a round, one a lane; the next round's ids are on their way
-            int next_id = -1;
-            auto fetch = [&](int t) {
-                const int page = (it.t0 + t) * kPages + lane;
-                next_id = page < npages && t + (lane >> 3) < it.nt ? a.pre.block_tables[row + page] : -1;
-            };
-            fetch(0);
             for (int t = 0; ok && t < it.nt; t += 4) {
                 const int id = next_id;
                 const bool there = id >= 0 && id < a.num_pages;
@@ -612,54 +602,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ks = a.k_scale[unit];
                     vs = a.v_scale[unit];
                 }
-                if (t + 4 < it.nt) fetch(t + 4);
-                for (int q = 0; ok && q < 4 && t + q < it.nt; ++q, ++pos) {
+                if (t + 4 < it.nt) next_id = fetch(t + 4);
+                const int live = min(4, it.nt - t);
+                // K of the tile that follows is on its way before the scales of this one are waited for
+                for (int q = 0; ok && q < live; ++q, ++pos) {
                     const int copy = lane / kPages;  // of a page
                     const int u = __shfl_sync(0xffffffffu, unit, q * kPages + lane % kPages);
                     const bool mine = copy < C::CPP && u >= 0;
                     const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * C::COPYB;
-                    const int off = copy * C::HALF + lane % kPages * C::COPYB;
-                    const uint32_t kslot = pos % C::NK;
-                    ok = __all_sync(0xffffffffu, bar_wait(&m.kempty[kslot], ((pos / C::NK) & 1) ^ 1, gave_up, tries));
+                    const uint32_t slot = pos % C::NK;
+                    ok = __all_sync(0xffffffffu, bar_wait(&m.kempty[slot], ((pos / C::NK) & 1) ^ 1, gave_up, tries));
                     if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&m.kfull[kslot], bytes);
+                    if (lane == 0) mbar_arrive_expect_tx(&m.kfull[slot], bytes);
                     __syncwarp();
-                    if (mine) tma_box3(psm + C::OFF_K + kslot * C::KB + off, &mapk, copy * 64, 0, u, &m.kfull[kslot], pol);
+                    if (mine)
+                        tma_box3(psm + C::OFF_K + slot * C::KB + copy * C::HALF + lane % kPages * C::COPYB, &mapk, copy * 64, 0, u,
+                                 &m.kfull[slot], pol);
                     if constexpr (FP8) {
 #pragma unroll 1
                         for (int g = 0; g < 2; ++g) {
-                            if (!wide && ((t + q) & 1) != g) continue;
-                            const uint32_t slot = info[g] % kInfo;
-                            ok = ok && bar_wait(&m.tempty[g][slot], ((info[g] / kInfo) & 1) ^ 1, gave_up, tries);
+                            if (!wide && (q & 1) != g) continue;
+                            const uint32_t at = info[g] % kInfo;
+                            ok = ok && bar_wait(&m.tempty[g][at], ((info[g] / kInfo) & 1) ^ 1, gave_up, tries);
                             ok = __all_sync(0xffffffffu, ok);
                             if (!ok) break;
                             if (lane / kPages == q) {
-                                m.info[g][slot].ks[lane % kPages] = ks;
-                                m.info[g][slot].vs[lane % kPages] = vs;
+                                m.info[g][at].ks[lane % kPages] = ks;
+                                m.info[g][at].vs[lane % kPages] = vs;
                             }
                             __syncwarp();
-                            if (lane == 0) bar_arrive(&m.tfull[g][slot]);
+                            if (lane == 0) bar_arrive(&m.tfull[g][at]);
                             ++info[g];
                         }
-                        if (!ok) break;
-                        const uint32_t slot = pos % (C::NR > 0 ? C::NR : 1);
-                        ok = __all_sync(0xffffffffu, bar_wait(&m.rempty[slot], ((pos / (C::NR > 0 ? C::NR : 1)) & 1) ^ 1, gave_up, tries));
-                        if (!ok) break;
-                        if (lane == 0) mbar_arrive_expect_tx(&m.rfull[slot], bytes);
-                        __syncwarp();
-                        if (mine) tma_box3(psm + C::OFF_R + slot * C::KB + off, &mapv, 0, 0, u, &m.rfull[slot], pol);
-                    } else {
-                        const uint32_t slot = pos % C::NV;
-                        ok = __all_sync(0xffffffffu, bar_wait(&m.vempty[slot], ((pos / C::NV) & 1) ^ 1, gave_up, tries));
-                        if (!ok) break;
-                        if (lane == 0) mbar_arrive_expect_tx(&m.vfull[slot], bytes);
-                        __syncwarp();
-                        if (mine) tma_box3(psm + C::OFF_V + slot * C::VB + off, &mapv, copy * 64, 0, u, &m.vfull[slot], pol);
                     }
                 }
             }
-            x = end;
-            ++k;
         }
         if (ok) {
             Item it{};
@@ -672,49 +649,101 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else {
-        // ------------------------------ V to f16 ------------------------------
+        // ------------------------------------ V ------------------------------------
         reg_share_less<88>();
-        if constexpr (FP8) {
-            const int j = (warp - 10) * 32 + lane;
-            uint32_t pos = 0;
-            bool ok = true;
-            for (int i = 0; ok && __all_sync(0xffffffffu, item_ready(i)); ++i) {
-                const int nt = m.item[i % kItems].nt, t0 = m.item[i % kItems].t0, len = m.item[i % kItems].len;
+        const uint64_t pol = l2_policy_evict_normal();
+        const int half = warp - 10;  // pages 4 half .. 4 half + 3 of every tile
+        uint32_t pos = 0;
+        bool ok = true;
+        for (int i = 0; ok && __all_sync(0xffffffffu, item_ready(i)); ++i) {
+            const Item it = m.item[i % kItems];
+            __syncwarp();
+            if (lane == 0) bar_arrive(&m.iempty[i % kItems]);
+            const int32_t *table = a.pre.block_tables + (long long)it.p * a.pre.bt_sb + (long long)it.h * a.pre.bt_sh;
+            const int npages = min((it.len + kPage - 1) / kPage, (it.t0 + it.nt) * kPages);
+            // the units of this half of eight tiles, four a tile; the next eight tiles' ids are on their way
+            auto fetch = [&](int t) {
+                const int page = (it.t0 + t + lane / 4) * kPages + half * 4 + lane % 4;
+                return page < npages ? table[page] : -1;
+            };
+            int id = fetch(0), next_id = it.nt > 8 ? fetch(8) : -1, batch = 0;
+            // copies of tile t (in order): of the item's tile number `at`, `full` counting their bytes
+            auto load = [&](int t, uint8_t *dst, uint64_t *full) {
+                if (t - batch == 8) {
+                    batch += 8;
+                    id = next_id;
+                    next_id = t + 8 < it.nt ? fetch(t + 8) : -1;
+                }
+                const int copy = lane / 4;  // of a page
+                const int u = __shfl_sync(0xffffffffu, id, (t - batch) * 4 + lane % 4);
+                const bool mine = copy < C::CPP && u >= 0 && u < a.num_pages;
+                const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * C::COPYB;
+                if (lane == 0) mbar_arrive_expect_tx(full, bytes);
                 __syncwarp();
-                if (lane == 0) bar_arrive(&m.iempty[i % kItems]);
-                for (int t = 0; ok && t < nt; ++t, ++pos) {
+                if (mine)
+                    tma_box3(dst + copy * C::HALF + (half * 4 + lane % 4) * C::COPYB, &mapv, copy * 64, 0, u * a.Hkv + it.h, full, pol);
+            };
+            if constexpr (!FP8) {
+                for (int t = 0; ok && t < it.nt; ++t, ++pos) {
+                    const uint32_t slot = pos % C::NV;
+                    ok = __all_sync(0xffffffffu, bar_wait(&m.vempty[slot], ((pos / C::NV) & 1) ^ 1, gave_up, tries));
+                    if (ok) load(t, psm + C::OFF_V + slot * C::VB, &m.vfull[slot]);
+                }
+            } else {
+                // this half's place of a tile as loaded is written and read by this warp alone
+                int ahead = 0;  // tiles whose copies have been issued
+                for (; ahead < min(C::NR, it.nt); ++ahead) {
+                    const uint32_t slot = (pos + ahead) % C::NR;
+                    load(ahead, psm + C::OFF_R + slot * C::KB, &m.rfull[half][slot]);
+                }
+                for (int t = 0; ok && t < it.nt; ++t, ++pos) {
                     const uint32_t rs = pos % C::NR, vslot = pos % C::NV;
-                    ok = bar_wait(&m.rfull[rs], (pos / C::NR) & 1, gave_up, tries) &&
+                    ok = bar_wait(&m.rfull[half][rs], (pos / C::NR) & 1, gave_up, tries) &&
                          bar_wait(&m.vempty[vslot], ((pos / C::NV) & 1) ^ 1, gave_up, tries);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    const int seen = len - (t0 + t) * kPrefixTile;
+                    const int seen = it.len - (it.t0 + t) * kPrefixTile;
                     const uint8_t *raw = psm + C::OFF_R + rs * C::KB;
                     uint8_t *dst = psm + C::OFF_V + vslot * C::VB;
-                    constexpr int CH = D / 16, RP = 64 / CH;  // chunks a row, rows at a time
-                    const int ch = j % CH, r0 = j / CH, flip = ch >> 2;
-#pragma unroll 4
-                    for (int p = 0; p < kPrefixTile / RP; ++p) {
-                        const int r = p * RP + r0;
-                        const int at = D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
-                        uint4 w = *reinterpret_cast<const uint4 *>(raw + at);
-                        if (r >= seen) w = make_uint4(0u, 0u, 0u, 0u);  // whatever follows the last token
-                        const uint2 h0 = e4m3x4_to_half4(w.x), h1 = e4m3x4_to_half4(w.y), h2 = e4m3x4_to_half4(w.z), h3 = e4m3x4_to_half4(w.w);
-                        uint8_t *to = dst + (ch >> 2) * C::HALF + r * 128;
-                        const int d0 = 2 * (ch & 3);
-                        const uint4 lo = make_uint4(h0.x, h0.y, h1.x, h1.y), hi = make_uint4(h2.x, h2.y, h3.x, h3.y);
-                        // the two halves' lanes store their chunks in opposite order, on banks of their own
-                        *reinterpret_cast<uint4 *>(to + (((d0 + flip) ^ (r & 7)) << 4)) = flip ? hi : lo;
-                        *reinterpret_cast<uint4 *>(to + (((d0 + 1 - flip) ^ (r & 7)) << 4)) = flip ? lo : hi;
+                    constexpr int CH = D / 16, RP = 32 / CH;  // chunks a row, rows at a time
+                    const int ch = lane % CH, r0 = half * 64 + lane / CH, flip = ch >> 2;
+                    constexpr int AHEAD = 8;  // loads on their way together
+#pragma unroll 1
+                    for (int p0 = 0; p0 < 64 / RP; p0 += AHEAD) {
+                        uint4 w[AHEAD];
+#pragma unroll
+                        for (int p = 0; p < AHEAD; ++p) {
+                            const int r = (p0 + p) * RP + r0;
+                            const int at = D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
+                            w[p] = *reinterpret_cast<const uint4 *>(raw + at);
+                        }
+#pragma unroll
+                        for (int p = 0; p < AHEAD; ++p) {
+                            const int r = (p0 + p) * RP + r0;
+                            if (r >= seen) w[p] = make_uint4(0u, 0u, 0u, 0u);  // whatever follows the last token
+                            const uint2 h0 = e4m3x4_to_half4(w[p].x), h1 = e4m3x4_to_half4(w[p].y);
+                            const uint2 h2 = e4m3x4_to_half4(w[p].z), h3 = e4m3x4_to_half4(w[p].w);
+                            uint8_t *to = dst + (ch >> 2) * C::HALF + r * 128;
+                            const int d0 = 2 * (ch & 3);
+                            const uint4 lo = make_uint4(h0.x, h0.y, h1.x, h1.y), hi = make_uint4(h2.x, h2.y, h3.x, h3.y);
+                            // the two halves' lanes store their chunks in opposite order, on banks of their own
+                            *reinterpret_cast<uint4 *>(to + (((d0 + flip) ^ (r & 7)) << 4)) = flip ? hi : lo;
+                            *reinterpret_cast<uint4 *>(to + (((d0 + 1 - flip) ^ (r & 7)) << 4)) = flip ? lo : hi;
+                        }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) {
-                        bar_arrive(&m.vfull[vslot]);
-                        bar_arrive(&m.rempty[rs]);
+                    if (lane == 0) bar_arrive(&m.vfull[vslot]);
+                    if (ahead < it.nt) {
+                        load(ahead, psm + C::OFF_R + rs * C::KB, &m.rfull[half][rs]);
+                        ++ahead;
                     }
                 }
             }
+        }
+        if (*gave_up) {  // copies in flight are left time to land
+            const unsigned long long t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < kWaitLimitNs) {}
         }
         __syncwarp();
     }

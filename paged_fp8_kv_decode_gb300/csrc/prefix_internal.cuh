@@ -30,7 +30,6 @@ struct PrefixTables {
 // [ceil(c U / W), ceil((c + 1) U / W)) of all U; each leaves a partial result for every segment it
 // touches.
 struct PrefixHead {
-    int U, W;
     uint32_t timeout;  // PFKV_FLAG_DEVICE_TIMEOUT once a wait has given up
 };
 struct PrefixSeg {
@@ -38,8 +37,14 @@ struct PrefixSeg {
     int tile0, ntiles;  // its first tile's number, and how many
     int base;           // first row of its partial results: rows8 for each CTA that touches it
     int len;            // tokens
+    int first, ctas;    // the first CTA that touches it, and how many do
+    int pad[2];
 };
-static_assert(sizeof(PrefixSeg) == 32, "two 16-byte loads");
+static_assert(sizeof(PrefixSeg) == 48, "three 16-byte loads");
+// A CTA's tiles x0 .. x1 - 1, and the segment of the first.
+struct PrefixRange {
+    int x0, x1, seg, pad;
+};
 
 __host__ __device__ inline int rows8(int rows) { return (rows + 7) & ~7; }
 
@@ -60,6 +65,7 @@ struct PrefixArgs {
     int *pos, *members;             // [B] position among its prefix's requests (-1: none); requests by prefix
     int *mstart, *seg0;             // [prefixes + 1] first entry of members; first segment
     PrefixSeg *seg;
+    PrefixRange *range;             // [ctas]
     float *po, *plse;               // partial results: [D / 4][rows8][4] and [rows8] a (segment, CTA)
     __nv_bfloat16 *packed_q;        // queries as the split kernel takes them, or null: they are so already
     int ctas;                       // of the attention kernel
