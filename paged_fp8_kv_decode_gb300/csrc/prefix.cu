@@ -18,29 +18,29 @@ namespace {
 // validate_kernel, with the tags as far as they are tracked, or pack the queries.  It waits for
 // its predecessor before it lets the next kernel start, so the call's inputs are final then.
 // --------------------------------------------------------------------------
-// Exclusive sum over the block of one number a thread; the total in *total.  Ends synchronised.
-__device__ __forceinline__ int block_sum_before(int v, int *part, int *total) {
-    const int tid = threadIdx.x;
-    __syncthreads();
-    part[tid] = v;
-    __syncthreads();
-    if (tid < 32) {
-        int carry = 0;
-        for (int at = 0; at < kValThreads; at += 32) {
-            const int x0 = part[at + tid];
-            int x = x0;
+// Exclusive sums over the block of two numbers a thread; the totals in total.  Ends synchronised.
+struct Two {
+    int x, y;
+};
+__device__ __forceinline__ Two block_sums_before(Two v, Two *part, Two *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int W = kValThreads / 32;
+    Two s = v;
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, off);
-                if (tid >= off) x += y;
-            }
-            part[at + tid] = carry + x - x0;
-            carry += __shfl_sync(0xffffffffu, x, 31);
+    for (int off = 1; off < 32; off <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, s.x, off), y = __shfl_up_sync(0xffffffffu, s.y, off);
+        if (lane >= off) {
+            s.x += x;
+            s.y += y;
         }
-        if (tid == 0) *total = carry;
     }
     __syncthreads();
-    return part[tid];
+    if (lane == 31) part[warp] = s;
+    __syncthreads();
+    const Two p = lane < W ? part[lane] : Two{0, 0};
+    const Two before{__reduce_add_sync(0xffffffffu, lane < warp ? p.x : 0), __reduce_add_sync(0xffffffffu, lane < warp ? p.y : 0)};
+    *total = Two{__reduce_add_sync(0xffffffffu, p.x), __reduce_add_sync(0xffffffffu, p.y)};
+    return Two{before.x + s.x - v.x, before.y + s.y - v.y};
 }
 
 // Tokens of row i for head h; -1 where a bound does not hold.
@@ -50,13 +50,21 @@ __device__ __forceinline__ int table_len(const PrefixTables &t, int i, int h) {
 }
 
 constexpr int kPlanChunk = 2048;
+constexpr int kPrefixFew = 512, kSegFew = 1024;  // what shared memory has room for
 
 __device__ void plan_segments(const PrefixArgs &a) {
     __shared__ int count[PFKV_PREFIX_MAX];  // requests of a prefix
-    __shared__ int of[kPlanChunk], part[kValThreads], total;
+    __shared__ int of[kPlanChunk], first_member[kPrefixFew], first_seg[kPrefixFew], seg_tile[kSegFew];
+    __shared__ Two part[kValThreads / 32];
+    Two total;
     const int tid = threadIdx.x, lane = tid & 31, NP = a.pre.count;
     if (tid == 0) a.head->timeout = 0u;
     for (int p = tid; p < NP; p += kValThreads) count[p] = 0;
+    // lengths are on their way while requests are counted (one a thread: the usual case)
+    const int pairs = NP * a.Hkv, per = (pairs + kValThreads - 1) / kValThreads;
+    const int x0 = min(pairs, tid * per), x1 = min(pairs, x0 + per);
+    const auto len_of = [&](int x) { return max(0, table_len(a.pre, x / a.Hkv, x % a.Hkv)); };
+    const int len0 = x0 < x1 ? len_of(x0) : 0;
     // positions, in the order of the batch: one warp takes 32 requests at a time
     for (int b0 = 0; b0 < a.B; b0 += kPlanChunk) {
         const int n = min(kPlanChunk, a.B - b0);
@@ -73,58 +81,66 @@ __device__ void plan_segments(const PrefixArgs &a) {
                 __syncwarp();
                 if (valid && rank == 0) count[p] = before + __popc(same);
                 __syncwarp();
-                if (i < n) a.pos[b0 + i] = valid ? before + rank : -1;
+                if (i < n) {
+                    of[i] = valid ? before + rank : -1;
+                    a.pos[b0 + i] = of[i];
+                }
             }
         }
     }
     __syncthreads();
     // first members and first segments
     const auto blocks = [&](int p) { return (int)(((long long)count[p] * a.kq * a.G + kPrefixBlock - 1) / kPrefixBlock); };
+    int segs = 0;
+    const bool few = NP <= kPrefixFew && a.B <= kPlanChunk;  // all in shared memory
     {
-        const int per = (NP + kValThreads - 1) / kValThreads, p0 = min(NP, tid * per), p1 = min(NP, p0 + per);
-        int members = 0, segs = 0;
+        const int each = (NP + kValThreads - 1) / kValThreads, p0 = min(NP, tid * each), p1 = min(NP, p0 + each);
+        Two v{0, 0};
         for (int p = p0; p < p1; ++p) {
-            members += count[p];
-            segs += blocks(p) * a.Hkv;
+            v.x += count[p];
+            v.y += blocks(p) * a.Hkv;
         }
-        members = block_sum_before(members, part, &total);
-        if (tid == 0) a.mstart[NP] = total;
-        segs = block_sum_before(segs, part, &total);
-        if (tid == 0) a.seg0[NP] = total;
+        v = block_sums_before(v, part, &total);
+        segs = total.y;
+        if (tid == 0) {
+            a.mstart[NP] = total.x;
+            a.seg0[NP] = total.y;
+        }
         for (int p = p0; p < p1; ++p) {
-            a.mstart[p] = members;
-            a.seg0[p] = segs;
-            members += count[p];
-            segs += blocks(p) * a.Hkv;
+            a.mstart[p] = v.x;
+            a.seg0[p] = v.y;
+            if (few) {
+                first_member[p] = v.x;
+                first_seg[p] = v.y;
+            }
+            v.x += count[p];
+            v.y += blocks(p) * a.Hkv;
         }
     }
     __syncthreads();
     for (int b = tid; b < a.B; b += kValThreads) {
-        const int p = a.prefix_of[b], at = a.pos[b];
-        if (at >= 0) a.members[a.mstart[p] + at] = b;
+        const int at = few ? of[b] : a.pos[b];
+        if (at < 0) continue;
+        const int p = a.prefix_of[b];
+        a.members[(few ? first_member[p] : a.mstart[p]) + at] = b;
     }
-    // tiles, and rows of partial results
-    const int pairs = NP * a.Hkv, per = (pairs + kValThreads - 1) / kValThreads;
-    const int x0 = min(pairs, tid * per), x1 = min(pairs, x0 + per);
-    const auto tiles = [&](int x) {
-        const int p = x / a.Hkv;
-        return (max(0, table_len(a.pre, p, x - p * a.Hkv)) + kPrefixTile - 1) / kPrefixTile;
-    };
-    int mine = 0;
-    for (int x = x0; x < x1; ++x) mine += blocks(x / a.Hkv) * tiles(x);
-    int tile = block_sum_before(mine, part, &total);
-    const int U = total, W = min(a.ctas, U), tile_first = tile;
+    // tiles, then rows of partial results
+    Two v{0, 0};
+    for (int x = x0; x < x1; ++x)
+        v.x += blocks(x / a.Hkv) * (((x == x0 ? len0 : len_of(x)) + kPrefixTile - 1) / kPrefixTile);
+    const int tile_first = block_sums_before(v, part, &total).x;
+    const int U = total.x, W = min(a.ctas, U);
     // CTAs without work; the others' ranges are written with the segment that holds their first tile
     for (int c = W + tid; c < a.ctas; c += kValThreads) a.range[c] = PrefixRange{0, 0, 0, 0};
     for (int pass = 0, base = 0; pass < 2; ++pass) {
-        int rows = 0;
-        tile = tile_first;
+        int rows = 0, tile = tile_first;
         for (int x = x0; x < x1; ++x) {
             const int p = x / a.Hkv, h = x - p * a.Hkv, nb = blocks(p);
             if (nb == 0) continue;
-            const int n = tiles(x), R = (int)((long long)count[p] * a.kq * a.G), len = max(0, table_len(a.pre, p, h));
+            const int len = x == x0 ? len0 : len_of(x), n = (len + kPrefixTile - 1) / kPrefixTile;
+            const int R = (int)((long long)count[p] * a.kq * a.G);
             for (int rb = 0; rb < nb; ++rb) {
-                PrefixSeg s;
+                PrefixSeg s{};
                 s.p = p;
                 s.h = h;
                 s.row0 = rb * kPrefixBlock;
@@ -133,24 +149,30 @@ __device__ void plan_segments(const PrefixArgs &a) {
                 s.ntiles = n;
                 s.base = base + rows;
                 s.len = len;
-                s.pad[0] = s.pad[1] = 0;
                 s.first = n > 0 ? pers_worker_of(tile, U, W) : 0;
                 s.ctas = n > 0 ? pers_worker_of(tile + n - 1, U, W) - s.first + 1 : 0;
                 if (pass) {
-                    const int k = a.seg0[p] + h * nb + rb;
+                    const int k = (few ? first_seg[p] : a.seg0[p]) + h * nb + rb;
                     a.seg[k] = s;
-                    // CTAs whose first tile is in this segment
-                    for (int c = s.first; c < s.first + s.ctas; ++c) {
-                        const int t0 = (int)(((long long)c * U + W - 1) / W);
-                        if (t0 >= tile && t0 < tile + n)
-                            a.range[c] = PrefixRange{t0, (int)(((long long)(c + 1) * U + W - 1) / W), k, 0};
-                    }
+                    if (k < kSegFew) seg_tile[k] = tile;
                 }
                 rows += rows8(s.rows) * s.ctas;
                 tile += n;
             }
         }
-        if (pass == 0) base = block_sum_before(rows, part, &total);
+        if (pass == 0) base = block_sums_before(Two{rows, 0}, part, &total).x;
+    }
+    __syncthreads();
+    // the segment of every CTA's first tile
+    for (int c = tid; c < W; c += kValThreads) {
+        const int t0 = (int)(((long long)c * U + W - 1) / W);
+        int lo = 0, hi = segs;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if ((segs <= kSegFew ? seg_tile[mid] : a.seg[mid].tile0) <= t0) lo = mid;
+            else hi = mid;
+        }
+        a.range[c] = PrefixRange{t0, (int)(((long long)(c + 1) * U + W - 1) / W), lo, 0};
     }
 }
 

@@ -74,7 +74,12 @@ struct Misc {
     uint64_t ifull[kItems], iempty[kItems], drain;
     Item item[kItems];
     Info info[2][kInfo];
-    float ref1[128], sum1[128];
+    union {  // the rows' factors at a segment's start; group 1's softmax at its end
+        float qmul[kPrefixBlock];
+        struct {
+            float ref1[128], sum1[128];
+        };
+    };
     uint32_t tmem, gave_up;
 };
 template <int D, bool FP8>
@@ -190,74 +195,80 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool live = row < it.rows;
             const bool warp_live = (row & ~31) < it.rows;
             bool ok = true;
-            // this row's query
-            float mul = a2;
-            if (live) {
-                const int R = it.row0 + row, per = a.kq * a.G, member = R / per, tg = R - member * per;
-                const int t = tg / a.G, g = tg - t * a.G;
-                const int b = a.members[a.mstart[it.p] + member];
-                const uint4 *src = reinterpret_cast<const uint4 *>(a.q.p + (long long)b * a.q.sb + (long long)t * a.q.st +
-                                                                   (long long)(it.h * a.G + g) * a.q.sh);
-                uint8_t *dst = psm + (wide ? grp : 0) * C::QB;
-                if constexpr (!FP8) {
-                    constexpr int N = D / 8;  // 16-byte chunks
-                    const int c0 = wide || grp == 0 ? 0 : N / 2, c1 = wide || grp == 1 ? N : N / 2;
-#pragma unroll 4
-                    for (int c = c0; c < c1; ++c)
-                        *reinterpret_cast<uint4 *>(dst + (c >> 3) * C::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = src[c];
-                } else {
-                    // (Loops, not straight code: this runs once a segment, and instructions that are met
-                    // for the first time cost more than the loops' tests.)
-                    uint32_t top = 0u;
+            // The queries: a warp takes 32 rows, or 16 where both groups have the same; LPR lanes read a
+            // row, 16 bytes each.
+            {
+                constexpr int LPR = D / 8, RPI = 32 / LPR;
+                const int rw = wide ? 32 : 16, first = warp * rw;
+                const __nv_bfloat16 *mine = nullptr;  // row `lane`
+                if (lane < rw && first + lane < it.rows) {
+                    const int R = it.row0 + first + lane, per = a.kq * a.G, member = R / per, tg = R - member * per;
+                    const int t = tg / a.G, g = tg - t * a.G;
+                    const int b = a.members[a.mstart[it.p] + member];
+                    mine = a.q.p + (long long)b * a.q.sb + (long long)t * a.q.st + (long long)(it.h * a.G + g) * a.q.sh;
+                }
+                const int c = lane % LPR;
+                uint8_t *const dst = psm + (wide ? grp : 0) * C::QB;
 #pragma unroll 1
-                    for (int c = 0; c < D / 8; c += 4) {
-                        uint4 w[4];
+                for (int n0 = 0; n0 < rw; n0 += 4 * RPI) {
+                    uint4 w[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) w[k] = src[c + k];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t hi = __vimax3_u16x2(w[k].x & 0x7fff7fffu, w[k].y & 0x7fff7fffu, w[k].z & 0x7fff7fffu);
-                            top = __vimax3_u16x2(top, hi, w[k].w & 0x7fff7fffu);
-                        }
+                    for (int n = 0; n < 4; ++n) {
+                        const uint4 *src = reinterpret_cast<const uint4 *>(
+                            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), (n0 + n * RPI + lane / LPR) & 31));
+                        w[n] = src ? src[c] : make_uint4(0u, 0u, 0u, 0u);
                     }
-                    top = max(top << 16, top & 0x7fff0000u);
-                    // the largest element between 128 and 256: hi is within 2^-4 of an element, and their
-                    // difference, four bits, is exact in lo down to 2^-9; what is not finite spoils the row
-                    const int e = min(126, max(-119, (int)(top >> 23) - 127));
-                    float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
-                    if (a.sm_scale < 0.f) up = -up;
-                    mul = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : a2 * __uint_as_float((uint32_t)(127 + e - 7) << 23);
-#pragma unroll 1
-                    for (int c = 0; c < D / 16; ++c) {
-                        uint32_t hi[4], lo[4];
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const uint4 w = src[2 * c + half];
-                            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                    for (int n = 0; n < 4; ++n) {
+                        const int at = first + n0 + n * RPI + lane / LPR, q = at & 127;  // in the block, and in its tile
+                        if constexpr (!FP8) {
+                            *reinterpret_cast<uint4 *>(dst + (c >> 3) * C::HALF + q * 128 + (((c & 7) ^ (q & 7)) << 4)) = w[n];
+                        } else {
+                            const uint32_t u[4] = {w[n].x, w[n].y, w[n].z, w[n].w};
+                            uint32_t top = __vimax3_u16x2(u[0] & 0x7fff7fffu, u[1] & 0x7fff7fffu, u[2] & 0x7fff7fffu);
+                            top = __vimax3_u16x2(top, u[3] & 0x7fff7fffu, 0u);
+                            top = max(top << 16, top & 0x7fff0000u);
 #pragma unroll
-                            for (int k = 0; k < 4; k += 2) {
-                                uint32_t h[2], l[2];
+                            for (int off = LPR / 2; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+                            // the largest element between 128 and 256: hi is within 2^-4 of an element, and their
+                            // difference, four bits, is exact in lo down to 2^-9; what is not finite spoils the row
+                            const int e = min(126, max(-119, (int)(top >> 23) - 127));
+                            float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+                            if (a.sm_scale < 0.f) up = -up;
+                            if (c == 0)
+                                m.qmul[at] = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu)
+                                                                : a2 * __uint_as_float((uint32_t)(127 + e - 7) << 23);
+                            uint32_t hi[2], lo[2];
 #pragma unroll
-                                for (int n = 0; n < 2; ++n) {
-                                    const float2 y = mul2(bf16x2_to_float2(u[k + n]), make_float2(up, up));
-                                    h[n] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
-                                    const float2 z = e4m3x2_to_float2((uint16_t)h[n]);
-                                    l[n] = __nv_cvt_float2_to_fp8x2(make_float2(y.x - z.x, y.y - z.y), __NV_SATFINITE, __NV_E4M3);
+                            for (int k = 0; k < 2; ++k) {
+                                uint32_t hh[2], ll[2];
+#pragma unroll
+                                for (int x = 0; x < 2; ++x) {
+                                    const float2 y = mul2(bf16x2_to_float2(u[2 * k + x]), make_float2(up, up));
+                                    hh[x] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+                                    const float2 z = e4m3x2_to_float2((uint16_t)hh[x]);
+                                    ll[x] = __nv_cvt_float2_to_fp8x2(make_float2(y.x - z.x, y.y - z.y), __NV_SATFINITE, __NV_E4M3);
                                 }
-                                hi[2 * half + k / 2] = h[0] | (h[1] << 16);
-                                lo[2 * half + k / 2] = l[0] | (l[1] << 16);
+                                hi[k] = hh[0] | (hh[1] << 16);
+                                lo[k] = ll[0] | (ll[1] << 16);
                             }
+                            const int cc = c >> 1;  // 16-byte chunk of e4m3
+                            const int to = (D == 128 ? q * 128 + ((cc ^ (q & 7)) << 4) : q * 64 + ((cc ^ ((q >> 1) & 3)) << 4)) + (c & 1) * 8;
+                            *reinterpret_cast<uint2 *>(dst + to) = make_uint2(hi[0], hi[1]);
+                            *reinterpret_cast<uint2 *>(dst + C::QB / 2 + to) = make_uint2(lo[0], lo[1]);
                         }
-                        const int at = D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-                        // both groups work on the same rows, or each on its own
-                        if (wide || grp == 0) *reinterpret_cast<uint4 *>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        if (wide || grp == 1) *reinterpret_cast<uint4 *>(dst + C::QB / 2 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                 }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) bar_arrive(&m.qfull);
+            float mul = a2;
+            if constexpr (FP8) {
+                ok = bar_wait(&m.qfull, i & 1, gave_up, tries);
+                mul = live ? m.qmul[row] : a2;
+            }
+            const float vinv = it.vinv;
 
             float ref = kMinusInf, sum = 0.f;
             for (int j = 0; j < steps; ++j, ++done) {
@@ -354,6 +365,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // while the second half is computed
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
+                        float vf[4];  // V scales (once in registers: a load in every pair took 2,000 cycles a tile)
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) vf[p] = FP8 && (4 * half + p) * kPage < seen ? inf.vs[4 * half + p] * vinv : 0.f;
 #pragma unroll
                         for (int g = 2 * half; g < 2 * half + 2; ++g) {
                             float w[16];  // packed pairs
@@ -364,10 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 float2 y = fma2(make_float2(x[g][e], x[g][e + 1]), make_float2(fp, fp), base2);
                                 y = make_float2(fast_exp2(y.x), fast_exp2(y.y));
                                 sums[(e >> 1) & 3] = add2(sums[(e >> 1) & 3], y);
-                                if constexpr (FP8) {
-                                    const float z = p * kPage < seen ? inf.vs[p] * it.vinv : 0.f;
-                                    y = mul2(y, make_float2(z, z));
-                                }
+                                if constexpr (FP8) y = mul2(y, make_float2(vf[p - 4 * half], vf[p - 4 * half]));
                                 w[e >> 1] = __uint_as_float(pack16(y.x, y.y, !FP8));
                             }
                             tmem_st16(cs + g * 16, w);
@@ -400,13 +411,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             float4 *part = reinterpret_cast<float4 *>(psm);  // the queries' place: [D / 4][128] of group 1's O
             if (both && grp == 1 && warp_live && ok) {
 #pragma unroll 1
-                for (int g = 0; g < D / 16; ++g) {
-                    float o[16];
-                    tmem_ld16(co + g * 16, o);
+                for (int g = 0; g < D / 32; ++g) {
+                    float o[32];
+                    tmem_ld32(co + g * 32, o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        part[(g * 4 + k) * 128 + r] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    for (int k = 0; k < 8; ++k)
+                        part[(g * 8 + k) * 128 + r] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                 }
                 m.ref1[r] = ref;
                 m.sum1[r] = sum;
@@ -435,21 +446,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int n8 = rows8(it.rows);
                 float4 *dst = reinterpret_cast<float4 *>(a.po + (long long)it.base * D) + row;
                 if (live) a.plse[it.base + row] = sum == 0.f ? kMinusInf : ref + log2f(sum);
+                f0 *= inv;
+                f1 *= inv;
 #pragma unroll 1
-                for (int g = 0; g < D / 16; ++g) {
-                    float o[16];
+                for (int g = 0; g < D / 32; ++g) {
+                    float o[32];
                     __syncwarp();
-                    tmem_ld16(co + g * 16, o);
+                    tmem_ld32(co + g * 32, o);
                     tmem_wait_ld();
                     if (!live) continue;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < 8; ++k) {
                         float4 y = make_float4(o[4 * k] * f0, o[4 * k + 1] * f0, o[4 * k + 2] * f0, o[4 * k + 3] * f0);
                         if (both) {
-                            const float4 z = part[(g * 4 + k) * 128 + r];
+                            const float4 z = part[(g * 8 + k) * 128 + r];
                             y = make_float4(fmaf(z.x, f1, y.x), fmaf(z.y, f1, y.y), fmaf(z.z, f1, y.z), fmaf(z.w, f1, y.w));
                         }
-                        dst[(long long)(g * 4 + k) * n8] = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+                        dst[(long long)(g * 8 + k) * n8] = y;
                     }
                 }
             }
