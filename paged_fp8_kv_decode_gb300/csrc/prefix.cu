@@ -120,9 +120,13 @@ __device__ void plan_segments(const PrefixArgs &a) {
     __syncthreads();
     for (int b = tid; b < a.B; b += kValThreads) {
         const int at = few ? of[b] : a.pos[b];
-        if (at < 0) continue;
-        const int p = a.prefix_of[b];
-        a.members[(few ? first_member[p] : a.mstart[p]) + at] = b;
+        PrefixPlace w{-1, 0, 0, 0};
+        if (at >= 0) {
+            const int p = a.prefix_of[b];
+            a.members[(few ? first_member[p] : a.mstart[p]) + at] = b;
+            w = PrefixPlace{at * a.kq * a.G, few ? first_seg[p] : a.seg0[p], blocks(p), 0};
+        }
+        a.place[b] = w;
     }
     // tiles, then rows of partial results
     Two v{0, 0};
@@ -173,6 +177,28 @@ __device__ void plan_segments(const PrefixArgs &a) {
             else hi = mid;
         }
         a.range[c] = PrefixRange{t0, (int)(((long long)(c + 1) * U + W - 1) / W), lo, 0};
+    }
+}
+
+// First units of the own tokens' segments, group by group, as the split kernel counts them.
+__device__ void plan_own_units(const PrefixArgs &a, const PrefixOwnRows &o) {
+    __shared__ Two part[kValThreads / 32];
+    for (int r0 = 0, g = 0; r0 < a.B; r0 += o.greq, ++g) {
+        const int K = min(o.greq, a.B - r0) * a.kq * a.Hkv, per = (K + kValThreads - 1) / kValThreads;
+        int *units = o.units + (long long)g * (o.greq * a.kq * a.Hkv + 1);
+        const int k0 = min(K, (int)threadIdx.x * per), k1 = min(K, k0 + per);
+        const auto count = [&](int k) {
+            const int v = k / a.Hkv, r = v / a.kq, n = table_len(a.own, r0 + r, k - v * a.Hkv);
+            return segment_units(n < 0 ? -1 : max(0, n - a.kq + 1 + (v - r * a.kq)), 0, o.chunk_tokens);
+        };
+        Two mine{0, 0}, total;
+        for (int k = k0; k < k1; ++k) mine.x += count(k);
+        int at = block_sums_before(mine, part, &total).x;
+        for (int k = k0; k < k1; ++k) {
+            units[k] = at;
+            at += count(k);
+        }
+        if (threadIdx.x == 0) units[K] = total.x;
     }
 }
 
@@ -227,14 +253,18 @@ __device__ void check_tile(const PrefixArgs &a, const PrefixTables &t, int ih, i
 constexpr int kPackPer = 4;  // 16-byte chunks a thread packs
 
 template <bool FP8>
-__global__ void __launch_bounds__(kValThreads) prefix_plan_kernel(PrefixArgs a, int D, int pre_tiles, int own_tiles) {
+__global__ void __launch_bounds__(kValThreads) prefix_plan_kernel(PrefixArgs a, PrefixOwnRows o, int D, int pre_tiles, int own_tiles) {
     pdl_enter();
     int x = blockIdx.x;
     if (x == 0) {
         plan_segments(a);
         return;
     }
-    x -= 1;
+    if (x == 1) {
+        if (o.status) plan_own_units(a, o);
+        return;
+    }
+    x -= 2;
     if (x < pre_tiles) {
         check_tile<FP8>(a, a.pre, x / a.pre.htiles, x % a.pre.htiles, a.pre_bits, a.pre_vmax);
         return;
@@ -265,90 +295,69 @@ __global__ void __launch_bounds__(kValThreads) prefix_plan_kernel(PrefixArgs a, 
 // The merge: a CTA a (request, query token, kv head).  Its partial results are those that the
 // CTAs of the attention over the prefix left for its rows, and those that the workers of the own
 // tokens' split kernel left for its segment; out = sum 2^(lse - M) o / sum 2^(lse - M).
+//
+// What it needs of the plan (and no partial result) is read before its wait: the plan had ended
+// when the kernel before this one let it start (`early`; not where the plan itself is that kernel).
 // --------------------------------------------------------------------------
 constexpr int kMergeThreads = 256;
 
 template <int D, int G>
-__global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(PrefixArgs a, PrefixOwnRows own) {
-    constexpr int C4 = D / 4, TPR = G * C4, WAYS = kMergeThreads / TPR;
-    static_assert(WAYS >= 1 && TPR % 32 == 0 || TPR < 32, "whole warps a way");
+__global__ void __launch_bounds__(kMergeThreads, 5) prefix_merge_kernel(PrefixArgs a, PrefixOwnRows own, int early) {
+    constexpr int C4 = D / 4, TPR = G * C4, WAYS = kMergeThreads / TPR, WARPS = kMergeThreads / 32;
+    static_assert(WAYS >= 1 && TPR * WAYS == kMergeThreads, "every thread has a place");
     __shared__ uint32_t s_flags;
     __shared__ float s_m[WAYS][G], s_s[WAYS][G];
     __shared__ float4 s_o[WAYS][TPR];
-    pdl_enter();
+    if (!early) pdl_enter();
     const int v = blockIdx.x / a.Hkv, h = blockIdx.x - v * a.Hkv, b = v / a.kq, t = v - b * a.kq;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) s_flags = 0u;
-    __syncthreads();
-    // the request's flags
+    // the request's flags, but for waits that gave up
     const int p = a.prefix_of[b];
-    const bool member = p >= 0 && p < a.pre.count;
+    const PrefixPlace place = a.place[b];
+    const bool member = place.row >= 0;
     uint32_t f = p < -1 || p >= a.pre.count ? PFKV_FLAG_BAD_PAGE : 0u;
-    if (member) {
-        f |= a.head->timeout;
+    if (member)
         for (int i = tid; i < a.Hkv * a.pre.htiles; i += kMergeThreads) f |= a.pre_bits[(long long)p * a.Hkv * a.pre.htiles + i];
-    }
-    if (own.status)
-        for (int i = tid; i < a.Hkv * a.own.htiles; i += kMergeThreads) f |= a.own_bits[(long long)b * a.Hkv * a.own.htiles + i];
     // own tokens: rows k + worker of the request's group of launches
     long long own_row = 0;
     int own_n = 0;
     size_t shift = 0;
     if (own.status) {
+        for (int i = tid; i < a.Hkv * a.own.htiles; i += kMergeThreads) f |= a.own_bits[(long long)b * a.Hkv * a.own.htiles + i];
         const int grp = b / own.greq, r0 = grp * own.greq, Bg = min(own.greq, a.B - r0);
         shift = (size_t)grp * own.group_bytes;
-        const int *prefix = reinterpret_cast<const int *>(reinterpret_cast<const uint8_t *>(own.prefix) + shift);
-        const uint32_t *status = reinterpret_cast<const uint32_t *>(reinterpret_cast<const uint8_t *>(own.status) + shift);
-        const int U = prefix[Bg * a.kq * a.Hkv], W = min(own.workers, U);
-        // every segment of the request: a warp each
-        for (int i = warp; i < a.kq * a.Hkv; i += kMergeThreads / 32) {
-            const int k = (b - r0) * a.kq * a.Hkv + i, u0 = prefix[k], u1 = prefix[k + 1];
-            if (u1 == u0) continue;
-            const int w0 = pers_worker_of(u0, U, W), w1 = pers_worker_of(u1 - 1, U, W);
-            for (int w = w0 + lane; w <= w1; w += 32) f |= status[k + w];
-        }
-        const int k = ((b - r0) * a.kq + t) * a.Hkv + h, u0 = prefix[k], u1 = prefix[k + 1];
+        const int *units = own.units + (long long)grp * (own.greq * a.kq * a.Hkv + 1);
+        const int U = units[Bg * a.kq * a.Hkv], W = min(own.workers, U);
+        const int k = ((b - r0) * a.kq + t) * a.Hkv + h, u0 = units[k], u1 = units[k + 1];
         if (u1 > u0) {
             const int w0 = pers_worker_of(u0, U, W);
             own_row = k + w0;
             own_n = pers_worker_of(u1 - 1, U, W) - w0 + 1;
         }
     }
-    f = __reduce_or_sync(0xffffffffu, f);
-    if (lane == 0 && f) atomicOr(&s_flags, f);
     // the prefix's: one a CTA that touched the rows' segment
     int pre_n = 0, pre_rows = 0, base = 0, block_row = 0;
     if (member) {
-        const int R = (a.pos[b] * a.kq + t) * G;
-        const int nb = (int)(((long long)(a.mstart[p + 1] - a.mstart[p]) * a.kq * G + kPrefixBlock - 1) / kPrefixBlock);
-        const PrefixSeg sg = a.seg[a.seg0[p] + h * nb + R / kPrefixBlock];
-        if (sg.ntiles > 0) {
-            pre_n = sg.ctas;
-            pre_rows = rows8(sg.rows);
-            base = sg.base;
-            block_row = R % kPrefixBlock;
-        }
+        const int R = place.row + t * G;
+        const PrefixSeg sg = a.seg[place.seg + h * place.nb + R / kPrefixBlock];
+        pre_n = sg.ctas;
+        pre_rows = rows8(sg.rows);
+        base = sg.base;
+        block_row = R % kPrefixBlock;
     }
-    __syncthreads();
-    const uint32_t flags = s_flags;
-    if (t == 0 && h == 0 && tid == 0) {
-        if (a.flags) a.flags[b] = (uint8_t)flags;
-        if (own.rflags) own.rflags[b] = (uint8_t)flags;
-    }
-    const int way = tid / TPR, e = tid - way * TPR, g = e / C4, c = e - g * C4;
-    const bool works = way < WAYS;
-    __nv_bfloat16 *out = a.out.p + (long long)b * a.out.sb + (long long)t * a.out.st;
-    if (flags) {
-        if (way == 0)
-            *reinterpret_cast<uint2 *>(out + (long long)(h * G + g) * a.out.sh + c * 4) = make_uint2(0u, 0u);
-        return;
-    }
+    __syncthreads();  // s_flags
+    if (early) pdl_enter();
+
+    // rows, several on their way together.  Threads of a way: query heads first, so that a warp reads
+    // pieces of G rows (64 bytes with four heads) of a prefix's result.
+    const int way = tid / TPR, e = tid - way * TPR, g = e % G, c = e / G;
     const float *own_lse = reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(own.lse) + shift);
     const float *own_o = reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(own.o) + shift);
     float M = -INFINITY, S = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int n = works ? pre_n + own_n : 0;
-    constexpr int RB = 4;  // rows in flight
+    const int n = pre_n + own_n;
+    constexpr int RB = 4;
     for (int j0 = way; j0 < n; j0 += RB * WAYS) {
         float l[RB];
         float4 x[RB];
@@ -381,42 +390,67 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(PrefixArgs 
             acc = make_float4(fmaf(w, x[r].x, acc.x), fmaf(w, x[r].y, acc.y), fmaf(w, x[r].z, acc.z), fmaf(w, x[r].w, acc.w));
         }
     }
+    // waits that gave up: those of the own tokens' workers (a worker's rows of the request's segments), and of
+    // the prefix's kernel
+    if (member) f |= a.head->timeout;
+    if (own.status) {
+        const uint32_t *status = reinterpret_cast<const uint32_t *>(reinterpret_cast<const uint8_t *>(own.status) + shift);
+        const int grp = b / own.greq, r0 = grp * own.greq, Bg = min(own.greq, a.B - r0);
+        const int *units = own.units + (long long)grp * (own.greq * a.kq * a.Hkv + 1);
+        const int U = units[Bg * a.kq * a.Hkv], W = min(own.workers, U);
+        for (int i = warp; i < a.kq * a.Hkv; i += WARPS) {
+            const int k = (b - r0) * a.kq * a.Hkv + i, u0 = units[k], u1 = units[k + 1];
+            if (u1 == u0) continue;
+            const int w0 = pers_worker_of(u0, U, W), w1 = pers_worker_of(u1 - 1, U, W);
+            for (int w = w0 + lane; w <= w1; w += 32) f |= status[k + w];
+        }
+    }
+    f = __reduce_or_sync(0xffffffffu, f);
+    if (lane == 0 && f) atomicOr(&s_flags, f);
     if (WAYS > 1) {
-        if (works) {
-            if (c == 0) {
-                s_m[way][g] = M;
-                s_s[way][g] = S;
-            }
-            s_o[way][e] = acc;
+        if (c == 0) {
+            s_m[way][g] = M;
+            s_s[way][g] = S;
         }
-        __syncthreads();
-        if (way != 0) return;
+        s_o[way][e] = acc;
+    }
+    __syncthreads();
+    const uint32_t flags = s_flags;
+    if (t == 0 && h == 0 && tid == 0) {
+        if (a.flags) a.flags[b] = (uint8_t)flags;
+        if (own.rflags) own.rflags[b] = (uint8_t)flags;
+    }
+    if (way != 0) return;
+    __nv_bfloat16 *out = a.out.p + (long long)b * a.out.sb + (long long)t * a.out.st + (long long)(h * G + g) * a.out.sh + c * 4;
+    if (flags) {
+        *reinterpret_cast<uint2 *>(out) = make_uint2(0u, 0u);
+        return;
+    }
 #pragma unroll
-        for (int w2 = 1; w2 < WAYS; ++w2) {
-            const float M2 = s_m[w2][g], S2 = s_s[w2][g];
-            const float4 y = s_o[w2][e];
-            if (S2 == 0.f) continue;
-            const float top = fmaxf(M, M2), f1 = M == top ? 1.f : exp2f(M - top), f2 = M2 == top ? 1.f : exp2f(M2 - top);
-            S = S * f1 + S2 * f2;
-            acc = make_float4(acc.x * f1 + y.x * f2, acc.y * f1 + y.y * f2, acc.z * f1 + y.z * f2, acc.w * f1 + y.w * f2);
-            M = top;
-        }
+    for (int w2 = 1; w2 < WAYS; ++w2) {
+        const float M2 = s_m[w2][g], S2 = s_s[w2][g];
+        const float4 y = s_o[w2][e];
+        if (S2 == 0.f) continue;
+        const float top = fmaxf(M, M2), f1 = M == top ? 1.f : exp2f(M - top), f2 = M2 == top ? 1.f : exp2f(M2 - top);
+        S = S * f1 + S2 * f2;
+        acc = make_float4(acc.x * f1 + y.x * f2, acc.y * f1 + y.y * f2, acc.z * f1 + y.z * f2, acc.w * f1 + y.w * f2);
+        M = top;
     }
     if (c == 0 && own.lse_fin) own.lse_fin[((long long)v * a.Hkv + h) * G + g] = S == 0.f ? -INFINITY : M + log2f(S);
     const float inv = S == 0.f ? 0.f : 1.f / S;
     const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-    *reinterpret_cast<uint2 *>(out + (long long)(h * G + g) * a.out.sh + c * 4) =
-        make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+    *reinterpret_cast<uint2 *>(out) = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
 }
 
 template <int D>
 cudaError_t launch_merge_d(const PrefixArgs &a, const PrefixOwnRows &o, cudaStream_t s) {
     const dim3 grid((unsigned)((long long)a.B * a.kq * a.Hkv)), block(kMergeThreads);
+    const int early = o.status != nullptr || a.pre.count > 0;
     switch (a.G) {
-        case 1: return launch_pdl(prefix_merge_kernel<D, 1>, grid, block, 0, s, a, o);
-        case 2: return launch_pdl(prefix_merge_kernel<D, 2>, grid, block, 0, s, a, o);
-        case 4: return launch_pdl(prefix_merge_kernel<D, 4>, grid, block, 0, s, a, o);
-        case 8: return launch_pdl(prefix_merge_kernel<D, 8>, grid, block, 0, s, a, o);
+        case 1: return launch_pdl(prefix_merge_kernel<D, 1>, grid, block, 0, s, a, o, early);
+        case 2: return launch_pdl(prefix_merge_kernel<D, 2>, grid, block, 0, s, a, o, early);
+        case 4: return launch_pdl(prefix_merge_kernel<D, 4>, grid, block, 0, s, a, o, early);
+        case 8: return launch_pdl(prefix_merge_kernel<D, 8>, grid, block, 0, s, a, o, early);
     }
     return cudaErrorInvalidValue;
 }
@@ -432,12 +466,12 @@ cudaError_t preload_merge_d() {
 
 }  // namespace
 
-cudaError_t launch_prefix_plan(const PrefixArgs &a, int D, bool fp8, cudaStream_t s) {
+cudaError_t launch_prefix_plan(const PrefixArgs &a, const PrefixOwnRows &o, int D, bool fp8, cudaStream_t s) {
     const long long pre = (long long)a.pre.count * a.Hkv * a.pre.htiles, own = (long long)a.own.count * a.Hkv * a.own.htiles;
     const long long chunks = a.packed_q ? (long long)a.B * a.kq * a.Hkv * a.G * (D / 8) : 0;
     const long long pack = (chunks + kPackPer * kValThreads - 1) / (kPackPer * kValThreads);
-    const dim3 grid((unsigned)(1 + pre + own + pack)), block(kValThreads);
-    return launch_pdl(fp8 ? prefix_plan_kernel<true> : prefix_plan_kernel<false>, grid, block, 0, s, a, D, (int)pre, (int)own);
+    const dim3 grid((unsigned)(2 + pre + own + pack)), block(kValThreads);
+    return launch_pdl(fp8 ? prefix_plan_kernel<true> : prefix_plan_kernel<false>, grid, block, 0, s, a, o, D, (int)pre, (int)own);
 }
 
 cudaError_t launch_prefix_merge(const PrefixArgs &a, const PrefixOwnRows &o, int D, cudaStream_t s) {
@@ -488,7 +522,7 @@ int check_words(const pfkv_pages *p) { return max(1, (p->max_pages + kValTile - 
 
 // Where everything lies in the workspace.
 struct Layout {
-    size_t head, pre_bits, pre_vmax, own_bits, pos, members, mstart, seg0, seg, range, plse, po, packed, own, mass, total;
+    size_t head, pre_bits, pre_vmax, own_bits, place, pos, members, mstart, seg0, seg, range, units, plse, po, packed, own, mass, total;
     size_t group_bytes;
     DecodePlan plan;  // of the own tokens
 };
@@ -505,7 +539,7 @@ pfkv_status lay_out(const pfkv_cache *c, const pfkv_pages *pages, const pfkv_pag
     const long long partial = NP > 0 ? H * rows + 8 * S + (long long)sms * kPrefixBlock : 0;
     const long long words = NP * H * pre_words + batch * H * own_words;
     const long long pack = rows * H * c->head_dim / (8 * kPackPer * kValThreads) + 1;
-    if (partial > 0x7fffffffLL || words + pack + 1 > 0x7fffffffLL) return PFKV_ERR_UNSUPPORTED;
+    if (partial > 0x7fffffffLL || words + pack + 2 > 0x7fffffffLL) return PFKV_ERR_UNSUPPORTED;
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -516,6 +550,7 @@ pfkv_status lay_out(const pfkv_cache *c, const pfkv_pages *pages, const pfkv_pag
     l->pre_bits = take(4 * (size_t)(NP * H * pre_words));
     l->pre_vmax = take(c->dtype == PFKV_KV_FP8_E4M3 ? 4 * (size_t)(NP * H * pre_words) : 0);
     l->own_bits = take(4 * (size_t)(batch * H * own_words));
+    l->place = take(sizeof(PrefixPlace) * (size_t)batch);
     l->pos = take(4 * (size_t)batch);
     l->members = take(4 * (size_t)batch);
     l->mstart = take(4 * (size_t)(NP + 1));
@@ -535,6 +570,7 @@ pfkv_status lay_out(const pfkv_cache *c, const pfkv_pages *pages, const pfkv_pag
         l->group_bytes = l->plan.off_mscore - l->plan.off_prefix;
         l->own = take(l->group_bytes * (size_t)l->plan.ngroups);
         l->mass = take(l->plan.total - l->plan.off_mscore);
+        l->units = take(4 * (size_t)l->plan.ngroups * ((size_t)l->plan.greq * kq * H + 1));
     }
     l->total = off;
     return PFKV_OK;
@@ -603,6 +639,7 @@ pfkv_status prefix_attn(int tries, const pfkv_cache *cache, const pfkv_pages *pa
     a.pre_bits = reinterpret_cast<uint32_t *>(ws + l.pre_bits);
     a.pre_vmax = reinterpret_cast<float *>(ws + l.pre_vmax);
     a.head = reinterpret_cast<PrefixHead *>(ws + l.head);
+    a.place = reinterpret_cast<PrefixPlace *>(ws + l.place);
     a.pos = reinterpret_cast<int *>(ws + l.pos);
     a.members = reinterpret_cast<int *>(ws + l.members);
     a.mstart = reinterpret_cast<int *>(ws + l.mstart);
@@ -617,8 +654,6 @@ pfkv_status prefix_attn(int tries, const pfkv_cache *cache, const pfkv_pages *pa
     a.tries = tries;
     a.after_own = pages != nullptr;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (launch_prefix_plan(a, D, fp8, s) != cudaSuccess) return PFKV_ERR_CUDA;
-
     DecodeArgs d{};
     PrefixOwnRows own{};
     if (pages) {
@@ -659,7 +694,12 @@ pfkv_status prefix_attn(int tries, const pfkv_cache *cache, const pfkv_pages *pa
             d.mass_sb = mass_stride_b;
             d.mass_sh = mass_stride_h;
         }
-        own = PrefixOwnRows{d.status, d.lse, d.o, d.ws_prefix, l.group_bytes, plan.greq, plan.workers, d.lse_fin, d.rflags};
+        own = PrefixOwnRows{d.status, d.lse, d.o, l.group_bytes, reinterpret_cast<int *>(ws + l.units), plan.greq,
+                            plan.workers, plan.chunk_tokens, d.lse_fin, d.rflags};
+    }
+    if (launch_prefix_plan(a, own, D, fp8, s) != cudaSuccess) return PFKV_ERR_CUDA;
+    if (pages) {
+        const DecodePlan &plan = l.plan;
         for (int g = 0; g < plan.ngroups; ++g) {
             DecodePlan pg = plan;
             pg.Breq = min(plan.greq, plan.Breq - g * plan.greq);

@@ -41,6 +41,13 @@ struct PrefixSeg {
     int pad[2];
 };
 static_assert(sizeof(PrefixSeg) == 48, "three 16-byte loads");
+// Where a request's partial results are.
+struct PrefixPlace {
+    int row;   // first of its query rows among those of its prefix; -1: no prefix
+    int seg;   // the prefix's first segment
+    int nb;    // blocks of rows of a head
+    int pad;
+};
 // A CTA's tiles x0 .. x1 - 1, and the segment of the first.
 struct PrefixRange {
     int x0, x1, seg, pad;
@@ -62,6 +69,7 @@ struct PrefixArgs {
     uint32_t *own_bits, *pre_bits;  // [count][Hkv][htiles] check bits
     float *pre_vmax;                // [prefixes][Hkv][htiles] largest |V scale| of the tile's pages
     PrefixHead *head;
+    PrefixPlace *place;             // [B]
     int *pos, *members;             // [B] position among its prefix's requests (-1: none); requests by prefix
     int *mstart, *seg0;             // [prefixes + 1] first entry of members; first segment
     PrefixSeg *seg;
@@ -78,14 +86,14 @@ struct PrefixArgs {
 struct PrefixOwnRows {
     const uint32_t *status;
     const float *lse, *o;
-    const int *prefix;
     size_t group_bytes;  // from one group's arrays to the next's
-    int greq, workers;
+    int *units;          // [groups][greq * kq * Hkv + 1] first unit of every segment (by the plan)
+    int greq, workers, chunk_tokens;
     float *lse_fin;      // for the mass pass, or null
     uint8_t *rflags;
 };
 
-cudaError_t launch_prefix_plan(const PrefixArgs &a, int D, bool fp8, cudaStream_t s);
+cudaError_t launch_prefix_plan(const PrefixArgs &a, const PrefixOwnRows &o, int D, bool fp8, cudaStream_t s);
 cudaError_t launch_prefix_attn(const PrefixArgs &a, int D, bool fp8, cudaStream_t s);
 cudaError_t launch_prefix_merge(const PrefixArgs &a, const PrefixOwnRows &o, int D, cudaStream_t s);
 cudaError_t preload_prefix();
