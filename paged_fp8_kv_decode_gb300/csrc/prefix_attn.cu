@@ -34,8 +34,16 @@ constexpr int kPages = kPrefixTile / kPage;  // pages of a tile
 constexpr int kInfo = 4;                     // tiles' scales kept ahead, a softmax group
 constexpr int kItems = 3;                    // segments found ahead
 constexpr uint32_t kColO = 256;
-constexpr float kGrowth = 8.f;
+// How far the maximum may outgrow the weights' reference (log2) before O is rescaled: f16 weights have
+// 2^7 below 2^8 of room, bf16's exponents are those of fp32, sums among them.
+template <bool FP8>
+constexpr float kGrowth = FP8 ? 8.f : 40.f;
 constexpr float kMinusInf = -INFINITY;
+
+template <int T>
+struct Group {
+    static constexpr int value = T;
+};
 
 template <int D, bool FP8>
 struct Cfg {
@@ -63,7 +71,7 @@ struct Item {
 };
 
 // Scales of a tile's pages.
-struct Info {
+struct alignas(16) Info {
     float ks[kPages], vs[kPages];
 };
 
@@ -302,14 +310,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_wait_ld();
                     float f[kPages];  // factors of 16 columns each
                     if constexpr (FP8) {
+                        const float4 k0 = *reinterpret_cast<const float4 *>(inf.ks), k1 = *reinterpret_cast<const float4 *>(inf.ks + 4);
+                        const float k[kPages] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+                        const float least = fminf(fminf(fminf(k0.x, k0.y), fminf(k0.z, k0.w)), fminf(fminf(k1.x, k1.y), fminf(k1.z, k1.w)));
+                        if (least < 0.f) {  // scales below zero: the scores' sign
+#pragma unroll
+                            for (int p = 0; p < kPages; ++p) {
+                                const float sign = k[p] < 0.f ? -1.f : 1.f;
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) x[p >> 1][(p & 1) * 16 + e] *= sign;
+                            }
+                        }
 #pragma unroll
                         for (int p = 0; p < kPages; ++p) {
-                            const float k = inf.ks[p];
-                            if (k < 0.f) {  // the scores' sign
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) x[p >> 1][(p & 1) * 16 + e] = -x[p >> 1][(p & 1) * 16 + e];
-                            }
-                            f[p] = fabsf(k) * mul;
+                            f[p] = fabsf(k[p]) * mul;
                             if (f[p] < 1.1754944e-38f) f[p] = 1.1754944e-38f;  // hidden scores stay -inf; NaN stays
                         }
                     }
@@ -341,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       fmaxf(fmaxf(tops[4], tops[5]), fmaxf(tops[6], tops[7])));
                     if constexpr (!FP8) top *= a2;
                     float shrink = 1.f;
-                    if (top > ref + kGrowth || (ref == kMinusInf && top > kMinusInf)) {
+                    if (top > ref + kGrowth<FP8> || (ref == kMinusInf && top > kMinusInf)) {
                         shrink = fast_exp2(ref - top);  // 0 when nothing was seen yet
                         sum *= shrink;
                         ref = top;
@@ -365,9 +379,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // while the second half is computed
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        float vf[4];  // V scales (once in registers: a load in every pair took 2,000 cycles a tile)
-#pragma unroll
-                        for (int p = 0; p < 4; ++p) vf[p] = FP8 && (4 * half + p) * kPage < seen ? inf.vs[4 * half + p] * vinv : 0.f;
+                        // V scales, once in registers: a load in every pair took 2,000 cycles a tile (those of pages
+                        // past the last are zero)
+                        float vf[4] = {};
+                        if constexpr (FP8) {
+                            const float4 v = *reinterpret_cast<const float4 *>(inf.vs + 4 * half);
+                            vf[0] = v.x * vinv;
+                            vf[1] = v.y * vinv;
+                            vf[2] = v.z * vinv;
+                            vf[3] = v.w * vinv;
+                        }
 #pragma unroll
                         for (int g = 2 * half; g < 2 * half + 2; ++g) {
                             float w[16];  // packed pairs
@@ -481,61 +502,83 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
             constexpr uint32_t idO = umma_idesc(128, D, !FP8, false, true);
             const uint32_t qa = smem_addr(psm), ka = qa + C::OFF_K, va = qa + C::OFF_V;
-            uint32_t weighed[2] = {0, 0}, pos = 0;
+            // Straight code, a copy a group: one thread issues all products of the CTA, and what it does
+            // between them is time that the tensor cores wait.  So each barrier is asked for while the
+            // products before are issued, and waited for only if it has not passed by then.
+            uint32_t weighed0 = 0, weighed1 = 0, pos = 0;  // steps whose weights were used, tiles so far
+            bool wide = false, ready = false;              // ready: the next group's first weights, asked ahead
+            int n0 = 0, n1 = 0;
+            // Step j of a group: O of its step j - 1, then S of step j.
+            auto step = [&](auto which, int j) {
+                constexpr int T = decltype(which)::value;
+                const uint32_t cs = tmem + T * 128, co = tmem + kColO + T * 128;
+                const int mine = T ? n1 : n0, other = T ? n0 : n1;
+                uint32_t &weighed = T ? weighed1 : weighed0;
+                const uint32_t at = pos + (wide ? j : 2 * j + T), kslot = at % C::NK, kparity = (at / C::NK) & 1;
+                const bool again = wide && T == 1;  // the tile is there already, and this group is done with it last
+                bool keys = again;
+                if (j > 0 && j <= mine) {
+                    const uint32_t vat = pos + (wide ? j - 1 : 2 * j - 2 + T), slot = vat % C::NV, parity = weighed++ & 1;
+                    const uint32_t db = umma_desc(va + slot * C::VB, C::HALF);
+                    if (!ready && !bar_wait(&m.pready[T][0], parity, gave_up, tries)) return false;
+                    if (!again && !bar_wait(&m.vfull[slot], (vat / C::NV) & 1, gave_up, tries)) return false;
+                    const bool rest = bar_passed(&m.pready[T][1], parity);
+                    tmem_fence_after();
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) umma_ts(co, cs + s * 8, db + s * 128, idO, j > 1 || s > 0);
+                    if (!rest && !bar_wait(&m.pready[T][1], parity, gave_up, tries)) return false;
+                    if (j < mine && !again) keys = bar_passed(&m.kfull[kslot], kparity);
+                    tmem_fence_after();
+#pragma unroll
+                    for (int s = 4; s < 8; ++s) umma_ts(co, cs + s * 8, db + s * 128, idO, true);
+                    if (!wide || T == 1) umma_commit(&m.vempty[slot]);
+                    if (j == mine) umma_commit(&m.odone[T]);
+                }
+                ready = false;
+                const int jn = j + T;  // the next group's step
+                const bool follows = jn > 0 && jn <= other;
+                const uint32_t next_parity = (T ? weighed0 : weighed1) & 1;
+                if (j >= mine) {
+                    if (follows) ready = bar_passed(&m.pready[T ^ 1][0], next_parity);
+                    return true;
+                }
+                const uint32_t qt = qa + (wide ? T : 0) * C::QB, kt = ka + kslot * C::KB;
+                if (!keys && !bar_wait(&m.kfull[kslot], kparity, gave_up, tries)) return false;
+                if (follows) ready = bar_passed(&m.pready[T ^ 1][0], next_parity);
+                tmem_fence_after();
+                if constexpr (!FP8) {
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c) {
+                        const uint32_t da = umma_desc(qt + c * C::HALF, 16), db = umma_desc(kt + c * C::HALF, 16);
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) umma_ss<1>(cs, da + 2 * s, db + 2 * s, idS, c > 0 || s > 0);
+                    }
+                } else {
+                    constexpr uint32_t UP = D == 128 ? kDescUpper : kDescUpper64;
+                    const uint32_t db = umma_desc(kt, 16);
+#pragma unroll
+                    for (int part = 0; part < 2; ++part) {
+                        const uint32_t da = umma_desc(qt + part * (C::QB / 2), 16);
+#pragma unroll
+                        for (int s = 0; s < D / 32; ++s) umma_ss_f8<UP>(cs, da + 2 * s, db + 2 * s, idS, part > 0 || s > 0);
+                    }
+                }
+                if (!wide || T == 1) umma_commit(&m.kempty[kslot]);
+                umma_commit(&m.sfull[T]);
+                return true;
+            };
             bool ok = true;
             for (int i = 0; ok && item_ready(i); ++i) {
-                const bool wide = m.item[i % kItems].rows > 128;
+                wide = m.item[i % kItems].rows > 128;
                 const int nt = m.item[i % kItems].nt;
-                const int n[2] = {steps_of(m.item[i % kItems], 0), steps_of(m.item[i % kItems], 1)};
+                n0 = steps_of(m.item[i % kItems], 0);
+                n1 = steps_of(m.item[i % kItems], 1);
                 bar_arrive(&m.iempty[i % kItems]);
                 ok = bar_wait(&m.qfull, i & 1, gave_up, item_tries);
-                // Step j of a group: O of its step j - 1, then S of step j.
-                auto step = [&](int T, int j) {
-                    const uint32_t cs = tmem + T * 128, co = tmem + kColO + T * 128;
-                    if (j > 0 && j <= n[T]) {
-                        const uint32_t at = pos + (wide ? j - 1 : 2 * (j - 1) + T), slot = at % C::NV, parity = weighed[T]++ & 1;
-                        if (!bar_wait(&m.vfull[slot], (at / C::NV) & 1, gave_up, tries)) return false;
-                        if (!bar_wait(&m.pready[T][0], parity, gave_up, tries)) return false;
-                        tmem_fence_after();
-                        const uint32_t db = umma_desc(va + slot * C::VB, C::HALF);
-#pragma unroll
-                        for (int s = 0; s < 4; ++s) umma_ts(co, cs + s * 8, db + s * 128, idO, j > 1 || s > 0);
-                        if (!bar_wait(&m.pready[T][1], parity, gave_up, tries)) return false;
-                        tmem_fence_after();
-#pragma unroll
-                        for (int s = 4; s < 8; ++s) umma_ts(co, cs + s * 8, db + s * 128, idO, true);
-                        if (!wide || T == 1) umma_commit(&m.vempty[slot]);
-                        if (j == n[T]) umma_commit(&m.odone[T]);
-                    }
-                    if (j >= n[T]) return true;
-                    const uint32_t at = pos + (wide ? j : 2 * j + T), slot = at % C::NK;
-                    if (!bar_wait(&m.kfull[slot], (at / C::NK) & 1, gave_up, tries)) return false;
-                    tmem_fence_after();
-                    const uint32_t qt = qa + (wide ? T : 0) * C::QB;
-                    if constexpr (!FP8) {
-#pragma unroll
-                        for (int c = 0; c < D / 64; ++c) {
-                            const uint32_t da = umma_desc(qt + c * C::HALF, 16), db = umma_desc(ka + slot * C::KB + c * C::HALF, 16);
-#pragma unroll
-                            for (int s = 0; s < 4; ++s) umma_ss<1>(cs, da + 2 * s, db + 2 * s, idS, c > 0 || s > 0);
-                        }
-                    } else {
-                        constexpr uint32_t UP = D == 128 ? kDescUpper : kDescUpper64;
-                        const uint32_t db = umma_desc(ka + slot * C::KB, 16);
-#pragma unroll
-                        for (int part = 0; part < 2; ++part) {
-                            const uint32_t da = umma_desc(qt + part * (C::QB / 2), 16);
-#pragma unroll
-                            for (int s = 0; s < D / 32; ++s) umma_ss_f8<UP>(cs, da + 2 * s, db + 2 * s, idS, part > 0 || s > 0);
-                        }
-                    }
-                    if (!wide || T == 1) umma_commit(&m.kempty[slot]);
-                    umma_commit(&m.sfull[T]);
-                    return true;
-                };
-                const int most = max(n[0], n[1]);
+                const int most = max(n0, n1);
+                ready = false;
 #pragma unroll 1
-                for (int j = 0; j <= most && ok; ++j) ok = step(0, j) && step(1, j);
+                for (int j = 0; j <= most && ok; ++j) ok = step(Group<0>{}, j) && step(Group<1>{}, j);
                 pos += nt;
             }
             // nothing in flight when the CTA leaves
