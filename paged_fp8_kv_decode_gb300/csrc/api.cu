@@ -177,7 +177,7 @@ pfkv_status append_args(const pfkv_cache *cache, const pfkv_pages *pages, const 
 
 pfkv_status make_plan(const pfkv_cache *c, const pfkv_pages *p, int32_t num_q_heads,
                       int32_t split_tokens, int32_t max_seq_len, int num_sms, DecodePlan *plan,
-                      bool mass, int32_t kq, bool cuda_cores) {
+                      bool mass, int32_t kq, bool cuda_cores, int per_worker) {
     const pfkv_status st = check_decode_args(c, num_q_heads, split_tokens, max_seq_len);
     if (st != PFKV_OK) return st;
     if (kq < 1 || (long long)p->batch * kq > 0x7fffffffLL) return PFKV_ERR_INVALID_ARG;
@@ -215,7 +215,7 @@ pfkv_status make_plan(const pfkv_cache *c, const pfkv_pages *p, int32_t num_q_he
         q.pers_ctas = num_sms;
         // every (virtual request, kv head) at max_seq_len: an upper bound on the units
         const long long units_bound = (long long)q.B * q.Hkv * pages;
-        q.workers = num_sms * pers_workers_for(units_bound, num_sms);
+        q.workers = num_sms * pers_workers_for(units_bound, num_sms, per_worker);
     } else {
         q.greq = q.Breq;
         q.ngroups = 1;

@@ -12,9 +12,10 @@ namespace pfkv {
 // large sweeps, by 1 us per step on the Llama-shaped layer (B=32, bound 131K
 // units) in back-to-back steps, and by 4 us on the B=8 BF16 sweep; with fewer
 // units per worker (the B=1 sweep: 16K units) the per-worker startup and the
-// partial rows weigh more and 8 workers were 1.5-2 us faster.
-int pers_workers_for(long long units_bound, int num_sms) {
-    return units_bound > (long long)num_sms * 8 * 64 ? 12 : 8;
+// partial rows weigh more and 8 workers were 1.5-2 us faster.  (per_worker is
+// 64 but where a caller has measured its own kind of batch.)
+int pers_workers_for(long long units_bound, int num_sms, int per_worker) {
+    return units_bound > (long long)num_sms * 8 * per_worker ? 12 : 8;
 }
 
 bool pers_supported(const DecodePlan &p) {

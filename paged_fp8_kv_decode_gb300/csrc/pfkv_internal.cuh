@@ -213,7 +213,7 @@ __device__ __forceinline__ bool request_rejected_cta(const DecodeArgs &a, int b,
 // The launch plan of an attention call, and the arguments of one of its request groups (api.cu)
 pfkv_status make_plan(const pfkv_cache *c, const pfkv_pages *p, int32_t num_q_heads, int32_t split_tokens,
                       int32_t max_seq_len, int num_sms, DecodePlan *plan, bool mass = false, int32_t kq = 1,
-                      bool cuda_cores = false);
+                      bool cuda_cores = false, int per_worker = 64);  // (pers_workers_for)
 DecodeArgs group_args(const DecodeArgs &a, const DecodePlan &p, int r0);
 
 // launchers (defined in the .cu files)
@@ -224,7 +224,7 @@ cudaError_t launch_append_validate(const AppendArgs &ap, int B, const DecodeArgs
 cudaError_t launch_split(const DecodeArgs &a, const DecodePlan &p, cudaStream_t s);
 cudaError_t launch_mass(const DecodeArgs &a, const DecodePlan &p, cudaStream_t s);
 bool pers_supported(const DecodePlan &p);
-int pers_workers_for(long long units_bound, int num_sms);
+int pers_workers_for(long long units_bound, int num_sms, int per_worker);
 cudaError_t launch_split_pers(const DecodeArgs &a, const DecodePlan &p, cudaStream_t s);
 cudaError_t launch_split_pers_d64(const DecodeArgs &a, const DecodePlan &p, cudaStream_t s);
 cudaError_t launch_combine_pers(const DecodeArgs &a, const DecodePlan &p, cudaStream_t s);

@@ -50,15 +50,20 @@ __device__ __forceinline__ int table_len(const PrefixTables &t, int i, int h) {
 }
 
 constexpr int kPlanChunk = 2048;
-constexpr int kPrefixFew = 512, kSegFew = 1024;  // what shared memory has room for
+constexpr int kPrefixFew = 512, kSegFew = 1024, kPairFew = 512;  // what shared memory has room for
 
 __device__ void plan_segments(const PrefixArgs &a) {
     __shared__ int count[PFKV_PREFIX_MAX];  // requests of a prefix
     __shared__ int of[kPlanChunk], first_member[kPrefixFew], first_seg[kPrefixFew], seg_tile[kSegFew];
+    __shared__ int2 pair_tile[kPairFew];
     __shared__ Two part[kValThreads / 32];
     Two total;
     const int tid = threadIdx.x, lane = tid & 31, NP = a.pre.count;
     if (tid == 0) a.head->timeout = 0u;
+    for (int b = tid; b < a.B; b += kValThreads) {  // the merge adds the bits
+        if (a.flags) a.flags[b] = 0;
+        if (a.rflags) a.rflags[b] = 0;
+    }
     for (int p = tid; p < NP; p += kValThreads) count[p] = 0;
     // lengths are on their way while requests are counted (one a thread: the usual case)
     const int pairs = NP * a.Hkv, per = (pairs + kValThreads - 1) / kValThreads;
@@ -128,50 +133,66 @@ __device__ void plan_segments(const PrefixArgs &a) {
         }
         a.place[b] = w;
     }
-    // tiles, then rows of partial results
+    // tiles: first ones of every (prefix, head)
     Two v{0, 0};
     for (int x = x0; x < x1; ++x)
         v.x += blocks(x / a.Hkv) * (((x == x0 ? len0 : len_of(x)) + kPrefixTile - 1) / kPrefixTile);
-    const int tile_first = block_sums_before(v, part, &total).x;
+    v.x = block_sums_before(v, part, &total).x;
     const int U = total.x, W = min(a.ctas, U);
-    // CTAs without work; the others' ranges are written with the segment that holds their first tile
+    for (int x = x0; x < x1; ++x) {
+        const int len = x == x0 ? len0 : len_of(x);
+        const int2 y = make_int2(v.x, len);
+        if (x < kPairFew) pair_tile[x] = y;
+        else a.pair[x] = y;
+        v.x += blocks(x / a.Hkv) * ((len + kPrefixTile - 1) / kPrefixTile);
+    }
+    __syncthreads();
+    // CTAs without work; the others' ranges follow
     for (int c = W + tid; c < a.ctas; c += kValThreads) a.range[c] = PrefixRange{0, 0, 0, 0};
-    for (int pass = 0, base = 0; pass < 2; ++pass) {
-        int rows = 0, tile = tile_first;
-        for (int x = x0; x < x1; ++x) {
-            const int p = x / a.Hkv, h = x - p * a.Hkv, nb = blocks(p);
-            if (nb == 0) continue;
-            const int len = x == x0 ? len0 : len_of(x), n = (len + kPrefixTile - 1) / kPrefixTile;
-            const int R = (int)((long long)count[p] * a.kq * a.G);
-            for (int rb = 0; rb < nb; ++rb) {
-                PrefixSeg s{};
-                s.p = p;
-                s.h = h;
-                s.row0 = rb * kPrefixBlock;
-                s.rows = min(kPrefixBlock, R - s.row0);
-                s.tile0 = tile;
-                s.ntiles = n;
-                s.base = base + rows;
-                s.len = len;
-                s.first = n > 0 ? pers_worker_of(tile, U, W) : 0;
-                s.ctas = n > 0 ? pers_worker_of(tile + n - 1, U, W) - s.first + 1 : 0;
-                if (pass) {
-                    const int k = (few ? first_seg[p] : a.seg0[p]) + h * nb + rb;
-                    a.seg[k] = s;
-                    if (k < kSegFew) seg_tile[k] = tile;
-                }
-                rows += rows8(s.rows) * s.ctas;
-                tile += n;
-            }
+    // segments, and the rows of their partial results
+    const int each = (segs + kValThreads - 1) / kValThreads, k0 = min(segs, tid * each), k1 = min(segs, k0 + each);
+    const auto segment = [&](int k) {
+        int lo = 0, hi = NP;  // the last prefix whose first segment is at most k
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if ((few ? first_seg[mid] : a.seg0[mid]) <= k) lo = mid;
+            else hi = mid;
         }
-        if (pass == 0) base = block_sums_before(Two{rows, 0}, part, &total).x;
+        const int nb = blocks(lo), at = k - (few ? first_seg[lo] : a.seg0[lo]), h = at / nb, rb = at - h * nb;
+        const int x = lo * a.Hkv + h;
+        const int2 y = x < kPairFew ? pair_tile[x] : a.pair[x];
+        PrefixSeg s{};
+        s.p = lo;
+        s.h = h;
+        s.row0 = rb * kPrefixBlock;
+        s.rows = (int)min((long long)kPrefixBlock, (long long)count[lo] * a.kq * a.G - s.row0);
+        s.len = y.y;
+        s.ntiles = (y.y + kPrefixTile - 1) / kPrefixTile;
+        s.tile0 = y.x + rb * s.ntiles;
+        s.first = s.ntiles > 0 ? pers_worker_of(s.tile0, U, W) : 0;
+        s.ctas = s.ntiles > 0 ? pers_worker_of(s.tile0 + s.ntiles - 1, U, W) - s.first + 1 : 0;
+        return s;
+    };
+    int rows = 0;
+    PrefixSeg s{};
+    for (int k = k0; k < k1; ++k) {
+        s = segment(k);
+        rows += rows8(s.rows) * s.ctas;
+    }
+    rows = block_sums_before(Two{rows, 0}, part, &total).x;
+    for (int k = k0; k < k1; ++k) {
+        if (each > 1) s = segment(k);
+        s.base = rows;
+        rows += rows8(s.rows) * s.ctas;
+        a.seg[k] = s;
+        if (k < kSegFew) seg_tile[k] = s.tile0;
     }
     __syncthreads();
     // the segment of every CTA's first tile
     for (int c = tid; c < W; c += kValThreads) {
         const int t0 = (int)(((long long)c * U + W - 1) / W);
         int lo = 0, hi = segs;
-        while (hi - lo > 1) {
+        while (hi - lo > 1) {  // (of equal first tiles the last segment, the one that has tiles)
             const int mid = (lo + hi) >> 1;
             if ((segs <= kSegFew ? seg_tile[mid] : a.seg[mid].tile0) <= t0) lo = mid;
             else hi = mid;
@@ -302,15 +323,15 @@ __global__ void __launch_bounds__(kValThreads) prefix_plan_kernel(PrefixArgs a, 
 constexpr int kMergeThreads = 256;
 
 template <int D, int G>
-__global__ void __launch_bounds__(kMergeThreads, 5) prefix_merge_kernel(PrefixArgs a, PrefixOwnRows own, int early) {
-    constexpr int C4 = D / 4, TPR = G * C4, WAYS = kMergeThreads / TPR, WARPS = kMergeThreads / 32;
+__global__ void __launch_bounds__(kMergeThreads, 4) prefix_merge_kernel(PrefixArgs a, PrefixOwnRows own, int early) {
+    constexpr int C4 = D / 4, TPR = G * C4, WAYS = kMergeThreads / TPR;
     static_assert(WAYS >= 1 && TPR * WAYS == kMergeThreads, "every thread has a place");
     __shared__ uint32_t s_flags;
     __shared__ float s_m[WAYS][G], s_s[WAYS][G];
     __shared__ float4 s_o[WAYS][TPR];
     if (!early) pdl_enter();
     const int v = blockIdx.x / a.Hkv, h = blockIdx.x - v * a.Hkv, b = v / a.kq, t = v - b * a.kq;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
     if (tid == 0) s_flags = 0u;
     // the request's flags, but for waits that gave up
     const int p = a.prefix_of[b];
@@ -352,32 +373,38 @@ __global__ void __launch_bounds__(kMergeThreads, 5) prefix_merge_kernel(PrefixAr
     // rows, several on their way together.  Threads of a way: query heads first, so that a warp reads
     // pieces of G rows (64 bytes with four heads) of a prefix's result.
     const int way = tid / TPR, e = tid - way * TPR, g = e % G, c = e / G;
+    const uint32_t *own_status = reinterpret_cast<const uint32_t *>(reinterpret_cast<const uint8_t *>(own.status) + shift);
     const float *own_lse = reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(own.lse) + shift);
     const float *own_o = reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(own.o) + shift);
     float M = -INFINITY, S = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     const int n = pre_n + own_n;
-    constexpr int RB = 4;
+    constexpr int RB = 6;
+    uint32_t gave_up = member && tid == 0 ? a.head->timeout : 0u;
     for (int j0 = way; j0 < n; j0 += RB * WAYS) {
         float l[RB];
         float4 x[RB];
+        uint32_t st[RB];
 #pragma unroll
         for (int r = 0; r < RB; ++r) {
             const int j = j0 + r * WAYS;
             l[r] = -INFINITY;
             x[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+            st[r] = 0u;
             if (j < pre_n) {
                 const long long first = base + (long long)j * pre_rows;
                 l[r] = a.plse[first + block_row + g];
                 x[r] = reinterpret_cast<const float4 *>(a.po + first * D)[(long long)c * pre_rows + block_row + g];
             } else if (j < n) {
-                const long long row = (own_row + j - pre_n) * G + g;
-                l[r] = own_lse[row];
-                x[r] = reinterpret_cast<const float4 *>(own_o + row * D)[c];
+                const long long row = own_row + j - pre_n;
+                l[r] = own_lse[row * G + g];
+                x[r] = reinterpret_cast<const float4 *>(own_o + (row * G + g) * D)[c];
+                if (e == 0) st[r] = own_status[row];
             }
         }
 #pragma unroll
         for (int r = 0; r < RB; ++r) {
+            gave_up |= st[r];
             if (l[r] == -INFINITY) continue;  // no token
             if (l[r] > M) {
                 const float down = exp2f(M - l[r]);
@@ -390,21 +417,7 @@ __global__ void __launch_bounds__(kMergeThreads, 5) prefix_merge_kernel(PrefixAr
             acc = make_float4(fmaf(w, x[r].x, acc.x), fmaf(w, x[r].y, acc.y), fmaf(w, x[r].z, acc.z), fmaf(w, x[r].w, acc.w));
         }
     }
-    // waits that gave up: those of the own tokens' workers (a worker's rows of the request's segments), and of
-    // the prefix's kernel
-    if (member) f |= a.head->timeout;
-    if (own.status) {
-        const uint32_t *status = reinterpret_cast<const uint32_t *>(reinterpret_cast<const uint8_t *>(own.status) + shift);
-        const int grp = b / own.greq, r0 = grp * own.greq, Bg = min(own.greq, a.B - r0);
-        const int *units = own.units + (long long)grp * (own.greq * a.kq * a.Hkv + 1);
-        const int U = units[Bg * a.kq * a.Hkv], W = min(own.workers, U);
-        for (int i = warp; i < a.kq * a.Hkv; i += WARPS) {
-            const int k = (b - r0) * a.kq * a.Hkv + i, u0 = units[k], u1 = units[k + 1];
-            if (u1 == u0) continue;
-            const int w0 = pers_worker_of(u0, U, W), w1 = pers_worker_of(u1 - 1, U, W);
-            for (int w = w0 + lane; w <= w1; w += 32) f |= status[k + w];
-        }
-    }
+    f |= gave_up;
     f = __reduce_or_sync(0xffffffffu, f);
     if (lane == 0 && f) atomicOr(&s_flags, f);
     if (WAYS > 1) {
@@ -415,10 +428,12 @@ __global__ void __launch_bounds__(kMergeThreads, 5) prefix_merge_kernel(PrefixAr
         s_o[way][e] = acc;
     }
     __syncthreads();
+    // The bits of checks are those of every CTA of the request; a wait that gave up in the own tokens'
+    // workers is known to the CTA of their head alone.
     const uint32_t flags = s_flags;
-    if (t == 0 && h == 0 && tid == 0) {
-        if (a.flags) a.flags[b] = (uint8_t)flags;
-        if (own.rflags) own.rflags[b] = (uint8_t)flags;
+    if (flags && tid == 0) {
+        if (a.flags) atomic_or_byte(a.flags, b, flags);
+        if (a.rflags) atomic_or_byte(a.rflags, b, flags);
     }
     if (way != 0) return;
     __nv_bfloat16 *out = a.out.p + (long long)b * a.out.sb + (long long)t * a.out.st + (long long)(h * G + g) * a.out.sh + c * 4;
@@ -518,11 +533,16 @@ pfkv_status check_prefix(const pfkv_cache *cache, const pfkv_pages *pages, const
     return PFKV_OK;
 }
 
+// Units a worker above which the split kernel takes 12 workers.  Behind a prefix requests' own tokens
+// are few and of many lengths; a batch of 32 (64 to 2,048 tokens) took 54 us with 8 workers and 51
+// with 12, one of 256 (16 to 512) 151 and 144, one of 16 (100 to 1,000) 110 and 113.
+constexpr int kOwnUnitsPerWorker = 16;
+
 int check_words(const pfkv_pages *p) { return max(1, (p->max_pages + kValTile - 1) / kValTile); }
 
 // Where everything lies in the workspace.
 struct Layout {
-    size_t head, pre_bits, pre_vmax, own_bits, place, pos, members, mstart, seg0, seg, range, units, plse, po, packed, own, mass, total;
+    size_t head, pre_bits, pre_vmax, own_bits, place, pos, members, mstart, seg0, pair, seg, range, units, plse, po, packed, own, mass, total;
     size_t group_bytes;
     DecodePlan plan;  // of the own tokens
 };
@@ -555,6 +575,7 @@ pfkv_status lay_out(const pfkv_cache *c, const pfkv_pages *pages, const pfkv_pag
     l->members = take(4 * (size_t)batch);
     l->mstart = take(4 * (size_t)(NP + 1));
     l->seg0 = take(4 * (size_t)(NP + 1));
+    l->pair = take(sizeof(int2) * (size_t)(NP * H));
     l->seg = take(sizeof(PrefixSeg) * (size_t)S);
     l->range = take(sizeof(PrefixRange) * (size_t)sms);
     l->plse = take(4 * (size_t)partial);
@@ -563,7 +584,7 @@ pfkv_status lay_out(const pfkv_cache *c, const pfkv_pages *pages, const pfkv_pag
     l->own = l->mass = off;
     l->group_bytes = 0;
     if (pages) {
-        const pfkv_status st = make_plan(c, pages, num_q_heads, 0, max_seq_len, sms, &l->plan, mass, kq);
+        const pfkv_status st = make_plan(c, pages, num_q_heads, 0, max_seq_len, sms, &l->plan, mass, kq, false, kOwnUnitsPerWorker);
         if (st != PFKV_OK) return st;
         if (l->plan.kind != 1 || l->plan.nchunks != 1) return PFKV_ERR_UNSUPPORTED;
         // a group of launches keeps its results until the merge; the mass pass's arrays are the call's
@@ -644,6 +665,7 @@ pfkv_status prefix_attn(int tries, const pfkv_cache *cache, const pfkv_pages *pa
     a.members = reinterpret_cast<int *>(ws + l.members);
     a.mstart = reinterpret_cast<int *>(ws + l.mstart);
     a.seg0 = reinterpret_cast<int *>(ws + l.seg0);
+    a.pair = reinterpret_cast<int2 *>(ws + l.pair);
     a.seg = reinterpret_cast<PrefixSeg *>(ws + l.seg);
     a.range = reinterpret_cast<PrefixRange *>(ws + l.range);
     a.plse = reinterpret_cast<float *>(ws + l.plse);
@@ -695,7 +717,8 @@ pfkv_status prefix_attn(int tries, const pfkv_cache *cache, const pfkv_pages *pa
             d.mass_sh = mass_stride_h;
         }
         own = PrefixOwnRows{d.status, d.lse, d.o, l.group_bytes, reinterpret_cast<int *>(ws + l.units), plan.greq,
-                            plan.workers, plan.chunk_tokens, d.lse_fin, d.rflags};
+                            plan.workers, plan.chunk_tokens, d.lse_fin};
+        a.rflags = d.rflags;
     }
     if (launch_prefix_plan(a, own, D, fp8, s) != cudaSuccess) return PFKV_ERR_CUDA;
     if (pages) {

@@ -65,6 +65,7 @@ struct PrefixArgs {
     RowsArg q, out;
     float sm_scale;
     uint8_t *flags;
+    uint8_t *rflags;                // the same for the mass pass, or null
     // workspace
     uint32_t *own_bits, *pre_bits;  // [count][Hkv][htiles] check bits
     float *pre_vmax;                // [prefixes][Hkv][htiles] largest |V scale| of the tile's pages
@@ -72,6 +73,7 @@ struct PrefixArgs {
     PrefixPlace *place;             // [B]
     int *pos, *members;             // [B] position among its prefix's requests (-1: none); requests by prefix
     int *mstart, *seg0;             // [prefixes + 1] first entry of members; first segment
+    int2 *pair;                     // [prefixes][Hkv] first tile and length
     PrefixSeg *seg;
     PrefixRange *range;             // [ctas]
     float *po, *plse;               // partial results: [D / 4][rows8][4] and [rows8] a (segment, CTA)
@@ -90,7 +92,6 @@ struct PrefixOwnRows {
     int *units;          // [groups][greq * kq * Hkv + 1] first unit of every segment (by the plan)
     int greq, workers, chunk_tokens;
     float *lse_fin;      // for the mass pass, or null
-    uint8_t *rflags;
 };
 
 cudaError_t launch_prefix_plan(const PrefixArgs &a, const PrefixOwnRows &o, int D, bool fp8, cudaStream_t s);
