@@ -12,7 +12,7 @@ namespace {
 
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 256;             // eight bits a digit
-constexpr int kSelCluster = 8;            // CTAs a (request, kv head), at most
+constexpr int kSelCluster = 16;           // CTAs a (request, kv head), at most
 constexpr int kGroup = 128;               // keys that a warp takes at a time
 constexpr int kSelSlice = 8192;           // totals that a CTA takes while there are CTAs to share with
 constexpr int kSelKeys = 48 * 1024;       // keys that a CTA keeps in shared memory, at most
@@ -45,7 +45,7 @@ __device__ __forceinline__ bool lengths(const EvictArgs &a, int b, int h, int &n
 }
 
 // --------------------------------------------------------------------------
-// The selection.  A cluster of one to eight CTAs a (request, kv head), each with a slice of the
+// The selection.  A cluster of one to sixteen CTAs a (request, kv head), each with a slice of the
 // totals between the protected ends, which it reads once and keeps as ordered keys in shared
 // memory (what does not fit is read again).  The m-th largest key is found digit by digit, from
 // the top, eight bits each: every CTA counts its keys' digits, the counts are added up over the
@@ -72,11 +72,24 @@ __device__ __forceinline__ int word_of_cta(const int *p, uint32_t rank) {
     return v;
 }
 
+// Sum of the words at this address in CTAs 0 .. n - 1 of the cluster, four on their way at once.
+__device__ __forceinline__ int sum_of_ctas(const int *p, int n) {
+    int sum = 0;
+    for (int r = 0; r < n; r += 4) {
+        int y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = word_of_cta(p, min(r + i, n - 1));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum += r + i < n ? y[i] : 0;
+    }
+    return sum;
+}
+
 struct SelShared {
     int hist[4][kSelBins];     // a digit's counts
     int warp_sum[kSelWarps], warp_eq[kSelWarps];
     int gt, eq;                // keys above and equal to the m-th in this CTA
-    uint32_t bits;             // flag bits
+    uint32_t bits, all_bits;   // flag bits, and those of the cluster
     int digit, need;
 };
 
@@ -148,9 +161,13 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs 
     sync_cluster(ctas);
     bits = sm.bits;
     if (ctas > 1) {
-#pragma unroll
-        for (int r = 0; r < kSelCluster; ++r)  // all on their way at once
-            bits |= (uint32_t)word_of_cta(reinterpret_cast<const int *>(&sm.bits), min(r, ctas - 1));
+        if (warp == 0) {  // a CTA a lane
+            const uint32_t all = __reduce_or_sync(
+                0xffffffffu, (uint32_t)word_of_cta(reinterpret_cast<const int *>(&sm.bits), min(lane, ctas - 1)));
+            if (lane == 0) sm.all_bits = all;
+        }
+        __syncthreads();
+        bits = sm.all_bits;
     }
     if (rank == 0 && tid == 0) a.status[bh] = make_int2((int)bits, k);
     int32_t *kept = a.kept + (long long)b * a.kept_sb + (long long)h * a.kept_sh;
@@ -190,13 +207,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs 
         const int bin = kSelBins - 1 - tid;
         if (tid < kSelBins) {
             if (ctas == 1) c = sum[bin];
-            else {
-                int y[kSelCluster];
-#pragma unroll
-                for (int r = 0; r < kSelCluster; ++r) y[r] = word_of_cta(&sum[bin], min(r, ctas - 1));
-#pragma unroll
-                for (int r = 0; r < kSelCluster; ++r) c += r < ctas ? y[r] : 0;
-            }
+            else c = sum_of_ctas(&sum[bin], ctas);
             x = c;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
@@ -247,17 +258,9 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs 
             }
         }
         sync_cluster(ctas);
-        int y[2][kSelCluster];
-#pragma unroll
-        for (int r = 0; r < kSelCluster; ++r) {
-            y[0][r] = word_of_cta(&sm.gt, min(r, ctas - 1));
-            y[1][r] = word_of_cta(&sm.eq, min(r, ctas - 1));
-        }
-#pragma unroll
-        for (int r = 0; r < kSelCluster; ++r) {
-            at_gt += r < rank ? y[0][r] : 0;
-            at_eq += r < rank ? y[1][r] : 0;
-        }
+        // those of the CTAs before: a CTA a lane
+        at_gt += __reduce_add_sync(0xffffffffu, lane < rank ? word_of_cta(&sm.gt, min(lane, ctas - 1)) : 0);
+        at_eq += __reduce_add_sync(0xffffffffu, lane < rank ? word_of_cta(&sm.eq, min(lane, ctas - 1)) : 0);
         // no CTA leaves while another reads its shared memory
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     }
@@ -435,12 +438,13 @@ __device__ __forceinline__ float new_codes(uint4 (&w)[MoveCfg<D, true>::PASSES],
     }
     if (__any_sync(0xffffffffu, ((lane & 15) < live && odd) || most == 0x7fu))
         return by_definition<D>(pool, row, mine, to, live, lane);
-    if (__any_sync(0xffffffffu, (lane & 15) < live && near)) {
-        const float inv = __frcp_rn(scale);
-        const float2 inv2 = make_float2(inv, inv), down = make_float2(-scale, -scale);
+    const uint32_t lanes = __ballot_sync(0xffffffffu, (lane & 15) < live && near), rows = lanes | (lanes >> 16);
+    const float inv = __frcp_rn(scale);
+    const float2 inv2 = make_float2(inv, inv), down = make_float2(-scale, -scale);
 #pragma unroll
-        for (int i = 0; i < C::PASSES; ++i) {
-            uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    for (int i = 0; i < C::PASSES; ++i) {
+        uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        if ((rows >> (i * C::RPP)) & ((1u << C::RPP) - 1u)) {  // the same for all lanes
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const uint32_t size = u[q] & 0x7f7f7f7fu;
@@ -455,13 +459,8 @@ __device__ __forceinline__ float new_codes(uint4 (&w)[MoveCfg<D, true>::PASSES],
                 }
                 u[q] = code;
             }
-            w[i] = make_uint4(u[0], u[1], u[2], u[3]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < C::PASSES; ++i) {
+        } else {
             const float f = __shfl_sync(0xffffffffu, ratio, i * C::RPP + lane / C::LPR);
-            uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const float2 y0 = mul2(__half22float2(codes_to_half2(u[q])), make_float2(f, f));
@@ -469,8 +468,8 @@ __device__ __forceinline__ float new_codes(uint4 (&w)[MoveCfg<D, true>::PASSES],
                 u[q] = (uint32_t)__nv_cvt_float2_to_fp8x2(y0, __NV_SATFINITE, __NV_E4M3) |
                        (uint32_t)__nv_cvt_float2_to_fp8x2(y1, __NV_SATFINITE, __NV_E4M3) << 16;
             }
-            w[i] = make_uint4(u[0], u[1], u[2], u[3]);
         }
+        w[i] = make_uint4(u[0], u[1], u[2], u[3]);
     }
     store_rows<D, true>(w, pool, to, live, lane);
     return scale;
@@ -480,7 +479,7 @@ __device__ __forceinline__ float new_codes(uint4 (&w)[MoveCfg<D, true>::PASSES],
 // A warp takes `each` units (at most kMoveUnits) of one (request, head), kMoveWarps apart.  What
 // leads to their rows (status, indices and new pages, then old pages) is loaded for all of them at
 // once, half a warp a unit: one after the other, these loads took most of a unit's time.
-constexpr int kMoveUnits = 4;
+constexpr int kMoveUnits = 2;
 
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kMoveWarps * 32, FP8 ? 3 : 4) evict_move_kernel(EvictArgs a, int chunks, int each) {
@@ -494,12 +493,8 @@ __global__ void __launch_bounds__(kMoveWarps * 32, FP8 ? 3 : 4) evict_move_kerne
     for (int i = lane; i < a.Hkv; i += 32) bits |= (uint32_t)a.status[(long long)b * a.Hkv + i].x;
     const int k = a.status[bh].y;
     const int32_t *kept = a.kept + (long long)b * a.kept_sb + (long long)h * a.kept_sh;
-    int from[kMoveUnits / 2], id[kMoveUnits / 2];
-#pragma unroll
-    for (int i = 0; i < kMoveUnits / 2; ++i) {
-        const int at = 2 * i + (lane >> 4), j = (u0 + at * kMoveWarps) * kPage + slot;
-        from[i] = at < each && j < a.max_keep ? kept[j] : 0;
-    }
+    const int at = lane >> 4, j = (u0 + at * kMoveWarps) * kPage + slot;  // this lane's unit and slot
+    const int from = at < each && j < a.max_keep ? kept[j] : 0;
     // a new page a unit, in lane `unit`
     const int up = u0 + min(lane, each - 1) * kMoveWarps;
     const int new_id = up < a.dst.max_pages ? a.dst.block_tables[(long long)b * a.dst.bt_sb + (long long)h * a.dst.bt_sh + up] : 0;
@@ -510,23 +505,16 @@ __global__ void __launch_bounds__(kMoveWarps * 32, FP8 ? 3 : 4) evict_move_kerne
     }
     if (bits) return;
     const int32_t *table = a.src.block_tables + (long long)b * a.src.bt_sb + (long long)h * a.src.bt_sh;
-#pragma unroll
-    for (int i = 0; i < kMoveUnits / 2; ++i) {
-        const int at = 2 * i + (lane >> 4), j = (u0 + at * kMoveWarps) * kPage + slot;
-        const bool there = at < each && j < k;
-        id[i] = there ? table[from[i] / kPage] : -1;
-        if (a.new_mass && at < each && j < a.nm_len)
-            a.new_mass[(long long)b * a.nm_sb + (long long)h * a.nm_sh + j] =
-                there ? a.mass[(long long)b * a.mass_sb + (long long)h * a.mass_sh + from[i]] : 0.f;
-    }
+    const bool there = at < each && j < k;
+    const int id = there ? table[from / kPage] : -1;
+    if (a.new_mass && at < each && j < a.nm_len)
+        a.new_mass[(long long)b * a.nm_sb + (long long)h * a.nm_sh + j] =
+            there ? a.mass[(long long)b * a.mass_sb + (long long)h * a.mass_sh + from] : 0.f;
 #pragma unroll 1
     for (int i = 0; i < each; ++i) {
         const int u = u0 + i * kMoveWarps, live = min(kPage, k - u * kPage);
         if (live <= 0) return;
-        static_assert(kMoveUnits == 4, "two registers of indices");
-        const int src = (i & 1) * 16 + slot;
-        const int page = __shfl_sync(0xffffffffu, i < 2 ? id[0] : id[1], src);
-        const int token = __shfl_sync(0xffffffffu, i < 2 ? from[0] : from[1], src);
+        const int page = __shfl_sync(0xffffffffu, id, i * 16 + slot), token = __shfl_sync(0xffffffffu, from, i * 16 + slot);
         const long long unit = (long long)page * a.Hkv + h, row = unit * kPage + token % kPage;
         const long long to = (long long)__shfl_sync(0xffffffffu, new_id, i) * a.Hkv + h;
         uint4 wk[C::PASSES], wv[C::PASSES];
@@ -597,6 +585,7 @@ cudaError_t launch_evict(const EvictArgs &a, int D, bool fp8, int num_sms, cudaS
 cudaError_t preload_evict() {
     cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)(sizeof(uint32_t) * kSelKeys));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess) e = preload_kernel(evict_select_kernel);
     for (auto *const kernel : {evict_move_kernel<128, true>, evict_move_kernel<128, false>, evict_move_kernel<64, true>,
                                evict_move_kernel<64, false>})

@@ -38,10 +38,11 @@ def _rows(t: Optional[torch.Tensor], dtype, name: str, batch: int, heads: int, l
     """(stride_b, stride_h, length) of rows [B][Hkv][length] with unit stride along tokens."""
     if t is None:
         return 0, 0, 0
-    if (t.dtype != dtype or t.dim() != 3 or t.shape[0] != batch or t.shape[1] != heads
-            or t.shape[2] < least or (t.stride(2) != 1 and t.shape[2] > 1)):
+    shape, stride = t.shape, t.stride()
+    if (t.dtype is not dtype or len(shape) != 3 or shape[0] != batch or shape[1] != heads
+            or shape[2] < least or (stride[2] != 1 and shape[2] > 1)):
         raise ValueError(f"{name}: {dtype} [B][Hkv][>= {least}] with unit stride along tokens")
-    return t.stride(0), t.stride(1), t.shape[2]
+    return stride[0], stride[1], shape[2]
 
 
 def pfkv_kv_evict_workspace_size(cache: B.Cache, pages: B.Pages, max_seq_len: int,

@@ -57,10 +57,9 @@ def pages_struct(p: Optional[B.Pages], dev: int) -> Optional[B._CPages]:
     """A batch's tables of a call on device `dev`, their types checked."""
     if p is None:
         return None
-    R._i32(p.block_tables, "block_tables", dev)
-    R._i32(p.seq_lens, "seq_lens", dev)
-    if p.expected_tags is not None and p.expected_tags.dtype not in R._TAGS:
-        raise ValueError("expected_tags: int32")
+    if (p.block_tables.dtype is not torch.int32 or p.seq_lens.dtype is not torch.int32
+            or p.expected_tags is not None and p.expected_tags.dtype not in R._TAGS):
+        raise ValueError("block_tables, seq_lens and expected_tags: int32")
     return R._pages(p, dev)
 
 
