@@ -52,8 +52,8 @@ __device__ __forceinline__ int table_len(const PrefixTables &t, int i, int h) {
 constexpr int kPlanChunk = 2048;
 constexpr int kPrefixFew = 512, kSegFew = 1024, kPairFew = 512;  // what shared memory has room for
 
-__device__ void plan_segments(const PrefixArgs &a) {
-    __shared__ int count[PFKV_PREFIX_MAX];  // requests of a prefix
+// count: requests of a prefix.
+__device__ void plan_segments(const PrefixArgs &a, int *count) {
     __shared__ int of[kPlanChunk], first_member[kPrefixFew], first_seg[kPrefixFew], seg_tile[kSegFew];
     __shared__ int2 pair_tile[kPairFew];
     __shared__ Two part[kValThreads / 32];
@@ -202,39 +202,53 @@ __device__ void plan_segments(const PrefixArgs &a) {
 }
 
 // First units of the own tokens' segments, group by group, as the split kernel counts them.
-__device__ void plan_own_units(const PrefixArgs &a, const PrefixOwnRows &o) {
+__device__ void plan_own_units(const PrefixArgs &a, const PrefixOwnRows &o, int *count) {
     __shared__ Two part[kValThreads / 32];
     for (int r0 = 0, g = 0; r0 < a.B; r0 += o.greq, ++g) {
         const int K = min(o.greq, a.B - r0) * a.kq * a.Hkv, per = (K + kValThreads - 1) / kValThreads;
         int *units = o.units + (long long)g * (o.greq * a.kq * a.Hkv + 1);
-        const int k0 = min(K, (int)threadIdx.x * per), k1 = min(K, k0 + per);
-        const auto count = [&](int k) {
+        __syncthreads();
+#pragma unroll 2
+        for (int k = threadIdx.x; k < K; k += kValThreads) {
             const int v = k / a.Hkv, r = v / a.kq, n = table_len(a.own, r0 + r, k - v * a.Hkv);
-            return segment_units(n < 0 ? -1 : max(0, n - a.kq + 1 + (v - r * a.kq)), 0, o.chunk_tokens);
-        };
+            count[k] = segment_units(n < 0 ? -1 : max(0, n - a.kq + 1 + (v - r * a.kq)), 0, o.chunk_tokens);
+        }
+        __syncthreads();
+        const int k0 = min(K, (int)threadIdx.x * per), k1 = min(K, k0 + per);
         Two mine{0, 0}, total;
-        for (int k = k0; k < k1; ++k) mine.x += count(k);
+#pragma unroll 1
+        for (int k = k0; k < k1; ++k) mine.x += count[k];
         int at = block_sums_before(mine, part, &total).x;
+#pragma unroll 1
         for (int k = k0; k < k1; ++k) {
             units[k] = at;
-            at += count(k);
+            at += count[k];
         }
         if (threadIdx.x == 0) units[K] = total.x;
     }
 }
 
 // Check bits of one tile of kValTile entries of table row i, head h; VMAX: and its pages' largest |V scale|.
-template <bool VMAX>
+// Rows: a warp a row of at most kValTile / 8 entries, eight rows a CTA (a batch of 256 requests of 8 heads
+// would be 2,048 CTAs).
+__host__ __device__ inline bool short_rows(const PrefixTables &t) { return t.max_pages <= kValTile / (kValThreads / 32); }
+
+template <bool VMAX, bool Rows>
 __device__ void check_tile(const PrefixArgs &a, const PrefixTables &t, int ih, int tile, uint32_t *bits_out, float *vmax_out) {
+    constexpr int STEP = Rows ? 32 : kValThreads;
+    if constexpr (Rows) {
+        ih = ih * (kValThreads / 32) + (threadIdx.x >> 5);
+        if (ih >= t.count * a.Hkv) return;
+    }
     const int i = ih / a.Hkv, h = ih - i * a.Hkv;
     const int n = table_len(t, i, h), np = (n + kPage - 1) / kPage;
-    const int p0 = tile * kValTile + threadIdx.x;
+    const int p0 = tile * kValTile + threadIdx.x % STEP;
     const long long row = (long long)i * t.bt_sb + (long long)h * t.bt_sh;
     int id[kValPer];
     uint32_t want[kValPer], tag[kValPer];
 #pragma unroll
     for (int j = 0; j < kValPer; ++j) {
-        const int p = p0 + j * kValThreads;
+        const int p = p0 + j * STEP;
         id[j] = p < t.max_pages ? t.block_tables[row + p] : 0;
         want[j] = p < t.max_pages && a.page_tags ? t.expected_tags[row + p] : 0u;
     }
@@ -242,7 +256,7 @@ __device__ void check_tile(const PrefixArgs &a, const PrefixTables &t, int ih, i
     float scale[kValPer];
 #pragma unroll
     for (int j = 0; j < kValPer; ++j) {
-        const bool live = p0 + j * kValThreads < np, in_pool = id[j] >= 0 && id[j] < a.num_pages;
+        const bool live = p0 + j * STEP < np, in_pool = id[j] >= 0 && id[j] < a.num_pages;
         if (live && !in_pool) bits |= PFKV_FLAG_BAD_PAGE;
         const long long unit = live && in_pool ? (long long)id[j] * a.Hkv + h : -1;
         tag[j] = unit >= 0 && a.page_tags ? a.page_tags[unit] : want[j];
@@ -255,11 +269,18 @@ __device__ void check_tile(const PrefixArgs &a, const PrefixTables &t, int ih, i
         if (tag[j] != want[j]) bits |= PFKV_FLAG_TAG_MISMATCH;
         top = fmaxf(top, scale[j]);
     }
+    bits = __reduce_or_sync(0xffffffffu, bits);
+    const uint32_t high = __reduce_max_sync(0xffffffffu, __float_as_uint(top));  // not negative: ordered as numbers
+    if constexpr (Rows) {
+        if ((threadIdx.x & 31) == 0) {
+            bits_out[ih] = bits;  // one word a row
+            if (VMAX) vmax_out[ih] = __uint_as_float(high);
+        }
+        return;
+    }
     __shared__ uint32_t all, most;
     if (threadIdx.x == 0) all = most = 0u;
     __syncthreads();
-    bits = __reduce_or_sync(0xffffffffu, bits);
-    const uint32_t high = __reduce_max_sync(0xffffffffu, __float_as_uint(top));  // not negative: ordered as numbers
     if ((threadIdx.x & 31) == 0) {
         if (bits) atomicOr(&all, bits);
         if (VMAX) atomicMax(&most, high);
@@ -276,23 +297,27 @@ constexpr int kPackPer = 4;  // 16-byte chunks a thread packs
 template <bool FP8>
 __global__ void __launch_bounds__(kValThreads) prefix_plan_kernel(PrefixArgs a, PrefixOwnRows o, int D, int pre_tiles, int own_tiles) {
     pdl_enter();
+    static_assert(PFKV_PREFIX_MAX <= kPersMaxSegments, "room for either");
+    __shared__ int count[kPersMaxSegments];
     int x = blockIdx.x;
     if (x == 0) {
-        plan_segments(a);
+        plan_segments(a, count);
         return;
     }
     if (x == 1) {
-        if (o.status) plan_own_units(a, o);
+        if (o.status) plan_own_units(a, o, count);
         return;
     }
     x -= 2;
     if (x < pre_tiles) {
-        check_tile<FP8>(a, a.pre, x / a.pre.htiles, x % a.pre.htiles, a.pre_bits, a.pre_vmax);
+        if (short_rows(a.pre)) check_tile<FP8, true>(a, a.pre, x, 0, a.pre_bits, a.pre_vmax);
+        else check_tile<FP8, false>(a, a.pre, x / a.pre.htiles, x % a.pre.htiles, a.pre_bits, a.pre_vmax);
         return;
     }
     x -= pre_tiles;
     if (x < own_tiles) {
-        check_tile<false>(a, a.own, x / a.own.htiles, x % a.own.htiles, a.own_bits, nullptr);
+        if (short_rows(a.own)) check_tile<false, true>(a, a.own, x, 0, a.own_bits, nullptr);
+        else check_tile<false, false>(a, a.own, x / a.own.htiles, x % a.own.htiles, a.own_bits, nullptr);
         return;
     }
     // queries as rows that follow each other
@@ -482,7 +507,11 @@ cudaError_t preload_merge_d() {
 }  // namespace
 
 cudaError_t launch_prefix_plan(const PrefixArgs &a, const PrefixOwnRows &o, int D, bool fp8, cudaStream_t s) {
-    const long long pre = (long long)a.pre.count * a.Hkv * a.pre.htiles, own = (long long)a.own.count * a.Hkv * a.own.htiles;
+    const auto checks = [&](const PrefixTables &t) {
+        const long long rows = (long long)t.count * a.Hkv;
+        return short_rows(t) ? (rows + kValThreads / 32 - 1) / (kValThreads / 32) : rows * t.htiles;
+    };
+    const long long pre = checks(a.pre), own = checks(a.own);
     const long long chunks = a.packed_q ? (long long)a.B * a.kq * a.Hkv * a.G * (D / 8) : 0;
     const long long pack = (chunks + kPackPer * kValThreads - 1) / (kPackPer * kValThreads);
     const dim3 grid((unsigned)(2 + pre + own + pack)), block(kValThreads);
