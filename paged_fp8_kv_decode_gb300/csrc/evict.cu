@@ -12,7 +12,7 @@ namespace {
 
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 256;             // eight bits a digit
-constexpr int kSelCluster = 16;           // CTAs a (request, kv head), at most
+constexpr int kSelCluster = 12;           // CTAs a (request, kv head), at most (of 16, the chip runs 15 clusters at once)
 constexpr int kGroup = 128;               // keys that a warp takes at a time
 constexpr int kSelSlice = 8192;           // totals that a CTA takes while there are CTAs to share with
 constexpr int kSelKeys = 48 * 1024;       // keys that a CTA keeps in shared memory, at most
@@ -45,7 +45,7 @@ __device__ __forceinline__ bool lengths(const EvictArgs &a, int b, int h, int &n
 }
 
 // --------------------------------------------------------------------------
-// The selection.  A cluster of one to sixteen CTAs a (request, kv head), each with a slice of the
+// The selection.  A cluster of one to twelve CTAs a (request, kv head), each with a slice of the
 // totals between the protected ends, which it reads once and keeps as ordered keys in shared
 // memory (what does not fit is read again).  The m-th largest key is found digit by digit, from
 // the top, eight bits each: every CTA counts its keys' digits, the counts are added up over the
@@ -555,7 +555,7 @@ cudaError_t launch_evict(const EvictArgs &a, int D, bool fp8, int num_sms, cudaS
     int ctas = 1;
     while (ctas < kSelCluster && a.max_seq_len > ctas * kSelSlice &&
            (bh * ctas * 2 <= 2LL * num_sms || a.max_seq_len > ctas * kSelKeys))
-        ctas *= 2;
+        ctas = min(2 * ctas, kSelCluster);
     const int room = min(kSelKeys, ((a.max_seq_len + ctas - 1) / ctas + kGroup - 1) / kGroup * kGroup);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(bh * ctas));
