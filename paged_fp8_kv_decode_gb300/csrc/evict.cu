@@ -482,7 +482,7 @@ __device__ __forceinline__ float new_codes(uint4 (&w)[MoveCfg<D, true>::PASSES],
 constexpr int kMoveUnits = 2;
 
 template <int D, bool FP8>
-__global__ void __launch_bounds__(kMoveWarps * 32, FP8 ? 3 : 4) evict_move_kernel(EvictArgs a, int chunks, int each) {
+__global__ void __launch_bounds__(kMoveWarps * 32, FP8 || D == 64 ? 4 : 3) evict_move_kernel(EvictArgs a, int chunks, int each) {
     pdl_enter();
     using C = MoveCfg<D, FP8>;
     const int bh = blockIdx.x / chunks, chunk = blockIdx.x - bh * chunks;
@@ -529,8 +529,20 @@ __global__ void __launch_bounds__(kMoveWarps * 32, FP8 ? 3 : 4) evict_move_kerne
             }
             // of one unit: bytes and scales as they are
             if (!__all_sync(0xffffffffu, lane >= live || unit == first)) {
-                ks = new_codes<D>(wk, a.k_pages, row, ks, to, live, lane);
-                vs = new_codes<D>(wv, a.v_pages, row, vs, to, live, lane);
+                // K, then V: one copy of the code, which is long
+                void *pool = a.k_pages;
+#pragma unroll 1
+                for (int which = 0; which < 2; ++which) {
+                    const float z = new_codes<D>(wk, pool, row, which ? vs : ks, to, live, lane);
+                    if (which) {
+                        vs = z;
+                    } else {
+                        ks = z;
+                        pool = a.v_pages;
+#pragma unroll
+                        for (int q = 0; q < C::PASSES; ++q) wk[q] = wv[q];
+                    }
+                }
             } else {
                 store_rows<D, FP8>(wk, a.k_pages, to, live, lane);
                 store_rows<D, FP8>(wv, a.v_pages, to, live, lane);

@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kValThreads) prefix_plan_kernel(PrefixArgs a, 
 constexpr int kMergeThreads = 256;
 
 template <int D, int G>
-__global__ void __launch_bounds__(kMergeThreads, 4) prefix_merge_kernel(PrefixArgs a, PrefixOwnRows own, int early) {
+__global__ void __launch_bounds__(kMergeThreads, G == 8 ? 5 : 4) prefix_merge_kernel(PrefixArgs a, PrefixOwnRows own, int early) {
     constexpr int C4 = D / 4, TPR = G * C4, WAYS = kMergeThreads / TPR;
     static_assert(WAYS >= 1 && TPR * WAYS == kMergeThreads, "every thread has a place");
     __shared__ uint32_t s_flags;
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) prefix_merge_kernel(PrefixAr
     float M = -INFINITY, S = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     const int n = pre_n + own_n;
-    constexpr int RB = 6;
+    constexpr int RB = G == 8 ? 4 : 6;
     uint32_t gave_up = member && tid == 0 ? a.head->timeout : 0u;
     for (int j0 = way; j0 < n; j0 += RB * WAYS) {
         float l[RB];
