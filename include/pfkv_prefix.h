@@ -44,7 +44,8 @@ extern "C" {
  *   q, out    : bf16 rows (b, t, hq) of head_dim elements; out may be q
  *   num_q_heads: a multiple G of num_kv_heads with G in {1, 2, 4, 8}
  *   max_seq_len, max_prefix_len: host-known upper bounds of the lengths (a longer one is
- *               flagged PFKV_FLAG_BAD_LENGTH); max_seq_len is not read without pages
+ *               flagged PFKV_FLAG_BAD_LENGTH), 2^30 at most; max_seq_len is not read without
+ *               pages
  *   attn_mass : NULL, or as in pfkv_paged_decode_attn_mass for the requests' own tokens:
  *               to each is added its softmax weight, normalised over all that the row
  *               sees, summed over the G query heads.  Needs pages and kq = 1
@@ -56,7 +57,10 @@ extern "C" {
  * The pools are device memory.  Page ids, lengths and tags of requests and prefixes are
  * checked before any page is read; a request that fails, or whose prefix does, is flagged
  * and all of its rows are zero (and add no mass), as is one whose prefix_of is neither -1
- * nor below prefixes->batch (PFKV_FLAG_BAD_PAGE).  Slots past a last token do not reach
+ * nor below prefixes->batch (PFKV_FLAG_BAD_PAGE).  Every wait of the kernels is bounded: when one over
+ * the prefixes gives up, all requests that have a prefix are flagged PFKV_FLAG_DEVICE_TIMEOUT and
+ * zero; when one over own tokens does, that request is flagged and its rows of that kv head are zero
+ * (and no mass is added).  Slots past a last token do not reach
  * any row, whatever they hold.
  *
  * Arithmetic: scores, softmax statistics, sums and the merge of partial results are fp32;

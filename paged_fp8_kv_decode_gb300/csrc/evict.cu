@@ -17,6 +17,7 @@ constexpr int kGroup = 128;               // keys that a warp takes at a time
 constexpr int kSelSlice = 8192;           // totals that a CTA takes while there are CTAs to share with
 constexpr int kSelKeys = 48 * 1024;       // keys that a CTA keeps in shared memory, at most
 constexpr int kMoveWarps = 8;
+constexpr int kMaxTokens = 1 << 30;       // of a (request, head): indices and their round-ups are ints
 
 // Order of totals as that of unsigned numbers: NaN above all, -0 as 0.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -49,9 +50,13 @@ __device__ __forceinline__ bool lengths(const EvictArgs &a, int b, int h, int &n
 // totals between the protected ends, which it reads once and keeps as ordered keys in shared
 // memory (what does not fit is read again).  The m-th largest key is found digit by digit, from
 // the top, eight bits each: every CTA counts its keys' digits, the counts are added up over the
-// cluster, and the digit is the one in which the m-th falls.  Then every warp counts, over its part of the slice, the keys above the m-th and those equal to it;
-// with the sums of the parts before it, it knows where its kept tokens go: larger ones all, equal
-// ones from the lowest index on.
+// cluster, and the digit is the one in which the m-th falls.  Then every warp counts, over its part
+// of the slice, the keys above the m-th and those equal to it; with the sums of the parts before it,
+// it knows where its kept tokens go: larger ones all, equal ones from the lowest index on.
+//
+// Bound by the latency of its passes: 15 us for 32 x 8 heads of 512 to 8,192 totals (one CTA each), 34 us
+// for 2 x 8 of 200,000 to 262,144 (twelve CTAs each).  Clusters of 16 were slower there (114 against 106
+// us a call), as the chip runs 15 of them at once and the 16th came after.
 // --------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t cta_of_cluster() {
     uint32_t r;
@@ -94,7 +99,7 @@ struct SelShared {
 };
 
 __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs a, int ctas, int room) {
-    extern __shared__ uint32_t keys[];
+    extern __shared__ __align__(16) uint32_t keys[];
     __shared__ SelShared sm;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = ctas == 1 ? 0 : (int)cta_of_cluster();
@@ -170,7 +175,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs 
         bits = sm.all_bits;
     }
     if (rank == 0 && tid == 0) a.status[bh] = make_int2((int)bits, k);
-    int32_t *kept = a.kept + (long long)b * a.kept_sb + (long long)h * a.kept_sh;
+    int32_t *kept = a.kept + (long long)bh * a.max_keep;
     if (bits || m == 0 || m == L) {
         // nothing to choose; the cluster's CTAs leave together (their shared memory is read by others)
         if (!bits)
@@ -301,7 +306,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs 
 }
 
 // --------------------------------------------------------------------------
-// The move.
+// The move: a warp a destination unit, its 16 rows gathered in 16-byte loads.  Bytes: both rows read and
+// written.  BF16: near memory's rate (24 us for 16 x 4 heads of 33 to 20,000 tokens of 64, half kept).  FP8:
+// bound by the ALU's conversions of codes: 46 us for 32 x 8 heads of 512 to 8,192 tokens, a quarter kept,
+// DRAM 35% busy.  (The whole call: 96 us while units with a code near a border took divisions, 57 now.)
 // --------------------------------------------------------------------------
 // Bytes of a row a lane takes, and which.
 template <int D, bool FP8>
@@ -391,7 +399,8 @@ __device__ __noinline__ float by_definition(void *pool, long long row, float min
 // c is subnormal.  Eight t a row say whether any code of it may come near a border.  A ratio
 // within 2^-21 of one keeps every code.  (Borders are met often: z is a code's value over 448, so
 // in the row of the largest, ratios are 14 / m.)
-// (2) Otherwise with a correctly rounded quotient, by Markstein's theorem (IBM J. Res. Dev. 34, 1990): two
+// (2) Otherwise (for the rows that are loaded together with such a row, not for the whole unit)
+// with a correctly rounded quotient, by Markstein's theorem (IBM J. Res. Dev. 34, 1990): two
 // corrections of x times the correctly rounded reciprocal of z.  Magnitudes: a sum would lose a
 // zero's sign.
 // (3) By divisions, for scales so small or large that (1) or (2) might not hold, and codes of NaN.
@@ -492,7 +501,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32, FP8 || D == 64 ? 4 : 3) evict
     uint32_t bits = 0u;
     for (int i = lane; i < a.Hkv; i += 32) bits |= (uint32_t)a.status[(long long)b * a.Hkv + i].x;
     const int k = a.status[bh].y;
-    const int32_t *kept = a.kept + (long long)b * a.kept_sb + (long long)h * a.kept_sh;
+    const int32_t *kept = a.kept + (long long)bh * a.max_keep;
     const int at = lane >> 4, j = (u0 + at * kMoveWarps) * kPage + slot;  // this lane's unit and slot
     const int from = at < each && j < a.max_keep ? kept[j] : 0;
     // a new page a unit, in lane `unit`
@@ -507,6 +516,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32, FP8 || D == 64 ? 4 : 3) evict
     const int32_t *table = a.src.block_tables + (long long)b * a.src.bt_sb + (long long)h * a.src.bt_sh;
     const bool there = at < each && j < k;
     const int id = there ? table[from / kPage] : -1;
+    if (a.kept_out && there) a.kept_out[(long long)b * a.kept_sb + (long long)h * a.kept_sh + j] = from;
     if (a.new_mass && at < each && j < a.nm_len)
         a.new_mass[(long long)b * a.nm_sb + (long long)h * a.nm_sh + j] =
             there ? a.mass[(long long)b * a.mass_sb + (long long)h * a.mass_sh + from] : 0.f;
@@ -617,6 +627,7 @@ pfkv_status evict_sizes(const pfkv_cache *cache, const pfkv_pages *src, int32_t 
     st = check_pages(cache, src);
     if (st != PFKV_OK) return st;
     if (max_seq_len < 0 || max_keep_len < 0) return PFKV_ERR_INVALID_ARG;
+    if (max_seq_len > kMaxTokens || max_keep_len > kMaxTokens) return PFKV_ERR_UNSUPPORTED;
     const long long bh = (long long)src->batch * cache->num_kv_heads;
     if (bh > 0x7fffffffLL) return PFKV_ERR_UNSUPPORTED;
     *status_bytes = up256(sizeof(int2) * (size_t)bh);
@@ -661,6 +672,7 @@ pfkv_status pfkv_kv_evict(const pfkv_cache *cache, const pfkv_pages *src, const 
     if (mass_stride_b < 0 || mass_stride_h < 0) return PFKV_ERR_INVALID_ARG;
     if (new_mass && (new_mass_stride_b < 0 || new_mass_stride_h < 0 || new_mass_len < max_keep_len))
         return PFKV_ERR_INVALID_ARG;
+    if (new_mass && new_mass_len > kMaxTokens) return PFKV_ERR_UNSUPPORTED;
     if (kept && (kept_stride_b < 0 || kept_stride_h < 0)) return PFKV_ERR_INVALID_ARG;
     // rows that results are written to, of max_keep_len or new_mass_len elements, must not overlap
     const auto apart = [&](int64_t sb, int64_t sh, int64_t len) {
@@ -717,9 +729,10 @@ pfkv_status pfkv_kv_evict(const pfkv_cache *cache, const pfkv_pages *src, const 
     a.nm_len = new_mass_len;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     a.status = reinterpret_cast<int2 *>(ws);
-    a.kept = kept ? kept : reinterpret_cast<int32_t *>(ws + status_bytes);
-    a.kept_sb = kept ? kept_stride_b : (long long)cache->num_kv_heads * max_keep_len;
-    a.kept_sh = kept ? kept_stride_h : (long long)max_keep_len;
+    a.kept = reinterpret_cast<int32_t *>(ws + status_bytes);
+    a.kept_out = kept;
+    a.kept_sb = kept_stride_b;
+    a.kept_sh = kept_stride_h;
     a.flags = flags;
     return launch_evict(a, cache->head_dim, cache->dtype == PFKV_KV_FP8_E4M3, sms, static_cast<cudaStream_t>(stream)) ==
                    cudaSuccess

@@ -31,9 +31,10 @@ struct EvictArgs {
     float *new_mass;
     long long nm_sb, nm_sh;
     int nm_len;
-    int32_t *kept;          // the caller's, or the workspace's
+    int32_t *kept_out;      // the caller's, or null
     long long kept_sb, kept_sh;
     int2 *status;           // [B][Hkv] flag bits, and tokens kept (workspace)
+    int32_t *kept;          // [B][Hkv][max_keep] old indices, in order (workspace)
     uint8_t *flags;
 };
 

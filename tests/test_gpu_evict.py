@@ -170,3 +170,18 @@ def test_flags(fp8):
     # bounds: k above the caller's bound
     _, _, _, flags = evict_call(pool, src, dst, k, mass, 1, 1, max_len=60, max_keep=29)
     assert flags[0] == 4 and flags[8] == 4
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_nothing_of_a_flagged_request(fp8):
+    """A request of which one head fails a check: no head's indices, totals or pages are written."""
+    pool = Pool(300, 2, 64, fp8, seed=17)
+    src, dst = pool.tables([60, 90], heads_apart=True), pool.tables([30, 40], heads_apart=True, fill=False)
+    src.block_tables[0, 1, 2] = -1
+    before = [t.clone() for t in (pool.cache.k_pages.view(torch.uint8), pool.cache.v_pages.view(torch.uint8))]
+    lens, new_mass, ids, flags = evict_call(pool, src, dst, i32([[30], [40]]), totals(pool, 2, 90, "plain"), 2, 3)
+    assert flags[:2].tolist() == [2, 0] and lens.tolist() == [[0], [40]]
+    assert (ids[0] == -3).all() and (ids[1] >= 0).all() and new_mass[0].isnan().all()
+    hers = dst.block_tables[0, :, :2].long().flatten()
+    for old, now in zip(before, (pool.cache.k_pages, pool.cache.v_pages)):
+        assert torch.equal(old[hers], now.view(torch.uint8)[hers])

@@ -89,7 +89,7 @@ PREFIX = [
     ({"pre.block_tables": None}, 1), ({"pre.seq_lens": None}, 1), ({"pre.seq_lens": 0x21002}, 3), ({"own.bt_stride_b": 3}, 1),
     ({"pre.bt_stride_h": -1}, 1), ({"pre.expected_tags": 0x90000}, 1), ({"own.expected_tags": 0x90000}, 1),
     ({"cache.page_tags": 0x90000}, 1), ({"cache.page_tags": 0x90000, "own.expected_tags": 0x91000}, 1),
-    ({"batch": 1 << 29, "own": None}, 2),
+    ({"batch": 1 << 29, "own": None}, 2), ({"max_pre": (1 << 30) + 1}, 2), ({"max_len": 0x7FFFFFFF}, 2),
 ]
 
 
@@ -130,6 +130,8 @@ EVICT = [
     ({"src.block_tables": None}, 1), ({"dst.block_tables": None}, 1), ({"dst.block_tables": 0x20002}, 3), ({"dst.bt_stride_b": 3}, 1),
     ({"src.seq_lens": None}, 1), ({"dst.expected_tags": 0xC0000}, 1), ({"cache.page_tags": 0xC0000}, 1),
     ({"cache.page_tags": 0xC0000, "src.expected_tags": 0xD0000}, 1), ({"nm_len": 0x7FFFFFFF, "nm_sh": 1 << 32, "nm_sb": 1 << 34, "src.batch": 16, "dst.batch": 16}, 2),
+    ({"nm_len": 0x7FFFFFFF, "nm_sh": 1 << 32, "nm_sb": 1 << 34}, 2), ({"max_len": 0x7FFFFFF0}, 2),
+    ({"max_keep": 0x7FFFFFFF, "nm": None, "ws_bytes": 1 << 40, "kept": None}, 2),
 ]
 
 
