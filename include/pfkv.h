@@ -206,6 +206,7 @@ pfkv_status pfkv_decode_workspace_size(const pfkv_cache *cache, const pfkv_pages
  *   K, V and q are exact in bf16 and each weight is a pair of bf16 values
  *   whose sum is within 2^-18 of it.  Scores, the running max and sums, and
  *   the merge of partial results are fp32.
+ * A score that is NaN or +inf makes its row NaN, one of -inf is a weight of zero.
  * out is zero for a zero-length head and for every head of a flagged request.
  * When page_tags is non-NULL every live entry's pool tag is compared with the
  * expected tag before any page of the batch is read (a separate validation

@@ -359,9 +359,9 @@ __global__ void __launch_bounds__(NW * 32, 16 / NW) decode_combine_pers_kernel(D
             s4.w = fmaf(sc, v.w, s4.w);
             ws = fmaf(sc, sm.u.red.wsum[w2][g], ws);
         }
-        const float inv = ws > 0.f ? 1.f / ws : 0.f;
+        const float inv = ws == 0.f ? 0.f : 1.f / ws;  // (NaN stays)
         if (a.lse_fin && d4 == 0)
-            a.lse_fin[(long long)(b * Hkv + h) * G + g0 + g] = ws > 0.f ? Mg + plog2(ws) : -INFINITY;
+            a.lse_fin[(long long)(b * Hkv + h) * G + g0 + g] = ws == 0.f ? -INFINITY : Mg + plog2(ws);
         const __nv_bfloat162 lo = __floats2bfloat162_rn(s4.x * inv, s4.y * inv);
         const __nv_bfloat162 hi = __floats2bfloat162_rn(s4.z * inv, s4.w * inv);
         out[i] = make_uint2(*reinterpret_cast<const uint32_t *>(&lo),

@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(SplitCfg<D, G, FP8>::NWARPS * 32)
     float m[G], l[G], o[G][C::E];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-        m[g] = -INFINITY;
+        m[g] = kNoScore;
         l[g] = 0.f;
 #pragma unroll
         for (int e = 0; e < C::E; ++e) o[g][e] = 0.f;
@@ -361,13 +361,14 @@ __global__ void __launch_bounds__(SplitCfg<D, G, FP8>::NWARPS * 32)
         float L = 0.f, O = 0.f;
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-            const float wt = sm.merge_m[w][g] == -INFINITY ? 0.f : fast_exp2(sm.merge_m[w][g] - M);
+            const float wt = fast_exp2(sm.merge_m[w][g] - M);
             L += sm.merge_l[w][g] * wt;
             O += sm.merge_o[w][g][d] * wt;
         }
         const long long row = row0 + (long long)g * nchunks;
-        a.o[row * D + d] = L > 0.f ? O / L : 0.f;
-        if (d == 0) a.lse[row] = L > 0.f ? M + fast_log2(L) : -INFINITY;
+        // (a score that is NaN or +inf makes L NaN, and with it the row and its lse)
+        a.o[row * D + d] = L == 0.f ? 0.f : O / L;
+        if (d == 0) a.lse[row] = L == 0.f ? -INFINITY : M + fast_log2(L);
     }
     if (threadIdx.x == 0) a.status[(long long)bh * nchunks + chunk] = sm.status;
 }
@@ -447,8 +448,8 @@ __global__ void __launch_bounds__(D) decode_combine_kernel(DecodeArgs a, int Hkv
         acc = fmaf(w, o[(long long)cc * D + tid], acc);
     }
     if (a.lse_fin && tid == 0)
-        a.lse_fin[(long long)b * Hq + hq] = wsum > 0.f ? M + __log2f(wsum) : -INFINITY;
-    out[tid] = __float2bfloat16_rn(wsum > 0.f ? acc / wsum : 0.f);
+        a.lse_fin[(long long)b * Hq + hq] = wsum == 0.f ? -INFINITY : M + __log2f(wsum);
+    out[tid] = __float2bfloat16_rn(wsum == 0.f ? 0.f : acc / wsum);
 }
 
 // --------------------------------------------------------------------------

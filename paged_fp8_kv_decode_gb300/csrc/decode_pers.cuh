@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(PersCfg<WK, BF, HD>::NT, 1)
     // o[mt][0] = (dim 16 fg + 2 mt, head A), [1] = (same dim, head B),
     // [2] = (dim + 1, head A), [3] = (dim + 1, head B); O is kept in units of
     // 2^eO (the V-scale reference)
-    float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
+    float mA = kNoScore, mB = kNoScore, lA = 0.f, lB = 0.f;
     float o[C::MT][4];
 #pragma unroll
     for (int mt = 0; mt < C::MT; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
@@ -817,8 +817,8 @@ __global__ void __launch_bounds__(PersCfg<WK, BF, HD>::NT, 1)
             }
             if (grow) {
                 const float nA = fmaxf(mA, mbA), nB = fmaxf(mB, mbB);
-                const float aA = mA == -INFINITY ? 0.f : pexp2(mA - nA);
-                const float aB = mB == -INFINITY ? 0.f : pexp2(mB - nB);
+                const float aA = mA == kNoScore ? 0.f : pexp2(mA - nA);
+                const float aB = mB == kNoScore ? 0.f : pexp2(mB - nB);
                 mA = nA;
                 mB = nB;
                 lA *= aA;
@@ -989,7 +989,9 @@ __global__ void __launch_bounds__(PersCfg<WK, BF, HD>::NT, 1)
 
         const bool seg_end = con.x + n_units >= con.seg_end;
         if (seg_end) {
-            // finish the segment: sum l over the token rows, normalise, write
+            // finish the segment: sum l over the token rows, normalise, write.  A score
+            // that is NaN or +inf makes the sum NaN, and so the row's lse: -inf, for which
+            // the merges skip a row, stands for a sum of zero alone
             float tA = lA, tB = lB;
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) {
@@ -997,7 +999,7 @@ __global__ void __launch_bounds__(PersCfg<WK, BF, HD>::NT, 1)
                 tB += __shfl_xor_sync(0xffffffffu, tB, off);
             }
             const float up = BF ? 1.f : (eO == kNoScale ? 0.f : pow2i(eO));
-            const float iA = tA > 0.f ? up / tA : 0.f, iB = tB > 0.f ? up / tB : 0.f;
+            const float iA = tA == 0.f ? 0.f : up / tA, iB = tB == 0.f ? 0.f : up / tB;
             const long long row = con.k + w;
             // tile mt holds dims (d, d + 1) in components (0, 2) for head A and
             // (1, 3) for head B, with d = obase + 2 mt (BF16 head_dim 128: plus
@@ -1015,15 +1017,15 @@ __global__ void __launch_bounds__(PersCfg<WK, BF, HD>::NT, 1)
             };
             if (2 * ft < G) {
                 store_head(2 * ft, 0, 2, iA);
-                if (fg == 0) a.lse[row * G + 2 * ft] = tA > 0.f ? mA + plog2(tA) : -INFINITY;
+                if (fg == 0) a.lse[row * G + 2 * ft] = tA == 0.f ? -INFINITY : mA + plog2(tA);
             }
             if (2 * ft + 1 < G) {
                 store_head(2 * ft + 1, 1, 3, iB);
-                if (fg == 0) a.lse[row * G + 2 * ft + 1] = tB > 0.f ? mB + plog2(tB) : -INFINITY;
+                if (fg == 0) a.lse[row * G + 2 * ft + 1] = tB == 0.f ? -INFINITY : mB + plog2(tB);
             }
             if (lane == 0) a.status[row] = seg_status;
             seg_status = 0;
-            mA = mB = -INFINITY;
+            mA = mB = kNoScore;
             lA = lB = 0.f;
 #pragma unroll
             for (int mt = 0; mt < C::MT; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;

@@ -28,6 +28,10 @@ constexpr int kValTile = kValThreads * kValPer;
 constexpr int kPersMaxSegments = 4096;
 constexpr int kPersMaxRequests = 4096;
 
+// A running maximum of scores before any was met: below every score, and finite, so that a
+// score of -inf has a weight of zero against it.
+constexpr float kNoScore = -3e38f;
+
 // A bounded wait gives up after this many nanoseconds of %globaltimer.
 constexpr unsigned long long kWaitLimitNs = 100ull * 1000ull * 1000ull;
 
