@@ -63,7 +63,7 @@ def pfkv_kv_evict(cache: B.Cache, pages: B.Pages, new_pages: B.Pages, keep_lens:
                   keep_first: int = 0, keep_last: int = 0, flags: Optional[torch.Tensor] = None,
                   stream=None) -> None:
     """``pages``: the tokens as they are; ``new_pages``: the tables that receive the kept ones
-    (its lengths are not read); keep_lens, new_lens: int32 with the length strides of ``pages``;
+    (its lengths are not read and may be None); keep_lens, new_lens: int32 with the length strides of ``pages``;
     attn_mass: float32 [B][Hkv][>= max_seq_len]; new_mass: float32 [B][Hkv][>= max_keep_len];
     kept: int32 [B][Hkv][>= max_keep_len]; workspace: uint8 of at least
     pfkv_kv_evict_workspace_size(...) bytes; flags uint8 [>= round_up(B, 4)]."""

@@ -54,10 +54,12 @@ def cache_struct(cache: B.Cache, dev: int) -> B._CCache:
 
 
 def pages_struct(p: Optional[B.Pages], dev: int) -> Optional[B._CPages]:
-    """A batch's tables of a call on device `dev`, their types checked."""
+    """A batch's tables of a call on device `dev`, their types checked (lengths may be None
+    where a call does not read them)."""
     if p is None:
         return None
-    if (p.block_tables.dtype is not torch.int32 or p.seq_lens.dtype is not torch.int32
+    if (p.block_tables.dtype is not torch.int32
+            or p.seq_lens is not None and p.seq_lens.dtype is not torch.int32
             or p.expected_tags is not None and p.expected_tags.dtype not in R._TAGS):
         raise ValueError("block_tables, seq_lens and expected_tags: int32")
     return R._pages(p, dev)
