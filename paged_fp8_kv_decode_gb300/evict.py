@@ -45,6 +45,16 @@ def _rows(t: Optional[torch.Tensor], dtype, name: str, batch: int, heads: int, l
     return stride[0], stride[1], shape[2]
 
 
+def _lengths(t: torch.Tensor, pages: B.Pages, heads: int, name: str, dev: int):
+    """Address of int32 numbers that lie as the lengths of `pages` do."""
+    last = (pages.batch - 1) * pages.len_stride_b + (heads - 1) * pages.len_stride_h
+    if not t.is_contiguous() or t.numel() <= last:
+        spans = sum((n - 1) * s for n, s in zip(t.shape, t.stride())) if t.numel() else -1
+        if pages.batch > 0 and spans < last:
+            raise ValueError(f"{name}: int32, one at every place that the lengths of pages have")
+    return R._i32(t, name, dev)
+
+
 def pfkv_kv_evict_workspace_size(cache: B.Cache, pages: B.Pages, max_seq_len: int,
                                  max_keep_len: int) -> int:
     dev = R._current()
@@ -72,10 +82,12 @@ def pfkv_kv_evict(cache: B.Cache, pages: B.Pages, new_pages: B.Pages, keep_lens:
     ms = _rows(attn_mass, torch.float32, "attn_mass", pages.batch, heads, max_seq_len)
     ns = _rows(new_mass, torch.float32, "new_mass", pages.batch, heads, max_keep_len)
     ks = _rows(kept, torch.int32, "kept", pages.batch, heads, max_keep_len)
+    kl = _lengths(keep_lens, pages, heads, "keep_lens", dev)
+    nl = _lengths(new_lens, pages, heads, "new_lens", dev)
     c, p, x = P.cache_struct(cache, dev), P.pages_struct(pages, dev), P.pages_struct(new_pages, dev)
     B._check(lib().pfkv_kv_evict(
-        ctypes.byref(c), ctypes.byref(p), ctypes.byref(x), R._i32(keep_lens, "keep_lens", dev),
+        ctypes.byref(c), ctypes.byref(p), ctypes.byref(x), kl,
         int(keep_first), int(keep_last), R._ptr(attn_mass, dev), ms[0], ms[1], int(max_seq_len),
         int(max_keep_len), R._ptr(workspace, dev), workspace.nbytes,
-        R._i32(new_lens, "new_lens", dev), R._ptr(new_mass, dev), ns[0], ns[1], ns[2],
+        nl, R._ptr(new_mass, dev), ns[0], ns[1], ns[2],
         R._ptr(kept, dev), ks[0], ks[1], R._ptr(flags, dev), R._stream(stream, dev)), "pfkv_kv_evict")

@@ -38,3 +38,20 @@ def test_lengths_of_the_new_pages_may_be_none(seen):
     assert len(seen) == 1 and seen[0][2]._obj.seq_lens is None and seen[0][1]._obj.seq_lens
     with pytest.raises(ValueError, match="int32"):
         P.pages_struct(B.Pages(2, 4, _i32(2, 4), 4, 0, torch.zeros(2), 1, 0), -1)
+
+
+@pytest.mark.parametrize("name", ["keep_lens", "new_lens"])
+def test_lengths_lie_as_those_of_the_pages(seen, name):
+    E.pfkv_kv_evict(**_args(**{name: _i32(6)}))             # as many, in another shape
+    E.pfkv_kv_evict(**_args(**{name: _i32(3, 5)[:, :2]}))   # a view that spans more
+    for t in (_i32(5), _i32(3), _i32(2, 2), _i32(0), _i32(3, 1), _i32(1, 1).expand(3, 2)):
+        with pytest.raises(ValueError, match=name):
+            E.pfkv_kv_evict(**_args(**{name: t}))
+    with pytest.raises(ValueError, match=name):
+        E.pfkv_kv_evict(**_args(**{name: torch.zeros(3, 2, dtype=torch.int64)}))
+    # one length a request for all heads
+    shared = B.Pages(3, 4, _i32(3, 4), 4, 0, _i32(3), 1, 0)
+    E.pfkv_kv_evict(**_args(pages=shared, keep_lens=_i32(3), new_lens=_i32(3)))
+    with pytest.raises(ValueError, match=name):
+        E.pfkv_kv_evict(**_args(**{"pages": shared, "keep_lens": _i32(3), "new_lens": _i32(3), name: _i32(2)}))
+    assert len(seen) == 3
