@@ -82,6 +82,8 @@ def pfkv_kv_evict(cache: B.Cache, pages: B.Pages, new_pages: B.Pages, keep_lens:
     ms = _rows(attn_mass, torch.float32, "attn_mass", pages.batch, heads, max_seq_len)
     ns = _rows(new_mass, torch.float32, "new_mass", pages.batch, heads, max_keep_len)
     ks = _rows(kept, torch.int32, "kept", pages.batch, heads, max_keep_len)
+    if workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace: contiguous uint8")
     kl = _lengths(keep_lens, pages, heads, "keep_lens", dev)
     nl = _lengths(new_lens, pages, heads, "new_lens", dev)
     c, p, x = P.cache_struct(cache, dev), P.pages_struct(pages, dev), P.pages_struct(new_pages, dev)

@@ -55,3 +55,12 @@ def test_lengths_lie_as_those_of_the_pages(seen, name):
     with pytest.raises(ValueError, match=name):
         E.pfkv_kv_evict(**_args(**{"pages": shared, "keep_lens": _i32(3), "new_lens": _i32(3), name: _i32(2)}))
     assert len(seen) == 3
+
+
+def test_workspace(seen):
+    for t in (torch.zeros(1 << 10), torch.zeros(1 << 13, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            E.pfkv_kv_evict(**_args(workspace=t))
+    assert not seen
+    E.pfkv_kv_evict(**_args())
+    assert seen[0][12] == 1 << 12
