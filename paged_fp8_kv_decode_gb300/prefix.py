@@ -109,6 +109,8 @@ def _attn(tries, cache, pages, prefixes, prefix_of, q, sm_scale, max_seq_len, ma
         raise ValueError("q and out: bfloat16 [B][kq][Hq][D]")
     if not (cache.k_pages.is_cuda and cache.v_pages.is_cuda):
         raise ValueError("a pool in device memory")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: contiguous")
     batch, kq, hq, D = q.shape
     if prefix_of.numel() != batch or not prefix_of.is_contiguous():
         raise ValueError("prefix_of: contiguous int32, one a request")
