@@ -680,6 +680,19 @@ __global__ void __launch_bounds__(PersCfg<WK, BF, HD>::NT, 1)
                 }
             }
             asm volatile("redux.sync.max.u32 %0, %0, 0xffffffff;" : "+r"(amax));
+            if (amax >= 0x7f800000u) {  // NaN or infinite in one query head: not the scale of the others
+                amax = 0;
+#pragma unroll
+                for (int j = 0; j < C::QW; ++j) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t wq = word_of(qraw[j], c);
+                        const uint32_t lo = (wq << 16) & 0x7fff0000u, hi = wq & 0x7fff0000u;
+                        amax = max(amax, max(lo < 0x7f800000u ? lo : 0u, hi < 0x7f800000u ? hi : 0u));
+                    }
+                }
+                asm volatile("redux.sync.max.u32 %0, %0, 0xffffffff;" : "+r"(amax));
+            }
             const int eq = min(126, max(-126, (int)(amax >> 23) - 127));
             const float down = pow2i(-eq);
             qmul = a.q_scale * pow2i(eq);

@@ -71,6 +71,28 @@ def test_query(fp8):
     assert not flags[:4].any() and out[[0, 1, 3], 0, 5].isnan().all() and not out[2].any()
 
 
+@pytest.mark.parametrize("what", [NAN, INF, -INF])
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_query_leaves_others(fp8, D, what):
+    """A query head that is not finite leaves the other heads, those of its kv head among them, as they are."""
+    pool = Pool(200, 2, D, fp8, seed=42)
+    pre, own, of = pool.tables([300]), pool.tables([20, 30, 0, 0]), [0, -1, -1, 0]
+    q = rows(pool.g, 4, 1, 8, D, outliers=0)
+    # no element of the head that is spoiled is the largest of its kv head's queries
+    q[:, 0, 5] = q[:, 0, 5].clamp(-1, 1)
+    want, _ = call(pool, own, pre, of, q, 0.125)
+    plain = _decode(pool, own, q[:, 0].contiguous(), 0, 30)
+    q[:, 0, 5, 33] = what
+    out, flags = call(pool, own, pre, of, q, 0.125)
+    again = _decode(pool, own, q[:, 0].contiguous(), 0, 30)
+    assert not flags[:4].any()
+    if what != what:
+        assert out[[0, 1, 3], 0, 5].isnan().all() and again[:2, 5].isnan().all()
+    out[:, 0, 5], again[:, 5] = want[:, 0, 5], plain[:, 5]
+    assert torch.equal(out, want) and torch.equal(again, plain)
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_candidates(fp8):
     """The last of three candidates has a key that is NaN: the rows of those before do not see it."""
