@@ -66,7 +66,8 @@ extern "C" {
  *
  * Arithmetic: scores, softmax statistics, sums and the merge of partial results are fp32;
  * own tokens are those of pfkv_paged_decode_attn.  Over a prefix, BF16 pools: q, k, v are
- * exact and a softmax weight is rounded once to bf16, where it enters the second product.
+ * exact and a softmax weight is rounded once to bf16, where it enters the second product;
+ * sums are finite for values up to 2^90, whatever the scores.
  * FP8 pools: e4m3 values are exact; q enters as a pair of e4m3 values after a power-of-two
  * scaling of its row (exact for elements within 2^9 of the row's largest, others within 2^-17 of it); a weight
  * times its unit's V scale is rounded once to f16 (within 2^-11, or 2^-31 of the prefix's
