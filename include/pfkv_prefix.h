@@ -70,8 +70,9 @@ extern "C" {
  * sums are finite for values up to 2^90, whatever the scores.
  * FP8 pools: e4m3 values are exact; q enters as a pair of e4m3 values after a power-of-two
  * scaling of its row (exact for elements within 2^9 of the row's largest, others within 2^-17 of it); a weight
- * times its unit's V scale is rounded once to f16 (within 2^-11, or 2^-31 of the prefix's
- * largest such product where that is more).
+ * times its unit's V scale is rounded once to f16 (within 2^-11, or, where that is more, within
+ * 2^-31 of the row's largest weight times the largest V scale that the prefix's pages have for
+ * the kv head, whether its page gets weight or holds zeros, whose scale is 1).
  */
 pfkv_status pfkv_prefix_decode_workspace_size(const pfkv_cache *cache, const pfkv_pages *pages,
                                               const pfkv_pages *prefixes, int32_t batch,

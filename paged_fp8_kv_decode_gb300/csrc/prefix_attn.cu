@@ -654,7 +654,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (__any_sync(0xffffffffu, bits != 0u)) continue;
             if constexpr (FP8) {
                 top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // not negative: ordered as numbers
-                // scales over a power of two above the largest, and 2^7: f16's subnormals begin 2^-31 below
+                // scales over a power of two above the largest, and 2^7: half a step of f16's subnormals is
+                // 2^-31 of the largest at most.  (The largest of all pages, by the plan: the scales of a tile
+                // that is not here yet cannot be asked.  Own tokens, a hi + lo pair, have a step of 2^-25.)
                 const int e = min(120, max(-112, (int)(__float_as_uint(top) >> 23) - 126));
                 it.vinv = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
                 it.vback = __uint_as_float((uint32_t)(127 + e - 7) << 23);

@@ -1,8 +1,9 @@
-"""Values of a prefix that are very large or small."""
+"""Values of a prefix that are very large or small, and V scales that are far apart."""
 import pytest
 import torch
 
-from prefix_cases import B, Pool, call, close, rows
+from prefix_cases import B, F16, Pool, call, close, rows
+from latent_cases import score_error, softmax_attend
 from test_gpu_prefix_many import attend_alone
 
 pytestmark = pytest.mark.gpu
@@ -32,3 +33,37 @@ def test_large_values_bf16(size, D, requests):
     out, flags = call(pool, None, pre, of, q, 0.1)
     assert not flags[:len(of)].any()
     close(out, want, tol, "out")
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("apart", [12, 20, 24])
+@pytest.mark.parametrize("D", [128, 64])
+def test_scales_apart_fp8(D, apart, zeros):
+    """A V scale 2^apart above the others, of a page that gets no weight, or that holds zeros: a weight
+    times its V scale is within 2^-11 of itself, or 2^-31 of the largest weight times that scale."""
+    pool = Pool(200, 2, D, True, seed=82)
+    pre, of, scale = pool.tables([700, 300]), [0, 1, 0], 0.125
+    q = rows(pool.g, 3, 1, 8, D, outliers=0).abs()
+    far = pool.row(pre, 0, 0)[9]
+    pool.cache.v_scale[far] = pool.cache.v_scale[pool.row(pre, 0, 0)[:44]].amax(0) * 2.0 ** apart
+    if zeros:
+        pool.cache.v_pages[far] = 0
+    else:  # scores far below all others
+        pool.cache.k_pages[far], pool.cache.k_scale[far] = 0xFE, 1.0
+    out, flags = call(pool, None, pre, of, q, scale)
+    assert not flags[:3].any()
+    for b, n in enumerate((700, 300, 700)):
+        ids = pool.row(pre, of[b], 0)[:(n + 15) // 16]
+        for h in range(2):
+            heads = slice(4 * h, 4 * h + 4)
+            k, v = (pool.values(pre, of[b], h, n, x) for x in "kv")
+            qq = q[b, 0, heads].double()
+            s = qq @ k.T * scale
+            seen = s > s.amax() - 200  # (the far page's weights are zero in any number of bits)
+            err = score_error(qq, k[seen.any(0)], scale) + 2.0 ** -17 * qq.abs().amax(-1) * k[seen.any(0)].abs().sum(-1).amax() * scale
+            want, tol = softmax_attend(s, v, F16, err)
+            p = torch.softmax(s, -1)
+            vs = pool.cache.v_scale[ids, h].double()
+            codes = v / vs.repeat_interleave(16)[:n, None]
+            tol = tol + 2.0 ** -31 * p.amax(-1, keepdim=True) * vs.amax() * codes.abs().sum(0)
+            close(out[b, 0, heads], want, tol, (b, h))
