@@ -124,10 +124,30 @@ struct AppendArgs {
 };
 
 // Launch with programmatic dependent launch allowed: the kernel may be
-// scheduled while the previous kernel in the stream still runs.  Every kernel
-// of this library starts with pdl_enter(), which waits for the previous
-// kernel's completion and memory before anything else, so the overlap is
-// limited to launch latency and is safe whatever precedes it in the stream.
+// scheduled while the previous kernel in the stream still runs.  The rules
+// that keep this safe:
+//  - A kernel touches what the kernel right before it wrote, or writes what
+//    that one reads, only after its wait (pdl_enter(), or
+//    griddepcontrol.wait), which ends when that kernel has ended and its
+//    memory is visible.  Most kernels start with pdl_enter() and are safe
+//    whatever precedes them in the stream.
+//  - Every kernel waits at some point before it ends, so the end of a kernel
+//    is the end of all before it.
+//  - The first kernel of a call starts with pdl_enter(): the call's inputs are
+//    final, and its workspace and outputs free, once that has returned.  (The
+//    COMBINE stage alone takes the place that it has after the SPLIT stage.)
+//  - A later kernel of a call may read, before its wait, the call's inputs, and
+//    what a kernel W of the call wrote if one between the two waited for W
+//    before it let the next one start.  Those that do:
+//      split, combine and latent merge (early parts): inputs; combine also the
+//        validation words, which the split kernel between waited for;
+//      prefix attention after own tokens: the plan, and it waits at its end
+//        alone.  The split kernel between waited for the plan, or for another
+//        split kernel that had;
+//      prefix merge (early part): the plan.  It starts once all CTAs of the
+//        prefix attention have started, which is after that split kernel's
+//        wait, or the prefix attention's own where there are no own tokens.
+//    A kernel put between two of these has to start with pdl_enter().
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                        cudaStream_t stream, Args... args) {

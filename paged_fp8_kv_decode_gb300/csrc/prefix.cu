@@ -345,7 +345,8 @@ __global__ void __launch_bounds__(kValThreads) prefix_plan_kernel(PrefixArgs a, 
 // tokens' split kernel left for its segment; out = sum 2^(lse - M) o / sum 2^(lse - M).
 //
 // What it needs of the plan (and no partial result) is read before its wait: the plan had ended
-// when the kernel before this one let it start (`early`; not where the plan itself is that kernel).
+// when the kernel before this one let it start (`early`; not where the plan itself is that kernel; the
+// rules are at launch_pdl).
 //
 // Bound by the latency of its rows, hence several a thread on their way at once: 9 us for 32 requests
 // of 32 heads, 17 us for 256 of 64 (about 44 MB of partial rows, 2.6 TB/s).

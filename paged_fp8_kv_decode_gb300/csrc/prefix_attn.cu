@@ -184,8 +184,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    // After the own tokens' split kernel, which started once the plan was complete and which this
-    // kernel does not read, only the end waits; the merge that follows needs both.
+    // After the own tokens' split kernel, which lets this one start once its own wait for the plan has
+    // passed and which this kernel does not read, only the end waits; the merge that follows needs both
+    // (the rules are at launch_pdl).
     if (a.after_own) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     else pdl_enter();
     const uint32_t tmem = m.tmem;
