@@ -12,7 +12,7 @@ namespace {
 
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 256;             // eight bits a digit
-constexpr int kSelCluster = 12;           // CTAs a (request, kv head), at most (of 16, the chip runs 15 clusters at once)
+constexpr int kSelCluster = 12;           // CTAs a (request, kv head), at most
 constexpr int kGroup = 128;               // keys that a warp takes at a time
 constexpr int kSelSlice = 8192;           // totals that a CTA takes while there are CTAs to share with
 constexpr int kSelKeys = 48 * 1024;       // keys that a CTA keeps in shared memory, at most
@@ -55,8 +55,9 @@ __device__ __forceinline__ bool lengths(const EvictArgs &a, int b, int h, int &n
 // it knows where its kept tokens go: larger ones all, equal ones from the lowest index on.
 //
 // Bound by the latency of its passes: 15 us for 32 x 8 heads of 512 to 8,192 totals (one CTA each), 34 us
-// for 2 x 8 of 200,000 to 262,144 (twelve CTAs each).  Clusters of 16 were slower there (114 against 106
-// us a call), as the chip runs 15 of them at once and the 16th came after.
+// for 2 x 8 of 200,000 to 262,144 (twelve CTAs each).  Clusters of 16 take 112 us a call there, of 12 103,
+// as the chip runs 15 of the former at once and the 16th came after.  The rule does not look at the
+// number of heads: 8 of them, up to 262,144 totals, take 67 us with 16 and 72 with 12; 24 and 32 the same.
 // --------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t cta_of_cluster() {
     uint32_t r;
@@ -308,8 +309,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs 
 // --------------------------------------------------------------------------
 // The move: a warp a destination unit, its 16 rows gathered in 16-byte loads.  Bytes: both rows read and
 // written.  BF16: near memory's rate (24 us for 16 x 4 heads of 33 to 20,000 tokens of 64, half kept).  FP8:
-// bound by the ALU's conversions of codes: 46 us for 32 x 8 heads of 512 to 8,192 tokens, a quarter kept,
-// DRAM 35% busy.  (The whole call: 96 us while units with a code near a border took divisions, 57 now.)
+// 46 us for 32 x 8 heads of 512 to 8,192 tokens, a quarter kept, and nothing is at its limit (ALU 56% busy
+// with conversions of codes, issue slots 60%, DRAM 35%): latency, at two fifths of the warps, which is what
+// 64 registers (some spilled) and two units a warp, one after the other, leave of it.  (The whole call: 96
+// us while units with a code near a border took divisions, 57 now.)
 // --------------------------------------------------------------------------
 // Bytes of a row a lane takes, and which.
 template <int D, bool FP8>
@@ -572,7 +575,10 @@ __global__ void __launch_bounds__(kMoveWarps * 32, FP8 || D == 64 ? 4 : 3) evict
 
 cudaError_t launch_evict(const EvictArgs &a, int D, bool fp8, int num_sms, cudaStream_t s) {
     // As many CTAs a (request, head) as keep a slice of at most kSelSlice totals, while all run at once
-    // or a slice would not fit in shared memory otherwise.
+    // or a slice would not fit in shared memory otherwise.  All by the bounds, which the host knows, not
+    // by the lengths: shared memory, clusters and grids for more than there is cost time.  32 x 8 heads of
+    // 512 to 8,192 tokens, a quarter kept, take 58 us with exact bounds, 79 with four times them, 185 with
+    // sixteen times; 2 x 8 heads 29, 30 and 31.
     const long long bh = (long long)a.B * a.Hkv;
     int ctas = 1;
     while (ctas < kSelCluster && a.max_seq_len > ctas * kSelSlice &&

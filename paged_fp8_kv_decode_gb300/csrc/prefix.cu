@@ -571,9 +571,12 @@ pfkv_status check_prefix(const pfkv_cache *cache, const pfkv_pages *pages, const
     return PFKV_OK;
 }
 
-// Units a worker above which the split kernel takes 12 workers.  Behind a prefix requests' own tokens
-// are few and of many lengths; a batch of 32 (64 to 2,048 tokens) took 54 us with 8 workers and 51
-// with 12, one of 256 (16 to 512) 151 and 144, one of 16 (100 to 1,000) 110 and 113.
+// Units a worker above which the split kernel takes 12 workers (by the bound of the lengths).  Behind a
+// prefix requests' own tokens are few and of many lengths.  Calls behind 16,384 tokens, 8 heads, lengths
+// up to n, with 8 and with 12 workers (us): 32 requests, n = 300: 40, 41; 600: 43, 42; 1,200 (just below
+// the border): 48, 46; 1,300 (just above): 49, 46; 2,048: 53, 50; 64 requests, n = 600: 56, 54; 650: 58, 55;
+// 128, n = 256: 80, 74; 350: 92, 78.  So 12 gain most where there are many requests and lose where few are long
+// (8 requests, n = 4,800: 47, 49; 5,200: 47, 50), which a border in units cannot tell apart.
 constexpr int kOwnUnitsPerWorker = 16;
 
 int check_words(const pfkv_pages *p) { return max(1, (p->max_pages + kValTile - 1) / kValTile); }
