@@ -14,10 +14,14 @@
 // both (a group's weights overwrite its scores and are read from there as the A operand) and O of
 // both.
 //
-// BF16 pools: K and V come by TMA as the operands that they are; weights are bf16.
+// A weight enters the second product as a pair of 16-bit values, upper bits and what is left of them, in
+// two instructions: rounded once to bf16 or f16 it would be off by 2^-8 or 2^-11 of w |v|, which a sum of
+// large values that cancel does not shrink, and the result by more than the library's bound for attention
+// (nine times it for BF16 pools where w |v| sums to 50).  The pair costs 2 to 11% of a call.
+// BF16 pools: K and V come by TMA as the operands that they are; weights are pairs of bf16.
 // FP8 pools: K comes as it is too, and Q enters as a pair of e4m3 values (hi + lo, two products of
 // half the cost of one in 16 bits); two warps convert V to f16 (exact), and weights times their
-// unit's V scale are f16.  K's scales are applied to the scores, 16 columns at a time.
+// unit's V scale are pairs of f16.  K's scales are applied to the scores, 16 columns at a time.
 //
 // Roles of the twelve warps: 0-3 and 4-7 softmax; 8 issues the products; 9 finds the segments and
 // loads K and the scales; 10 and 11 load the V of four pages of every tile each (FP8: and convert it).  A
@@ -402,19 +406,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                             vf[3] = v.w * vinv;
                         }
 #pragma unroll
-                        for (int g = 2 * half; g < 2 * half + 2; ++g) {
-                            float w[16];  // packed pairs
+                        for (int p = 4 * half; p < 4 * half + 4; ++p) {
+                            float w[16];  // packed pairs of 16 weights: upper parts, then what is left of them
 #pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                const int p = 2 * g + (e >> 4);
+                            for (int e = 0; e < 16; e += 2) {
+                                const float *const s2 = &x[p >> 1][(p & 1) * 16 + e];
                                 const float fp = FP8 ? f[p] : a2;
-                                float2 y = fma2(make_float2(x[g][e], x[g][e + 1]), make_float2(fp, fp), base2);
+                                float2 y = fma2(make_float2(s2[0], s2[1]), make_float2(fp, fp), base2);
                                 y = make_float2(fast_exp2(y.x), fast_exp2(y.y));
                                 sums[(e >> 1) & 3] = add2(sums[(e >> 1) & 3], y);
                                 if constexpr (FP8) y = mul2(y, make_float2(vf[p - 4 * half], vf[p - 4 * half]));
-                                w[e >> 1] = __uint_as_float(pack16(y.x, y.y, !FP8));
+                                // the bits that f16 or bf16 holds, cut off, so that nothing has to be converted back
+                                constexpr uint32_t kUpper = FP8 ? 0xffffe000u : 0xffff0000u;
+                                const uint32_t ux = __float_as_uint(y.x) & kUpper, uy = __float_as_uint(y.y) & kUpper;
+                                const float hx = __uint_as_float(ux), hy = __uint_as_float(uy);
+                                w[e >> 1] = __uint_as_float(FP8 ? pack16(hx, hy, false) : __byte_perm(ux, uy, 0x7632));
+                                const float2 rest = add2(y, make_float2(-hx, -hy));
+                                w[8 + (e >> 1)] = __uint_as_float(pack16(rest.x, rest.y, !FP8));
                             }
-                            tmem_st16(cs + g * 16, w);
+                            tmem_st16(cs + p * 16, w);
                         }
                         tmem_wait_st();
                         tmem_fence_before();
@@ -537,12 +547,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool rest = bar_passed(&m.pready[T][1], parity);
                     tmem_fence_after();
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) umma_ts(co, cs + s * 8, db + s * 128, idO, j > 1 || s > 0);
+                    for (int s = 0; s < 4; ++s) {
+                        umma_ts(co, cs + s * 16, db + s * 128, idO, j > 1 || s > 0);
+                        umma_ts(co, cs + s * 16 + 8, db + s * 128, idO, true);
+                    }
                     if (!rest && !bar_wait(&m.pready[T][1], parity, gave_up, tries)) return false;
                     if (j < mine && !again) keys = bar_passed(&m.kfull[kslot], kparity);
                     tmem_fence_after();
 #pragma unroll
-                    for (int s = 4; s < 8; ++s) umma_ts(co, cs + s * 8, db + s * 128, idO, true);
+                    for (int s = 4; s < 8; ++s) {
+                        umma_ts(co, cs + s * 16, db + s * 128, idO, true);
+                        umma_ts(co, cs + s * 16 + 8, db + s * 128, idO, true);
+                    }
                     if (!wide || T == 1) umma_commit(&m.vempty[slot]);
                     if (j == mine) umma_commit(&m.odone[T]);
                 }
@@ -655,9 +671,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (__any_sync(0xffffffffu, bits != 0u)) continue;
             if constexpr (FP8) {
                 top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // not negative: ordered as numbers
-                // scales over a power of two above the largest, and 2^7: half a step of f16's subnormals is
-                // 2^-31 of the largest at most.  (The largest of all pages, by the plan: the scales of a tile
-                // that is not here yet cannot be asked.  Own tokens, a hi + lo pair, have a step of 2^-25.)
+                // scales over a power of two above the largest, and 2^7: half a step of f16's subnormals, for
+                // either of a pair, is 2^-31 of the largest at most.  (The largest of all pages, by the plan: the
+                // scales of a tile that is not here yet cannot be asked.)
                 const int e = min(120, max(-112, (int)(__float_as_uint(top) >> 23) - 126));
                 it.vinv = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
                 it.vback = __uint_as_float((uint32_t)(127 + e - 7) << 23);
