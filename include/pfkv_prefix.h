@@ -68,8 +68,9 @@ extern "C" {
  * own tokens are those of pfkv_paged_decode_attn.  Over a prefix, BF16 pools: q, k, v are
  * exact and a softmax weight enters the second product as a pair of bf16 values whose sum is
  * within 2^-16 of it; sums are finite for values up to 2^90, whatever the scores.
- * FP8 pools: e4m3 values are exact; q enters as a pair of e4m3 values after a power-of-two
- * scaling of its row (exact for elements within 2^9 of the row's largest, others within 2^-17 of it); a weight
+ * FP8 pools: e4m3 values are exact; q enters as a pair of an e4m3 and an e5m2 value after a
+ * power-of-two scaling of its row (exact for elements within 2^13 of the row's largest, others
+ * within 2^-21 of it); a weight
  * times its unit's V scale enters as a pair of f16 values (within 2^-22 of it, or, where that is
  * more, within 2^-30 of the row's largest weight times the largest V scale that the prefix's pages
  * have for the kv head, whether its page gets weight or holds zeros, whose scale is 1).

@@ -19,7 +19,7 @@
 // large values that cancel does not shrink, and the result by more than the library's bound for attention
 // (nine times it for BF16 pools where w |v| sums to 50).  The pair costs 2 to 11% of a call.
 // BF16 pools: K and V come by TMA as the operands that they are; weights are pairs of bf16.
-// FP8 pools: K comes as it is too, and Q enters as a pair of e4m3 values (hi + lo, two products of
+// FP8 pools: K comes as it is too, and Q enters as a pair of 8-bit values (hi e4m3, lo e5m2: two products of
 // half the cost of one in 16 bits); two warps convert V to f16 (exact), and weights times their
 // unit's V scale are pairs of f16.  K's scales are applied to the scores, 16 columns at a time.
 //
@@ -110,7 +110,9 @@ constexpr size_t smem_bytes() {
 }
 static_assert(smem_bytes<128, true>() <= 232448 && smem_bytes<128, false>() <= 232448, "shared memory of one CTA");
 
-// D (+)= A B of 8-bit operands (both e4m3); `up` is the descriptors' upper word.
+// D (+)= A B of 8-bit operands (B e4m3; A e4m3, or e5m2 with this bit of the instruction's descriptor); `up` is
+// the descriptors' upper word.
+constexpr uint32_t kQueryE5M2 = 1u << 7;
 template <uint32_t UP>
 __device__ __forceinline__ void umma_ss_f8(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
     asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\t"
@@ -253,8 +255,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             top = max(top << 16, top & 0x7fff0000u);
 #pragma unroll
                             for (int off = LPR / 2; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-                            // the largest element between 128 and 256: hi is within 2^-4 of an element, and their
-                            // difference, four bits, is exact in lo down to 2^-9; what is not finite spoils the row
+                            // The largest element between 128 and 256.  hi (e4m3) is within 2^-4 of an element down
+                            // to 2^-6, so what is left is 0 to 8 of the element's last places: three bits, or a power
+                            // of two, exact in lo as e5m2, whose steps end at 2^-16.  (As e4m3, whose steps end at
+                            // 2^-9, lo rounded elements below 2^-9 of the largest.)  Smaller elements are within
+                            // 2^-14.  What is not finite spoils the row.
                             const int e = min(126, max(-119, (int)(top >> 23) - 127));
                             float up = __uint_as_float((uint32_t)(127 + 7 - e) << 23);
                             if (a.sm_scale < 0.f) up = -up;
@@ -270,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     const float2 y = mul2(bf16x2_to_float2(u[2 * k + x]), make_float2(up, up));
                                     hh[x] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
                                     const float2 z = e4m3x2_to_float2((uint16_t)hh[x]);
-                                    ll[x] = __nv_cvt_float2_to_fp8x2(make_float2(y.x - z.x, y.y - z.y), __NV_SATFINITE, __NV_E4M3);
+                                    ll[x] = __nv_cvt_float2_to_fp8x2(make_float2(y.x - z.x, y.y - z.y), __NV_SATFINITE, __NV_E5M2);
                                 }
                                 hi[k] = hh[0] | (hh[1] << 16);
                                 lo[k] = ll[0] | (ll[1] << 16);
@@ -588,7 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int part = 0; part < 2; ++part) {
                         const uint32_t da = umma_desc(qt + part * (C::QB / 2), 16);
 #pragma unroll
-                        for (int s = 0; s < D / 32; ++s) umma_ss_f8<UP>(cs, da + 2 * s, db + 2 * s, idS, part > 0 || s > 0);
+                        for (int s = 0; s < D / 32; ++s)
+                            umma_ss_f8<UP>(cs, da + 2 * s, db + 2 * s, part ? idS | kQueryE5M2 : idS, part > 0 || s > 0);
                     }
                 }
                 if (!wide || T == 1) umma_commit(&m.kempty[kslot]);

@@ -1,5 +1,5 @@
 """Attention over a prefix where a rounding of its weights shows most: a few dominant tokens whose large
-values nearly cancel.
+values nearly cancel, and queries whose elements are far apart.
 
 The library's bound for attention, |got - ref| <= 1e-2 + 1e-2 |ref|, holds for requests that have the
 tokens as their own (a weight rounded once to 16 bits would be off by up to 2^-8 or 2^-11 of w |v|, which
@@ -86,4 +86,23 @@ def test_values_that_cancel(fp8, D, requests):
         within(call(pool, pre, no_prefixes(2), [-1], q[:1], scale)[0], want[:1])
         out, flags = call(pool, None, pre, [0] * requests, q, scale)
         assert not flags[:requests].any()
+        within(out, want)
+
+
+@pytest.mark.parametrize("D", [128, 64])
+def test_queries_far_apart(D):
+    """FP8 pools: one element of a query 2,000 to 8,000 times as large as the others, whose products with the
+    keys decide all the same (the key's elements there are zero): queries are exact for such elements."""
+    for k, far in enumerate((2.0 ** 9, 2.0 ** 10, 2.0 ** 11)):
+        pool = Pool(200, 2, D, True, seed=50 + k)
+        pre = pool.tables([500])
+        live = pool.row(pre, 0, 0)[:32]
+        pool.cache.k_pages[live, :, :, 11] = 0
+        pool.cache.k_scale[live] = 0.05
+        q = rows(pool.g, 3, 1, 16, D, outliers=0)
+        q = q.sign() * (q.abs().clamp(0.5, 4))
+        q[..., 11] = 4 * far
+        want, _ = exact(pool, pre, q, D ** -0.5, 500)
+        out, flags = call(pool, None, pre, [0, 0, 0], q, D ** -0.5)
+        assert not flags[:3].any()
         within(out, want)
