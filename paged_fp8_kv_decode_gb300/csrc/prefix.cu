@@ -573,10 +573,10 @@ pfkv_status check_prefix(const pfkv_cache *cache, const pfkv_pages *pages, const
 
 // Units a worker above which the split kernel takes 12 workers (by the bound of the lengths).  Behind a
 // prefix requests' own tokens are few and of many lengths.  Calls behind 16,384 tokens, 8 heads, lengths
-// up to n, with 8 and with 12 workers (us): 32 requests, n = 300: 40, 41; 600: 43, 42; 1,200 (just below
-// the border): 48, 46; 1,300 (just above): 49, 46; 2,048: 53, 50; 64 requests, n = 600: 56, 54; 650: 58, 55;
-// 128, n = 256: 80, 74; 350: 92, 78.  So 12 gain most where there are many requests and lose where few are long
-// (8 requests, n = 4,800: 47, 49; 5,200: 47, 50), which a border in units cannot tell apart.
+// up to n, with 8 and with 12 workers (us): 32 requests, n = 300: 42, 43; 600: 45, 44; 1,200 (just below
+// the border): 50, 48; 1,300 (just above): 51, 49; 2,048: 54, 52; 64 requests, n = 600: 60, 58; 650: 62, 58;
+// 128, n = 256: 87, 82; 350: 99, 86.  So 12 gain most where there are many requests and lose where few are long
+// (8 requests, n = 4,800: 49, 51; 5,200: 49, 53), which a border in units cannot tell apart.
 constexpr int kOwnUnitsPerWorker = 16;
 
 int check_words(const pfkv_pages *p) { return max(1, (p->max_pages + kValTile - 1) / kValTile); }

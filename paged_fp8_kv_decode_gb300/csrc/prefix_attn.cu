@@ -28,10 +28,10 @@
 // page's slab of 2 KB is a copy, and a warp issues one in 67 cycles whatever its size (measured), so three
 // warps share them: one alone would feed 28 bytes a cycle.
 //
-// Measured (among other kernels, inputs not in L2): BF16, 64 rows, 131,072 tokens of 8 heads: 84 us, 6.4
-// TB/s, 94% of the copy rate.  BF16, blocks of 256 rows, 8,192 tokens, 2,048 rows a head: 62 us, 1.1
-// PFLOP/s; what bounds it are the two groups' chains (scores, 32-column loads, maximum, weights, product),
-// with the tensor pipe 51% busy.  FP8, 128 rows, 16,384 tokens of 8 heads: 15 to 22 us, of which the start
+// Measured (inputs not in L2): BF16, 64 rows, 131,072 tokens of 8 heads: 87 us, 6.1 TB/s, 91% of the copy
+// rate.  BF16, blocks of 256 rows, 8,192 tokens, 2,048 rows a head: 78 us, 0.88 PFLOP/s (1.3 with the second
+// products); what bounds it are the two groups' chains (scores, 32-column loads, maximum, weights, products),
+// with the tensor pipe 60% busy.  FP8, 128 rows, 16,384 tokens of 8 heads: 17 to 24 us, of which the start
 // (segment, ids, queries, first copies) and the end of a CTA take as long as four of its seven tiles.
 #include "prefix_internal.cuh"
 #include "umma.cuh"
@@ -47,7 +47,7 @@ constexpr uint32_t kColO = 256;
 // Weights are 2^(score - reference).  The reference is set so far above the maximum, and O rescaled once
 // the maximum is so far above the reference (log2).  f16 weights have 2^7 below 2^8 of room.  bf16's
 // exponents are those of fp32: weights grow from 2^-32, so that O is rescaled as seldom as the maximum
-// grows by 2^40 (8,192 tokens, 256 requests: 136 us a call, 145 with 2^8), and never above 2^8, so that
+// grows by 2^40 (8,192 tokens, 256 requests: 151 us a call, 156 with 2^8), and never above 2^8, so that
 // sums with values up to 2^100 are finite (growing from 1, weights of 2^40 left room for 2^70).
 template <bool FP8>
 constexpr float kAbove = FP8 ? 0.f : 32.f;
