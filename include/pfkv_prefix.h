@@ -62,7 +62,8 @@ extern "C" {
  * zero; when one over own tokens does, that request is flagged and its rows of that kv head are zero
  * (and no mass is added).  Slots past a last token do not reach
  * any row, whatever they hold; a score that is NaN or +inf, over the prefix or among own tokens,
- * makes its row NaN, and the totals that the row adds to.
+ * makes its row NaN, and the totals that the row adds to; a value that is NaN or infinite makes
+ * its element of the rows that see it NaN or infinite.
  *
  * Arithmetic: scores, softmax statistics, sums and the merge of partial results are fp32;
  * own tokens are those of pfkv_paged_decode_attn.  Over a prefix, BF16 pools: q, k, v are

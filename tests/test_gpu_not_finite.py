@@ -108,6 +108,29 @@ def test_candidates(fp8):
     assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_values(fp8, bad):
+    """A value that is not finite, over a prefix and among own tokens: one element of the rows that see it."""
+    pool = Pool(200, 2, 64, fp8, seed=47)
+    pre, own, of = pool.tables([300, 140]), pool.tables([90, 60, 33]), [0, -1, 1]
+    q = rows(pool.g, 3, 1, 8, 64, outliers=0)
+    mass = [torch.zeros(3, 2, 90, device="cuda") for _ in range(2)]
+    want, _ = call(pool, own, pre, of, q, 0.1, mass=mass[0])
+    for pages, i, token, d in ((pre, 0, 210, 5), (own, 1, 17, 40)):
+        page = pool.row(pages, i, 1)[token // PAGE]
+        if fp8:
+            pool.cache.v_pages[page, 1, token % PAGE, d] = 0x7F
+        else:
+            pool.cache.v_pages[page, 1, token % PAGE, d] = bad
+    out, flags = call(pool, own, pre, of, q, 0.1, mass=mass[1])
+    assert not flags[:3].any() and torch.equal(*mass)
+    for b, d in ((0, 5), (1, 40)):
+        assert not out[b, 0, 4:, d].isfinite().any()
+        out[b, 0, 4:, d] = want[b, 0, 4:, d]
+    assert torch.equal(out, want)
+
+
 @pytest.mark.parametrize("first,last", [(21, 22), (0, 16), (0, 48), (3, 50)])
 def test_minus_infinity(first, last):
     """A score of -inf is a weight of zero, for the row and for the totals, whole units of them too."""
